@@ -16,9 +16,10 @@ LIB_PATH = os.path.join(_PKG, "_build", "libjvp_attn.so")
 
 JVP_OK, JVP_ERR_INVALID_ARG, JVP_ERR_UNSUPPORTED, JVP_ERR_ALIGNMENT = 0, 1, 2, 3
 JVP_ERR_CUDA, JVP_ERR_DEVICE_TIMEOUT, JVP_ERR_WORKSPACE, JVP_ERR_BOUNDS = 4, 5, 6, 7
+JVP_ERR_INDEX = 8
 # fixed device scratch of jvp_attn_bwd_dual_noalloc (JVP_BWD_NOALLOC_SCRATCH_BYTES)
 JVP_BWD_NOALLOC_SCRATCH_BYTES = 4 << 20
-JVP_F32, JVP_F16, JVP_BF16 = 0, 1, 2
+JVP_F32, JVP_F16, JVP_BF16, JVP_E4M3 = 0, 1, 2, 3
 JVP_MASK_NONE, JVP_MASK_BOOL, JVP_MASK_ADDITIVE, JVP_MASK_CAUSAL = 0, 1, 2, 3
 JVP_MASK_BOOL_CAUSAL, JVP_MASK_ADDITIVE_CAUSAL = 4, 5
 
@@ -35,6 +36,10 @@ EXPORTS = (
     "jvp_attn_bwd_dual_noalloc",
     "jvp_attn_bwd",
     "jvp_attn_bwd_workspace_size",
+    "jvp_attn_cache_write",
+    "jvp_attn_cache_read",
+    "jvp_attn_decode",
+    "jvp_attn_decode_workspace_size",
     "jvp_attn_get_device_status",
     "jvp_attn_status_string",
     "jvp_attn_last_error",
@@ -60,6 +65,14 @@ class Mask(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
                 ("stride_h", ctypes.c_int64), ("stride_q", ctypes.c_int64),
                 ("stride_k", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    # a paged key-value cache: sizes, type and strides (jvp_cache_t)
+    _fields_ = [("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("B", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("k_strides", Strides), ("v_strides", Strides)]
 
 
 _lock = threading.Lock()
@@ -124,6 +137,22 @@ def load(path: str | None = None):
         lib.jvp_attn_bwd.restype = i32
         lib.jvp_attn_bwd_workspace_size.argtypes = [SP, i32]
         lib.jvp_attn_bwd_workspace_size.restype = ctypes.c_size_t
+        CP, i64 = ctypes.POINTER(Cache), ctypes.c_int64
+        # cache, dtype, T, k, v, strides, block_table, start_pos, cu_seqlens,
+        # k_cache, v_cache, k_scale, v_scale, stream
+        lib.jvp_attn_cache_write.argtypes = [CP, i32, i64, vp, vp, STP] + [vp] * 8
+        lib.jvp_attn_cache_write.restype = i32
+        # cache, dtype, T, k_cache, v_cache, k_scale, v_scale, block_table,
+        # start_pos, cu_seqlens, k, v, strides, stream
+        lib.jvp_attn_cache_read.argtypes = [CP, i32, i64] + [vp] * 9 + [STP, vp]
+        lib.jvp_attn_cache_read.restype = i32
+        # cache, H, dtype, q, q_strides, k_cache, v_cache, k_scale, v_scale,
+        # block_table, seq_lens, scale, o, o_strides, lse, workspace, bytes, stream
+        lib.jvp_attn_decode.argtypes = [CP, i64, i32, vp, STP] + [vp] * 6 + \
+            [f32, vp, STP, vp, vp, ctypes.c_size_t, vp]
+        lib.jvp_attn_decode.restype = i32
+        lib.jvp_attn_decode_workspace_size.argtypes = [CP, i64, i32]
+        lib.jvp_attn_decode_workspace_size.restype = ctypes.c_size_t
         lib.jvp_attn_get_device_status.argtypes = [vp]
         lib.jvp_attn_get_device_status.restype = i32
         lib.jvp_attn_status_string.argtypes = [i32]

@@ -462,6 +462,286 @@ def fwd_dual_host(q, k, v, dq, dk, dv, attn_mask: Optional[torch.Tensor] = None,
     return o_h, t_h
 
 
+# ---- paged key-value cache and the attention over it
+_E4M3 = torch.float8_e4m3fn
+_PLANS = {}
+_PLANS_MAX = 512
+
+
+def _remember(key, plan):
+    """Keeps a validated call description (sizes, types, strides; no addresses)."""
+    if len(_PLANS) >= _PLANS_MAX:
+        _PLANS.clear()
+    _PLANS[key] = plan
+    return plan
+
+
+def _layout(t):
+    """What a call description depends on: all of a tensor but its address and values."""
+    return None if t is None else (t.dtype, t.device, t.shape, t.stride())
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_int32(t, name, shape, device):
+    if t.dtype != torch.int32 or t.device != device:
+        raise ValueError(f"{name} must be an int32 tensor on {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have a unit innermost stride")
+
+
+def _row_strides(t):
+    """Stride record of a packed [T, heads, D] tensor."""
+    return _abi.Strides(0, t.stride(1), t.stride(0), 1)
+
+
+def _check_packed(t, name, ref_dtype, device, shape):
+    if t.dim() != 3 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be [rows, heads, D] = {shape}, got {tuple(t.shape)}")
+    if t.dtype != ref_dtype or t.device != device:
+        raise ValueError(f"{name} must be a {ref_dtype} tensor on {device}")
+    if t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must have a unit innermost stride")
+
+
+def _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale):
+    """Checks the tensors of a paged cache; its description for the library."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, Hkv, page_size, D], got {tuple(k_cache.shape)}")
+    if k_cache.dtype not in _DT and k_cache.dtype != _E4M3:
+        raise TypeError(f"unsupported cache dtype {k_cache.dtype}")
+    if k_cache.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    dev = k_cache.device
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != dev:
+        raise ValueError("v_cache must have k_cache's shape, dtype and device")
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.stride(-1) != 1 and t.numel() > 0:
+            raise ValueError(f"{n} must have a unit innermost stride")
+    pages, hkv, page, D = k_cache.shape
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _check_int32(block_table, "block_table", tuple(block_table.shape), dev)
+    if k_cache.dtype == _E4M3:
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if (t is None or t.dtype != torch.uint8 or t.device != dev
+                    or tuple(t.shape) != (pages, hkv, page) or not t.is_contiguous()):
+                raise ValueError(f"{n} must be a contiguous uint8 [pages, Hkv, page_size] tensor "
+                                 "on the cache's device")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale belong to an e4m3 cache only")
+    sk, sv = k_cache.stride(), v_cache.stride()
+    return _abi.Cache(pages, page, hkv, D, block_table.shape[0], block_table.shape[1],
+                      block_table.stride(0),
+                      _abi.JVP_E4M3 if k_cache.dtype == _E4M3 else _DT[k_cache.dtype],
+                      _abi.Strides(sk[0], sk[1], sk[2], 1), _abi.Strides(sv[0], sv[1], sv[2], 1))
+
+
+class _OnDevice:
+    """Makes a device current for a call, if it is not already."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, index):
+        self.ctx = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens, k_scale, v_scale, k, v):
+    """Description shared by cache_write and cache_read for packed rows k, v."""
+    desc = _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale)
+    dev = k_cache.device
+    if k.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    if k_cache.dtype != _E4M3 and k.dtype != k_cache.dtype:
+        raise ValueError("k and v must have the cache's dtype (unless the cache is e4m3)")
+    shape = (k.shape[0] if k.dim() == 3 else -1, desc.Hkv, desc.D)
+    _check_packed(k, "k", k.dtype, dev, shape)
+    _check_packed(v, "v", k.dtype, dev, shape)
+    if start_pos is not None:
+        _check_int32(start_pos, "start_pos", (desc.B,), dev)
+    if cu_seqlens is not None:
+        _check_int32(cu_seqlens, "cu_seqlens", (desc.B + 1,), dev)
+    elif shape[0] != desc.B:
+        raise ValueError("without cu_seqlens there must be one row per sequence")
+    return desc, (_abi.Strides * 2)(_row_strides(k), _row_strides(v)), _DT[k.dtype]
+
+
+def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                block_table: torch.Tensor, start_pos: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                v_scale: Optional[torch.Tensor] = None) -> None:
+    """Writes new rows of keys and values into the pages of their sequences.
+
+    k, v are [T, Hkv, D], the new rows of all sequences behind one another:
+    sequence b's are ``cu_seqlens[b]:cu_seqlens[b + 1]`` (int32, on the device;
+    None: one row per sequence), and go to its positions ``start_pos[b]`` and
+    on (int32; None: 0).  Position r is row ``r % page_size`` of page
+    ``block_table[b, r // page_size]`` of k_cache, v_cache [pages, Hkv,
+    page_size, D].  The cache has k's dtype, or is ``torch.float8_e4m3fn`` with
+    one scale byte per (page, head, row) in k_scale, v_scale (uint8 [pages,
+    Hkv, page_size]): an entry is ``code * 2**(byte - 127)``, the scale the
+    smallest power of two that fits the row's largest magnitude.  Rows that
+    belong to no sequence are ignored; rows whose place is out of range are
+    skipped and reported by ``device_status`` (JVP_ERR_INDEX).  No two rows of
+    a call may have the same place.
+    """
+    key = ("write", _layout(k), _layout(v), _layout(k_cache), _layout(v_cache),
+           _layout(block_table), _layout(start_pos), _layout(cu_seqlens), _layout(k_scale),
+           _layout(v_scale))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _remember(key, _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens,
+                                         k_scale, v_scale, k, v))
+    desc, strides, dt = plan
+    dev = k_cache.device.index
+    with _OnDevice(dev):
+        st = _abi.load().jvp_attn_cache_write(
+            desc, dt, k.shape[0], k.data_ptr(), v.data_ptr(), strides, block_table.data_ptr(),
+            _data(start_pos), _data(cu_seqlens), k_cache.data_ptr(), v_cache.data_ptr(),
+            _data(k_scale), _data(v_scale), torch.cuda.current_stream(dev).cuda_stream)
+    _abi.check(st)
+
+
+def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+               start_pos: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+               num_rows: Optional[int] = None, k_scale: Optional[torch.Tensor] = None,
+               v_scale: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+               out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """Rows of the cache back as packed k, v [num_rows, Hkv, D].
+
+    The reverse of ``cache_write``: sequence b's positions ``start_pos[b]`` (None:
+    0) and on become rows ``cu_seqlens[b]:cu_seqlens[b + 1]``.  ``num_rows`` is
+    the number of rows to allocate, at least ``cu_seqlens[-1]`` (which lives on
+    the device); ``out`` = (k, v) gives preallocated ones instead.  Without
+    cu_seqlens one row per sequence.  An e4m3 cache's entries become their
+    values in ``dtype`` (default bfloat16).  Rows that belong to no sequence,
+    or whose place is out of range, are not written.
+    """
+    if out is None:
+        if num_rows is None:
+            if cu_seqlens is not None:
+                raise ValueError("num_rows (or out) is needed with cu_seqlens")
+            num_rows = block_table.shape[0]
+        if dtype is None:
+            dtype = torch.bfloat16 if k_cache.dtype == _E4M3 else k_cache.dtype
+        shape = (num_rows, k_cache.shape[1], k_cache.shape[-1])
+        k = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    else:
+        k, v = out
+        if dtype is not None and k.dtype != dtype:
+            raise ValueError(f"out has dtype {k.dtype}, not {dtype}")
+    key = ("read", _layout(k), _layout(v), _layout(k_cache), _layout(v_cache),
+           _layout(block_table), _layout(start_pos), _layout(cu_seqlens), _layout(k_scale),
+           _layout(v_scale))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _remember(key, _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens,
+                                         k_scale, v_scale, k, v))
+    desc, strides, dt = plan
+    dev = k_cache.device.index
+    with _OnDevice(dev):
+        st = _abi.load().jvp_attn_cache_read(
+            desc, dt, k.shape[0], k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale),
+            _data(v_scale), block_table.data_ptr(), _data(start_pos), _data(cu_seqlens),
+            k.data_ptr(), v.data_ptr(), strides, torch.cuda.current_stream(dev).cuda_stream)
+    _abi.check(st)
+    return k, v
+
+
+def _decode_plan(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out):
+    desc = _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale)
+    dev = k_cache.device
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if k_cache.dtype != _E4M3 and q.dtype != k_cache.dtype:
+        raise ValueError("q must have the cache's dtype (unless the cache is e4m3)")
+    H = q.shape[1] if q.dim() == 3 else -1
+    shape = (desc.B, H, desc.D)
+    _check_packed(q, "q", q.dtype, dev, shape)
+    if desc.Hkv <= 0 and H > 0 or desc.Hkv > 0 and H % desc.Hkv != 0:
+        raise ValueError(f"query heads ({H}) must be a multiple of key/value heads ({desc.Hkv})")
+    _check_int32(seq_lens, "seq_lens", (desc.B,), dev)
+    if out is not None:
+        _check_packed(out, "out", q.dtype, dev, shape)
+    with _OnDevice(dev.index):
+        need = int(_abi.load().jvp_attn_decode_workspace_size(desc, H, _DT[q.dtype]))
+    o_strides = _abi.Strides(H * desc.D, desc.D, 0, 1) if out is None else \
+        _abi.Strides(out.stride(0), out.stride(1), 0, 1)
+    return (desc, H, _DT[q.dtype], _abi.Strides(q.stride(0), q.stride(1), 0, 1), o_strides, need,
+            1.0 / math.sqrt(desc.D) if desc.D else 1.0)
+
+
+def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Attention of one new token per sequence over its cached keys and values.
+
+    q is [B, H, D]; the cache and block_table are as for ``cache_write`` (which
+    puts the token's own row in first, if it is to attend to itself); seq_lens
+    (int32 [B], on the device) is the number of positions each sequence
+    attends to.  H is a multiple of the cache's heads (grouped-query
+    attention).  Returns o [B, H, D], or (o, lse) with ``return_lse`` (float32
+    [B, H]); a sequence without keys gets o = 0 and lse = -inf.  ``workspace``
+    (uint8, 16-byte aligned, ``decode_workspace_size`` bytes) is allocated here
+    if not given; calls that share one must not overlap.
+    """
+    key = ("decode", _layout(q), _layout(k_cache), _layout(v_cache), _layout(block_table),
+           _layout(seq_lens), _layout(k_scale), _layout(v_scale), _layout(out))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _remember(key, _decode_plan(q, k_cache, v_cache, block_table, seq_lens, k_scale,
+                                           v_scale, out))
+    desc, H, dt, q_strides, o_strides, need, default_scale = plan
+    device = k_cache.device
+    o = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else out
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if return_lse else None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    with _OnDevice(device.index):
+        st = _abi.load().jvp_attn_decode(
+            desc, H, dt, q.data_ptr(), q_strides, k_cache.data_ptr(), v_cache.data_ptr(),
+            _data(k_scale), _data(v_scale), block_table.data_ptr(), seq_lens.data_ptr(),
+            default_scale if scale is None else float(scale), o.data_ptr(), o_strides, _data(lse),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            torch.cuda.current_stream(device.index).cuda_stream)
+    _abi.check(st)
+    return (o, lse) if return_lse else o
+
+
+def decode_workspace_size(k_cache: torch.Tensor, block_table: torch.Tensor, H: int,
+                          dtype: Optional[torch.dtype] = None) -> int:
+    """Bytes of scratch that attention_decode needs for H query heads over this
+    cache (``dtype``: of the queries; default the cache's, bfloat16 over e4m3)."""
+    sk = k_cache.stride()
+    strides = _abi.Strides(sk[0], sk[1], sk[2], 1)
+    e4m3 = k_cache.dtype == _E4M3
+    if dtype is None:
+        dtype = torch.bfloat16 if e4m3 else k_cache.dtype
+    pages, hkv, page, D = k_cache.shape
+    desc = _abi.Cache(pages, page, hkv, D, block_table.shape[0], block_table.shape[1],
+                      block_table.stride(0), _abi.JVP_E4M3 if e4m3 else _DT[k_cache.dtype],
+                      strides, strides)
+    with _OnDevice(k_cache.device.index):
+        return int(_abi.load().jvp_attn_decode_workspace_size(desc, int(H), _DT[dtype]))
+
+
 def device_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     """Synchronise the stream and return (and clear) the library's device status."""
     lib = _abi.load()

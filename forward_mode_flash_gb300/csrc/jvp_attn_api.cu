@@ -16,12 +16,15 @@
 
 #include "jvp_attn.h"
 #include "jvp_internal.h"
+#include "serve_internal.h"
 #include "sm103_ptx.cuh"
 
 namespace jvp {
 
-// Bit 0: some bounded device wait ran out.  One word per device (each device
-// that loads the library gets its own copy of this variable).
+// Bit 0: some bounded device wait ran out; bit 1: a bounds check of the debug
+// build failed; bit 2 (kStatusIndex): an index read on the device was out of
+// range.  One word per device (each device that loads the library gets its own
+// copy of this variable).
 __device__ unsigned int g_device_status = 0;
 
 namespace {
@@ -693,6 +696,26 @@ cudaError_t launch_bwd_tc(DType dt, int D, int mask_kind, bool primal, const Bwd
   return cudaErrorInvalidValue;
 }
 
+
+// ---- shared with the other entry points (serve_internal.h)
+jvp_status_t api_fail(jvp_status_t s, const char* msg) { return fail(s, msg); }
+jvp_status_t api_cuda_fail(cudaError_t e) {
+  return fail(JVP_ERR_CUDA, std::string("kernel launch: ") + cudaGetErrorString(e));
+}
+jvp_status_t api_ok() { return ok(); }
+void api_set_path(int path) { t_last_path = path; }
+jvp_status_t api_device(int* num_sms, unsigned int** status) {
+  DeviceInfo* dev = nullptr;
+  const jvp_status_t s = current_device(&dev);
+  if (s != JVP_OK) return s;
+  if (!dev->sm103)
+    return fail(JVP_ERR_UNSUPPORTED, "the current device is not an sm_103 (GB300-class) GPU");
+  *num_sms = dev->num_sms;
+  *status = dev->status;
+  return JVP_OK;
+}
+void* api_tensor_map_encoder() { return reinterpret_cast<void*>(tensor_map_encoder()); }
+
 }  // namespace jvp
 
 extern "C" {
@@ -855,7 +878,10 @@ jvp_status_t jvp_attn_get_device_status(void* stream) {
         if (word & (1u << (8 + k))) what += std::string(what.empty() ? "" : ", ") + kinds[k];
       return jvp::fail(JVP_ERR_BOUNDS, "a device-side bounds check failed (" + what + ")");
     }
-    return jvp::fail(JVP_ERR_DEVICE_TIMEOUT, "a device-side wait ran out of time");
+    if (word & 1u) return jvp::fail(JVP_ERR_DEVICE_TIMEOUT, "a device-side wait ran out of time");
+    return jvp::fail(JVP_ERR_INDEX,
+                     "a page index, position, length or offset read on the device was out of range "
+                     "(what it would have reached was skipped)");
   }
   return jvp::ok();
 }
@@ -870,6 +896,7 @@ const char* jvp_attn_status_string(jvp_status_t status) {
     case JVP_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case JVP_ERR_WORKSPACE: return "workspace missing or too small";
     case JVP_ERR_BOUNDS: return "device-side bounds check failed (debug build)";
+    case JVP_ERR_INDEX: return "index read on the device out of range";
   }
   return "unknown status";
 }

@@ -1,0 +1,122 @@
+// serve_internal.h -- launch descriptions of the packed-prompt attention, the
+// paged key-value cache and the single-token attention over it (not part of
+// the public ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "jvp_attn.h"
+#include "jvp_internal.h"
+
+namespace jvp {
+
+// Bit of the device status word: a page index, length or offset read on the
+// device was out of range (the rows it would have reached were skipped).
+constexpr unsigned kStatusIndex = 4u;
+
+// The caller's cache: key rows [pages, Hkv, page_size, D] (strides b, h, n in
+// elements), value rows likewise, one scale byte per (page, head, row) of an
+// e4m3 cache, and the sequences' pages.
+struct PagedCache {
+  int pages, Hkv, page_size, D;
+  int page_shift;  // log2(page_size) where that is a whole number, else -1
+  int B, max_pages;
+  long long table_stride;
+  const int* table;
+  void *k, *v;
+  Strides sk, sv;
+  uint8_t *k_scale, *v_scale;
+  unsigned int* status;
+};
+
+struct CacheRowsParams {
+  PagedCache c;
+  long long T;      // rows of the packed tensors
+  const int* cu;    // [B + 1], or nullptr: row r belongs to sequence r
+  const int* start; // [B] position of each sequence's first row, or nullptr: 0
+  const void *k, *v;  // rows to write (or, reading, outputs)
+  Strides srk, srv;
+  int vec;          // 16-byte accesses of the packed rows (and as wide ones of the cache) are aligned
+};
+// Writes packed rows into the cache / reads them back.  dt: type of the packed
+// rows; e4m3: the cache holds codes and scales, else entries of type dt.
+cudaError_t launch_cache_write(DType dt, bool e4m3, const CacheRowsParams& p, cudaStream_t stream);
+cudaError_t launch_cache_read(DType dt, bool e4m3, const CacheRowsParams& p, cudaStream_t stream);
+
+struct DecodeParams {
+  PagedCache c;
+  int H, group;        // query heads, and query heads per key/value head
+  int head_blocks;     // blocks of heads_per_block query heads per key/value head
+  int grid;            // CTAs of the attention kernel (the partial states' slots)
+  const int* lens;     // [B] keys of each sequence
+  const void* q;
+  Strides sq;          // b, h
+  void* o;
+  Strides so;
+  float* lse;          // [B, H] or nullptr
+  float scale_log2;    // logit scale * log2(e)
+  float* ws_lse;       // [grid][2][heads_per_block]
+  float* ws_o;         // [grid][2][heads_per_block][D]
+};
+
+constexpr int kDecodeTile = 64;  // keys per scheduling unit
+
+// Which kernel a call takes: tensor cores (16-bit queries, 16-byte aligned
+// rows, D a multiple of 8, of 16 for an e4m3 cache) or CUDA cores.
+// Query heads per CTA: 8 or 16 of a key/value head's group on the tensor
+// cores, 2 or 4 on the CUDA cores.
+inline int decode_heads_per_block(bool tc, int D, int group) {
+  if (tc) return group > 8 ? 16 : 8;
+  return D > 64 ? 2 : 4;
+}
+// CTAs per SM that the split is made for: one resident wave (registers: 168 a
+// thread at three CTAs of 128; the widest variant, 16 heads of 128 columns,
+// spills there).
+constexpr int decode_ctas_per_sm(int D, int head_groups) {
+  return D > 64 && head_groups > 1 ? 2 : 3;
+}
+
+cudaError_t launch_decode(DType dt, bool e4m3, bool tc, bool vec, const DecodeParams& p,
+                          cudaStream_t stream);
+
+struct PackedParams {
+  int T, B, H, Hkv, D, group;
+  int causal;
+  int tok;             // query tokens of one 128-row tile (tensor cores): 128 / group
+  int tiles;           // upper bound of the CTAs a key/value head needs
+  float scale, scale_log2;
+  int neg_scores;      // scale < 0: the score products are formed negated, |scale| applied
+  const int* cu;
+  const void *q, *k, *v;
+  Strides sq, sk, sv;  // h, n
+  void* o;
+  Strides so;
+  float* lse;          // [H, T] or nullptr
+  int out_vec;         // output rows are 16-byte aligned
+  unsigned int* status;
+};
+struct PackedMaps {
+  CUtensorMap q, k, v;
+};
+// Tensor-core kernel (fp16 / bf16, D a multiple of 8 up to 128, group <= 128).
+cudaError_t launch_packed_tc(DType dt, int kernel_d, const PackedMaps& maps, const PackedParams& p,
+                             cudaStream_t stream);
+constexpr int kPackedTileRows = 128;  // rows of a query tile; a CTA has two
+constexpr int kPackedBlockN = 128;    // keys per tile
+// CUDA-core kernel (any type, any D up to 128).
+cudaError_t launch_packed_simt(DType dt, const PackedParams& p, cudaStream_t stream);
+constexpr int kPackedSimtRows = 64;
+
+// What the entry points of the other translation unit share with jvp_attn_api.cu.
+jvp_status_t api_fail(jvp_status_t s, const char* msg);
+jvp_status_t api_cuda_fail(cudaError_t e);
+jvp_status_t api_ok();
+void api_set_path(int path);
+// Current device: JVP_OK with its SM count and status word, or the error.
+jvp_status_t api_device(int* num_sms, unsigned int** status);
+// cuTensorMapEncodeTiled, or nullptr.
+void* api_tensor_map_encoder();
+
+}  // namespace jvp

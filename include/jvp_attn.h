@@ -59,11 +59,19 @@ typedef enum {
   JVP_ERR_CUDA = 4,           /* a CUDA runtime call failed (launch, attribute, ...) */
   JVP_ERR_DEVICE_TIMEOUT = 5, /* a device-side wait ran out (reported asynchronously) */
   JVP_ERR_WORKSPACE = 6,      /* workspace missing or too small */
-  JVP_ERR_BOUNDS = 7          /* debug build only: a device-side bounds check failed
+  JVP_ERR_BOUNDS = 7,         /* debug build only: a device-side bounds check failed
                                  (reported asynchronously, like a timeout) */
+  JVP_ERR_INDEX = 8           /* a page index, position, length or offset that a kernel
+                                 read from device memory was out of range; what it would
+                                 have reached was skipped (reported asynchronously) */
 } jvp_status_t;
 
-typedef enum { JVP_F32 = 0, JVP_F16 = 1, JVP_BF16 = 2 } jvp_dtype_t;
+typedef enum {
+  JVP_F32 = 0,
+  JVP_F16 = 1,
+  JVP_BF16 = 2,
+  JVP_E4M3 = 3 /* 8-bit entries of a paged cache (jvp_cache_t) only */
+} jvp_dtype_t;
 
 /* Mask kinds.  BOOL: uint8 elements, nonzero = the key takes part (SDPA's
  * boolean attn_mask).  ADDITIVE: float32 elements added to the scaled logits;
@@ -361,11 +369,123 @@ jvp_status_t jvp_attn_bwd_dual_noalloc(const jvp_shape_t* shape, jvp_dtype_t dty
                                        void* stream);
 
 /*
+ * Paged key-value cache.  Keys and values of many sequences live in pages of
+ * page_size rows, [pages, Hkv, page_size, D] each for K and V (the strides are
+ * the caller's, innermost 1; k_strides.b is the distance between pages, .n
+ * between rows of a page).  Row r of sequence b's context (its position) is
+ * row r % page_size of page block_table[b, r / page_size]; a sequence's pages
+ * may lie anywhere and in any order, and block-table entries behind its last
+ * page are not read.
+ *
+ * `dtype` is the type of the cache's entries: that of the tensors a call
+ * brings (JVP_F32, JVP_F16, JVP_BF16), or JVP_E4M3: 8-bit codes with one
+ * power-of-two scale per (page, head, row), held as a byte in k_scale and
+ * v_scale (uint8 [pages, Hkv, page_size], contiguous): the entry stands for
+ * code * 2^(byte - 127).
+ *
+ * Block-table entries, positions and lengths are read on the device when the
+ * work runs (so a captured graph follows their current values).  They are
+ * checked there: an entry that names no page, a position outside the block
+ * table, or a length outside [0, max_pages * page_size] reaches no memory;
+ * what it would have reached is skipped, and
+ * jvp_attn_get_device_status() reports JVP_ERR_INDEX.
+ */
+typedef struct {
+  int64_t pages, page_size, Hkv, D; /* D: 1..128 */
+  int64_t B, max_pages;             /* block_table is int32 [B, max_pages] */
+  int64_t table_stride;             /* elements between its rows (>= max_pages, or 0 if B <= 1) */
+  int32_t dtype;                    /* jvp_dtype_t of the entries */
+  jvp_strides_t k_strides, v_strides;
+} jvp_cache_t;
+
+/*
+ * Writes T new rows of keys and values into the pages of their sequences.
+ *
+ *   dtype        element type of k and v (F32, F16, BF16); the cache's, or any
+ *                of the three when the cache holds e4m3.
+ *   k, v         [T, Hkv, D] (in_strides: 2 records; .n is the distance between
+ *                rows, .h between heads, .b unused): the new rows of all
+ *                sequences, one sequence behind the other.
+ *   cu_seqlens   int32 [B + 1], non-decreasing: sequence b's rows are
+ *                cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows before the first
+ *                and behind the last sequence are ignored (a padded batch).
+ *                NULL: one row per sequence (T = B), as for single tokens.
+ *   start_pos    int32 [B]: position of the sequence's first new row; NULL: 0.
+ *   k_cache, v_cache, k_scale, v_scale   written (the scales for e4m3 only).
+ *
+ * e4m3: with top = max |x| over a row's head, the scale is the smallest power
+ * of two 2^e, -127 <= e <= 120, with top <= 448 * 2^e, and each entry is
+ * x / 2^e (exact) rounded to the nearest e4m3 value, ties to even.  A NaN
+ * stays NaN and is not counted in top; an infinity takes e = 120 and reads
+ * back as an infinity.  Rows whose place is out of range are skipped (see
+ * above).  No two rows of a call may have the same place: the pages that a
+ * call writes belong to one sequence each (sequences may share pages that
+ * hold a common prefix and are only read).
+ */
+jvp_status_t jvp_attn_cache_write(const jvp_cache_t* cache, jvp_dtype_t dtype, int64_t T,
+                                  const void* k, const void* v, const jvp_strides_t* in_strides,
+                                  const int32_t* block_table, const int32_t* start_pos,
+                                  const int32_t* cu_seqlens, void* k_cache, void* v_cache,
+                                  uint8_t* k_scale, uint8_t* v_scale, void* stream);
+
+/*
+ * The reverse: copies rows out of the cache into packed k, v [T, Hkv, D]
+ * (out_strides: 2 records), sequence b's positions start_pos[b] (NULL: 0) and
+ * on, as many as cu_seqlens (NULL: one each) gives it.  An e4m3 cache's entries
+ * become their values, rounded once to `dtype`; otherwise `dtype` is the
+ * cache's.  Rows of k and v that belong to no sequence, or whose place is out
+ * of range, are left as they are.
+ */
+jvp_status_t jvp_attn_cache_read(const jvp_cache_t* cache, jvp_dtype_t dtype, int64_t T,
+                                 const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                 const uint8_t* v_scale, const int32_t* block_table,
+                                 const int32_t* start_pos, const int32_t* cu_seqlens, void* k,
+                                 void* v, const jvp_strides_t* out_strides, void* stream);
+
+/*
+ * Attention of one new token per sequence over its cached keys and values:
+ *   s_j = scale q . k_j,  o = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ * over positions j < seq_lens[b] (the token's own row included, if it has been
+ * written).  Query head h reads key/value head h / (H / Hkv).
+ *
+ *   H            query heads, a multiple of the cache's Hkv.
+ *   dtype        element type of q and o; the cache's entries have it too, or
+ *                are e4m3.
+ *   q, o         [B, H, D] (one stride record each: .b, .h; .n unused).
+ *   seq_lens     int32 [B].  A sequence without keys gets o = 0, lse = -inf.
+ *   lse          NULL or [B, H] contiguous float32.
+ *   workspace    device scratch of at least jvp_attn_decode_workspace_size()
+ *                bytes, 16-byte aligned, owned by the caller; contents on entry
+ *                do not matter.  Calls that share one must not overlap.
+ *
+ * The keys of all sequences are split evenly over the GPU whatever their
+ * lengths and joined by a second kernel, in an order that depends on the
+ * lengths only (the same call gives the same bits).  Accumulation and softmax
+ * in fp32; fp16/bf16 queries with D a multiple of 8 (of 16 over e4m3),
+ * 16-byte aligned cache rows and 8-byte aligned query rows use the tensor
+ * cores with 16-bit weights, every other case CUDA cores in fp32.  Keys past
+ * seq_lens and pages that are skipped are never multiplied, whatever they
+ * hold.
+ */
+jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, const void* q,
+                             const jvp_strides_t* q_strides, const void* k_cache,
+                             const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                             const int32_t* block_table, const int32_t* seq_lens, float scale,
+                             void* o, const jvp_strides_t* o_strides, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of jvp_attn_decode on the current device: partial outputs of
+ * at most one resident wave of CTAs, whatever the lengths (a few MiB); 0 for an
+ * empty problem, an invalid description or no device. */
+size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side status word:
  * JVP_ERR_BOUNDS if a kernel of a debug build of the library found an index
  * out of its bounds (and skipped that access), else JVP_ERR_DEVICE_TIMEOUT if
- * any kernel gave up on a wait since the last call, JVP_ERR_CUDA if the
- * stream reports an error, else JVP_OK.
+ * any kernel gave up on a wait since the last call, else JVP_ERR_INDEX if any
+ * kernel read an index out of range, JVP_ERR_CUDA if the stream reports an
+ * error, else JVP_OK.
  */
 jvp_status_t jvp_attn_get_device_status(void* stream);
 
