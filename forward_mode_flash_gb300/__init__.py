@@ -7,6 +7,8 @@ this package holds the ctypes binding (``attention``), work/traffic counts
 does, and raises if it has not been built.
 """
 
-from .api import attention, device_status, fwd_dual, last_path  # noqa: F401
+from .api import (attention, attention_decode, attention_packed, cache_read,  # noqa: F401
+                  cache_write, device_status, fwd_dual, last_path)
 
-__all__ = ["attention", "fwd_dual", "device_status", "last_path"]
+__all__ = ["attention", "attention_decode", "attention_packed", "cache_read", "cache_write",
+           "fwd_dual", "device_status", "last_path"]

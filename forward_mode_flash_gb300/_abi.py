@@ -36,6 +36,7 @@ EXPORTS = (
     "jvp_attn_bwd_dual_noalloc",
     "jvp_attn_bwd",
     "jvp_attn_bwd_workspace_size",
+    "jvp_attn_fwd_packed",
     "jvp_attn_cache_write",
     "jvp_attn_cache_read",
     "jvp_attn_decode",
@@ -65,6 +66,12 @@ class Mask(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
                 ("stride_h", ctypes.c_int64), ("stride_q", ctypes.c_int64),
                 ("stride_k", ctypes.c_int64)]
+
+
+class PackedShape(ctypes.Structure):
+    # Hkv = 0 means Hkv = H
+    _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("Hkv", ctypes.c_int64), ("D", ctypes.c_int64)]
 
 
 class Cache(ctypes.Structure):
@@ -137,6 +144,11 @@ def load(path: str | None = None):
         lib.jvp_attn_bwd.restype = i32
         lib.jvp_attn_bwd_workspace_size.argtypes = [SP, i32]
         lib.jvp_attn_bwd_workspace_size.restype = ctypes.c_size_t
+        # shape, dtype, q, k, v, in_strides, cu_seqlens, causal, scale, o,
+        # out_strides, lse, stream
+        lib.jvp_attn_fwd_packed.argtypes = [ctypes.POINTER(PackedShape), i32, vp, vp, vp, STP, vp,
+                                            i32, f32, vp, STP, vp, vp]
+        lib.jvp_attn_fwd_packed.restype = i32
         CP, i64 = ctypes.POINTER(Cache), ctypes.c_int64
         # cache, dtype, T, k, v, strides, block_table, start_pos, cu_seqlens,
         # k_cache, v_cache, k_scale, v_scale, stream

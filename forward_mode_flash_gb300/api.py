@@ -462,7 +462,7 @@ def fwd_dual_host(q, k, v, dq, dk, dv, attn_mask: Optional[torch.Tensor] = None,
     return o_h, t_h
 
 
-# ---- paged key-value cache and the attention over it
+# ---- packed prompts, the paged key-value cache and the attention over it
 _E4M3 = torch.float8_e4m3fn
 _PLANS = {}
 _PLANS_MAX = 512
@@ -555,6 +555,63 @@ class _OnDevice:
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
+
+
+def _packed_plan(q, k, v, cu_seqlens, out):
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H, D], got {tuple(q.shape)}")
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if q.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    T, H, D = q.shape
+    hkv = k.shape[1] if k.dim() == 3 else -1
+    if hkv <= 0 and H > 0 or hkv > 0 and H % hkv != 0:
+        raise ValueError(f"query heads ({H}) must be a multiple of key/value heads ({hkv})")
+    _check_packed(q, "q", q.dtype, q.device, (T, H, D))
+    _check_packed(k, "k", q.dtype, q.device, (T, hkv, D))
+    _check_packed(v, "v", q.dtype, q.device, (T, hkv, D))
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    B = cu_seqlens.shape[0] - 1
+    _check_int32(cu_seqlens, "cu_seqlens", (B + 1,), q.device)
+    if out is not None:
+        _check_packed(out, "out", q.dtype, q.device, (T, H, D))
+    o_strides = _abi.Strides(0, D, H * D, 1) if out is None else _row_strides(out)
+    return (_abi.PackedShape(T, B, H, hkv, D), _DT[q.dtype],
+            (_abi.Strides * 3)(*[_row_strides(t) for t in (q, k, v)]), o_strides,
+            1.0 / math.sqrt(D) if D else 1.0)
+
+
+def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     is_causal: bool = False, scale: Optional[float] = None,
+                     return_lse: bool = False, out: Optional[torch.Tensor] = None):
+    """Attention over whole prompts of different lengths, packed one behind the other.
+
+    q is [T, H, D], k and v [T, Hkv, D] with H a multiple of Hkv (grouped-query
+    attention); sequence b's rows are ``cu_seqlens[b]:cu_seqlens[b + 1]``
+    (int32 [B + 1], non-decreasing, on the device, read when the work runs) and
+    attend to each other only (``is_causal``: row i to rows j <= i).  Returns o
+    [T, H, D], or (o, lse) with ``return_lse`` (float32 [H, T]).  Rows that
+    belong to no sequence are not written (give ``out`` to keep what it holds).
+    Forward only, as ``attention``.
+    """
+    key = ("packed", _layout(q), _layout(k), _layout(v), _layout(cu_seqlens), _layout(out))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _remember(key, _packed_plan(q, k, v, cu_seqlens, out))
+    shape, dt, strides, o_strides, default_scale = plan
+    device = q.device
+    o = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else out
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=device) \
+        if return_lse else None
+    with _OnDevice(device.index):
+        st = _abi.load().jvp_attn_fwd_packed(
+            shape, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, cu_seqlens.data_ptr(),
+            1 if is_causal else 0, default_scale if scale is None else float(scale), o.data_ptr(),
+            o_strides, _data(lse), torch.cuda.current_stream(device.index).cuda_stream)
+    _abi.check(st)
+    return (o, lse) if return_lse else o
 
 
 def _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens, k_scale, v_scale, k, v):

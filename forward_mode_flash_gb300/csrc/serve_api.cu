@@ -1,5 +1,7 @@
-// serve_api.cu -- entry points of the paged key-value cache and the
-// attention over it: argument checks, path selection and launch descriptions.
+// serve_api.cu -- entry points of the attention over packed prompts, the paged
+// key-value cache and the single-token attention over it: argument checks,
+// path selection and launch descriptions.
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -183,10 +185,115 @@ jvp_status_t check_decode(const jvp_cache_t* c, int64_t H, int dtype) {
   return JVP_OK;
 }
 
+// Tiled map of a packed 16-bit tensor: `inner`, `mid` and `outer` are (D and)
+// two dimensions with their strides in elements, the box {64, bmid, bouter},
+// 128-byte swizzle.  False if the layout cannot be described.
+bool encode_packed(CUtensorMap* map, int dt, const void* ptr, int64_t D, int64_t mid,
+                   int64_t mid_stride, int64_t outer, int64_t outer_stride, int bmid, int bouter) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(api_tensor_map_encoder());
+  if (!enc || !aligned_to(ptr, 16)) return false;
+  // a size-1 dimension's stride is never used; give it a well-formed value
+  if (mid == 1) mid_stride = D;
+  if (outer == 1) outer_stride = D;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(mid),
+                        static_cast<cuuint64_t>(outer), 1};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(mid_stride * 2),
+                           static_cast<cuuint64_t>(outer_stride * 2), static_cast<cuuint64_t>(D * 2)};
+  for (auto s : strides)
+    if (s == 0 || s % 16 != 0 || s >= (1ull << 40)) return false;
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(bmid), static_cast<cuuint32_t>(bouter), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, dt == JVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             4, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace jvp
 
 extern "C" {
+
+jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dtype, const void* q,
+                                 const void* k, const void* v, const jvp_strides_t* in_strides,
+                                 const int32_t* cu_seqlens, int causal, float scale, void* o,
+                                 const jvp_strides_t* out_strides, float* lse, void* stream) {
+  using namespace jvp;
+  api_set_path(0);
+  if (!shape) return api_fail(JVP_ERR_INVALID_ARG, "shape is NULL");
+  const int64_t T = shape->T, B = shape->B, H = shape->H, D = shape->D;
+  const int64_t Hkv = shape->Hkv == 0 ? H : shape->Hkv;
+  if (T < 0 || B < 0 || H < 0 || Hkv < 0) return api_fail(JVP_ERR_INVALID_ARG, "negative size");
+  if (D <= 0) return api_fail(JVP_ERR_INVALID_ARG, "D must be positive");
+  if (D > 128) return api_fail(JVP_ERR_UNSUPPORTED, "D > 128 is not supported");
+  if (!tensor_type(dtype)) return api_fail(JVP_ERR_INVALID_ARG, "unknown dtype");
+  if (!in_strides || !out_strides) return api_fail(JVP_ERR_INVALID_ARG, "strides are NULL");
+  if (!std::isfinite(scale)) return api_fail(JVP_ERR_INVALID_ARG, "scale is not finite");
+  if (causal != 0 && causal != 1) return api_fail(JVP_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (H > 0 && H % Hkv != 0)
+    return api_fail(JVP_ERR_INVALID_ARG, "H must be a multiple of Hkv (grouped-query attention)");
+  // the largest grid: one block per (query head, 1-row sequence or tile)
+  if (T > kMax || B > kMax || H > kMax || T + B > kMax || (H > 0 && T + B > kMax / H))
+    return api_fail(JVP_ERR_UNSUPPORTED, "problem too large for one launch");
+  for (int i = 0; i < 4; ++i) {
+    const jvp_status_t st = check_strides(i < 3 ? in_strides[i] : *out_strides,
+                                          "innermost (d) stride must be 1", "negative stride");
+    if (st != JVP_OK) return st;
+  }
+  if ((T > 1 && out_strides->n == 0) || (H > 1 && out_strides->h == 0))
+    return api_fail(JVP_ERR_INVALID_ARG, "an output must not have a stride of 0");
+  if (T == 0 || B == 0 || H == 0) return api_ok();
+  if (!q || !k || !v || !o || !cu_seqlens)
+    return api_fail(JVP_ERR_INVALID_ARG, "q, k, v, o or cu_seqlens is NULL");
+  const int64_t e = elem_bytes(dtype);
+  if (!aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(v, e) || !aligned_to(o, e))
+    return api_fail(JVP_ERR_ALIGNMENT, "a tensor is not aligned to its element size");
+  if (!aligned_to(lse, 4) || !aligned_to(cu_seqlens, 4))
+    return api_fail(JVP_ERR_ALIGNMENT, "lse or cu_seqlens not 4-byte aligned");
+  int sms = 0;
+  unsigned int* status = nullptr;
+  const jvp_status_t st = api_device(&sms, &status);
+  if (st != JVP_OK) return st;
+
+  PackedParams p{};
+  p.T = static_cast<int>(T), p.B = static_cast<int>(B), p.H = static_cast<int>(H);
+  p.Hkv = static_cast<int>(Hkv), p.D = static_cast<int>(D), p.group = static_cast<int>(H / Hkv);
+  p.causal = causal;
+  p.scale = scale, p.scale_log2 = scale * 1.4426950408889634f;
+  p.cu = cu_seqlens;
+  p.q = q, p.k = k, p.v = v, p.o = o, p.lse = lse, p.status = status;
+  p.sq = used(in_strides[0], 0, H, T), p.sk = used(in_strides[1], 0, Hkv, T);
+  p.sv = used(in_strides[2], 0, Hkv, T), p.so = used(*out_strides, 0, H, T);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool tc = e == 2 && D % 8 == 0 && p.group <= kPackedTileRows && scale != 0.f &&
+            aligned_to(o, 16) && multiple(p.so, 8);
+  PackedMaps maps;
+  if (tc) {
+    // Q: boxes of `tok` tokens times a key/value head's query heads; K, V: key
+    // tiles of one head.  (D < 64 or 128: columns past D are zero-filled.)
+    p.tok = kPackedTileRows / p.group;
+    tc = encode_packed(&maps.q, dtype, q, D, H, p.sq.h, T, p.sq.n, p.group, p.tok) &&
+         encode_packed(&maps.k, dtype, k, D, T, p.sk.n, Hkv, p.sk.h, kPackedBlockN, 1) &&
+         encode_packed(&maps.v, dtype, v, D, T, p.sv.n, Hkv, p.sv.h, kPackedBlockN, 1);
+  }
+  cudaError_t err;
+  if (tc) {
+    p.tiles = static_cast<int>(T / (2 * p.tok) + B);  // >= sum of ceil(length / (2 tok))
+    if (scale < 0.f) {  // negated score products, |scale|
+      p.neg_scores = 1;
+      p.scale = -p.scale, p.scale_log2 = -p.scale_log2;
+    }
+    err = launch_packed_tc(static_cast<DType>(dtype), D <= 64 ? 64 : 128, maps, p, s);
+  } else {
+    p.tiles = static_cast<int>(T / kPackedSimtRows + B);
+    p.vec = e == 4 && D % 4 == 0 && aligned_to(q, 16) && aligned_to(k, 16) && aligned_to(v, 16) &&
+            multiple(p.sq, 4) && multiple(p.sk, 4) && multiple(p.sv, 4);
+    err = launch_packed_simt(static_cast<DType>(dtype), p, s);
+  }
+  if (err != cudaSuccess) return api_cuda_fail(err);
+  api_set_path(tc ? 1 : 2);
+  return api_ok();
+}
 
 jvp_status_t jvp_attn_cache_write(const jvp_cache_t* cache, jvp_dtype_t dtype, int64_t T,
                                   const void* k, const void* v, const jvp_strides_t* in_strides,

@@ -94,7 +94,7 @@ struct PackedParams {
   void* o;
   Strides so;
   float* lse;          // [H, T] or nullptr
-  int out_vec;         // output rows are 16-byte aligned
+  int vec;             // CUDA cores: fp32 input rows are 16-byte aligned, D % 4 == 0
   unsigned int* status;
 };
 struct PackedMaps {

@@ -369,6 +369,40 @@ jvp_status_t jvp_attn_bwd_dual_noalloc(const jvp_shape_t* shape, jvp_dtype_t dty
                                        void* stream);
 
 /*
+ * Attention over whole prompts of different lengths, packed one behind the
+ * other: per sequence b with rows r0 = cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
+ *   S = scale Q K^T,  O = softmax(S) V,  lse = log rowsum(exp S)
+ * over the sequence's own rows (with `causal`, key j for query i iff j <= i).
+ *
+ *   shape        T rows in all, B sequences, H query heads, Hkv key/value heads
+ *                (0: H; query head h reads key/value head h / (H / Hkv)), D.
+ *   q, o         [T, H, D];  k, v [T, Hkv, D].
+ *   in_strides   3 records (q, k, v), out_strides 1 (o): .n between rows, .h
+ *                between heads, .b unused, .d must be 1.
+ *   cu_seqlens   int32 [B + 1] on the device, non-decreasing, within [0, T];
+ *                read when the work runs.  Rows before the first and behind the
+ *                last sequence are neither read nor written (a padded batch).
+ *                Offsets that break this rule reach no memory: their
+ *                sequences are skipped (with none of their rows written) and
+ *                jvp_attn_get_device_status() reports JVP_ERR_INDEX.
+ *   lse          NULL or [H, T] contiguous float32.
+ *
+ * A sequence's results do not depend on the rows of others, whatever they hold.
+ * fp16/bf16 with D a multiple of 8 up to 128, H / Hkv at most 128, a nonzero
+ * scale and 16-byte aligned rows run on the tensor cores (weights rounded to
+ * 16 bits, fp32 accumulation); every other case on the CUDA cores in fp32.
+ * No workspace.
+ */
+typedef struct {
+  int64_t T, B, H, Hkv, D;
+} jvp_packed_shape_t;
+
+jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dtype, const void* q,
+                                 const void* k, const void* v, const jvp_strides_t* in_strides,
+                                 const int32_t* cu_seqlens, int causal, float scale, void* o,
+                                 const jvp_strides_t* out_strides, float* lse, void* stream);
+
+/*
  * Paged key-value cache.  Keys and values of many sequences live in pages of
  * page_size rows, [pages, Hkv, page_size, D] each for K and V (the strides are
  * the caller's, innermost 1; k_strides.b is the distance between pages, .n

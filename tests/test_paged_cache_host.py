@@ -1,4 +1,5 @@
-"""Refusals of the paged-cache entry points: every one before a device is touched."""
+"""Refusals of the packed-prompt and paged-cache entry points: every one before
+a device is touched."""
 
 import ctypes
 
@@ -124,3 +125,42 @@ def test_the_binding_refuses_before_it_calls():
         api.cache_write(x, x, c[0], c[0], t, n)
     with pytest.raises(TypeError):
         api.attention_decode(q, c.long(), c.long(), t, n)
+
+
+def packed(lib, T=8, B=2, H=4, Hkv=2, D=64, dtype=_abi.JVP_BF16, ptr=P, cu=P, causal=1, scale=0.125,
+           ins=None, outs=None, lse=None, no_shape=False):
+    sh = _abi.PackedShape(T, B, H, Hkv, D)
+    st = _abi.Strides(0, 64, 256, 1)
+    return lib.jvp_attn_fwd_packed(None if no_shape else ctypes.byref(sh), dtype, ptr, ptr, ptr,
+                                   ins or (_abi.Strides * 3)(st, st, st), cu, causal, scale, ptr,
+                                   outs or st, lse, None)
+
+
+def test_packed(lib):
+    BAD, UNS = _abi.JVP_ERR_INVALID_ARG, _abi.JVP_ERR_UNSUPPORTED
+    assert packed(lib, no_shape=True) == BAD
+    for kw in (dict(T=-1), dict(B=-1), dict(H=-1), dict(Hkv=-1), dict(D=0), dict(Hkv=3),
+               dict(dtype=_abi.JVP_E4M3), dict(dtype=7), dict(causal=2), dict(scale=float("inf")),
+               dict(ptr=None), dict(cu=None), dict(outs=_abi.Strides(0, 64, 0, 1)),
+               dict(outs=_abi.Strides(0, 0, 256, 1)), dict(outs=_abi.Strides(0, 64, -256, 1)),
+               dict(ins=(_abi.Strides * 3)(*[_abi.Strides(0, 64, 256, 2)] * 3))):
+        assert packed(lib, **kw) == BAD, kw
+    for kw in (dict(D=136), dict(T=1 << 31), dict(B=1 << 31), dict(T=1 << 30, H=4)):
+        assert packed(lib, **kw) == UNS, kw
+    for kw in (dict(ptr=ctypes.c_void_p(0x10001)), dict(cu=ctypes.c_void_p(0x10002)),
+               dict(lse=ctypes.c_void_p(0x10002))):
+        assert packed(lib, **kw) == _abi.JVP_ERR_ALIGNMENT, kw
+    for kw in (dict(T=0), dict(B=0), dict(H=0, Hkv=0)):
+        assert packed(lib, ptr=None, cu=None, **kw) == _abi.JVP_OK, kw
+    assert lib.jvp_attn_debug_last_path() == 0
+
+
+def test_the_packed_binding_refuses_before_it_calls():
+    q, k = torch.zeros(5, 4, 64), torch.zeros(5, 2, 64)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.attention_packed(q, k, k, cu)
+    with pytest.raises(ValueError, match="T, H, D"):
+        api.attention_packed(q[0], k, k, cu)
+    with pytest.raises(TypeError):
+        api.attention_packed(q.long(), k.long(), k.long(), cu)
