@@ -88,7 +88,7 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float a, float b) {
 // ------------------------------------------------------------------ writing
 // VEC elements of type T are 16 bytes; D is a multiple of VEC.
 template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) cache_write_vec(const CacheRowsParams p, int lanes) {
+__global__ void __launch_bounds__(kWarps * 32, 4) cache_write_vec(const CacheRowsParams p, int lanes) {
   constexpr int VEC = 16 / sizeof(T);
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_vec(const CacheRowsPa
   // group of `lanes` lanes (a power of two) per head, 32 / lanes heads at once
   const int per = 32 / lanes, sub = lane / lanes, dl = (lane & (lanes - 1)) * VEC;
   const bool in_row = dl < p.c.D;
-  constexpr int UN = 4;  // heads of one lane group in flight, for K and V each
+  constexpr int UN = E4M3 ? 2 : 4;  // heads of one lane group in flight, for K and V each
   for (int h0 = 0; h0 < p.c.Hkv; h0 += per * UN) {
     uint4 x[2][UN];
 #pragma unroll

@@ -6,32 +6,38 @@
 // with the running maximum m and sum l of an online softmax (fp32).
 //
 // Bound: memory.  Every cached row is read once by the query heads of its
-// group; nothing is reused beyond that.  So the kernel moves rows from global
-// memory straight into the registers that hold the matrix operands and keeps
-// enough loads in flight; there is no shared-memory staging of K or V.
+// group; nothing is reused beyond that, so what counts is bytes in flight: each
+// warp keeps its own ring of row groups in shared memory, filled by 16-byte
+// asynchronous copies some groups ahead, and no warp waits for another until
+// the end of a segment.
 //
-// Split: the work is the list of 64-key tiles of all (sequence, key/value
-// head, block of query heads) segments, in that order, and CTA c takes the
-// c-th of `grid` equal ranges of it.  So CTAs are equally loaded whatever the
+// Split: the work is the list of key tiles of all (sequence, key/value head,
+// block of query heads) segments, in that order, and CTA c takes the c-th of
+// `grid` equal ranges of it.  So CTAs are equally loaded whatever the
 // lengths (which only the device knows), a captured launch follows lengths that
 // change, and a CTA has at most two segments it shares with other CTAs.  A
 // segment inside one CTA is written to the output at once; the others leave a
 // normalised fp32 partial output and its log-sum-exp in the workspace, two
 // slots per CTA, and the join kernel combines them in a fixed order (no
-// atomics: results do not depend on timing).
+// atomics: results do not depend on timing).  Where no sequence can have more
+// than a few tiles (a small block table), a CTA takes a whole segment and there
+// is no second kernel.
 //
 // Tensor-core path (mma.sync m16n8k16): the products are formed transposed,
 // S^T = K Q^T and O^T = V^T P^T, so that the 16 rows of the instruction are
 // keys (or head-dimension columns) and its 8 columns the query heads of the
-// group; each of a CTA's four warps takes 16 keys of a tile.  The order of the
-// contraction index is free as long as both operands agree, so a lane's
-// operand registers are whole 16-byte pieces of a cached row: for K the lane
-// (g = lane / 4, t = lane % 4) holds pieces t, t + 4, ... of keys g and g + 8
-// and Q is permuted to match; for V it holds pieces g, g + 8, ... of keys 2t,
-// 2t + 1, 2t + 8, 2t + 9, whose values are paired by key with byte permutes,
-// and the permuted head-dimension order of O^T is undone at the store.
-// (tcgen05 would need K and V staged in shared memory and 64 or more rows per
-// product, and the tensor work here is a fraction of a per cent of its rate.)
+// group; each of a CTA's four warps takes 16 or 32 keys of a tile (8 KB of rows
+// or less).  The order of the contraction index is free as long as both
+// operands agree, so a lane's operand registers are whole 16-byte pieces of a
+// cached row: for K the lane (g = lane / 4, t = lane % 4) holds pieces t,
+// t + 4, ... of keys g and g + 8 and Q is permuted to match; for V it holds
+// pieces g, g + 8, ... of keys 2t, 2t + 1, 2t + 8, 2t + 9, whose values are
+// paired by key with byte permutes, and the permuted head-dimension order of
+// O^T is undone at the store.  Pieces of a row are permuted in shared memory
+// (K: by the row's lowest bit, V: by the next two) so that these reads hit
+// distinct banks.  (tcgen05 wants 64 or more rows per product and its
+// accumulator in TMEM; the tensor work here is a fraction of a per cent of its
+// rate.)
 //
 // e4m3 caches: codes are converted to fp16 exactly.  The key scale 2^(ek-127)
 // multiplies the logit.  The value scale goes into the exponent of the weight,
@@ -56,10 +62,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kWarpKeys = kDecodeTile / kWarps;  // 16
-static_assert(kWarpKeys == 16, "a warp takes the 16 rows of one matrix product");
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + kDecodeTile - 1) / kDecodeTile; }
+__device__ __forceinline__ int tiles_of(int len, int tile) { return (len + tile - 1) / tile; }
 
 // m16n8k16, fp32 accumulation, in place.
 template <bool BF16>
@@ -161,7 +165,8 @@ __device__ __forceinline__ long long block_exclusive(long long x, long long* tot
   return base + incl - x;
 }
 
-// Merge of the warps' states of one piece, in shared memory.
+// The warps' states of one piece, in shared memory; their accumulators are
+// behind it, one row of DPAD + 1 floats per warp and head (bank spread).
 template <int HPB, int DPAD>
 struct Shared {
   long long scan[kWarps];
@@ -170,29 +175,42 @@ struct Shared {
   // factor of each warp's accumulator in the merged output; lse of the piece
   float f[kWarps][HPB], lse[HPB];
   float qs[HPB];  // e4m3: logit factor of a head (scale * log2(e) * 2^eq)
-  // accumulators, one row of D + 1 floats per head (bank spread)
-  float acc[kWarps][HPB][DPAD + 1];
+  static constexpr int kAccBytes = kWarps * HPB * (DPAD + 1) * 4;
 };
+template <int HPB, int DPAD>
+constexpr int shared_bytes() {
+  return (static_cast<int>(sizeof(Shared<HPB, DPAD>)) + 127) & ~127;
+}
 
 struct Segment {
   int b, hk, hb;      // sequence, key/value head, block of its query heads
-  long long first;    // first tile of the segment in the list
   int tiles, len;
 };
 
 // Walks this CTA's range of the list: calls piece(segment, tile0, tile1, slot)
 // for each segment it touches; slot -1: the whole segment is here.
-template <typename Sh, typename F>
+template <int TILE, typename Sh, typename F>
 __device__ __forceinline__ void walk(const DecodeParams& p, Sh* sh, F&& piece) {
   const PagedCache& c = p.c;
+  const long long HH = static_cast<long long>(c.Hkv) * p.head_blocks;
+  bool bad = false;
+  if (p.direct) {  // one segment per CTA
+    Segment s;
+    s.b = static_cast<int>(blockIdx.x / HH);
+    const int seg = static_cast<int>(blockIdx.x % HH);
+    s.hk = seg / p.head_blocks, s.hb = seg % p.head_blocks;
+    s.len = clamp_len(c, __ldg(p.lens + s.b), &bad);
+    if (bad && seg == 0 && threadIdx.x == 0) atomicOr(c.status, kStatusIndex);
+    s.tiles = tiles_of(s.len, TILE);
+    piece(s, 0, s.tiles, -1);
+    return;
+  }
   const int per = (c.B + kThreads - 1) / kThreads;  // sequences per thread
   const int b_lo = min(c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(c.B, b_lo + per);
-  bool bad = false;
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(clamp_len(c, __ldg(p.lens + b), &bad));
+  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), TILE);
   long long seq_total;
   const long long before = block_exclusive<kThreads>(mine, &seq_total, sh->scan);
-  const long long HH = static_cast<long long>(c.Hkv) * p.head_blocks;
   const long long W = seq_total * HH;
   const long long G = min(static_cast<long long>(p.grid), W);
   if (static_cast<long long>(blockIdx.x) >= G) return;
@@ -202,7 +220,7 @@ __device__ __forceinline__ void walk(const DecodeParams& p, Sh* sh, F&& piece) {
     long long at = before;
     int b = b_lo;
     for (; b < b_hi; ++b) {
-      const int t = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad));
+      const int t = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), TILE);
       if (lo < (at + t) * HH) break;
       at += t;
     }
@@ -212,23 +230,23 @@ __device__ __forceinline__ void walk(const DecodeParams& p, Sh* sh, F&& piece) {
   __syncthreads();
   int b = sh->place.b;
   long long seq_first = sh->place.before * HH;
-  int len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len);
+  int len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
   for (long long at = lo; at < hi;) {
     while (at >= seq_first + nt * HH) {  // next sequence with keys (at < hi <= W: there is one)
       seq_first += nt * HH;
       ++b;
-      len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len);
+      len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
     }
     const int seg = static_cast<int>((at - seq_first) / nt);
     Segment s;
     s.b = b, s.hk = seg / p.head_blocks, s.hb = seg % p.head_blocks;
-    s.first = seq_first + static_cast<long long>(seg) * nt;
     s.tiles = nt, s.len = len;
-    const int t0 = static_cast<int>(at - s.first);
-    const int t1 = static_cast<int>(min(hi - s.first, static_cast<long long>(nt)));
+    const long long first = seq_first + static_cast<long long>(seg) * nt;
+    const int t0 = static_cast<int>(at - first);
+    const int t1 = static_cast<int>(min(hi - first, static_cast<long long>(nt)));
     const int slot = (t0 == 0 && t1 == nt) ? -1 : (t0 > 0 ? 0 : 1);
     piece(s, t0, t1, slot);
-    at = s.first + t1;
+    at = first + t1;
   }
 }
 
@@ -236,7 +254,7 @@ __device__ __forceinline__ void walk(const DecodeParams& p, Sh* sh, F&& piece) {
 // output tensor (slot < 0) or the workspace.
 template <typename T, int HPB, int DPAD>
 __device__ __forceinline__ void store_piece(const DecodeParams& p, Shared<HPB, DPAD>* sh,
-                                            const Segment& s, int slot) {
+                                            const float* acc, const Segment& s, int slot) {
   const int D = p.c.D;
   const int h0 = s.hk * p.group + s.hb * HPB;            // first query head
   const int nh = min(HPB, p.group - s.hb * HPB);         // heads of this block
@@ -245,7 +263,7 @@ __device__ __forceinline__ void store_piece(const DecodeParams& p, Shared<HPB, D
     if (d >= D) continue;
     float o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) o += sh->f[w][h] * sh->acc[w][h][d];
+    for (int w = 0; w < kWarps; ++w) o += sh->f[w][h] * acc[(w * HPB + h) * (DPAD + 1) + d];
     if (slot < 0) {
       T* dst = static_cast<T*>(p.o) + s.b * p.so.b + (h0 + h) * p.so.h + d;
       *dst = Elem<T>::put(o);
@@ -292,11 +310,51 @@ __device__ __forceinline__ void merge_stats(Shared<HPB, DPAD>* sh, float shift) 
 }
 
 // ------------------------------------------------------------------ tensor cores
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool on) {
+  // copies 16 bytes, or writes 16 zero bytes and reads nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ld_shared(uint32_t a, uint32_t (&x)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ld_shared(uint32_t a, uint32_t (&x)[2]) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(a) : "memory");
+}
+
+// The ring of one warp: kDecodeStages groups of KT keys, K rows then V rows.
+template <int DPAD, bool E4M3>
+struct Ring {
+  static constexpr int ROWB = DPAD * (E4M3 ? 1 : 2);  // bytes of a row
+  static constexpr int KT = decode_warp_keys(DPAD, E4M3);
+  static constexpr int PIECES = ROWB / 16;
+  static constexpr int STAGE = 2 * KT * ROWB;
+  static constexpr int WARP = kDecodeStages * STAGE;
+  // byte offset of 16-byte piece x of a row
+  static __device__ __forceinline__ int k_at(int row, int x) {
+    return row * ROWB + ((PIECES >= 8 ? x ^ ((row & 1) << 2) : x) << 4);
+  }
+  static __device__ __forceinline__ int v_at(int row, int x) {
+    return KT * ROWB + row * ROWB + ((PIECES >= 8 ? x ^ (row & 6) : x ^ ((row >> 1) & 3)) << 4);
+  }
+};
+
 // TQ: type of q and o, and of a 16-bit cache.  NG: groups of 8 query heads.
 template <typename TQ, int DPAD, bool E4M3, int NG>
 __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
     decode_tc_kernel(const DecodeParams p) {
+  using R = Ring<DPAD, E4M3>;
   constexpr int HPB = 8 * NG;
+  constexpr int KT = R::KT, RG = KT / 16, TILE = kWarps * KT, ST = kDecodeStages;
+  static_assert(ST == 2, "one group is read while the next is copied");
   constexpr bool kBF16 = Elem<TQ>::kBF16 && !E4M3;  // operand type of the products
   constexpr float kShift = kBF16 ? 0.f : 14.f;      // fp16 weights: largest at 2^14
   constexpr int KS = DPAD / 16;                     // contraction steps of S^T
@@ -307,23 +365,112 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
   constexpr int VW = E4M3 ? DPAD / 32 : 4;          // 32-bit words of a V piece (8 lanes a row)
   constexpr int VP = E4M3 ? 1 : DPAD / 64;          // V pieces per lane and key
   constexpr int VE = E4M3 ? DPAD / 8 : 8;           // elements of a V piece
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   auto* sh = reinterpret_cast<Shared<HPB, DPAD>*>(smem_raw);
+  // the rings; at the end of a piece the accumulators lie over them
+  uint8_t* rings = smem_raw + shared_bytes<HPB, DPAD>();
+  float* acc_sh = reinterpret_cast<float*>(rings);
   const PagedCache& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(rings) + warp * R::WARP;
   const int D = c.D;
   using TC = typename std::conditional<E4M3, uint8_t, TQ>::type;
   const TC* kc = static_cast<const TC*>(c.k);
   const TC* vc = static_cast<const TC*>(c.v);
-  // every 16 keys of a warp within one page
-  const bool one_page = c.page_size % kWarpKeys == 0;
+  // every aligned run of 16 keys lies in one page
+  const bool runs = c.page_size % 16 == 0;
+  // this lane's part of a group's copies: piece x of rows lr, lr + RS, ...
+  constexpr int RS = 32 / R::PIECES, NCP = KT / RS;
+  const int lr = lane / R::PIECES, x = lane % R::PIECES;
+  const bool col_on = x * EPC < D;
+  const int xcol = col_on ? x * EPC : 0;
 
-  walk(p, sh, [&](const Segment& s, int t0, int t1, int slot) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  walk<TILE>(p, sh, [&](const Segment& s, int t0, int t1, int slot) {
     const int h0 = s.hk * p.group + s.hb * HPB;
     const int nh = min(HPB, p.group - s.hb * HPB);
+    __syncthreads();  // the previous piece's use of shared memory is over
+
+    auto first_key = [&](int it) { return (t0 + it) * TILE + warp * KT; };
+    const int n_it = t1 - t0;
+    // Block-table entry of this lane's key of group it (its 16-key run's first
+    // key where runs lie in one page), unchecked, and that key's row of the
+    // page.  Loaded a group ahead of the copies that need it.
+    int raw = -1, row = 0;
+    bool looked = false;
+    auto look_up = [&](int it) {
+      const int j = first_key(it) + (runs ? (KT == 32 ? lane & 16 : 0) : lane);
+      looked = it < n_it && (runs || lane < KT) && j < s.len;
+      if (looked) {
+        int entry;
+        split_position(c, j, &entry, &row);
+        raw = __ldg(c.table + s.b * c.table_stride + entry);
+      }
+    };
+    // Starts the copies of group it (whose entries have been looked up) into
+    // its stage; e4m3: also loads the scale bytes of key `lane` (K low, V high
+    // byte).  keep_next: keys of the group that exist and whose page does.
+    unsigned sb_next = 0;
+    uint32_t keep_next = 0;
+    auto issue = [&](int it) {
+      const int j0 = first_key(it);
+      if (it < n_it && j0 < s.len) {
+        const bool have = looked && raw >= 0 && raw < c.pages;
+        if (looked && !have) atomicOr(c.status, kStatusIndex);
+        const int left = s.len - j0;
+        keep_next = __ballot_sync(0xffffffffu, have) & (KT == 32 ? 0xFFFFFFFFu : 0xFFFFu) &
+                    (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u);
+        const int page = have ? raw : 0, r0 = have ? row : 0;
+        const TC* kp = kc + page * c.sk.b + s.hk * c.sk.h + r0 * c.sk.n;
+        const TC* vp = vc + page * c.sv.b + s.hk * c.sv.h + r0 * c.sv.n;
+        if (E4M3 && ((keep_next >> lane) & 1u)) {
+          const long long at = (static_cast<long long>(page) * c.Hkv + s.hk) * c.page_size + r0 +
+                               (runs ? lane & 15 : 0);
+          sb_next = __ldg(c.k_scale + at) | (static_cast<unsigned>(__ldg(c.v_scale + at)) << 8);
+        }
+        const uint32_t dst = ring + (it % ST) * R::STAGE;
+        if (runs) {
+          // (the pointers of run h of the group are lane 16 h's)
+#pragma unroll
+          for (int h = 0; h < RG; ++h) {
+            const TC* kr = reinterpret_cast<const TC*>(__shfl_sync(
+                               0xffffffffu, reinterpret_cast<unsigned long long>(kp), 16 * h)) +
+                           lr * c.sk.n + xcol;
+            const TC* vr = reinterpret_cast<const TC*>(__shfl_sync(
+                               0xffffffffu, reinterpret_cast<unsigned long long>(vp), 16 * h)) +
+                           lr * c.sv.n + xcol;
+            const uint32_t keep = (keep_next >> (16 * h)) & 0xFFFFu;
+#pragma unroll
+            for (int i = 0; i < 16 / RS; ++i) {
+              const int r = 16 * h + i * RS + lr;
+              const bool on = col_on && (keep == 0xFFFFu || ((keep >> (i * RS + lr)) & 1u));
+              copy_async16(dst + R::k_at(r, x), kr, on);
+              copy_async16(dst + R::v_at(r, x), vr, on);
+              kr += RS * c.sk.n, vr += RS * c.sv.n;
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < NCP; ++i) {
+            const int r = i * RS + lr;
+            const TC* kr = reinterpret_cast<const TC*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kp), r));
+            const TC* vr = reinterpret_cast<const TC*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vp), r));
+            const bool on = col_on && ((keep_next >> r) & 1u);
+            copy_async16(dst + R::k_at(r, x), kr + xcol, on);
+            copy_async16(dst + R::v_at(r, x), vr + xcol, on);
+          }
+        }
+      }
+      copy_async_commit();
+    };
+    look_up(0);
+    issue(0);
+    look_up(1);
+
     // ---- Q^T operand: lane (g, t) holds head g (+ 8 n), permuted to match K
     uint32_t qf[NG][KS][2];
-    __syncthreads();  // the previous piece's use of shared memory is over
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       const int h = n * 8 + g;
@@ -346,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
       }
       if constexpr (E4M3) {
         // q * 2^-eq with the largest magnitude in [2^14, 2^15) (an exponent
-        // outside [-126, 127] is clamped: such a head's logits are 0 or huge)
+        // outside [-126, 126] is clamped: such a head's logits are 0 or huge)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;  // eq
@@ -379,139 +526,85 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
         for (int i = 0; i < 4; ++i) acc[n][mt][i] = 0.f;
     }
 
-    for (int tile = t0; tile < t1; ++tile) {
-      const int j0 = tile * kDecodeTile + warp * kWarpKeys;
-      if (j0 >= s.len) break;  // uniform over the warp
-      // ---- places of the 16 keys: lane i < 16 looks up key j0 + i
-      long long ko = 0, vo = 0;  // element offsets of the row within this head
-      long long so = 0;          // index of its scale bytes
-      bool on = false;
-      if (one_page || lane < kWarpKeys) {
-        const int j = j0 + (one_page ? 0 : lane);
-        if (j < s.len) {
-          int entry, row;
-          split_position(c, j, &entry, &row);
-          const int page = page_of(c, s.b, entry);
-          on = page >= 0;
-          if (on) {
-            ko = page * c.sk.b + s.hk * c.sk.h + row * c.sk.n;
-            vo = page * c.sv.b + s.hk * c.sv.h + row * c.sv.n;
-            so = (static_cast<long long>(page) * c.Hkv + s.hk) * c.page_size + row;
-          }
-        }
-      }
-      auto k_at = [&](int i) -> long long {
-        return one_page ? ko + i * c.sk.n : __shfl_sync(0xffffffffu, ko, i);
-      };
-      auto v_at = [&](int i) -> long long {
-        return one_page ? vo + i * c.sv.n : __shfl_sync(0xffffffffu, vo, i);
-      };
-      auto s_at = [&](int i) -> long long {
-        return one_page ? so + i : __shfl_sync(0xffffffffu, so, i);
-      };
-      // keys of this warp that exist and whose page does: bit i = key j0 + i
-      uint32_t keep;
-      {
-        const int left = s.len - j0;
-        const uint32_t in_len = left >= 16 ? 0xFFFFu : (1u << left) - 1u;
-        keep = one_page ? (on ? in_len : 0u) : (__ballot_sync(0xffffffffu, on) & 0xFFFFu);
-      }
+    for (int it = 0; it < n_it && first_key(it) < s.len; ++it) {
+      copy_async_wait<0>();
+      __syncwarp();  // every lane's copies of group it are in; group it - 1 has been read
+      const unsigned sb = sb_next;
+      const uint32_t keep = keep_next;
+      issue(it + 1);
+      look_up(it + 2);
       auto kept = [&](int i) -> bool { return (keep >> i) & 1u; };
-
-      // ---- loads: K pieces of keys g, g + 8; V pieces of keys 2t, 2t + 1, + 8
-      uint4 kf[2][KP];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int i = g + 8 * r;
-        const TC* src = kc + k_at(i);
-#pragma unroll
-        for (int u = 0; u < KP; ++u) {
-          const int d = (t + 4 * u) * EPC;
-          kf[r][u] = (kept(i) && d < D) ? __ldg(reinterpret_cast<const uint4*>(src + d))
-                                        : make_uint4(0, 0, 0, 0);
-        }
-      }
-      unsigned ek[2] = {0, 0}, ev[2] = {0, 0};
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = g + 8 * r;
-          const long long at = s_at(i);
-          if (kept(i)) ek[r] = __ldg(c.k_scale + at), ev[r] = __ldg(c.v_scale + at);
-        }
-      }
-      uint32_t vf[4][VP][VW];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 2 * t + (r & 1) + 8 * (r >> 1);
-        const TC* src = vc + v_at(i);
-#pragma unroll
-        for (int u = 0; u < VP; ++u) {
-          const int d = (g + 8 * u) * VE;
-#pragma unroll
-          for (int x = 0; x < VW; ++x) vf[r][u][x] = 0u;
-          if (kept(i) && d < D) {
-            if constexpr (VW == 4) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + d));
-              vf[r][u][0] = x.x, vf[r][u][1] = x.y, vf[r][u][2] = x.z, vf[r][u][3] = x.w;
-            } else {
-              const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + d));
-              vf[r][u][0] = x.x, vf[r][u][1] = x.y;
-            }
-          }
-        }
-      }
+      const uint32_t st = ring + (it % ST) * R::STAGE;
 
       // ---- S^T = K Q^T
-      float sc[NG][4];
+      float sc[RG][NG][4];
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t a[4];  // (key g, lo), (key g + 8, lo), (key g, hi), (key g + 8, hi)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&kf[r][ks / KSP]);
-          if constexpr (E4M3) {
-            const uint32_t x = w[ks % KSP];
-            a[r] = e4m3x2_to_half2(x & 0xFFFFu);
-            a[2 + r] = e4m3x2_to_half2(x >> 16);
-          } else {
-            a[r] = w[2 * (ks % KSP)];
-            a[2 + r] = w[2 * (ks % KSP) + 1];
-          }
-        }
+      for (int rg = 0; rg < RG; ++rg) {
 #pragma unroll
         for (int n = 0; n < NG; ++n)
-          mma16816<kBF16>(sc[n], a[0], a[1], a[2], a[3], qf[n][ks][0], qf[n][ks][1]);
-      }
-      // ---- logits in log2 units, weights
-      uint32_t pf[NG][2];  // P^T operand: keys 2t, 2t + 1 (and + 8) of head g
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        float x[2][2], wx[2][2];  // [key g + 8 r][head 2t + i]
+          for (int i = 0; i < 4; ++i) sc[rg][n][i] = 0.f;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float kscale = E4M3 ? scale_value(ek[r]) : 1.f;
+        for (int u = 0; u < KP; ++u) {
+          uint32_t w[2][4];  // piece t + 4u of keys g and g + 8
+          ld_shared(st + R::k_at(rg * 16 + g, t + 4 * u), w[0]);
+          ld_shared(st + R::k_at(rg * 16 + g + 8, t + 4 * u), w[1]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float y = sc[n][2 * r + i] * (E4M3 ? kscale * qs[n][i] : qs[n][i]);
-            x[r][i] = kept(g + 8 * r) ? y : -INFINITY;
-            wx[r][i] = E4M3 ? x[r][i] + static_cast<float>(static_cast<int>(ev[r]) - 127) : x[r][i];
+          for (int k = 0; k < KSP; ++k) {
+            uint32_t a[4];  // (key g, lo), (key g + 8, lo), (key g, hi), (key g + 8, hi)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if constexpr (E4M3) {
+                e4m3x4_to_half2x2(w[r][k], a[r], a[2 + r]);
+              } else {
+                a[r] = w[r][2 * k];
+                a[2 + r] = w[r][2 * k + 1];
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+              mma16816<kBF16>(sc[rg][n], a[0], a[1], a[2], a[3], qf[n][u * KSP + k][0],
+                              qf[n][u * KSP + k][1]);
           }
         }
-        float pw[2][2];
+      }
+      // scales of this lane's keys g + 8 r
+      float kscale[2 * RG], vexp[2 * RG];
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int r = 0; r < 2 * RG; ++r) {
+          const unsigned x = __shfl_sync(0xffffffffu, sb, g + 8 * r);
+          kscale[r] = scale_value(x & 0xFFu);
+          vexp[r] = static_cast<float>(static_cast<int>(x >> 8) - 127);
+        }
+      }
+      // ---- logits in log2 units, weights
+      uint32_t pf[RG][NG][2];  // P^T operand: keys 2t, 2t + 1 (and + 8) of head g
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float x[2 * RG][2], pw[2 * RG][2];  // [key g + 8 r][head 2t + i]
+#pragma unroll
+        for (int r = 0; r < 2 * RG; ++r)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float y = sc[r / 2][n][2 * (r & 1) + i] * (E4M3 ? kscale[r] * qs[n][i] : qs[n][i]);
+            x[r][i] = kept(g + 8 * r) ? y : -INFINITY;
+          }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float m_new = fmaxf(m[n][i], max_over_g(fmaxf(x[0][i], x[1][i])));
+          float top = -INFINITY, topw = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < 2 * RG; ++r) {
+            top = fmaxf(top, x[r][i]);
+            if constexpr (E4M3) topw = fmaxf(topw, x[r][i] + vexp[r]);
+          }
+          const float m_new = fmaxf(m[n][i], max_over_g(top));
           const float mu = m_new == -INFINITY ? 0.f : m_new;
           const float a_m = exp2f(m[n][i] - mu);
           l[n][i] *= a_m, lx[n][i] *= a_m;
           float a_w = a_m, mwu = mu;
           if constexpr (E4M3) {
-            const float mw_new = fmaxf(mw[n][i], max_over_g(fmaxf(wx[0][i], wx[1][i])));
+            const float mw_new = fmaxf(mw[n][i], max_over_g(topw));
             mwu = mw_new == -INFINITY ? 0.f : mw_new;
             a_w = exp2f(mw[n][i] - mwu);
             mw[n][i] = mw_new;
@@ -520,12 +613,14 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
           }
           m[n][i] = m_new;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int r = 0; r < 2 * RG; ++r) {
             if constexpr (E4M3) {
               const float e = ex2_approx(x[r][i] - mu);
               l[n][i] += e, lx[n][i] += e;
+              pw[r][i] = ex2_approx(x[r][i] + vexp[r] - mwu + kShift);
+            } else {
+              pw[r][i] = ex2_approx(x[r][i] - mwu + kShift);
             }
-            pw[r][i] = ex2_approx(wx[r][i] - mwu + kShift);
           }
           if (__any_sync(0xffffffffu, a_w != 1.f)) {
 #pragma unroll
@@ -536,40 +631,54 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
           }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 2 * RG; ++r) {
           const uint32_t w = pack2(pw[r][0], pw[r][1], kBF16);
           if constexpr (!E4M3) {  // sums of the rounded and the unrounded weights
             const float2 f = unpack2(w, kBF16);
             l[n][0] += f.x, l[n][1] += f.y;
             lx[n][0] += pw[r][0], lx[n][1] += pw[r][1];
           }
-          pf[n][r] = transpose8x8(w);
+          pf[r / 2][n][r & 1] = transpose8x8(w);
         }
       }
       // ---- O^T += V^T P^T
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t a[4];  // (column a, keys 2t, 2t+1), (column b, ..), (a, keys + 8), (b, ..)
+      for (int rg = 0; rg < RG; ++rg) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if constexpr (E4M3) {
-            const uint32_t x0 = vf[2 * r][0][mt / 2], x1 = vf[2 * r + 1][0][mt / 2];
-            const uint32_t w = __byte_perm(x0, x1, (mt & 1) ? 0x7362 : 0x5140);
-            a[2 * r] = e4m3x2_to_half2(w & 0xFFFFu);
-            a[2 * r + 1] = e4m3x2_to_half2(w >> 16);
-          } else {
-            const uint32_t x0 = vf[2 * r][mt / 4][mt % 4], x1 = vf[2 * r + 1][mt / 4][mt % 4];
-            a[2 * r] = __byte_perm(x0, x1, 0x5410);
-            a[2 * r + 1] = __byte_perm(x0, x1, 0x7632);
+        for (int u = 0; u < VP; ++u) {
+          uint32_t vf[4][VW];  // piece g + 8u of keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = rg * 16 + 2 * t + (r & 1) + 8 * (r >> 1);
+            if constexpr (VW == 4) ld_shared(st + R::v_at(row, g + 8 * u), vf[r]);
+            else ld_shared(st + R::v_at(row, g >> 1) + 8 * (g & 1), vf[r]);
+          }
+#pragma unroll
+          for (int k = 0; k < MT / VP; ++k) {
+            const int mt = u * (MT / VP) + k;
+            uint32_t a[4];  // (column a, keys 2t, 2t+1), (column b, ..), (a, keys + 8), (b, ..)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if constexpr (E4M3) {
+                const uint32_t w =
+                    __byte_perm(vf[2 * r][k / 2], vf[2 * r + 1][k / 2], (k & 1) ? 0x7362 : 0x5140);
+                e4m3x4_to_half2x2(w, a[2 * r], a[2 * r + 1]);
+              } else {
+                a[2 * r] = __byte_perm(vf[2 * r][k], vf[2 * r + 1][k], 0x5410);
+                a[2 * r + 1] = __byte_perm(vf[2 * r][k], vf[2 * r + 1][k], 0x7632);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+              mma16816<kBF16>(acc[n][mt], a[0], a[1], a[2], a[3], pf[rg][n][0], pf[rg][n][1]);
           }
         }
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-          mma16816<kBF16>(acc[n][mt], a[0], a[1], a[2], a[3], pf[n][0], pf[n][1]);
       }
     }
 
     // ---- join of the four warps
+    copy_async_wait<0>();
+    __syncthreads();  // no ring is read any more
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -589,13 +698,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
         const int d = E4M3 ? g * VE + 2 * mt : (g + 8 * (mt / 4)) * 8 + 2 * (mt % 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sh->acc[warp][n * 8 + 2 * t + (i & 1)][d + (i >> 1)] = acc[n][mt][i];
+          acc_sh[(warp * HPB + n * 8 + 2 * t + (i & 1)) * (DPAD + 1) + d + (i >> 1)] = acc[n][mt][i];
       }
     }
     __syncthreads();
     merge_stats(sh, kShift);
     __syncthreads();
-    store_piece<TQ, HPB, DPAD>(p, sh, s, slot);
+    store_piece<TQ, HPB, DPAD>(p, sh, acc_sh, s, slot);
   });
 }
 
@@ -637,9 +746,12 @@ __device__ __forceinline__ float4 load4(const T* row, int d, int D) {
 template <typename TQ, int DPAD, bool E4M3, int HPB, bool VEC>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParams p) {
   constexpr int NC = DPAD / 16;  // 4-column pieces per lane
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  constexpr int TILE = kDecodeSimtTile, KT = TILE / kWarps;
+  static_assert(KT == 16, "a warp takes two rounds of eight keys");
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   auto* sh = reinterpret_cast<Shared<HPB, DPAD>*>(smem_raw);
-  auto* sq = reinterpret_cast<float(*)[DPAD]>(smem_raw + ((sizeof(Shared<HPB, DPAD>) + 15) & ~15));
+  auto* sq = reinterpret_cast<float(*)[DPAD]>(smem_raw + shared_bytes<HPB, DPAD>());
+  float* acc_sh = reinterpret_cast<float*>(sq + HPB);
   const PagedCache& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int D = c.D;
@@ -647,7 +759,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
   const TC* kc = static_cast<const TC*>(c.k);
   const TC* vc = static_cast<const TC*>(c.v);
 
-  walk(p, sh, [&](const Segment& s, int t0, int t1, int slot) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  walk<TILE>(p, sh, [&](const Segment& s, int t0, int t1, int slot) {
     const int h0 = s.hk * p.group + s.hb * HPB;
     const int nh = min(HPB, p.group - s.hb * HPB);
     __syncthreads();
@@ -667,7 +780,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
       for (int u = 0; u < NC; ++u) acc[h][u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int tile = t0; tile < t1; ++tile) {
-      const int j0 = tile * kDecodeTile + warp * kWarpKeys;
+      const int j0 = tile * TILE + warp * KT;
       if (j0 >= s.len) break;
 #pragma unroll 1
       for (int r = 0; r < 2; ++r) {
@@ -738,7 +851,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
         const float4 a = make_float4(sum_over_g(acc[h][u].x), sum_over_g(acc[h][u].y),
                                      sum_over_g(acc[h][u].z), sum_over_g(acc[h][u].w));
         if (g == 0) {
-          float* dst = &sh->acc[warp][h][4 * (t + 4 * u)];
+          float* dst = acc_sh + (warp * HPB + h) * (DPAD + 1) + 4 * (t + 4 * u);
           dst[0] = a.x, dst[1] = a.y, dst[2] = a.z, dst[3] = a.w;
         }
       }
@@ -746,7 +859,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
     __syncthreads();
     merge_stats(sh, 0.f);
     __syncthreads();
-    store_piece<TQ, HPB, DPAD>(p, sh, s, slot);
+    store_piece<TQ, HPB, DPAD>(p, sh, acc_sh, s, slot);
   });
 }
 
@@ -755,16 +868,16 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
 // segment, weighted by their log-sum-exps, in CTA order.  Sequences without
 // keys get the empty row (0, -inf).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParams p, int hpb) {
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParams p, int hpb,
+                                                               int tile) {
   const PagedCache& c = p.c;
   const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (item >= static_cast<long long>(c.B) * p.H) return;
   const int b = static_cast<int>(item / p.H), h = static_cast<int>(item % p.H);
   bool bad = false;
   long long before = 0, total = 0;
   for (int i = lane; i < c.B; i += 32) {
-    const int nt = tiles_of(clamp_len(c, __ldg(p.lens + i), &bad));
+    const int nt = tiles_of(clamp_len(c, __ldg(p.lens + i), &bad), tile);
     total += nt;
     if (i < b) before += nt;
   }
@@ -774,8 +887,13 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   if (bad && item == 0) atomicOr(c.status, kStatusIndex);
+  // This kernel may be placed while the attention kernel runs: from here on
+  // that one is complete and its partial states are visible.  (Every warp
+  // waits, so that this kernel never ends before it.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (b >= c.B) return;
   T* dst = static_cast<T*>(p.o) + b * p.so.b + h * p.so.h;
-  const int nt = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad));
+  const int nt = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), tile);
   if (nt == 0) {
     for (int d = lane; d < c.D; d += 32) dst[d] = Elem<T>::put(0.f);
     if (lane == 0 && p.lse) p.lse[static_cast<long long>(b) * p.H + h] = -INFINITY;
@@ -823,29 +941,39 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
 template <typename K>
 cudaError_t launch_with_smem(K kern, int bytes, const DecodeParams& p, cudaStream_t stream) {
   if (bytes > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
   }
   kern<<<p.grid, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <typename TQ, int DPAD, bool E4M3>
+template <typename TQ, int DPAD, bool E4M3, int NG>
 cudaError_t launch_tc(const DecodeParams& p, cudaStream_t stream) {
-  if constexpr (sizeof(TQ) == 4) {
-    return cudaErrorInvalidValue;
-  } else {
-    if (p.group > 8)
-      return launch_with_smem(decode_tc_kernel<TQ, DPAD, E4M3, 2>, sizeof(Shared<16, DPAD>), p, stream);
-    return launch_with_smem(decode_tc_kernel<TQ, DPAD, E4M3, 1>, sizeof(Shared<8, DPAD>), p, stream);
-  }
+  using S = Shared<8 * NG, DPAD>;
+  constexpr int rings = kWarps * Ring<DPAD, E4M3>::WARP;
+  constexpr int bytes =
+      shared_bytes<8 * NG, DPAD>() + (rings > S::kAccBytes ? rings : S::kAccBytes);
+  static_assert(decode_ctas_per_sm(DPAD, NG) * (bytes + 1024) <= 228 * 1024, "resident CTAs");
+  return launch_with_smem(decode_tc_kernel<TQ, DPAD, E4M3, NG>, bytes, p, stream);
 }
 template <typename TQ, int DPAD, bool E4M3>
 cudaError_t launch_simt(bool vec, const DecodeParams& p, cudaStream_t stream) {
   constexpr int HPB = DPAD > 64 ? 2 : 4;
-  const int bytes = ((sizeof(Shared<HPB, DPAD>) + 15) & ~15) + HPB * DPAD * 4;
+  constexpr int bytes =
+      shared_bytes<HPB, DPAD>() + HPB * DPAD * 4 + Shared<HPB, DPAD>::kAccBytes;
   return vec ? launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, true>, bytes, p, stream)
              : launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, false>, bytes, p, stream);
+}
+
+template <typename TQ, int DPAD, bool E4M3>
+cudaError_t launch_attention(bool tc, bool vec, const DecodeParams& p, cudaStream_t stream) {
+  if constexpr (sizeof(TQ) == 2) {
+    if (tc)
+      return p.group > 8 ? launch_tc<TQ, DPAD, E4M3, 2>(p, stream)
+                         : launch_tc<TQ, DPAD, E4M3, 1>(p, stream);
+  }
+  return launch_simt<TQ, DPAD, E4M3>(vec, p, stream);
 }
 
 template <typename TQ>
@@ -853,20 +981,27 @@ cudaError_t launch_typed(bool e4m3, bool tc, bool vec, const DecodeParams& p, cu
   cudaError_t e = cudaSuccess;
   const bool wide = p.c.D > 64;
   if (p.grid > 0) {
-    if (tc)
-      e = wide ? (e4m3 ? launch_tc<TQ, 128, true>(p, stream) : launch_tc<TQ, 128, false>(p, stream))
-               : (e4m3 ? launch_tc<TQ, 64, true>(p, stream) : launch_tc<TQ, 64, false>(p, stream));
-    else
-      e = wide ? (e4m3 ? launch_simt<TQ, 128, true>(vec, p, stream)
-                       : launch_simt<TQ, 128, false>(vec, p, stream))
-               : (e4m3 ? launch_simt<TQ, 64, true>(vec, p, stream)
-                       : launch_simt<TQ, 64, false>(vec, p, stream));
-    if (e != cudaSuccess) return e;
+    e = wide ? (e4m3 ? launch_attention<TQ, 128, true>(tc, vec, p, stream)
+                     : launch_attention<TQ, 128, false>(tc, vec, p, stream))
+             : (e4m3 ? launch_attention<TQ, 64, true>(tc, vec, p, stream)
+                     : launch_attention<TQ, 64, false>(tc, vec, p, stream));
+    if (e != cudaSuccess || p.direct) return e;
   }
+  // The join may be placed on the GPU while the attention kernel still runs
+  // (programmatic dependent launch); it waits for it before it reads.
   const long long rows = static_cast<long long>(p.c.B) * p.H;
-  const unsigned grid = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-  decode_join_kernel<TQ><<<grid, kThreads, 0, stream>>>(p, decode_heads_per_block(tc, p.c.D, p.group));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.grid > 0 ? 1 : 0;
+  const int tile = decode_tile(tc, p.c.D, e4m3);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ>, p,
+                            decode_heads_per_block(tc, p.c.D, p.group), tile);
 }
 
 }  // namespace

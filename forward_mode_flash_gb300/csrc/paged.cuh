@@ -60,4 +60,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t x) {
   return r;
 }
 
+// Four e4m3 codes as two pairs of fp16 values (codes 0, 1 and codes 2, 3).
+__device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+
 }  // namespace jvp

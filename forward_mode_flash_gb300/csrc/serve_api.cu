@@ -151,7 +151,7 @@ jvp_status_t cache_rows(bool write, const jvp_cache_t* c, jvp_dtype_t dtype, int
 
 // CTAs of the single-token attention and the query heads each takes.
 struct DecodePlan {
-  int heads_per_block = 0, head_blocks = 0, grid = 0;
+  int heads_per_block = 0, head_blocks = 0, grid = 0, direct = 0;
   size_t bytes = 0;
 };
 DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
@@ -162,9 +162,14 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
   const int64_t most = c->max_pages * c->page_size;
   const int64_t wave =
       static_cast<int64_t>(num_sms) * decode_ctas_per_sm(D, tc ? d.heads_per_block / 8 : 1);
-  const int64_t tiles = (most + kDecodeTile - 1) / kDecodeTile;
+  const int tile = decode_tile(tc, D, c->dtype == JVP_E4M3);
+  const int64_t tiles = (most + tile - 1) / tile;
   // B * Hkv * head_blocks <= B * H <= 2^31 - 1 (checked by the caller), tiles < 2^31
   const int64_t segments = c->B * c->Hkv * d.head_blocks;
+  if (tiles > 0 && tiles <= kDecodeDirectTiles) {
+    d.grid = static_cast<int>(segments), d.direct = 1;
+    return d;
+  }
   d.grid = static_cast<int>(std::min<int64_t>(wave, tiles ? (segments > wave ? wave : segments * tiles) : 0));
   const size_t slots = static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
   d.bytes = ((slots * 4 + 255) & ~static_cast<size_t>(255)) + slots * D * 4;
@@ -371,12 +376,12 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
   const bool vec = D % 4 == 0 && aligned_to(k_cache, 4 * ce) && aligned_to(v_cache, 4 * ce) &&
                    multiple(p.c.sk, 4) && multiple(p.c.sv, 4);
   const DecodePlan d = plan_decode(cache, H, tc, sms);
-  if (d.grid > 0 && (!workspace || workspace_bytes < d.bytes))
+  if (d.bytes > 0 && (!workspace || workspace_bytes < d.bytes))
     return api_fail(JVP_ERR_WORKSPACE,
                     "workspace is NULL or smaller than jvp_attn_decode_workspace_size()");
   if (!aligned_to(workspace, 16)) return api_fail(JVP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-  p.head_blocks = d.head_blocks, p.grid = d.grid;
-  const size_t slots = static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
+  p.head_blocks = d.head_blocks, p.grid = d.grid, p.direct = d.direct;
+  const size_t slots = d.direct ? 0 : static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
   p.ws_lse = static_cast<float*>(workspace);
   p.ws_o = p.ws_lse + ((slots * 4 + 255) & ~static_cast<size_t>(255)) / 4;
   const cudaError_t err = launch_decode(static_cast<DType>(dtype), e4m3, tc, vec, p,

@@ -50,6 +50,7 @@ struct DecodeParams {
   int H, group;        // query heads, and query heads per key/value head
   int head_blocks;     // blocks of heads_per_block query heads per key/value head
   int grid;            // CTAs of the attention kernel (the partial states' slots)
+  int direct;          // 1: CTA i takes segment i whole; no join
   const int* lens;     // [B] keys of each sequence
   const void* q;
   Strides sq;          // b, h
@@ -61,8 +62,6 @@ struct DecodeParams {
   float* ws_o;         // [grid][2][heads_per_block][D]
 };
 
-constexpr int kDecodeTile = 64;  // keys per scheduling unit
-
 // Which kernel a call takes: tensor cores (16-bit queries, 16-byte aligned
 // rows, D a multiple of 8, of 16 for an e4m3 cache) or CUDA cores.
 // Query heads per CTA: 8 or 16 of a key/value head's group on the tensor
@@ -71,12 +70,23 @@ inline int decode_heads_per_block(bool tc, int D, int group) {
   if (tc) return group > 8 ? 16 : 8;
   return D > 64 ? 2 : 4;
 }
+// Tensor cores: keys of a warp's group of rows (K and V rows of 8 KB at most)
+// and groups in a warp's ring; four warps' groups are the split's tile.
+constexpr int decode_warp_keys(int D, bool e4m3) { return D > 64 && !e4m3 ? 16 : 32; }
+constexpr int kDecodeStages = 2;
+constexpr int kDecodeSimtTile = 64;
+constexpr int decode_tile(bool tc, int D, bool e4m3) {
+  return tc ? 4 * decode_warp_keys(D, e4m3) : kDecodeSimtTile;
+}
 // CTAs per SM that the split is made for: one resident wave (registers: 168 a
 // thread at three CTAs of 128; the widest variant, 16 heads of 128 columns,
 // spills there).
 constexpr int decode_ctas_per_sm(int D, int head_groups) {
   return D > 64 && head_groups > 1 ? 2 : 3;
 }
+// Where no sequence can have more tiles than this, a CTA takes a whole segment
+// and nothing is joined.
+constexpr int kDecodeDirectTiles = 4;
 
 cudaError_t launch_decode(DType dt, bool e4m3, bool tc, bool vec, const DecodeParams& p,
                           cudaStream_t stream);
