@@ -14,11 +14,12 @@
 // while one tile's softmax runs, the tensor core works for the other.
 //   warp 0      TMA producer: Q of both tiles, then K and V tiles through two
 //               rings
-//   warp 1      TMEM allocator; one thread issues every MMA:
+//   warp 1      TMEM allocator; issues every MMA:
 //               S_A(t + 1) right after O_A += P_A(t) V(t), then the same for B
-//   warps 2..5  softmax of tile A, one row per thread; warps 6..9 of tile B
+//   warps 4..7  softmax of tile A, one row per thread; warps 8..11 of tile B
 // P~ overwrites the first half of its S columns as 16-bit values and is the A
-// operand of the second product from TMEM.  MMAs of one thread complete in
+// operand of the second product from TMEM; it is published in two halves, so
+// that the product starts while the second half's exponentials are formed.  MMAs of one thread complete in
 // order, so "S(t + 1) is final" also says that O has tile t's contribution:
 // the (rare) rescale of O needs no barrier of its own.
 //
@@ -80,7 +81,10 @@ struct PackedLayout {
   static constexpr uint32_t TM_COLS = 512;
 };
 
-constexpr int kPackedThreads = 320;  // producer, MMA and eight softmax warps
+// Three warpgroups: producer and MMA warps (two more only fill the group),
+// softmax of tile A, softmax of tile B.  A softmax thread holds a whole row of
+// scores, so its group takes registers from the first (168 * 3 = 72 + 2 * 216).
+constexpr int kPackedThreads = 384;
 
 template <int NS>
 struct PackedCtrl {
@@ -88,7 +92,8 @@ struct PackedCtrl {
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
   uint64_t v_tail;     // the last V tile's rows behind the sequence are zero
   uint64_t s_full[2];  // S of the next key tile is final (and O has the previous one's)
-  uint64_t p_full[2];  // P~ is stored
+  uint64_t p_half[2];  // P~ of the tile's first 64 keys is stored
+  uint64_t p_full[2];  // P~ of the others is
   uint64_t o_full[2];  // O is complete
   uint64_t drain;
   uint32_t tmem_base;
@@ -160,7 +165,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctrl->q_full[x], 1);
       mbar_init(&ctrl->s_full[x], 1);
-      mbar_init(&ctrl->p_full[x], 4);  // one arrival per softmax warp of the tile
+      mbar_init(&ctrl->p_half[x], 4);  // one arrival per softmax warp of the tile
+      mbar_init(&ctrl->p_full[x], 4);
       mbar_init(&ctrl->o_full[x], 1);
     }
     for (int s = 0; s < NS; ++s) {
@@ -183,6 +189,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     bool ok = true;
@@ -246,81 +254,83 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t neg_a = p.neg_scores ? (1u << 13) : 0u;
-      // S of tile x against key tile t (whose K has landed)
-      auto scores = [&](int x, int t) {
-        const uint32_t q = smem_u32(smem + L::OFF_Q + x * L::Q_BYTES);
-        const uint32_t k = smem_u32(smem + L::OFF_K + (t % NS) * L::KV_BYTES);
+    // The whole warp walks this loop; one elected lane issues.
+    const uint32_t neg_a = p.neg_scores ? (1u << 13) : 0u;
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::OFF_V), BN * 128, 1024);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = packed_warp_wait(bar, parity, p.status, abort);
+      tc_fence_after();
+      return got;
+    };
+    // S of tile x against key tile t (whose K has landed).  (Descriptor
+    // addresses are in units of 16 bytes.)
+    auto scores = [&](int x, int t) {
+      const uint64_t q = q_desc + x * (L::Q_BYTES >> 4);
+      const uint64_t k = k_desc + (t % NS) * (L::KV_BYTES >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk & 3) * 32;
-          mma_ss(tmem + L::TM_S + x * BN, sdesc_sw128(q + (kk >> 2) * BM * 128 + off, 16, 1024),
-                 sdesc_sw128(k + (kk >> 2) * BN * 128 + off, 16, 1024), IDESC_S | neg_a,
-                 kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&ctrl->s_full[x]);
-      };
-      auto values = [&](int x, int t) {
-        const uint32_t v = smem_u32(smem + L::OFF_V + (t % NS) * L::KV_BYTES);
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss_warp(tmem + L::TM_S + x * BN, q + ((kk >> 2) * BM * 128 + (kk & 3) * 32) / 16,
+                    k + ((kk >> 2) * BN * 128 + (kk & 3) * 32) / 16, IDESC_S | neg_a,
+                    kk > 0 ? 1u : 0u);
+      mma_commit_warp(&ctrl->s_full[x]);
+    };
+    // O of tile x: the products of half a key tile
+    auto values = [&](int x, int t, int half) {
+      const uint64_t v = v_desc + (t % NS) * (L::KV_BYTES >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tmem + L::TM_O + x * D, tmem + L::TM_S + x * BN + kk * 8,
-                 sdesc_sw128(v + kk * 16 * 128, BN * 128, 1024), IDESC_O,
-                 (t > 0 || kk > 0) ? 1u : 0u);
-      };
-      bool ok = mbar_wait(&ctrl->q_full[0], 0, abort) && mbar_wait(&ctrl->k_full[0], 0, abort);
-      if (ok) {
-        tc_fence_after();
-        scores(0, 0);
-        if (n_b > 0) {
-          ok = mbar_wait(&ctrl->q_full[1], 0, abort);
-          if (ok) scores(1, 0);
-        }
-        mma_commit(&ctrl->k_empty[0]);
+      for (int k2 = 0; k2 < BN / 32; ++k2) {
+        const int kk = half * (BN / 32) + k2;
+        mma_ts_warp(tmem + L::TM_O + x * D, tmem + L::TM_S + x * BN + kk * 8,
+                    v + kk * (16 * 128 / 16), IDESC_O, (t > 0 || kk > 0) ? 1u : 0u);
       }
-      for (int t = 0; ok && t < n; ++t) {
-        const bool b_last = t < n_b;           // B is the last user of V(t) ...
-        const bool b_last_k = t + 1 < n_b;     // ... and of K(t + 1)
-        bool v_here = false, k_here = false;
-        for (int x = 0; ok && x < 2; ++x) {
-          const int nx = x ? n_b : n_a;
-          if (t >= nx) continue;
-          if (!v_here) {
-            ok = (t == n - 1 && tail < BN) ? mbar_wait(&ctrl->v_tail, 0, abort)
-                                           : mbar_wait(&ctrl->v_full[t % NS], (t / NS) & 1, abort);
-            v_here = true;
-          }
-          if (!ok || !mbar_wait(&ctrl->p_full[x], t & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          values(x, t);
-          if (b_last ? x == 1 : x == 0) mma_commit(&ctrl->v_empty[t % NS]);
-          if (t + 1 < nx) {
-            if (!k_here) {
-              ok = mbar_wait(&ctrl->k_full[(t + 1) % NS], ((t + 1) / NS) & 1, abort);
-              if (!ok) break;
-              tc_fence_after();
-              k_here = true;
-            }
-            scores(x, t + 1);
-            if (b_last_k ? x == 1 : x == 0) mma_commit(&ctrl->k_empty[(t + 1) % NS]);
-          } else {
-            mma_commit(&ctrl->o_full[x]);
-          }
-        }
+    };
+    bool ok = wait(&ctrl->q_full[0], 0) && wait(&ctrl->k_full[0], 0);
+    if (ok) {
+      scores(0, 0);
+      if (n_b > 0) {
+        ok = wait(&ctrl->q_full[1], 0);
+        if (ok) scores(1, 0);
       }
-      if (!ok) packed_timeout(p.status, abort);
-      // every MMA issued completes before TMEM is freed
-      mma_commit(&ctrl->drain);
-      const int zero = 0;
-      mbar_wait(&ctrl->drain, 0, &zero);
+      mma_commit_warp(&ctrl->k_empty[0]);
     }
+    for (int t = 0; ok && t < n; ++t) {
+      const bool b_last = t < n_b;           // B is the last user of V(t) ...
+      const bool b_last_k = t + 1 < n_b;     // ... and of K(t + 1)
+      bool v_here = false, k_here = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int nx = x ? n_b : n_a;
+        if (!ok || t >= nx) continue;
+        if (!v_here)
+          ok = (t == n - 1 && tail < BN) ? wait(&ctrl->v_tail, 0)
+                                         : wait(&ctrl->v_full[t % NS], (t / NS) & 1);
+        v_here = true;
+        if (!ok || !(ok = wait(&ctrl->p_half[x], t & 1))) continue;
+        values(x, t, 0);
+        if (!(ok = wait(&ctrl->p_full[x], t & 1))) continue;
+        values(x, t, 1);
+        if (b_last ? x == 1 : x == 0) mma_commit_warp(&ctrl->v_empty[t % NS]);
+        if (t + 1 < nx) {
+          if (!k_here && !(ok = wait(&ctrl->k_full[(t + 1) % NS], ((t + 1) / NS) & 1))) continue;
+          k_here = true;
+          scores(x, t + 1);
+          if (b_last_k ? x == 1 : x == 0) mma_commit_warp(&ctrl->k_empty[(t + 1) % NS]);
+        } else {
+          mma_commit_warp(&ctrl->o_full[x]);
+        }
+      }
+    }
+    // every MMA issued completes before TMEM is freed
+    mma_commit_warp(&ctrl->drain);
+    const int zero = 0;
+    mbar_wait(&ctrl->drain, 0, &zero);
+  }
   } else {
     // ------------------------------------------------------------ softmax
-    const int x = (warp - 2) >> 2;  // query tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int x = (warp - 4) >> 2;  // query tile
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..
     const int r = sub * 32 + lane;
     const int nx = x ? n_b : n_a;
@@ -394,6 +404,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           pk[e >> 1] = PackedElem<T>::pack(w.x, w.y);
         }
         tmem_st16(s_tm + q / 2, pk);
+        if (q == BN / 2 - 32) {  // the second product starts on the first half
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctrl->p_half[x]);
+        }
       }
       l_run += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
                ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
