@@ -21,10 +21,12 @@ __device__ __forceinline__ bool find_packed_tile(const int* cu, int B, int T, in
   const int lane = threadIdx.x & 31;
   int base = 0;
   bool bad = false, found = false;
+  int next0 = lane < B ? __ldg(cu + lane) : 0, next1 = lane < B ? __ldg(cu + lane + 1) : 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    int r0 = 0, r1 = 0;
-    if (b < B) r0 = __ldg(cu + b), r1 = __ldg(cu + b + 1);
+    int r0 = next0, r1 = next1;
+    // (the next 32 offsets are fetched while these are summed)
+    const int nb = b0 + 32 + lane;
+    next0 = nb < B ? __ldg(cu + nb) : 0, next1 = nb < B ? __ldg(cu + nb + 1) : 0;
     if (r0 < 0 || r1 < r0 || r1 > T) {
       bad = true;
       r0 = r1 = 0;

@@ -14,22 +14,37 @@
 // while one tile's softmax runs, the tensor core works for the other.
 //   warp 0      TMA producer: Q of both tiles, then K and V tiles through two
 //               rings
-//   warp 1      TMEM allocator; issues every MMA:
-//               S_A(t + 1) right after O_A += P_A(t) V(t), then the same for B
+//   warp 1      TMEM allocator; issues every MMA
+//   warps 2, 3  only fill the warpgroup
 //   warps 4..7  softmax of tile A, one row per thread; warps 8..11 of tile B
-// P~ overwrites the first half of its S columns as 16-bit values and is the A
-// operand of the second product from TMEM; it is published in two halves, so
-// that the product starts while the second half's exponentials are formed.  MMAs of one thread complete in
-// order, so "S(t + 1) is final" also says that O has tile t's contribution:
-// the (rare) rescale of O needs no barrier of its own.
+//
+// The scores of a step (query tile, key tile) are formed in a buffer in TMEM,
+// the softmax writes the weights P~ over their first half as 16-bit values, and
+// the second product O += P~ V reads them from there as its A operand.  P~ is
+// published in two halves, so that the product starts while the second half's
+// exponentials are formed.  Behind the product, in the same warp and therefore
+// in order, go the next scores into that buffer: at D = 128 (two buffers; they
+// and both O fill the 512 columns) the same tile's, at D = 64 (three) those of
+// three steps on in the order A(0), B(0), A(1), B(1), ..., so that a softmax
+// warpgroup finds its next scores ready.
 //
 // The row maximum in the exponent moves only when a tile's maximum exceeds it
-// by 2^8; ratios are exact for any stale maximum.
+// by 2^8 (ratios are exact for any stale maximum), so O is rarely rescaled.
 //
 // The last key tile of a sequence may end inside the box: the rows behind it
 // are another sequence's.  Their scores are replaced before the maximum, and
 // their V rows, whose weights are 0, are overwritten with zeros in shared
 // memory (0 * NaN would not be 0).
+//
+// What bounds it: at D = 128 the tensor core's operand reads (one step's
+// products, 2 x 128 x 128 x 128, read 96 KB of shared memory for 1024 cycles of
+// tensor work at 128 bytes a cycle, and copies write 32 KB more); at D = 64 the
+// exponentials and the rest of the softmax.  Measured and not kept: a
+// persistent CTA that takes over blocks through the launch control (8 % slower
+// on long prompts: its item rings keep more warps polling; 20 % faster on
+// prompts of one tile); one issuing warp per query tile (the tiles' products
+// interleave and both scores come late: 1182 against 1154 us); waits with a
+// suspend-time hint (5 % slower).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -76,9 +91,11 @@ struct PackedLayout {
   static constexpr int SMEM_BYTES = OFF_CTRL + 1024 + 1024;  // control block, alignment
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(SMEM_BYTES > 114 * 1024, "one CTA per SM: it owns all TMEM columns");
-  static constexpr uint32_t TM_S = 0;            // S / P~ of tile x at x * BN
-  static constexpr uint32_t TM_O = 2 * BN;       // O of tile x at TM_O + x * D
+  static constexpr int NB = D == 128 ? 2 : 3;    // score buffers
+  static constexpr uint32_t TM_S = 0;            // S / P~ of buffer b at b * BN
+  static constexpr uint32_t TM_O = NB * BN;      // O of tile x at TM_O + x * D
   static constexpr uint32_t TM_COLS = 512;
+  static_assert(NB * BN + 2 * D <= TM_COLS, "TMEM columns");
 };
 
 // Three warpgroups: producer and MMA warps (two more only fill the group),
@@ -86,15 +103,17 @@ struct PackedLayout {
 // scores, so its group takes registers from the first (168 * 3 = 72 + 2 * 216).
 constexpr int kPackedThreads = 384;
 
-template <int NS>
+template <int NS, int NB>
 struct PackedCtrl {
   uint64_t q_full[2];
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  uint64_t v_tail;     // the last V tile's rows behind the sequence are zero
-  uint64_t s_full[2];  // S of the next key tile is final (and O has the previous one's)
-  uint64_t p_half[2];  // P~ of the tile's first 64 keys is stored
-  uint64_t p_full[2];  // P~ of the others is
-  uint64_t o_full[2];  // O is complete
+  uint64_t v_tail;      // the last V tile's rows behind the sequence are zero
+  uint64_t s_full[NB];  // scores of the step in the buffer are final
+  uint64_t p_half[NB];  // its P~ of the first 64 keys is stored
+  uint64_t p_full[NB];  // P~ of the others is
+  uint64_t o_done[2];   // O of a query tile has its next key tile's product (NB = 3)
+  uint64_t o_full[2];   // O has the last key tile's product
+  uint64_t staged[2];   // the tile's output rows are in shared memory
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -108,7 +127,7 @@ __device__ __forceinline__ void packed_timeout(unsigned int* status, volatile in
 // instructions that follow are warp-collective).
 __device__ __forceinline__ bool packed_warp_wait(uint64_t* bar, uint32_t parity,
                                                  unsigned int* status, volatile int* abort) {
-  const bool got = mbar_wait(bar, parity, abort);
+  const bool got = mbar_wait<false>(bar, parity, abort);
   if (!got) packed_timeout(status, abort);
   return __all_sync(0xffffffffu, got);
 }
@@ -130,7 +149,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     packed_tc_kernel(const __grid_constant__ PackedMaps maps, const PackedParams p) {
   using L = PackedLayout<D>;
-  constexpr int BM = L::BM, BN = L::BN, NS = L::NS, KCH = L::KCH;
+  constexpr int BM = L::BM, BN = L::BN, NS = L::NS, NB = L::NB, KCH = L::KCH;
   constexpr bool kBF16 = PackedElem<T>::kBF16;
   constexpr uint32_t IDESC_S = idesc_f16(kBF16, BM, BN, false);
   constexpr uint32_t IDESC_O = idesc_f16(kBF16, BM, D, true);
@@ -138,36 +157,28 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  static_assert(sizeof(PackedCtrl<NS>) <= 1024, "control block budget");
-  PackedCtrl<NS>* ctrl = reinterpret_cast<PackedCtrl<NS>*>(smem + L::OFF_CTRL);
+  using Ctrl = PackedCtrl<NS, NB>;
+  static_assert(sizeof(Ctrl) <= 1024, "control block budget");
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + L::OFF_CTRL);
   volatile int* abort = &ctrl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // Heads outermost, so that the CTAs in flight share a key/value head's rows
-  // in L2; causal sequences begin with their last (longest) tile.
-  const int hk = static_cast<int>(blockIdx.x) / p.tiles;
-  const int u = static_cast<int>(blockIdx.x) % p.tiles;
-  PackedTile pt;
-  if (!find_packed_tile(p.cu, p.B, p.T, 2 * p.tok, u, p.causal != 0, p.status, &pt)) return;
-  const int len = pt.len, r0 = pt.r0;
-  const int tok0 = pt.tile * 2 * p.tok;  // first token of tile A; B follows
-  // key tiles of a query tile whose first token is a
-  auto key_tiles = [&](int a) {
-    if (a >= len) return 0;
-    const int keys = p.causal ? min(a + p.tok, len) : len;
-    return (keys + BN - 1) / BN;
-  };
-  const int n_a = key_tiles(tok0), n_b = key_tiles(tok0 + p.tok);
-  const int n = max(n_a, n_b);
-  const int tail = len - (n - 1) * BN;  // keys of the last tile (>= BN: all of its rows)
-
-  if (threadIdx.x == 0) {
+  // Set-up first, so that it runs while the offsets are fetched.
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+    tma_prefetch_desc(&maps.o);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctrl->q_full[x], 1);
-      mbar_init(&ctrl->s_full[x], 1);
-      mbar_init(&ctrl->p_half[x], 4);  // one arrival per softmax warp of the tile
-      mbar_init(&ctrl->p_full[x], 4);
+      mbar_init(&ctrl->o_done[x], 1);
       mbar_init(&ctrl->o_full[x], 1);
+      mbar_init(&ctrl->staged[x], 4);  // one arrival per softmax warp of the tile
+    }
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(&ctrl->s_full[b], 1);
+      mbar_init(&ctrl->p_half[b], 4);
+      mbar_init(&ctrl->p_full[b], 4);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&ctrl->k_full[s], 1);
@@ -180,153 +191,241 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     ctrl->abort = 0;
     fence_barrier_init();
   }
+  __syncwarp();
+  // Key/value heads in groups whose rows stay in L2, the heads of a group
+  // innermost; causal sequences begin with their last (longest) tile.
+  const int per_group = p.tiles * p.head_group;
+  const int hg = static_cast<int>(blockIdx.x) / per_group;
+  const int in_group = static_cast<int>(blockIdx.x) - hg * per_group;
+  const int heads = min(p.head_group, p.Hkv - hg * p.head_group);
+  const int hk = hg * p.head_group + in_group % heads;
+  const int u = in_group / heads;
+  PackedTile pt;
+  const bool have = find_packed_tile(p.cu, p.B, p.T, 2 * p.tok, u, p.causal != 0, p.status, &pt);
+  if (!have) return;  // (the list is shorter than its bound; the same for every warp)
   if (warp == 1) {
     tmem_alloc(&ctrl->tmem_base, L::TM_COLS);
     tmem_relinquish();
   }
+  const int len = pt.len, r0 = pt.r0;
+  const int tok0 = pt.tile * 2 * p.tok;  // first token of tile A; B follows
+  // key tiles of a query tile whose first token is a
+  auto key_tiles = [&](int a) {
+    if (a >= len) return 0;
+    const int keys = p.causal ? min(a + p.tok, len) : len;
+    return (keys + BN - 1) / BN;
+  };
+  const int n_a = key_tiles(tok0), n_b = key_tiles(tok0 + p.tok);
+  const int n = max(n_a, n_b), both = min(n_a, n_b);
+  const int tail = len - (n - 1) * BN;  // keys of the last tile (>= BN: all of its rows)
+  // score buffer of query tile x against key tile t, and its use
+  auto buffer_of = [&](int x, int t, uint32_t* use) {
+    if (NB == 2) {
+      *use = t;
+      return x;
+    }
+    const int step = t < both ? 2 * t + x : both + t;
+    *use = step / NB;
+    return step % NB;
+  };
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return packed_warp_wait(bar, parity & 1, p.status, abort);
+  };
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    bool ok = true;
-    if (lane == 0) {
-      tma_prefetch_desc(&maps.q);
-      tma_prefetch_desc(&maps.k);
-      tma_prefetch_desc(&maps.v);
-      auto load_q = [&](int x) {
-        mbar_arrive_expect_tx(&ctrl->q_full[x], KCH * p.group * p.tok * 128);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      bool ok = true;
+      if (lane == 0) {
+        auto load_q = [&](int x) {
+          mbar_arrive_expect_tx(&ctrl->q_full[x], KCH * p.group * p.tok * 128);
+          for (int c = 0; c < KCH; ++c)
+            tma_load_4d(smem + L::OFF_Q + x * L::Q_BYTES + c * BM * 128, &maps.q, &ctrl->q_full[x],
+                        c * 64, hk * p.group, r0 + tok0 + x * p.tok, 0);
+        };
+        int k_fills = 0, v_fills = 0;
+        auto load_kv = [&](int t, bool v) -> bool {
+          const int s = t % NS;
+          uint64_t* empty = v ? &ctrl->v_empty[s] : &ctrl->k_empty[s];
+          uint64_t* full = v ? &ctrl->v_full[s] : &ctrl->k_full[s];
+          if (!mbar_wait<false>(empty, ((t / NS) & 1) ^ 1, abort)) return false;
+          mbar_arrive_expect_tx(full, L::KV_BYTES);
+          uint8_t* dst = smem + (v ? L::OFF_V : L::OFF_K) + s * L::KV_BYTES;
+          for (int c = 0; c < KCH; ++c)
+            tma_load_4d(dst + c * BN * 128, v ? &maps.v : &maps.k, full, c * 64, r0 + t * BN, hk,
+                        0);
+          ++(v ? v_fills : k_fills);
+          return true;
+        };
+        load_q(0);
+        ok = load_kv(0, false);
+        if (n_b > 0) load_q(1);
+        for (int t = 0; ok && t < n; ++t) {
+          if (t + 1 < n) ok = load_kv(t + 1, false);  // (needed before V(t))
+          if (ok) ok = load_kv(t, true);
+        }
+        if (!ok) {
+          packed_timeout(p.status, abort);
+          // let every copy already issued land before the CTA can exit
+          const int zero = 0;
+          mbar_wait(&ctrl->q_full[0], 0, &zero);
+          if (n_b > 0) mbar_wait(&ctrl->q_full[1], 0, &zero);
+          for (int t = max(0, k_fills - NS); t < k_fills; ++t)
+            mbar_wait(&ctrl->k_full[t % NS], (t / NS) & 1, &zero);
+          for (int t = max(0, v_fills - NS); t < v_fills; ++t)
+            mbar_wait(&ctrl->v_full[t % NS], (t / NS) & 1, &zero);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && tail < BN) {
+        // rows of the last V tile behind the sequence: zero
+        const int s = (n - 1) % NS;
+        ok = wait(&ctrl->v_full[s], (n - 1) / NS);
+        if (ok) {
+          const uint32_t v = smem_u32(smem + L::OFF_V + s * L::KV_BYTES);
+          for (int e = lane; e < (BN - tail) * KCH * 8; e += 32) {
+            const int piece = e % 8, c = (e / 8) % KCH, row = tail + e / (8 * KCH);
+            st_shared_v4(v + c * BN * 128 + row * 128 + piece * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctrl->v_tail);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMAs
+      // The whole warp walks the steps; one elected lane issues.  (Descriptor
+      // addresses are in units of 16 bytes.)
+      const uint32_t neg_a = p.neg_scores ? (1u << 13) : 0u;
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::OFF_V), BN * 128, 1024);
+      // The pace of this warp is the kernel's: between two products there is
+      // little but their waits, and the buffers of the main loops are constants.
+      auto scores = [&](int x, int t, int buf) {
+        const uint64_t qd = q_desc + x * (L::Q_BYTES >> 4);
+        const uint64_t kd = k_desc + (t % NS) * (L::KV_BYTES >> 4);
+#pragma unroll
         for (int c = 0; c < KCH; ++c)
-          tma_load_4d(smem + L::OFF_Q + x * L::Q_BYTES + c * BM * 128, &maps.q, &ctrl->q_full[x],
-                      c * 64, hk * p.group, r0 + tok0 + x * p.tok, 0);
+          mma_ss_x4_warp<2, 2>(tmem + L::TM_S + buf * BN, qd + c * (BM * 128 / 16),
+                               kd + c * (BN * 128 / 16), IDESC_S | neg_a, c > 0 ? 1u : 0u);
+        mma_commit_warp(&ctrl->s_full[buf]);
       };
-      int k_fills = 0, v_fills = 0;
-      auto load_kv = [&](int t, bool v) -> bool {
-        const int s = t % NS;
-        uint64_t* empty = v ? &ctrl->v_empty[s] : &ctrl->k_empty[s];
-        uint64_t* full = v ? &ctrl->v_full[s] : &ctrl->k_full[s];
-        if (!mbar_wait(empty, ((t / NS) & 1) ^ 1, abort)) return false;
-        mbar_arrive_expect_tx(full, L::KV_BYTES);
-        uint8_t* dst = smem + (v ? L::OFF_V : L::OFF_K) + s * L::KV_BYTES;
-        for (int c = 0; c < KCH; ++c)
-          tma_load_4d(dst + c * BN * 128, v ? &maps.v : &maps.k, full, c * 64, r0 + t * BN, hk, 0);
-        ++(v ? v_fills : k_fills);
+      auto k_landed = [&](int t) {
+        const bool got = wait(&ctrl->k_full[t % NS], t / NS);
+        tc_fence_after();
+        return got;
+      };
+      auto v_landed = [&](int t) {
+        return (t == n - 1 && tail < BN) ? wait(&ctrl->v_tail, 0)
+                                         : wait(&ctrl->v_full[t % NS], t / NS);
+      };
+      // O of query tile x: the product with the weights in buffer buf (its
+      // use-th), half a key tile as soon as its weights are there
+      auto values = [&](int x, int t, int buf, uint32_t use) {
+        const uint64_t vd = v_desc + (t % NS) * (L::KV_BYTES >> 4);
+        const uint32_t p_tm = tmem + L::TM_S + buf * BN, o_tm = tmem + L::TM_O + x * D;
+        if (!wait(&ctrl->p_half[buf], use)) return false;
+        tc_fence_after();
+        mma_ts_x4_warp<8, 128>(o_tm, p_tm, vd, IDESC_O, t > 0 ? 1u : 0u);
+        if (!wait(&ctrl->p_full[buf], use)) return false;
+        tc_fence_after();
+        mma_ts_x4_warp<8, 128>(o_tm, p_tm + 32, vd + 4 * 128, IDESC_O, 1u);
         return true;
       };
-      load_q(0);
-      ok = load_kv(0, false);
-      if (n_b > 0) load_q(1);
-      for (int t = 0; ok && t < n; ++t) {
-        ok = load_kv(t, true);
-        if (ok && t + 1 < n) ok = load_kv(t + 1, false);
-      }
-      if (!ok) {
-        packed_timeout(p.status, abort);
-        // let every copy already issued land before the CTA can exit
-        const int zero = 0;
-        mbar_wait(&ctrl->q_full[0], 0, &zero);
-        if (n_b > 0) mbar_wait(&ctrl->q_full[1], 0, &zero);
-        for (int t = max(0, k_fills - NS); t < k_fills; ++t)
-          mbar_wait(&ctrl->k_full[t % NS], (t / NS) & 1, &zero);
-        for (int t = max(0, v_fills - NS); t < v_fills; ++t)
-          mbar_wait(&ctrl->v_full[t % NS], (t / NS) & 1, &zero);
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && tail < BN) {
-      // rows of the last V tile behind the sequence: zero
-      const int t = n - 1, s = t % NS;
-      ok = packed_warp_wait(&ctrl->v_full[s], (t / NS) & 1, p.status, abort);
+      bool ok = wait(&ctrl->q_full[0], 0) && k_landed(0);
       if (ok) {
-        const uint32_t v = smem_u32(smem + L::OFF_V + s * L::KV_BYTES);
-        for (int e = lane; e < (BN - tail) * KCH * 8; e += 32) {
-          const int piece = e % 8, c = (e / 8) % KCH, row = tail + e / (8 * KCH);
-          st_shared_v4(v + c * BN * 128 + row * 128 + piece * 16, 0u, 0u, 0u, 0u);
+        scores(0, 0, 0);
+        if (n_b > 0) {
+          ok = wait(&ctrl->q_full[1], 0);
+          tc_fence_after();
+          if (ok) scores(1, 0, 1);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->v_tail);
+        mma_commit_warp(&ctrl->k_empty[0]);
       }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs
-    // The whole warp walks this loop; one elected lane issues.
-    const uint32_t neg_a = p.neg_scores ? (1u << 13) : 0u;
-    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::OFF_V), BN * 128, 1024);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool got = packed_warp_wait(bar, parity, p.status, abort);
-      tc_fence_after();
-      return got;
-    };
-    // S of tile x against key tile t (whose K has landed).  (Descriptor
-    // addresses are in units of 16 bytes.)
-    auto scores = [&](int x, int t) {
-      const uint64_t q = q_desc + x * (L::Q_BYTES >> 4);
-      const uint64_t k = k_desc + (t % NS) * (L::KV_BYTES >> 4);
+      if constexpr (NB == 2) {
+        for (int t = 0; ok && t < n; ++t) {
+          const bool b_last = t < n_b;        // B is the last user of V(t) ...
+          const bool b_last_k = t + 1 < n_b;  // ... and of K(t + 1)
+          bool v_here = false, k_here = false;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_warp(tmem + L::TM_S + x * BN, q + ((kk >> 2) * BM * 128 + (kk & 3) * 32) / 16,
-                    k + ((kk >> 2) * BN * 128 + (kk & 3) * 32) / 16, IDESC_S | neg_a,
-                    kk > 0 ? 1u : 0u);
-      mma_commit_warp(&ctrl->s_full[x]);
-    };
-    // O of tile x: the products of half a key tile
-    auto values = [&](int x, int t, int half) {
-      const uint64_t v = v_desc + (t % NS) * (L::KV_BYTES >> 4);
-#pragma unroll
-      for (int k2 = 0; k2 < BN / 32; ++k2) {
-        const int kk = half * (BN / 32) + k2;
-        mma_ts_warp(tmem + L::TM_O + x * D, tmem + L::TM_S + x * BN + kk * 8,
-                    v + kk * (16 * 128 / 16), IDESC_O, (t > 0 || kk > 0) ? 1u : 0u);
-      }
-    };
-    bool ok = wait(&ctrl->q_full[0], 0) && wait(&ctrl->k_full[0], 0);
-    if (ok) {
-      scores(0, 0);
-      if (n_b > 0) {
-        ok = wait(&ctrl->q_full[1], 0);
-        if (ok) scores(1, 0);
-      }
-      mma_commit_warp(&ctrl->k_empty[0]);
-    }
-    for (int t = 0; ok && t < n; ++t) {
-      const bool b_last = t < n_b;           // B is the last user of V(t) ...
-      const bool b_last_k = t + 1 < n_b;     // ... and of K(t + 1)
-      bool v_here = false, k_here = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int nx = x ? n_b : n_a;
-        if (!ok || t >= nx) continue;
-        if (!v_here)
-          ok = (t == n - 1 && tail < BN) ? wait(&ctrl->v_tail, 0)
-                                         : wait(&ctrl->v_full[t % NS], (t / NS) & 1);
-        v_here = true;
-        if (!ok || !(ok = wait(&ctrl->p_half[x], t & 1))) continue;
-        values(x, t, 0);
-        if (!(ok = wait(&ctrl->p_full[x], t & 1))) continue;
-        values(x, t, 1);
-        if (b_last ? x == 1 : x == 0) mma_commit_warp(&ctrl->v_empty[t % NS]);
-        if (t + 1 < nx) {
-          if (!k_here && !(ok = wait(&ctrl->k_full[(t + 1) % NS], ((t + 1) / NS) & 1))) continue;
-          k_here = true;
-          scores(x, t + 1);
-          if (b_last_k ? x == 1 : x == 0) mma_commit_warp(&ctrl->k_empty[(t + 1) % NS]);
-        } else {
-          mma_commit_warp(&ctrl->o_full[x]);
+          for (int x = 0; x < 2; ++x) {
+            const int nx = x ? n_b : n_a;
+            if (!ok || t >= nx) continue;
+            if (!v_here) ok = v_landed(t);
+            v_here = true;
+            if (!ok || !(ok = values(x, t, x, t))) continue;
+            if (b_last ? x == 1 : x == 0) mma_commit_warp(&ctrl->v_empty[t % NS]);
+            if (t + 1 < nx) {
+              if (!k_here && !(ok = k_landed(t + 1))) continue;
+              k_here = true;
+              scores(x, t + 1, x);
+              if (b_last_k ? x == 1 : x == 0) mma_commit_warp(&ctrl->k_empty[(t + 1) % NS]);
+            } else {
+              mma_commit_warp(&ctrl->o_full[x]);
+            }
+          }
+        }
+      } else {
+        // While both tiles have keys: step i's product, then step i + 3's scores.
+        if (ok && both > 1) {
+          ok = k_landed(1);
+          if (ok) scores(0, 1, 2);
+        }
+        auto step = [&](int x, int t, int buf, uint32_t use) {
+          if (x == 0 && !(ok = v_landed(t))) return;
+          if (!(ok = values(x, t, buf, use))) return;
+          mma_commit_warp(&ctrl->o_done[x]);
+          if (t + 1 == (x ? n_b : n_a)) mma_commit_warp(&ctrl->o_full[x]);
+          if (x == 1) mma_commit_warp(&ctrl->v_empty[t % NS]);
+          if (x == 0 && t + 1 < both) {
+            scores(1, t + 1, buf);
+            mma_commit_warp(&ctrl->k_empty[(t + 1) % NS]);
+          }
+          if (x == 1 && t + 2 < both) {
+            if (!(ok = k_landed(t + 2))) return;
+            scores(0, t + 2, buf);
+          }
+        };
+        for (int t = 0; ok && t < both; t += 3) {
+          const uint32_t use = 2 * (t / 3);
+          step(0, t, 0, use);
+          if (ok) step(1, t, 1, use);
+          if (ok && t + 1 < both) step(0, t + 1, 2, use);
+          if (ok && t + 1 < both) step(1, t + 1, 0, use + 1);
+          if (ok && t + 2 < both) step(0, t + 2, 1, use + 1);
+          if (ok && t + 2 < both) step(1, t + 2, 2, use + 1);
+        }
+        // Then one tile alone, its scores up to two key tiles ahead of its
+        // products (no more: the softmax relies on it, see its wait on o_done).
+        const int x = n_a > n_b ? 0 : 1;
+        auto solo_scores = [&](int t) {
+          if (t >= n || (t == 0 && both == 0)) return true;
+          if (!k_landed(t)) return false;
+          scores(x, t, (both + t) % NB);
+          mma_commit_warp(&ctrl->k_empty[t % NS]);
+          return true;
+        };
+        if (ok && both < n) ok = solo_scores(both) && solo_scores(both + 1);
+        for (int t = both; ok && t < n; ++t) {
+          if (!(ok = v_landed(t) && values(x, t, (both + t) % NB, (both + t) / NB))) break;
+          mma_commit_warp(&ctrl->o_done[x]);
+          if (t + 1 == n) mma_commit_warp(&ctrl->o_full[x]);
+          mma_commit_warp(&ctrl->v_empty[t % NS]);
+          ok = solo_scores(t + 2);
         }
       }
+      if (!ok) packed_timeout(p.status, abort);
+      // every MMA issued completes before TMEM is freed
+      mma_commit_warp(&ctrl->drain);
+      const int zero = 0;
+      mbar_wait(&ctrl->drain, 0, &zero);
     }
-    // every MMA issued completes before TMEM is freed
-    mma_commit_warp(&ctrl->drain);
-    const int zero = 0;
-    mbar_wait(&ctrl->drain, 0, &zero);
-  }
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -334,9 +433,10 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..
     const int r = sub * 32 + lane;
     const int nx = x ? n_b : n_a;
-    const int i = tok0 + x * p.tok + r / p.group;  // token within the sequence
-    const int h = hk * p.group + r % p.group;
-    const bool row_ok = r < p.tok * p.group && i < len;
+    const int rt = r / p.group, rh = r - rt * p.group;  // token and head of the row
+    const int first = tok0 + x * p.tok;                 // first token of the tile
+    const int i = first + rt;                           // token within the sequence
+    const bool row_ok = rt < p.tok && i < len;
     // keys j < limit count; for the rows of the tile that are not used: all
     const int limit = (p.causal && row_ok) ? i + 1 : len;
     int warp_limit = limit;
@@ -344,15 +444,15 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     for (int o = 16; o > 0; o >>= 1)
       warp_limit = min(warp_limit, __shfl_xor_sync(0xffffffffu, warp_limit, o));
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-    const uint32_t s_tm = lane_base + L::TM_S + x * BN, o_tm = lane_base + L::TM_O + x * D;
+    const uint32_t o_tm = lane_base + L::TM_O + x * D;
     const float c = p.scale_log2;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int t = 0; t < nx; ++t) {
-      if (!packed_warp_wait(&ctrl->s_full[x], t & 1, p.status, abort)) {
-        ok = false;
-        break;
-      }
+      uint32_t use;
+      const int buf = buffer_of(x, t, &use);
+      const uint32_t s_tm = lane_base + L::TM_S + buf * BN;
+      if (!(ok = wait(&ctrl->s_full[buf], use))) break;
       tc_fence_after();
       float s[BN];
 #pragma unroll
@@ -379,6 +479,14 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         l_run *= alpha;
         m_run = m_new;
         if (t > 0) {
+          // O has tile t - 1's product: with two buffers because these scores
+          // were issued behind it, with three by the barrier.  (Of that phase
+          // the barrier can be at most one behind, so the parity tells: these
+          // scores were issued behind tile t - 2's product.)
+          if (NB > 2) {
+            if (!(ok = wait(&ctrl->o_done[x], t - 1))) break;
+            tc_fence_after();
+          }
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
             uint32_t o[32];
@@ -408,7 +516,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->p_half[x]);
+          if (lane == 0) mbar_arrive(&ctrl->p_half[buf]);
         }
       }
       l_run += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
@@ -416,46 +524,50 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->p_full[x]);
+      if (lane == 0) mbar_arrive(&ctrl->p_full[buf]);
     }
     // ------------------------------------------------------------ epilogue
-    if (nx > 0 && ok) ok = packed_warp_wait(&ctrl->o_full[x], 0, p.status, abort);
-    if (nx > 0 && ok) {
+    if (nx > 0 && ok && (ok = wait(&ctrl->o_full[x], 0))) {
       tc_fence_after();
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (NaN stays NaN)
       if (row_ok && p.lse)
-        p.lse[static_cast<long long>(h) * p.T + r0 + i] =
+        p.lse[static_cast<long long>(hk * p.group + rh) * p.T + r0 + i] =
             l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
-      // Rows through the (now idle) Q tile, so that a warp's stores cover
-      // whole rows; 16-byte piece k of row r at position k ^ (r % 8).
-      constexpr int PIECES = D / 8;
-      const uint32_t stage = smem_u32(smem + L::OFF_Q + x * L::Q_BYTES);
+      // All tokens of the tile exist: through the (now idle) Q tile, 16-byte
+      // piece k of row r at position k ^ (r % 8), and a TMA store of the box.
+      // Else the sequence ends inside the tile: each thread writes its row.
+      const bool whole = first + p.tok <= len;
+      const uint32_t stage = smem_u32(smem + L::OFF_Q + x * L::Q_BYTES) + r * 128;
+      T* dst = static_cast<T*>(p.o) + static_cast<long long>(r0 + i) * p.so.n +
+               static_cast<long long>(hk * p.group + rh) * p.so.h;
 #pragma unroll
-      for (int col = 0; col < D; col += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_tm + col, o);
+      for (int col = 0; col < D; col += 64) {
+        uint32_t o[2][32];
+        tmem_ld32x2(o_tm + col, o_tm + col + 32, o[0], o[1]);
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
+        for (int e = 0; e < 64; e += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = PackedElem<T>::pack(__uint_as_float(o[e + 2 * k]) * inv,
-                                       __uint_as_float(o[e + 2 * k + 1]) * inv);
-          const int piece = (col + e) / 8;
-          st_shared_v4(stage + r * (D * 2) + ((piece ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+            w[k] = PackedElem<T>::pack(__uint_as_float(o[e / 32][e % 32 + 2 * k]) * inv,
+                                       __uint_as_float(o[e / 32][e % 32 + 2 * k + 1]) * inv);
+          if (whole)
+            st_shared_v4(stage + (col / 64) * BM * 128 + (((e / 8) ^ (r & 7)) << 4), w[0], w[1],
+                         w[2], w[3]);
+          else if (row_ok && col + e < p.D)
+            *reinterpret_cast<uint4*>(dst + col + e) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
-      const int piece = lane % PIECES, d = piece * 8;
-#pragma unroll 4
-      for (int k = 0; k < 32; k += 32 / PIECES) {
-        const int rr = sub * 32 + k + lane / PIECES;
-        const int ii = tok0 + x * p.tok + rr / p.group;
-        const float4 w = ld_shared_v4f(stage + rr * (D * 2) + ((piece ^ (rr & 7)) << 4));
-        if (rr < p.tok * p.group && ii < len && d < p.D) {
-          T* dst = static_cast<T*>(p.o) + static_cast<long long>(r0 + ii) * p.so.n +
-                   static_cast<long long>(hk * p.group + rr % p.group) * p.so.h + d;
-          *reinterpret_cast<float4*>(dst) = w;
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->staged[x]);
+        if (warp == 4 + 4 * x && wait(&ctrl->staged[x], 0) && lane == 0) {
+          for (int ch = 0; ch < KCH; ++ch)
+            tma_store_4d(&maps.o, smem + L::OFF_Q + x * L::Q_BYTES + ch * BM * 128, ch * 64,
+                         hk * p.group, r0 + first, 0);
+          tma_store_commit();
+          tma_store_wait_read();  // shared memory stays valid until then
         }
       }
     }

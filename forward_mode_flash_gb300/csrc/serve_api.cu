@@ -274,16 +274,20 @@ jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dt
             aligned_to(o, 16) && multiple(p.so, 8);
   PackedMaps maps;
   if (tc) {
-    // Q: boxes of `tok` tokens times a key/value head's query heads; K, V: key
+    // Q, O: boxes of `tok` tokens times a key/value head's query heads; K, V: key
     // tiles of one head.  (D < 64 or 128: columns past D are zero-filled.)
     p.tok = kPackedTileRows / p.group;
     tc = encode_packed(&maps.q, dtype, q, D, H, p.sq.h, T, p.sq.n, p.group, p.tok) &&
+         encode_packed(&maps.o, dtype, o, D, H, p.so.h, T, p.so.n, p.group, p.tok) &&
          encode_packed(&maps.k, dtype, k, D, T, p.sk.n, Hkv, p.sk.h, kPackedBlockN, 1) &&
          encode_packed(&maps.v, dtype, v, D, T, p.sv.n, Hkv, p.sv.h, kPackedBlockN, 1);
   }
   cudaError_t err;
   if (tc) {
     p.tiles = static_cast<int>(T / (2 * p.tok) + B);  // >= sum of ceil(length / (2 tok))
+    // as many key/value heads side by side as keep their rows within 32 MB of L2
+    p.head_group = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(Hkv, (32ll << 20) / std::max<int64_t>(1, T * D * 2 * e))));
     if (scale < 0.f) {  // negated score products, |scale|
       p.neg_scores = 1;
       p.scale = -p.scale, p.scale_log2 = -p.scale_log2;

@@ -95,7 +95,8 @@ struct PackedParams {
   int T, B, H, Hkv, D, group;
   int causal;
   int tok;             // query tokens of one 128-row tile (tensor cores): 128 / group
-  int tiles;           // upper bound of the CTAs a key/value head needs
+  int tiles;           // upper bound of the blocks a key/value head needs
+  int head_group;      // tensor cores: key/value heads scheduled together
   float scale, scale_log2;
   int neg_scores;      // scale < 0: the score products are formed negated, |scale| applied
   const int* cu;
@@ -108,7 +109,7 @@ struct PackedParams {
   unsigned int* status;
 };
 struct PackedMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 // Tensor-core kernel (fp16 / bf16, D a multiple of 8 up to 128, group <= 128).
 cudaError_t launch_packed_tc(DType dt, int kernel_d, const PackedMaps& maps, const PackedParams& p,

@@ -311,28 +311,44 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
       : "memory");
 }
 
-// The same three for a whole, converged warp: one lane, always the same
-// (elect.sync is deterministic), issues.  With the operands uniform over the
-// warp they stay in uniform registers; issued from a single-lane branch, each
-// product costs that thread about 70 cycles of moves.
-__device__ __forceinline__ void mma_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// The same for a whole, converged warp: one lane, always the same (elect.sync
+// is deterministic), issues.  With the operands uniform over the warp they stay
+// in uniform registers; issued from a single-lane branch, each product costs
+// that thread about 70 cycles.  Four products along K at once: the descriptors
+// advance by AS (A in shared memory), AT (A in TMEM, columns) and BS (B), in
+// the descriptor's units of 16 bytes.
+template <int AS, int BS>
+__device__ __forceinline__ void mma_ss_x4_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q, one;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 one, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, one;\n\t"
+      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, one;\n\t"
+      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, one;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
+template <int AT, int BS>
+__device__ __forceinline__ void mma_ts_x4_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q, one;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 one, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
+      "add.s32 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
+      "add.s32 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(AT), "n"(BS)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
