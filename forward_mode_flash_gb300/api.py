@@ -478,7 +478,7 @@ def _remember(key, plan):
 
 def _layout(t):
     """What a call description depends on: all of a tensor but its address and values."""
-    return None if t is None else (t.dtype, t.device, t.shape, t.stride())
+    return None if t is None else (t.dtype, t.get_device(), t.shape, t.stride())
 
 
 def _data(t):
@@ -541,20 +541,21 @@ def _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale):
                       _abi.Strides(sk[0], sk[1], sk[2], 1), _abi.Strides(sv[0], sv[1], sv[2], 1))
 
 
-class _OnDevice:
-    """Makes a device current for a call, if it is not already."""
-    __slots__ = ("ctx",)
+# Handle of the current stream of a device, without the Stream object that
+# torch.cuda.current_stream makes (1 us of a 10 us call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, index):
-        self.ctx = None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _call(index, entry, *args):
+    """Calls an entry point with a device current and its current stream as the
+    last argument, and raises on an error status."""
+    if torch.cuda.current_device() == index:
+        st = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = entry(*args, _raw_stream(index))
+    if st != _abi.JVP_OK:
+        _abi.check(st)
 
 
 def _packed_plan(q, k, v, cu_seqlens, out):
@@ -605,12 +606,9 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     o = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else out
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=device) \
         if return_lse else None
-    with _OnDevice(device.index):
-        st = _abi.load().jvp_attn_fwd_packed(
-            shape, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, cu_seqlens.data_ptr(),
-            1 if is_causal else 0, default_scale if scale is None else float(scale), o.data_ptr(),
-            o_strides, _data(lse), torch.cuda.current_stream(device.index).cuda_stream)
-    _abi.check(st)
+    _call(device.index, _abi.load().jvp_attn_fwd_packed, shape, dt, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), strides, cu_seqlens.data_ptr(), 1 if is_causal else 0,
+          default_scale if scale is None else float(scale), o.data_ptr(), o_strides, _data(lse))
     return (o, lse) if return_lse else o
 
 
@@ -661,13 +659,10 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
         plan = _remember(key, _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens,
                                          k_scale, v_scale, k, v))
     desc, strides, dt = plan
-    dev = k_cache.device.index
-    with _OnDevice(dev):
-        st = _abi.load().jvp_attn_cache_write(
-            desc, dt, k.shape[0], k.data_ptr(), v.data_ptr(), strides, block_table.data_ptr(),
-            _data(start_pos), _data(cu_seqlens), k_cache.data_ptr(), v_cache.data_ptr(),
-            _data(k_scale), _data(v_scale), torch.cuda.current_stream(dev).cuda_stream)
-    _abi.check(st)
+    _call(k_cache.get_device(), _abi.load().jvp_attn_cache_write, desc, dt, k.shape[0],
+          k.data_ptr(), v.data_ptr(), strides, block_table.data_ptr(), _data(start_pos),
+          _data(cu_seqlens), k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale),
+          _data(v_scale))
 
 
 def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -707,13 +702,10 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         plan = _remember(key, _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens,
                                          k_scale, v_scale, k, v))
     desc, strides, dt = plan
-    dev = k_cache.device.index
-    with _OnDevice(dev):
-        st = _abi.load().jvp_attn_cache_read(
-            desc, dt, k.shape[0], k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale),
-            _data(v_scale), block_table.data_ptr(), _data(start_pos), _data(cu_seqlens),
-            k.data_ptr(), v.data_ptr(), strides, torch.cuda.current_stream(dev).cuda_stream)
-    _abi.check(st)
+    _call(k_cache.get_device(), _abi.load().jvp_attn_cache_read, desc, dt, k.shape[0],
+          k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale), _data(v_scale),
+          block_table.data_ptr(), _data(start_pos), _data(cu_seqlens), k.data_ptr(), v.data_ptr(),
+          strides)
     return k, v
 
 
@@ -732,7 +724,7 @@ def _decode_plan(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, o
     _check_int32(seq_lens, "seq_lens", (desc.B,), dev)
     if out is not None:
         _check_packed(out, "out", q.dtype, dev, shape)
-    with _OnDevice(dev.index):
+    with torch.cuda.device(dev):
         need = int(_abi.load().jvp_attn_decode_workspace_size(desc, H, _DT[q.dtype]))
     o_strides = _abi.Strides(H * desc.D, desc.D, 0, 1) if out is None else \
         _abi.Strides(out.stride(0), out.stride(1), 0, 1)
@@ -767,18 +759,17 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     device = k_cache.device
     o = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else out
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if return_lse else None
-    if workspace is None:
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        need = workspace.numel() * workspace.element_size()
+    elif need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError(f"workspace must be on {device}")
-    with _OnDevice(device.index):
-        st = _abi.load().jvp_attn_decode(
-            desc, H, dt, q.data_ptr(), q_strides, k_cache.data_ptr(), v_cache.data_ptr(),
-            _data(k_scale), _data(v_scale), block_table.data_ptr(), seq_lens.data_ptr(),
-            default_scale if scale is None else float(scale), o.data_ptr(), o_strides, _data(lse),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            torch.cuda.current_stream(device.index).cuda_stream)
-    _abi.check(st)
+    _call(device.index, _abi.load().jvp_attn_decode, desc, H, dt, q.data_ptr(), q_strides,
+          k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale), _data(v_scale),
+          block_table.data_ptr(), seq_lens.data_ptr(),
+          default_scale if scale is None else float(scale), o.data_ptr(), o_strides, _data(lse),
+          _data(workspace), need)
     return (o, lse) if return_lse else o
 
 
@@ -795,7 +786,7 @@ def decode_workspace_size(k_cache: torch.Tensor, block_table: torch.Tensor, H: i
     desc = _abi.Cache(pages, page, hkv, D, block_table.shape[0], block_table.shape[1],
                       block_table.stride(0), _abi.JVP_E4M3 if e4m3 else _DT[k_cache.dtype],
                       strides, strides)
-    with _OnDevice(k_cache.device.index):
+    with torch.cuda.device(k_cache.device):
         return int(_abi.load().jvp_attn_decode_workspace_size(desc, int(H), _DT[dtype]))
 
 

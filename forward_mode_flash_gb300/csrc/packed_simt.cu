@@ -1,13 +1,15 @@
 // packed_simt.cu -- attention over packed prompts on the CUDA cores: fp32
 // arithmetic, any element type, any head dimension up to 128, any alignment.
 //
-// The same online softmax as the tensor-core kernel.  A block of 256 threads
-// takes 64 query rows of one head against 64-key tiles: Q and K are held
-// transposed in shared memory ([d][row]), so a thread forms a 4 x 4 piece of
-// S from two 16-byte reads per column of the head dimension, and after the
-// softmax a 4 x D/16 piece of O from the transposed P.  Bound by fp32 FMA
-// issue: 16 FMAs against two shared-memory reads in the first product, 4 D/16
-// against 1 + D/64 in the second.
+// The same online softmax as the tensor-core kernel.  A block of 128 threads
+// takes 32 query rows of one head against 64-key tiles in shared memory; a
+// thread forms a 4 x 4 piece of S (rows ty + 8 i, keys tx + 16 j: 16-byte reads
+// along the head dimension, K rows padded by 4 floats so that 16 lanes' rows
+// hit distinct banks) and then a 4 x D/16 piece of O.  Either product reads
+// 8 x 16 bytes of shared memory for 64 FMAs.  Bound by fp32 FMA issue.
+// float32 tiles are copied asynchronously, K's next tile during the softmax
+// and the second product, V's during the next scores; four blocks per SM (two
+// at D > 64) overlap the rest.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,8 +20,9 @@
 namespace jvp {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int BM = kPackedSimtRows, BN = 64;
+constexpr int kThreads = 128;
+constexpr int BM = kPackedSimtRows, BN = 64, TY = kThreads / 16;
+static_assert(BM == 4 * TY, "four rows per thread");
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -29,19 +32,20 @@ __device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn
 __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
 template <int DP>
-constexpr int smem_floats() {
-  return DP * BM + DP * BN + BN * DP + BN * BM;  // Q^T, K^T, V, P^T
-}
+struct Smem {
+  static constexpr int LD = DP + 4;  // Q and K rows
+  static constexpr int LP = BN + 4;  // P rows
+  static constexpr int Q = 0, K = Q + BM * LD, V = K + BN * LD, P = V + BN * DP;
+  static constexpr int FLOATS = P + BM * LP;
+};
 
-// VEC: rows are 16-byte aligned and D is a multiple of 4 (float only).
+// VEC: float rows that are 16-byte aligned, D a multiple of 4.
 template <typename T, int DP, bool VEC>
 __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParams p) {
-  constexpr int DC = DP / 16;  // output columns per thread: 4 (tx + 16 i) .. + 3
+  using L = Smem<DP>;
+  constexpr int DC = DP / 16;  // output columns per thread: 4 tx + 64 e .. + 3
   extern __shared__ __align__(16) float sm[];
-  float* sQ = sm;             // [DP][BM]
-  float* sK = sQ + DP * BM;   // [DP][BN]
-  float* sV = sK + DP * BN;   // [BN][DP]
-  float* sP = sV + BN * DP;   // [BN][BM]
+  float *sQ = sm + L::Q, *sK = sm + L::K, *sV = sm + L::V, *sP = sm + L::P;
   const int h = static_cast<int>(blockIdx.x) / p.tiles, hk = h / p.group;
   const int u = static_cast<int>(blockIdx.x) % p.tiles;
   PackedTile pt;
@@ -53,27 +57,38 @@ __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParam
   const T* k = static_cast<const T*>(p.k) + pt.r0 * p.sk.n + hk * p.sk.h;
   const T* v = static_cast<const T*>(p.v) + pt.r0 * p.sv.n + hk * p.sv.h;
 
-  // four columns from d of a row, zeros past D and for rows that do not exist
-  auto load4 = [&](const T* base, long long stride, int row, bool on, int d) {
-    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!on || d >= p.D) return f;
-    const T* src = base + row * stride + d;
-    if constexpr (VEC) {
-      f = __ldg(reinterpret_cast<const float4*>(src));
-    } else {
-      float* e = &f.x;
+  // rows [row0, row0 + ROWS) of a tensor into shared memory (leading dimension
+  // ld): zeros past D and for rows that do not exist
+  auto load_rows = [&](float* dst, int ld, int rows, const T* base, long long stride, int row0) {
+    for (int e = tid; e < rows * (DP / 4); e += kThreads) {
+      const int row = e / (DP / 4), d = 4 * (e % (DP / 4));
+      const bool on = row0 + row < len && d < p.D;
+      const T* src = base + (on ? (row0 + row) * stride + d : 0);
+      float* to = dst + row * ld + d;
+      if constexpr (VEC) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                     "l"(src), "r"(on ? 16 : 0)
+                     : "memory");
+      } else {
+        float f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (d + i < p.D) e[i] = to_f(src[i]);
+        for (int i = 0; i < 4; ++i) f[i] = (on && d + i < p.D) ? to_f(src[i]) : 0.f;
+        *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+      }
     }
-    return f;
+    if (VEC) asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  for (int e = tid; e < BM * (DP / 4); e += kThreads) {
-    const int row = e % BM, d = 4 * (e / BM);
-    const float4 f = load4(q, p.sq.n, q0 + row, q0 + row < len, d);
-    sQ[d * BM + row] = f.x, sQ[(d + 1) * BM + row] = f.y;
-    sQ[(d + 2) * BM + row] = f.z, sQ[(d + 3) * BM + row] = f.w;
-  }
+  // all but the latest group of copies have landed / all have
+  auto wait_but_latest = [&]() {
+    if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  };
+  auto wait_all = [&]() {
+    if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  };
+  load_rows(sQ, L::LD, BM, q, p.sq.n, q0);
+  load_rows(sK, L::LD, BN, k, p.sk.n, 0);
+  load_rows(sV, DP, BN, v, p.sv.n, 0);
   float m[4], l[4], acc[4][DC];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -82,42 +97,39 @@ __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParam
     for (int e = 0; e < DC; ++e) acc[i][e] = 0.f;
   }
   for (int j0 = 0; j0 < keys; j0 += BN) {
-    __syncthreads();  // the previous tile is no longer read
-    for (int e = tid; e < BN * (DP / 4); e += kThreads) {
-      const int row = e % BN, d = 4 * (e / BN);
-      const float4 f = load4(k, p.sk.n, j0 + row, j0 + row < len, d);
-      sK[d * BN + row] = f.x, sK[(d + 1) * BN + row] = f.y;
-      sK[(d + 2) * BN + row] = f.z, sK[(d + 3) * BN + row] = f.w;
-    }
-    for (int e = tid; e < BN * (DP / 4); e += kThreads) {
-      const int d = 4 * (e % (DP / 4)), row = e / (DP / 4);
-      *reinterpret_cast<float4*>(sV + row * DP + d) =
-          load4(v, p.sv.n, j0 + row, j0 + row < len, d);
-    }
+    wait_but_latest();  // K (and Q); V may be on its way
     __syncthreads();
     float s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 8
-    for (int d = 0; d < DP; ++d) {
-      const float4 a = *reinterpret_cast<const float4*>(sQ + d * BM + 4 * ty);
-      const float4 b = *reinterpret_cast<const float4*>(sK + d * BN + 4 * tx);
-      const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = *reinterpret_cast<const float4*>(sQ + (ty + TY * i) * L::LD + d);
+        b[i] = *reinterpret_cast<const float4*>(sK + (tx + 16 * i) * L::LD + d);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+          s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+          s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+          s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = q0 + 4 * ty + i;
+      const int row = q0 + ty + TY * i;
       const int limit = p.causal ? min(row + 1, len) : len;
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = (j0 + 4 * tx + j < limit) ? s[i][j] * p.scale_log2 : -INFINITY;
+        s[i][j] = (j0 + tx + 16 * j < limit) ? s[i][j] * p.scale_log2 : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
@@ -131,36 +143,43 @@ __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParam
       for (int j = 0; j < 4; ++j) {
         s[i][j] = exp2f(s[i][j] - mu);
         sum += s[i][j];
+        sP[(ty + TY * i) * L::LP + tx + 16 * j] = s[i][j];
       }
-      l[i] = l[i] * a + sum;  // this thread's columns
+      l[i] = l[i] * a + sum;  // this thread's keys
 #pragma unroll
       for (int e = 0; e < DC; ++e) acc[i][e] *= a;
     }
+    wait_all();       // V
+    __syncthreads();  // P is written, V has landed, K has been read
+    const bool more = j0 + BN < keys;
+    if (more) load_rows(sK, L::LD, BN, k, p.sk.n, j0 + BN);
+#pragma unroll 2
+    for (int j = 0; j < BN; j += 4) {
+      float4 a[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(sP + (4 * tx + j) * BM + 4 * ty) =
-          make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-    __syncthreads();
-#pragma unroll 4
-    for (int j = 0; j < BN; ++j) {
-      const float4 a = *reinterpret_cast<const float4*>(sP + j * BM + 4 * ty);
-      const float av[4] = {a.x, a.y, a.z, a.w};
+      for (int i = 0; i < 4; ++i)
+        a[i] = *reinterpret_cast<const float4*>(sP + (ty + TY * i) * L::LP + j);
 #pragma unroll
-      for (int e = 0; e < DC; e += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(sV + j * DP + 4 * tx + 16 * e);
+      for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i][e] = fmaf(av[i], b.x, acc[i][e]);
-          acc[i][e + 1] = fmaf(av[i], b.y, acc[i][e + 1]);
-          acc[i][e + 2] = fmaf(av[i], b.z, acc[i][e + 2]);
-          acc[i][e + 3] = fmaf(av[i], b.w, acc[i][e + 3]);
+        for (int e = 0; e < DC; e += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(sV + (j + jj) * DP + 4 * tx + 16 * e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = jj == 0 ? a[i].x : jj == 1 ? a[i].y : jj == 2 ? a[i].z : a[i].w;
+            acc[i][e] = fmaf(w, b.x, acc[i][e]);
+            acc[i][e + 1] = fmaf(w, b.y, acc[i][e + 1]);
+            acc[i][e + 2] = fmaf(w, b.z, acc[i][e + 2]);
+            acc[i][e + 3] = fmaf(w, b.w, acc[i][e + 3]);
+          }
         }
-      }
     }
+    __syncthreads();  // V and P have been read
+    if (more) load_rows(sV, DP, BN, v, p.sv.n, j0 + BN);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = q0 + 4 * ty + i;
+    const int row = q0 + ty + TY * i;
     float sum = l[i];
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -180,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParam
 
 template <typename T, int DP, bool VEC>
 cudaError_t launch_variant(const PackedParams& p, cudaStream_t stream) {
-  constexpr int bytes = smem_floats<DP>() * 4;
+  constexpr int bytes = Smem<DP>::FLOATS * 4;
   auto kern = packed_simt_kernel<T, DP, VEC>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;

@@ -3,13 +3,20 @@
 
 namespace jvp {
 
+template <typename T>
+static cudaError_t launch_typed(int kernel_d, const PackedMaps& maps, const PackedParams& p,
+                                cudaStream_t stream) {
+  if (kernel_d == 64)
+    return p.query_tiles == 1 ? launch_packed_tc_variant<T, 64, 1>(maps, p, stream)
+                              : launch_packed_tc_variant<T, 64, 2>(maps, p, stream);
+  return p.query_tiles == 1 ? launch_packed_tc_variant<T, 128, 1>(maps, p, stream)
+                            : launch_packed_tc_variant<T, 128, 2>(maps, p, stream);
+}
+
 cudaError_t launch_packed_tc(DType dt, int kernel_d, const PackedMaps& maps, const PackedParams& p,
                              cudaStream_t stream) {
-  if (dt == kF16)
-    return kernel_d == 64 ? launch_packed_tc_variant<__half, 64>(maps, p, stream)
-                          : launch_packed_tc_variant<__half, 128>(maps, p, stream);
-  return kernel_d == 64 ? launch_packed_tc_variant<__nv_bfloat16, 64>(maps, p, stream)
-                        : launch_packed_tc_variant<__nv_bfloat16, 128>(maps, p, stream);
+  return dt == kF16 ? launch_typed<__half>(kernel_d, maps, p, stream)
+                    : launch_typed<__nv_bfloat16>(kernel_d, maps, p, stream);
 }
 
 }  // namespace jvp

@@ -20,9 +20,8 @@
 //
 // The scores of a step (query tile, key tile) are formed in a buffer in TMEM,
 // the softmax writes the weights P~ over their first half as 16-bit values, and
-// the second product O += P~ V reads them from there as its A operand.  P~ is
-// published in two halves, so that the product starts while the second half's
-// exponentials are formed.  Behind the product, in the same warp and therefore
+// the second product O += P~ V reads them from there as its A operand.  Behind
+// the product, in the same warp and therefore
 // in order, go the next scores into that buffer: at D = 128 (two buffers; they
 // and both O fill the 512 columns) the same tile's, at D = 64 (three) those of
 // three steps on in the order A(0), B(0), A(1), B(1), ..., so that a softmax
@@ -77,44 +76,52 @@ struct PackedElem<__nv_bfloat16> {
   }
 };
 
-template <int D>
+template <int D, int NQ>
 struct PackedLayout {
   static constexpr int BM = kPackedTileRows, BN = kPackedBlockN;
   static constexpr int KCH = D / 64;             // 128-byte chunks along D
-  static constexpr int NS = D == 128 ? 2 : 4;    // stages of each ring
+  // stages of each ring
+  static constexpr int NS = NQ == 2 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);
   static constexpr int Q_BYTES = KCH * BM * 128; // one query tile
   static constexpr int KV_BYTES = KCH * BN * 128;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_K = OFF_Q + NQ * Q_BYTES;
   static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
   static constexpr int OFF_CTRL = OFF_V + NS * KV_BYTES;
   static constexpr int SMEM_BYTES = OFF_CTRL + 1024 + 1024;  // control block, alignment
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(SMEM_BYTES > 114 * 1024, "one CTA per SM: it owns all TMEM columns");
-  static constexpr int NB = D == 128 ? 2 : 3;    // score buffers
+  static_assert((3 - NQ) * (SMEM_BYTES + 1024) <= 228 * 1024 &&
+                    (4 - NQ) * (SMEM_BYTES + 1024) > 228 * 1024,
+                "3 - NQ CTAs per SM, which share the TMEM columns");
+  static constexpr int NB = NQ == 1 ? 1 : D == 128 ? 2 : 3;  // score buffers
   static constexpr uint32_t TM_S = 0;            // S / P~ of buffer b at b * BN
   static constexpr uint32_t TM_O = NB * BN;      // O of tile x at TM_O + x * D
-  static constexpr uint32_t TM_COLS = 512;
-  static_assert(NB * BN + 2 * D <= TM_COLS, "TMEM columns");
+  static constexpr uint32_t TM_COLS = NQ * 256;
+  static_assert(NB * BN + NQ * D <= TM_COLS, "TMEM columns");
 };
 
-// Three warpgroups: producer and MMA warps (two more only fill the group),
-// softmax of tile A, softmax of tile B.  A softmax thread holds a whole row of
-// scores, so its group takes registers from the first (168 * 3 = 72 + 2 * 216).
-constexpr int kPackedThreads = 384;
+// One warpgroup for the copies and the MMAs and one for the softmax of each
+// query tile.  A softmax thread holds a whole row of scores, so its group
+// takes registers from the first (of 384 threads: 168 * 3 = 72 + 2 * 216; of
+// 256: 128 * 2 = 48 + 208).
+constexpr int packed_threads(int NQ) { return 128 + 128 * NQ; }
 
-template <int NS, int NB>
+template <int NS>
 struct PackedCtrl {
   uint64_t q_full[2];
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
   uint64_t v_tail;      // the last V tile's rows behind the sequence are zero
-  uint64_t s_full[NB];  // scores of the step in the buffer are final
-  uint64_t p_half[NB];  // its P~ of the first 64 keys is stored
-  uint64_t p_full[NB];  // P~ of the others is
-  uint64_t o_done[2];   // O of a query tile has its next key tile's product (NB = 3)
-  uint64_t o_full[2];   // O has the last key tile's product
+  // By query tile and, with three buffers, by key tile modulo 3.  (A parity
+  // cannot tell a phase from the one two before or behind it, so a waiter must
+  // know the phase before to be over and the one behind not to be.  With three
+  // buffers the two issuing warps drive each other, and a tile's scores and
+  // weights can be up to three key tiles ahead of its own products.)
+  uint64_t s_full[2][3];  // scores against the next key tile are final
+  uint64_t p_full[2][3];  // its P~ is stored
+  uint64_t o_done[2][3];  // O has its product (NB = 3)
+  uint64_t o_full[2];     // O has the last key tile's product
   uint64_t staged[2];   // the tile's output rows are in shared memory
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -145,10 +152,10 @@ __device__ __forceinline__ float packed_max(const float (&x)[N]) {
   return fmaxf(fmax3(y[0], y[1], y[2]), y[3]);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kPackedThreads, 1)
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
     packed_tc_kernel(const __grid_constant__ PackedMaps maps, const PackedParams p) {
-  using L = PackedLayout<D>;
+  using L = PackedLayout<D, NQ>;
   constexpr int BM = L::BM, BN = L::BN, NS = L::NS, NB = L::NB, KCH = L::KCH;
   constexpr bool kBF16 = PackedElem<T>::kBF16;
   constexpr uint32_t IDESC_S = idesc_f16(kBF16, BM, BN, false);
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  using Ctrl = PackedCtrl<NS, NB>;
+  using Ctrl = PackedCtrl<NS>;
   static_assert(sizeof(Ctrl) <= 1024, "control block budget");
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + L::OFF_CTRL);
   volatile int* abort = &ctrl->abort;
@@ -171,23 +178,22 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     tma_prefetch_desc(&maps.o);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctrl->q_full[x], 1);
-      mbar_init(&ctrl->o_done[x], 1);
+      for (int i = 0; i < 3; ++i) {
+        mbar_init(&ctrl->s_full[x][i], 1);
+        mbar_init(&ctrl->p_full[x][i], 4);  // one arrival per softmax warp of the tile
+        mbar_init(&ctrl->o_done[x][i], 1);
+      }
       mbar_init(&ctrl->o_full[x], 1);
-      mbar_init(&ctrl->staged[x], 4);  // one arrival per softmax warp of the tile
-    }
-    for (int b = 0; b < NB; ++b) {
-      mbar_init(&ctrl->s_full[b], 1);
-      mbar_init(&ctrl->p_half[b], 4);
-      mbar_init(&ctrl->p_full[b], 4);
+      mbar_init(&ctrl->drain[x], 1);
+      mbar_init(&ctrl->staged[x], 4);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&ctrl->k_full[s], 1);
-      mbar_init(&ctrl->k_empty[s], 1);
+      mbar_init(&ctrl->k_empty[s], NB == 3 ? 2 : 1);  // one arrival per issuing warp
       mbar_init(&ctrl->v_full[s], 1);
-      mbar_init(&ctrl->v_empty[s], 1);
+      mbar_init(&ctrl->v_empty[s], NB == 3 ? 2 : 1);
     }
     mbar_init(&ctrl->v_tail, 1);
-    mbar_init(&ctrl->drain, 1);
     ctrl->abort = 0;
     fence_barrier_init();
   }
@@ -201,33 +207,31 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   const int hk = hg * p.head_group + in_group % heads;
   const int u = in_group / heads;
   PackedTile pt;
-  const bool have = find_packed_tile(p.cu, p.B, p.T, 2 * p.tok, u, p.causal != 0, p.status, &pt);
+  const bool have = find_packed_tile(p.cu, p.B, p.T, NQ * p.tok, u, p.causal != 0, p.status, &pt);
   if (!have) return;  // (the list is shorter than its bound; the same for every warp)
   if (warp == 1) {
     tmem_alloc(&ctrl->tmem_base, L::TM_COLS);
     tmem_relinquish();
   }
   const int len = pt.len, r0 = pt.r0;
-  const int tok0 = pt.tile * 2 * p.tok;  // first token of tile A; B follows
+  const int tok0 = pt.tile * NQ * p.tok;  // first token of tile A; B follows
   // key tiles of a query tile whose first token is a
   auto key_tiles = [&](int a) {
     if (a >= len) return 0;
     const int keys = p.causal ? min(a + p.tok, len) : len;
     return (keys + BN - 1) / BN;
   };
-  const int n_a = key_tiles(tok0), n_b = key_tiles(tok0 + p.tok);
+  const int n_a = key_tiles(tok0), n_b = NQ == 2 ? key_tiles(tok0 + p.tok) : 0;
   const int n = max(n_a, n_b), both = min(n_a, n_b);
   const int tail = len - (n - 1) * BN;  // keys of the last tile (>= BN: all of its rows)
-  // score buffer of query tile x against key tile t, and its use
-  auto buffer_of = [&](int x, int t, uint32_t* use) {
-    if (NB == 2) {
-      *use = t;
-      return x;
-    }
-    const int step = t < both ? 2 * t + x : both + t;
-    *use = step / NB;
-    return step % NB;
+  // score buffer of query tile x against key tile t: steps go A(0), B(0), A(1),
+  // ... round the three buffers; of two, each tile has its own
+  auto buffer_of = [&](int x, int t) {
+    return NB <= 2 ? x : (t < both ? 2 * t + x : both + t) % NB;
   };
+  // which of a tile's barriers is key tile t's, and its phase
+  auto bar_of = [&](int t) { return NB == 3 ? t % 3 : 0; };
+  auto phase_of = [&](int t) { return NB == 3 ? t / 3 : t; };
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -237,7 +241,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       bool ok = true;
@@ -266,8 +271,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         ok = load_kv(0, false);
         if (n_b > 0) load_q(1);
         for (int t = 0; ok && t < n; ++t) {
-          if (t + 1 < n) ok = load_kv(t + 1, false);  // (needed before V(t))
-          if (ok) ok = load_kv(t, true);
+          ok = load_kv(t, true);
+          if (ok && t + 1 < n) ok = load_kv(t + 1, false);
         }
         if (!ok) {
           packed_timeout(p.status, abort);
@@ -297,24 +302,25 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           if (lane == 0) mbar_arrive(&ctrl->v_tail);
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || (NB == 3 && warp == 2)) {
       // ---------------------------------------------------------- MMAs
       // The whole warp walks the steps; one elected lane issues.  (Descriptor
       // addresses are in units of 16 bytes.)
+      const int w = warp - 1;
       const uint32_t neg_a = p.neg_scores ? (1u << 13) : 0u;
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::OFF_V), BN * 128, 1024);
       // The pace of this warp is the kernel's: between two products there is
       // little but their waits, and the buffers of the main loops are constants.
-      auto scores = [&](int x, int t, int buf) {
+      auto scores = [&](int x, int t, int buf, int bar) {
         const uint64_t qd = q_desc + x * (L::Q_BYTES >> 4);
         const uint64_t kd = k_desc + (t % NS) * (L::KV_BYTES >> 4);
 #pragma unroll
         for (int c = 0; c < KCH; ++c)
           mma_ss_x4_warp<2, 2>(tmem + L::TM_S + buf * BN, qd + c * (BM * 128 / 16),
                                kd + c * (BN * 128 / 16), IDESC_S | neg_a, c > 0 ? 1u : 0u);
-        mma_commit_warp(&ctrl->s_full[buf]);
+        mma_commit_warp(&ctrl->s_full[x][bar]);
       };
       auto k_landed = [&](int t) {
         const bool got = wait(&ctrl->k_full[t % NS], t / NS);
@@ -325,46 +331,43 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         return (t == n - 1 && tail < BN) ? wait(&ctrl->v_tail, 0)
                                          : wait(&ctrl->v_full[t % NS], t / NS);
       };
-      // O of query tile x: the product with the weights in buffer buf (its
-      // use-th), half a key tile as soon as its weights are there
-      auto values = [&](int x, int t, int buf, uint32_t use) {
+      // O of query tile x: the product with the weights in buffer buf.  (The
+      // tensor core runs one warp's products in order: scores issued behind it
+      // may overwrite the weights.)
+      auto values = [&](int x, int t, int buf, int bar, int phase) {
         const uint64_t vd = v_desc + (t % NS) * (L::KV_BYTES >> 4);
         const uint32_t p_tm = tmem + L::TM_S + buf * BN, o_tm = tmem + L::TM_O + x * D;
-        if (!wait(&ctrl->p_half[buf], use)) return false;
+        if (!wait(&ctrl->p_full[x][bar], phase)) return false;
         tc_fence_after();
         mma_ts_x4_warp<8, 128>(o_tm, p_tm, vd, IDESC_O, t > 0 ? 1u : 0u);
-        if (!wait(&ctrl->p_full[buf], use)) return false;
-        tc_fence_after();
         mma_ts_x4_warp<8, 128>(o_tm, p_tm + 32, vd + 4 * 128, IDESC_O, 1u);
         return true;
       };
       bool ok = wait(&ctrl->q_full[0], 0) && k_landed(0);
-      if (ok) {
-        scores(0, 0, 0);
-        if (n_b > 0) {
-          ok = wait(&ctrl->q_full[1], 0);
-          tc_fence_after();
-          if (ok) scores(1, 0, 1);
-        }
-        mma_commit_warp(&ctrl->k_empty[0]);
+      if (ok && w == 0) scores(0, 0, 0, 0);
+      if (ok && n_b > 0) {
+        ok = wait(&ctrl->q_full[1], 0);
+        tc_fence_after();
+        if (ok && w == 0) scores(1, 0, 1, 0);
       }
-      if constexpr (NB == 2) {
+      if (ok) mma_commit_warp(&ctrl->k_empty[0]);
+      if constexpr (NB <= 2) {
         for (int t = 0; ok && t < n; ++t) {
           const bool b_last = t < n_b;        // B is the last user of V(t) ...
           const bool b_last_k = t + 1 < n_b;  // ... and of K(t + 1)
           bool v_here = false, k_here = false;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < NQ; ++x) {
             const int nx = x ? n_b : n_a;
             if (!ok || t >= nx) continue;
             if (!v_here) ok = v_landed(t);
             v_here = true;
-            if (!ok || !(ok = values(x, t, x, t))) continue;
+            if (!ok || !(ok = values(x, t, x, 0, t))) continue;
             if (b_last ? x == 1 : x == 0) mma_commit_warp(&ctrl->v_empty[t % NS]);
             if (t + 1 < nx) {
               if (!k_here && !(ok = k_landed(t + 1))) continue;
               k_here = true;
-              scores(x, t + 1, x);
+              scores(x, t + 1, x, 0);
               if (b_last_k ? x == 1 : x == 0) mma_commit_warp(&ctrl->k_empty[(t + 1) % NS]);
             } else {
               mma_commit_warp(&ctrl->o_full[x]);
@@ -372,63 +375,80 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           }
         }
       } else {
-        // While both tiles have keys: step i's product, then step i + 3's scores.
-        if (ok && both > 1) {
-          ok = k_landed(1);
-          if (ok) scores(0, 1, 2);
-        }
-        auto step = [&](int x, int t, int buf, uint32_t use) {
-          if (x == 0 && !(ok = v_landed(t))) return;
-          if (!(ok = values(x, t, buf, use))) return;
-          mma_commit_warp(&ctrl->o_done[x]);
-          if (t + 1 == (x ? n_b : n_a)) mma_commit_warp(&ctrl->o_full[x]);
-          if (x == 1) mma_commit_warp(&ctrl->v_empty[t % NS]);
-          if (x == 0 && t + 1 < both) {
-            scores(1, t + 1, buf);
-            mma_commit_warp(&ctrl->k_empty[(t + 1) % NS]);
+        // Two issuing warps, each releasing every K and V tile once.  While
+        // both query tiles have keys, warp w has tile w's products; behind
+        // step i's come the scores of step i + 3 (the other tile's) into the
+        // same buffer: tile A's product is followed by B's scores one key tile
+        // on, B's by A's two key tiles on.
+        if (ok && both > 1) {  // A's scores against key tile 1: the third buffer
+          if (w == 0) {
+            ok = k_landed(1);
+            if (ok) scores(0, 1, 2, 1);
+          } else {
+            mma_commit_warp(&ctrl->k_empty[1]);
           }
-          if (x == 1 && t + 2 < both) {
-            if (!(ok = k_landed(t + 2))) return;
-            scores(0, t + 2, buf);
+        }
+        auto step = [&](int x, int t, int buf, int bar, int phase) {
+          if (!(ok = v_landed(t) && values(x, t, buf, bar, phase))) return;
+          mma_commit_warp(&ctrl->o_done[x][bar]);
+          if (t + 1 == (x ? n_b : n_a)) mma_commit_warp(&ctrl->o_full[x]);
+          mma_commit_warp(&ctrl->v_empty[t % NS]);
+          const int ts = t + 1 + x;
+          if (ts < both) {
+            if (!(ok = k_landed(ts))) return;
+            scores(1 - x, ts, buf, (bar + 1 + x) % 3);
+            mma_commit_warp(&ctrl->k_empty[ts % NS]);
           }
         };
-        for (int t = 0; ok && t < both; t += 3) {
-          const uint32_t use = 2 * (t / 3);
-          step(0, t, 0, use);
-          if (ok) step(1, t, 1, use);
-          if (ok && t + 1 < both) step(0, t + 1, 2, use);
-          if (ok && t + 1 < both) step(1, t + 1, 0, use + 1);
-          if (ok && t + 2 < both) step(0, t + 2, 1, use + 1);
-          if (ok && t + 2 < both) step(1, t + 2, 2, use + 1);
+        for (int t = 0; ok && t < both; t += 3) {  // three key tiles are six steps
+          const int ph = t / 3;
+          if (w == 0) {
+            step(0, t, 0, 0, ph);
+            if (ok && t + 1 < both) step(0, t + 1, 2, 1, ph);
+            if (ok && t + 2 < both) step(0, t + 2, 1, 2, ph);
+          } else {
+            step(1, t, 1, 0, ph);
+            if (ok && t + 1 < both) step(1, t + 1, 0, 1, ph);
+            if (ok && t + 2 < both) step(1, t + 2, 2, 2, ph);
+          }
         }
-        // Then one tile alone, its scores up to two key tiles ahead of its
-        // products (no more: the softmax relies on it, see its wait on o_done).
+        // Then one tile alone, issued by its own warp, its scores two key tiles
+        // ahead of its products.  (B goes on alone for at most one key tile, as
+        // its tokens end at most 128 behind A's: that step's buffer is the one
+        // that B's own product against tile both - 2 has released.)
         const int x = n_a > n_b ? 0 : 1;
+        auto release = [&](uint64_t* bar) {  // for both warps
+          mma_commit_warp(bar);
+          mma_commit_warp(bar);
+        };
         auto solo_scores = [&](int t) {
           if (t >= n || (t == 0 && both == 0)) return true;
           if (!k_landed(t)) return false;
-          scores(x, t, (both + t) % NB);
-          mma_commit_warp(&ctrl->k_empty[t % NS]);
+          scores(x, t, (both + t) % NB, bar_of(t));
+          release(&ctrl->k_empty[t % NS]);
           return true;
         };
-        if (ok && both < n) ok = solo_scores(both) && solo_scores(both + 1);
-        for (int t = both; ok && t < n; ++t) {
-          if (!(ok = v_landed(t) && values(x, t, (both + t) % NB, (both + t) / NB))) break;
-          mma_commit_warp(&ctrl->o_done[x]);
-          if (t + 1 == n) mma_commit_warp(&ctrl->o_full[x]);
-          mma_commit_warp(&ctrl->v_empty[t % NS]);
-          ok = solo_scores(t + 2);
+        if (w == x) {
+          if (ok && both < n) ok = solo_scores(both) && solo_scores(both + 1);
+          for (int t = both; ok && t < n; ++t) {
+            if (!(ok = v_landed(t) && values(x, t, (both + t) % NB, bar_of(t), phase_of(t)))) break;
+            mma_commit_warp(&ctrl->o_done[x][bar_of(t)]);
+            if (t + 1 == n) mma_commit_warp(&ctrl->o_full[x]);
+            release(&ctrl->v_empty[t % NS]);
+            ok = solo_scores(t + 2);
+          }
         }
       }
       if (!ok) packed_timeout(p.status, abort);
       // every MMA issued completes before TMEM is freed
-      mma_commit_warp(&ctrl->drain);
+      mma_commit_warp(&ctrl->drain[w]);
       const int zero = 0;
-      mbar_wait(&ctrl->drain, 0, &zero);
+      mbar_wait(&ctrl->drain[w], 0, &zero);
     }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int x = (warp - 4) >> 2;  // query tile
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..
     const int r = sub * 32 + lane;
@@ -449,10 +469,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int t = 0; t < nx; ++t) {
-      uint32_t use;
-      const int buf = buffer_of(x, t, &use);
-      const uint32_t s_tm = lane_base + L::TM_S + buf * BN;
-      if (!(ok = wait(&ctrl->s_full[buf], use))) break;
+      const uint32_t s_tm = lane_base + L::TM_S + buffer_of(x, t) * BN;
+      if (!(ok = wait(&ctrl->s_full[x][bar_of(t)], phase_of(t)))) break;
       tc_fence_after();
       float s[BN];
 #pragma unroll
@@ -479,12 +497,14 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         l_run *= alpha;
         m_run = m_new;
         if (t > 0) {
-          // O has tile t - 1's product: with two buffers because these scores
-          // were issued behind it, with three by the barrier.  (Of that phase
-          // the barrier can be at most one behind, so the parity tells: these
-          // scores were issued behind tile t - 2's product.)
-          if (NB > 2) {
-            if (!(ok = wait(&ctrl->o_done[x], t - 1))) break;
+          // O has tile t - 1's product: with up to two buffers because these
+          // scores were issued behind it, with three by the barrier.  (Its
+          // phase before, tile t - 4's product, is over: these scores were
+          // issued behind the other tile's product of t - 2 or t - 1, whose
+          // weights come from scores that were committed behind this tile's
+          // product of t - 3; alone, behind its own of t - 2.)
+          if (NB == 3) {
+            if (!(ok = wait(&ctrl->o_done[x][bar_of(t - 1)], phase_of(t - 1)))) break;
             tc_fence_after();
           }
 #pragma unroll 1
@@ -512,19 +532,13 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           pk[e >> 1] = PackedElem<T>::pack(w.x, w.y);
         }
         tmem_st16(s_tm + q / 2, pk);
-        if (q == BN / 2 - 32) {  // the second product starts on the first half
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->p_half[buf]);
-        }
       }
       l_run += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
                ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->p_full[buf]);
+      if (lane == 0) mbar_arrive(&ctrl->p_full[x][bar_of(t)]);
     }
     // ------------------------------------------------------------ epilogue
     if (nx > 0 && ok && (ok = wait(&ctrl->o_full[x], 0))) {
@@ -580,22 +594,22 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int NQ>
 cudaError_t launch_packed_tc_variant(const PackedMaps& maps, const PackedParams& p,
                                      cudaStream_t stream) {
-  auto kern = packed_tc_kernel<T, D>;
+  auto kern = packed_tc_kernel<T, D, NQ>;
+  constexpr int smem = PackedLayout<D, NQ>::SMEM_BYTES;
   static std::atomic<unsigned long long> attr_done{0};  // per device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(attr_done.load(std::memory_order_relaxed) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PackedLayout<D>::SMEM_BYTES);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   const long long grid = static_cast<long long>(p.tiles) * p.Hkv;
-  kern<<<static_cast<unsigned>(grid), kPackedThreads, PackedLayout<D>::SMEM_BYTES, stream>>>(maps, p);
+  kern<<<static_cast<unsigned>(grid), packed_threads(NQ), smem, stream>>>(maps, p);
   return cudaGetLastError();
 }
 

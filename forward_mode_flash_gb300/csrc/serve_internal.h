@@ -96,6 +96,7 @@ struct PackedParams {
   int causal;
   int tok;             // query tokens of one 128-row tile (tensor cores): 128 / group
   int tiles;           // upper bound of the blocks a key/value head needs
+  int query_tiles;     // tensor cores: query tiles of a CTA (1 or 2)
   int head_group;      // tensor cores: key/value heads scheduled together
   float scale, scale_log2;
   int neg_scores;      // scale < 0: the score products are formed negated, |scale| applied
@@ -118,7 +119,7 @@ constexpr int kPackedTileRows = 128;  // rows of a query tile; a CTA has two
 constexpr int kPackedBlockN = 128;    // keys per tile
 // CUDA-core kernel (any type, any D up to 128).
 cudaError_t launch_packed_simt(DType dt, const PackedParams& p, cudaStream_t stream);
-constexpr int kPackedSimtRows = 64;
+constexpr int kPackedSimtRows = 32;
 
 // What the entry points of the other translation unit share with jvp_attn_api.cu.
 jvp_status_t api_fail(jvp_status_t s, const char* msg);
