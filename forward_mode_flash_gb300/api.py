@@ -541,19 +541,17 @@ def _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale):
                       _abi.Strides(sk[0], sk[1], sk[2], 1), _abi.Strides(sv[0], sv[1], sv[2], 1))
 
 
-# Handle of the current stream of a device, without the Stream object that
-# torch.cuda.current_stream makes (1 us of a 10 us call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _call(index, entry, *args):
     """Calls an entry point with a device current and its current stream as the
     last argument, and raises on an error status."""
+    # the stream's handle without the object that torch.cuda.current_stream
+    # makes (1 us of a 10 us call)
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
-        st = entry(*args, _raw_stream(index))
+        st = entry(*args, stream)
     else:
         with torch.cuda.device(index):
-            st = entry(*args, _raw_stream(index))
+            st = entry(*args, stream)
     if st != _abi.JVP_OK:
         _abi.check(st)
 

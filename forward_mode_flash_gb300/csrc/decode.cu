@@ -48,8 +48,8 @@
 // queries of any magnitude keep their 8 bits.
 //
 // Rounding: the weights are rounded to 16 bits for the matrix product (fp16
-// ones with their largest at 2^14, to keep small weights out of the
-// subnormals).  With a 16-bit cache the row sum adds the same rounded weights,
+// ones scaled by 2^6, to keep small weights out of the subnormals and the
+// largest, 2^8 past a stale maximum, in range).  With a 16-bit cache the row sum adds the same rounded weights,
 // so the output is the exact average under slightly perturbed weights; the
 // log-sum-exp uses the unrounded sum.
 #include <cmath>
@@ -165,148 +165,96 @@ __device__ __forceinline__ long long block_exclusive(long long x, long long* tot
   return base + incl - x;
 }
 
-// The warps' states of one piece, in shared memory; their accumulators are
-// behind it, one row of DPAD + 1 floats per warp and head (bank spread).
-template <int HPB, int DPAD>
-struct Shared {
+struct SplitShared {
   long long scan[kWarps];
   Place place;
-  float m[kWarps][HPB], mw[kWarps][HPB], l[kWarps][HPB], lx[kWarps][HPB];
-  // factor of each warp's accumulator in the merged output; lse of the piece
-  float f[kWarps][HPB], lse[HPB];
-  float qs[HPB];  // e4m3: logit factor of a head (scale * log2(e) * 2^eq)
-  static constexpr int kAccBytes = kWarps * HPB * (DPAD + 1) * 4;
-};
-template <int HPB, int DPAD>
-constexpr int shared_bytes() {
-  return (static_cast<int>(sizeof(Shared<HPB, DPAD>)) + 127) & ~127;
-}
-
-struct Segment {
-  int b, hk, hb;      // sequence, key/value head, block of its query heads
-  int tiles, len;
 };
 
-// Walks this CTA's range of the list: calls piece(segment, tile0, tile1, slot)
-// for each segment it touches; slot -1: the whole segment is here.
-template <int TILE, typename Sh, typename F>
-__device__ __forceinline__ void walk(const DecodeParams& p, Sh* sh, F&& piece) {
-  const PagedCache& c = p.c;
-  const long long HH = static_cast<long long>(c.Hkv) * p.head_blocks;
-  bool bad = false;
-  if (p.direct) {  // one segment per CTA
-    Segment s;
-    s.b = static_cast<int>(blockIdx.x / HH);
-    const int seg = static_cast<int>(blockIdx.x % HH);
-    s.hk = seg / p.head_blocks, s.hb = seg % p.head_blocks;
-    s.len = clamp_len(c, __ldg(p.lens + s.b), &bad);
-    if (bad && seg == 0 && threadIdx.x == 0) atomicOr(c.status, kStatusIndex);
-    s.tiles = tiles_of(s.len, TILE);
-    piece(s, 0, s.tiles, -1);
-    return;
-  }
-  const int per = (c.B + kThreads - 1) / kThreads;  // sequences per thread
-  const int b_lo = min(c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(c.B, b_lo + per);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), TILE);
-  long long seq_total;
-  const long long before = block_exclusive<kThreads>(mine, &seq_total, sh->scan);
-  const long long W = seq_total * HH;
-  const long long G = min(static_cast<long long>(p.grid), W);
-  if (static_cast<long long>(blockIdx.x) >= G) return;
-  const long long lo = W * blockIdx.x / G, hi = W * (blockIdx.x + 1) / G;
-  // the thread whose run of sequences holds tile lo finds the sequence
-  if (lo >= before * HH && lo < (before + mine) * HH) {
-    long long at = before;
-    int b = b_lo;
-    for (; b < b_hi; ++b) {
-      const int t = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), TILE);
-      if (lo < (at + t) * HH) break;
-      at += t;
+// A CTA's part of one segment: keys of tiles [t0, t1) of sequence b for
+// key/value head hk and block hb of its query heads.  slot: where its partial
+// output goes (-1: it is the whole segment).
+struct Piece {
+  int b, hk, hb, len, t0, t1, slot;
+};
+
+// This CTA's range of the list, segment by segment.
+template <int TILE>
+struct Walker {
+  long long at, hi, seq_first, HH;
+  int b, len, nt;
+
+  // False: nothing to do here.  Executed by the whole block.
+  __device__ __forceinline__ bool start(const DecodeParams& p, SplitShared* sh) {
+    const PagedCache& c = p.c;
+    HH = static_cast<long long>(c.Hkv) * p.head_blocks;
+    bool bad = false;
+    if (p.direct) {  // one segment per CTA, with or without keys
+      at = blockIdx.x, hi = at + 1, seq_first = 0;
+      b = static_cast<int>(at / HH);
+      len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
+      if (bad && at % HH == 0 && threadIdx.x == 0) atomicOr(c.status, kStatusIndex);
+      return true;
     }
-    sh->place.b = b;
-    sh->place.before = at;
+    const int per = (c.B + kThreads - 1) / kThreads;  // sequences per thread
+    const int b_lo = min(c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(c.B, b_lo + per);
+    long long mine = 0;
+    for (int i = b_lo; i < b_hi; ++i) mine += tiles_of(clamp_len(c, __ldg(p.lens + i), &bad), TILE);
+    long long seq_total;
+    const long long before = block_exclusive<kThreads>(mine, &seq_total, sh->scan);
+    const long long W = seq_total * HH;
+    const long long G = min(static_cast<long long>(p.grid), W);
+    if (static_cast<long long>(blockIdx.x) >= G) return false;
+    at = W * blockIdx.x / G, hi = W * (blockIdx.x + 1) / G;
+    // the thread whose run of sequences holds tile `at` finds the sequence
+    if (at >= before * HH && at < (before + mine) * HH) {
+      long long first = before;
+      int i = b_lo;
+      for (; i < b_hi; ++i) {
+        const int t = tiles_of(clamp_len(c, __ldg(p.lens + i), &bad), TILE);
+        if (at < (first + t) * HH) break;
+        first += t;
+      }
+      sh->place.b = i;
+      sh->place.before = first;
+    }
+    __syncthreads();
+    b = sh->place.b;
+    seq_first = sh->place.before * HH;
+    len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
+    return true;
   }
-  __syncthreads();
-  int b = sh->place.b;
-  long long seq_first = sh->place.before * HH;
-  int len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
-  for (long long at = lo; at < hi;) {
+  __device__ __forceinline__ bool next(const DecodeParams& p, Piece* s) {
+    if (at >= hi) return false;
+    if (p.direct) {
+      const int seg = static_cast<int>(at % HH);
+      s->hk = seg / p.head_blocks, s->hb = seg % p.head_blocks;
+      s->b = b, s->len = len, s->t0 = 0, s->t1 = nt, s->slot = -1;
+      at = hi;
+      return true;
+    }
+    bool bad = false;
     while (at >= seq_first + nt * HH) {  // next sequence with keys (at < hi <= W: there is one)
       seq_first += nt * HH;
       ++b;
-      len = clamp_len(c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
+      len = clamp_len(p.c, __ldg(p.lens + b), &bad), nt = tiles_of(len, TILE);
     }
     const int seg = static_cast<int>((at - seq_first) / nt);
-    Segment s;
-    s.b = b, s.hk = seg / p.head_blocks, s.hb = seg % p.head_blocks;
-    s.tiles = nt, s.len = len;
+    s->hk = seg / p.head_blocks, s->hb = seg % p.head_blocks;
     const long long first = seq_first + static_cast<long long>(seg) * nt;
-    const int t0 = static_cast<int>(at - first);
-    const int t1 = static_cast<int>(min(hi - first, static_cast<long long>(nt)));
-    const int slot = (t0 == 0 && t1 == nt) ? -1 : (t0 > 0 ? 0 : 1);
-    piece(s, t0, t1, slot);
-    at = first + t1;
+    s->b = b, s->len = len;
+    s->t0 = static_cast<int>(at - first);
+    s->t1 = static_cast<int>(min(hi - first, static_cast<long long>(nt)));
+    s->slot = (s->t0 == 0 && s->t1 == nt) ? -1 : (s->t0 > 0 ? 0 : 1);
+    at = first + s->t1;
+    return true;
   }
-}
+};
 
-// Merged output of a piece: from the warps' states in shared memory to the
-// output tensor (slot < 0) or the workspace.
-template <typename T, int HPB, int DPAD>
-__device__ __forceinline__ void store_piece(const DecodeParams& p, Shared<HPB, DPAD>* sh,
-                                            const float* acc, const Segment& s, int slot) {
-  const int D = p.c.D;
-  const int h0 = s.hk * p.group + s.hb * HPB;            // first query head
-  const int nh = min(HPB, p.group - s.hb * HPB);         // heads of this block
-  for (int e = threadIdx.x; e < nh * DPAD; e += kThreads) {
-    const int h = e / DPAD, d = e % DPAD;
-    if (d >= D) continue;
-    float o = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) o += sh->f[w][h] * acc[(w * HPB + h) * (DPAD + 1) + d];
-    if (slot < 0) {
-      T* dst = static_cast<T*>(p.o) + s.b * p.so.b + (h0 + h) * p.so.h + d;
-      *dst = Elem<T>::put(o);
-    } else {
-      p.ws_o[((static_cast<long long>(blockIdx.x) * 2 + slot) * HPB + h) * D + d] = o;
-    }
-  }
-  if (threadIdx.x < nh) {
-    const int h = threadIdx.x;
-    if (slot < 0) {
-      if (p.lse)
-        p.lse[static_cast<long long>(s.b) * p.H + h0 + h] = sh->lse[h] * 0.6931471805599453f;
-    } else {
-      p.ws_lse[(static_cast<long long>(blockIdx.x) * 2 + slot) * HPB + h] = sh->lse[h];
-    }
-  }
-}
-
-// Factors of the warps' accumulators, from their (m, mw, l, lx): the output is
-// sum_w f_w acc_w with f_w = 2^(base_w - M) / sum_w 2^(m_w - M) l_w, base_w the
-// exponent that acc_w is relative to (less `shift`), and the log-sum-exp (log2
-// units) of the piece.  One thread per head.
-template <int HPB, int DPAD>
-__device__ __forceinline__ void merge_stats(Shared<HPB, DPAD>* sh, float shift) {
-  if (threadIdx.x < HPB) {
-    const int h = threadIdx.x;
-    float M = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh->m[w][h]);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f, lx = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = exp2f(sh->m[w][h] - mu);
-      l += a * sh->l[w][h];
-      lx += a * sh->lx[w][h];
-    }
-    // (l may be NaN: a NaN among the logits reaches every output of the row)
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int w = 0; w < kWarps; ++w) {
-      const float base = sh->mw[w][h];
-      sh->f[w][h] = base == -INFINITY ? 0.f : exp2f(base - shift - mu) * inv;
-    }
-    sh->lse[h] = lx == 0.f ? -INFINITY : mu + log2f(lx);
-  }
+// Slot of a partial output: log-sum-exp (log2 units) per head, and a row of
+// ws_ld floats per head.
+__device__ __forceinline__ long long slot_row(const DecodeParams& p, long long cta, int slot,
+                                              int hpb, int h) {
+  return (cta * 2 + slot) * hpb + h;
 }
 
 // ------------------------------------------------------------------ tensor cores
@@ -330,14 +278,15 @@ __device__ __forceinline__ void ld_shared(uint32_t a, uint32_t (&x)[2]) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(a) : "memory");
 }
 
-// The ring of one warp: kDecodeStages groups of KT keys, K rows then V rows.
+// The ring of one warp: ST groups of KT keys, K rows then V rows.
 template <int DPAD, bool E4M3>
 struct Ring {
   static constexpr int ROWB = DPAD * (E4M3 ? 1 : 2);  // bytes of a row
   static constexpr int KT = decode_warp_keys(DPAD, E4M3);
   static constexpr int PIECES = ROWB / 16;
   static constexpr int STAGE = 2 * KT * ROWB;
-  static constexpr int WARP = kDecodeStages * STAGE;
+  static constexpr int ST = decode_stages(E4M3);
+  static constexpr int WARP = ST * STAGE;
   // byte offset of 16-byte piece x of a row
   static __device__ __forceinline__ int k_at(int row, int x) {
     return row * ROWB + ((PIECES >= 8 ? x ^ ((row & 1) << 2) : x) << 4);
@@ -347,16 +296,24 @@ struct Ring {
   }
 };
 
+// A warp's state in shared memory: accumulator fragments, and (m, mw, l, lx) of
+// heads 2t, 2t + 1 (+ 8 n).
+template <int DPAD, int NG>
+struct Exchange {
+  float4 acc[NG * DPAD / 16][32];
+  float4 stat[NG * 2][4];
+};
+
 // TQ: type of q and o, and of a 16-bit cache.  NG: groups of 8 query heads.
 template <typename TQ, int DPAD, bool E4M3, int NG>
-__global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
+__global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
     decode_tc_kernel(const DecodeParams p) {
   using R = Ring<DPAD, E4M3>;
   constexpr int HPB = 8 * NG;
-  constexpr int KT = R::KT, RG = KT / 16, TILE = kWarps * KT, ST = kDecodeStages;
-  static_assert(ST == 2, "one group is read while the next is copied");
+  constexpr int KT = R::KT, RG = KT / 16, TILE = kWarps * KT, ST = R::ST;
+  static_assert(ST == 2 || !E4M3, "scale bytes are held for one group ahead");
   constexpr bool kBF16 = Elem<TQ>::kBF16 && !E4M3;  // operand type of the products
-  constexpr float kShift = kBF16 ? 0.f : 14.f;      // fp16 weights: largest at 2^14
+  constexpr float kShift = kBF16 ? 0.f : 6.f;       // fp16 weights: at most 2^(6 + 8)
   constexpr int KS = DPAD / 16;                     // contraction steps of S^T
   constexpr int EPC = E4M3 ? 16 : 8;                // elements of a 16-byte piece
   constexpr int KSP = EPC / 4;                      // contraction steps per K piece
@@ -366,13 +323,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
   constexpr int VP = E4M3 ? 1 : DPAD / 64;          // V pieces per lane and key
   constexpr int VE = E4M3 ? DPAD / 8 : 8;           // elements of a V piece
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto* sh = reinterpret_cast<Shared<HPB, DPAD>*>(smem_raw);
-  // the rings; at the end of a piece the accumulators lie over them
-  uint8_t* rings = smem_raw + shared_bytes<HPB, DPAD>();
-  float* acc_sh = reinterpret_cast<float*>(rings);
+  using X = Exchange<DPAD, NG>;
+  auto* sh = reinterpret_cast<SplitShared*>(smem_raw);
+  X* xch = reinterpret_cast<X*>(smem_raw + 128);  // two warps' states
+  static_assert(sizeof(SplitShared) <= 128, "shared memory layout");
   const PagedCache& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(rings) + warp * R::WARP;
+  const uint32_t ring = smem_u32(smem_raw + 128 + 2 * sizeof(X)) + warp * R::WARP;
   const int D = c.D;
   using TC = typename std::conditional<E4M3, uint8_t, TQ>::type;
   const TC* kc = static_cast<const TC*>(c.k);
@@ -386,91 +343,99 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
   const int xcol = col_on ? x * EPC : 0;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  walk<TILE>(p, sh, [&](const Segment& s, int t0, int t1, int slot) {
+  Walker<TILE> walker;
+  if (!walker.start(p, sh)) return;
+  Piece s;  // the piece whose groups are being copied
+  walker.next(p, &s);
+
+  auto first_key = [&](int it) { return (s.t0 + it) * TILE + warp * KT; };
+  // Block-table entry of this lane's key of group it (its 16-key run's first
+  // key where runs lie in one page), unchecked, and that key's row of the
+  // page.  Loaded a group ahead of the copies that need it.
+  int raw = -1, row = 0;
+  bool looked = false;
+  auto look_up = [&](int it) {
+    const int j = first_key(it) + (runs ? (KT == 32 ? lane & 16 : 0) : lane);
+    looked = it < s.t1 - s.t0 && (runs || lane < KT) && j < s.len;
+    if (looked) {
+      int entry;
+      split_position(c, j, &entry, &row);
+      raw = __ldg(c.table + s.b * c.table_stride + entry);
+    }
+  };
+  // Starts the copies of group it (whose entries have been looked up) into
+  // its stage; e4m3: also loads the scale bytes of key `lane` (K low, V high
+  // byte).  keep_next: keys of the group that exist and whose page does.
+  unsigned sb_next = 0;
+  uint32_t keep_next = 0, keeps[ST - 1];  // of the group issued last; of the groups in flight
+  auto issue = [&](int it) {
+    const int j0 = first_key(it);
+    if (it < s.t1 - s.t0 && j0 < s.len) {
+      const bool have = looked && raw >= 0 && raw < c.pages;
+      if (looked && !have) atomicOr(c.status, kStatusIndex);
+      const int left = s.len - j0;
+      keep_next = __ballot_sync(0xffffffffu, have) & (KT == 32 ? 0xFFFFFFFFu : 0xFFFFu) &
+                  (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u);
+      const int page = have ? raw : 0, r0 = have ? row : 0;
+      const TC* kp = kc + page * c.sk.b + s.hk * c.sk.h + r0 * c.sk.n;
+      const TC* vp = vc + page * c.sv.b + s.hk * c.sv.h + r0 * c.sv.n;
+      if (E4M3 && ((keep_next >> lane) & 1u)) {
+        const long long at = (static_cast<long long>(page) * c.Hkv + s.hk) * c.page_size + r0 +
+                             (runs ? lane & 15 : 0);
+        sb_next = __ldg(c.k_scale + at) | (static_cast<unsigned>(__ldg(c.v_scale + at)) << 8);
+      }
+      const uint32_t dst = ring + (it % ST) * R::STAGE;
+      if (runs) {
+        // (the pointers of run h of the group are lane 16 h's)
+#pragma unroll
+        for (int h = 0; h < RG; ++h) {
+          const TC* kr = reinterpret_cast<const TC*>(__shfl_sync(
+                             0xffffffffu, reinterpret_cast<unsigned long long>(kp), 16 * h)) +
+                         lr * c.sk.n + xcol;
+          const TC* vr = reinterpret_cast<const TC*>(__shfl_sync(
+                             0xffffffffu, reinterpret_cast<unsigned long long>(vp), 16 * h)) +
+                         lr * c.sv.n + xcol;
+          const uint32_t keep = (keep_next >> (16 * h)) & 0xFFFFu;
+#pragma unroll
+          for (int i = 0; i < 16 / RS; ++i) {
+            const int r = 16 * h + i * RS + lr;
+            const bool on = col_on && (keep == 0xFFFFu || ((keep >> (i * RS + lr)) & 1u));
+            copy_async16(dst + R::k_at(r, x), kr, on);
+            copy_async16(dst + R::v_at(r, x), vr, on);
+            kr += RS * c.sk.n, vr += RS * c.sv.n;
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int i = 0; i < NCP; ++i) {
+          const int r = i * RS + lr;
+          const TC* kr = reinterpret_cast<const TC*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kp), r));
+          const TC* vr = reinterpret_cast<const TC*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vp), r));
+          const bool on = col_on && ((keep_next >> r) & 1u);
+          copy_async16(dst + R::k_at(r, x), kr + xcol, on);
+          copy_async16(dst + R::v_at(r, x), vr + xcol, on);
+        }
+      }
+    }
+    copy_async_commit();
+  };
+  uint32_t qf[NG][KS][2];
+  float qs[NG][2];
+  // The first groups of piece s on their way, and its query operand.
+  auto begin = [&]() {
+    __syncwarp();  // the ring has been read
+#pragma unroll
+    for (int it = 0; it < ST - 1; ++it) {
+      look_up(it);
+      issue(it);
+      keeps[it] = keep_next;
+    }
+    look_up(ST - 1);
     const int h0 = s.hk * p.group + s.hb * HPB;
     const int nh = min(HPB, p.group - s.hb * HPB);
-    __syncthreads();  // the previous piece's use of shared memory is over
-
-    auto first_key = [&](int it) { return (t0 + it) * TILE + warp * KT; };
-    const int n_it = t1 - t0;
-    // Block-table entry of this lane's key of group it (its 16-key run's first
-    // key where runs lie in one page), unchecked, and that key's row of the
-    // page.  Loaded a group ahead of the copies that need it.
-    int raw = -1, row = 0;
-    bool looked = false;
-    auto look_up = [&](int it) {
-      const int j = first_key(it) + (runs ? (KT == 32 ? lane & 16 : 0) : lane);
-      looked = it < n_it && (runs || lane < KT) && j < s.len;
-      if (looked) {
-        int entry;
-        split_position(c, j, &entry, &row);
-        raw = __ldg(c.table + s.b * c.table_stride + entry);
-      }
-    };
-    // Starts the copies of group it (whose entries have been looked up) into
-    // its stage; e4m3: also loads the scale bytes of key `lane` (K low, V high
-    // byte).  keep_next: keys of the group that exist and whose page does.
-    unsigned sb_next = 0;
-    uint32_t keep_next = 0;
-    auto issue = [&](int it) {
-      const int j0 = first_key(it);
-      if (it < n_it && j0 < s.len) {
-        const bool have = looked && raw >= 0 && raw < c.pages;
-        if (looked && !have) atomicOr(c.status, kStatusIndex);
-        const int left = s.len - j0;
-        keep_next = __ballot_sync(0xffffffffu, have) & (KT == 32 ? 0xFFFFFFFFu : 0xFFFFu) &
-                    (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u);
-        const int page = have ? raw : 0, r0 = have ? row : 0;
-        const TC* kp = kc + page * c.sk.b + s.hk * c.sk.h + r0 * c.sk.n;
-        const TC* vp = vc + page * c.sv.b + s.hk * c.sv.h + r0 * c.sv.n;
-        if (E4M3 && ((keep_next >> lane) & 1u)) {
-          const long long at = (static_cast<long long>(page) * c.Hkv + s.hk) * c.page_size + r0 +
-                               (runs ? lane & 15 : 0);
-          sb_next = __ldg(c.k_scale + at) | (static_cast<unsigned>(__ldg(c.v_scale + at)) << 8);
-        }
-        const uint32_t dst = ring + (it % ST) * R::STAGE;
-        if (runs) {
-          // (the pointers of run h of the group are lane 16 h's)
-#pragma unroll
-          for (int h = 0; h < RG; ++h) {
-            const TC* kr = reinterpret_cast<const TC*>(__shfl_sync(
-                               0xffffffffu, reinterpret_cast<unsigned long long>(kp), 16 * h)) +
-                           lr * c.sk.n + xcol;
-            const TC* vr = reinterpret_cast<const TC*>(__shfl_sync(
-                               0xffffffffu, reinterpret_cast<unsigned long long>(vp), 16 * h)) +
-                           lr * c.sv.n + xcol;
-            const uint32_t keep = (keep_next >> (16 * h)) & 0xFFFFu;
-#pragma unroll
-            for (int i = 0; i < 16 / RS; ++i) {
-              const int r = 16 * h + i * RS + lr;
-              const bool on = col_on && (keep == 0xFFFFu || ((keep >> (i * RS + lr)) & 1u));
-              copy_async16(dst + R::k_at(r, x), kr, on);
-              copy_async16(dst + R::v_at(r, x), vr, on);
-              kr += RS * c.sk.n, vr += RS * c.sv.n;
-            }
-          }
-        } else {
-#pragma unroll 4
-          for (int i = 0; i < NCP; ++i) {
-            const int r = i * RS + lr;
-            const TC* kr = reinterpret_cast<const TC*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kp), r));
-            const TC* vr = reinterpret_cast<const TC*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vp), r));
-            const bool on = col_on && ((keep_next >> r) & 1u);
-            copy_async16(dst + R::k_at(r, x), kr + xcol, on);
-            copy_async16(dst + R::v_at(r, x), vr + xcol, on);
-          }
-        }
-      }
-      copy_async_commit();
-    };
-    look_up(0);
-    issue(0);
-    look_up(1);
-
     // ---- Q^T operand: lane (g, t) holds head g (+ 8 n), permuted to match K
-    uint32_t qf[NG][KS][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       const int h = n * 8 + g;
@@ -504,17 +469,18 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
           qf[n][ks][0] = pack2(x[ks][0] * down, x[ks][1] * down, false);
           qf[n][ks][1] = pack2(x[ks][2] * down, x[ks][3] * down, false);
         }
-        if (warp == 0 && t == 0)
-          sh->qs[h] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 + ec) << 23);
+        // (of the head that this lane loads; lane 4 h has head h's)
+        const float f = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 + ec) << 23);
+        qs[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+        qs[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      } else {
+        qs[n][0] = qs[n][1] = p.scale_log2;
       }
     }
-    if constexpr (E4M3) __syncthreads();
-    float qs[NG][2];
-#pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) qs[n][i] = E4M3 ? sh->qs[n * 8 + 2 * t + i] : p.scale_log2;
+  };
 
+  begin();
+  while (true) {
     float m[NG][2], mw[NG][2], l[NG][2], lx[NG][2], acc[NG][MT][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
@@ -526,13 +492,16 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
         for (int i = 0; i < 4; ++i) acc[n][mt][i] = 0.f;
     }
 
-    for (int it = 0; it < n_it && first_key(it) < s.len; ++it) {
-      copy_async_wait<0>();
+    for (int it = 0; it < s.t1 - s.t0 && first_key(it) < s.len; ++it) {
+      copy_async_wait<ST - 2>();
       __syncwarp();  // every lane's copies of group it are in; group it - 1 has been read
       const unsigned sb = sb_next;
-      const uint32_t keep = keep_next;
-      issue(it + 1);
-      look_up(it + 2);
+      const uint32_t keep = keeps[0];
+      issue(it + ST - 1);
+      look_up(it + ST);
+#pragma unroll
+      for (int i = 0; i + 1 < ST - 1; ++i) keeps[i] = keeps[i + 1];
+      keeps[ST - 2] = keep_next;
       auto kept = [&](int i) -> bool { return (keep >> i) & 1u; };
       const uint32_t st = ring + (it % ST) * R::STAGE;
 
@@ -583,50 +552,57 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         float x[2 * RG][2], pw[2 * RG][2];  // [key g + 8 r][head 2t + i]
+        // The maxima in the exponents move only where a logit exceeds them by
+        // 2^8 (ratios are exact for any stale maximum): one vote, and the
+        // reductions over the keys only then.
+        bool need = false;
 #pragma unroll
         for (int r = 0; r < 2 * RG; ++r)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float y = sc[r / 2][n][2 * (r & 1) + i] * (E4M3 ? kscale[r] * qs[n][i] : qs[n][i]);
             x[r][i] = kept(g + 8 * r) ? y : -INFINITY;
+            need |= x[r][i] > m[n][i] + 8.f;
+            if constexpr (E4M3) need |= x[r][i] + vexp[r] > mw[n][i] + 8.f;
           }
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = -INFINITY, topw = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 2 * RG; ++r) {
+              top = fmaxf(top, x[r][i]);
+              if constexpr (E4M3) topw = fmaxf(topw, x[r][i] + vexp[r]);
+            }
+            const float m_new = fmaxf(m[n][i], max_over_g(top));
+            float a = m_new == m[n][i] ? 1.f : exp2f(m[n][i] - m_new);
+            m[n][i] = m_new;
+            l[n][i] *= a, lx[n][i] *= a;
+            if constexpr (E4M3) {
+              const float mw_new = fmaxf(mw[n][i], max_over_g(topw));
+              a = mw_new == mw[n][i] ? 1.f : exp2f(mw[n][i] - mw_new);
+              mw[n][i] = mw_new;
+            } else {
+              mw[n][i] = m_new;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              acc[n][mt][i] *= a;
+              acc[n][mt][2 + i] *= a;
+            }
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float top = -INFINITY, topw = -INFINITY;
-#pragma unroll
-          for (int r = 0; r < 2 * RG; ++r) {
-            top = fmaxf(top, x[r][i]);
-            if constexpr (E4M3) topw = fmaxf(topw, x[r][i] + vexp[r]);
-          }
-          const float m_new = fmaxf(m[n][i], max_over_g(top));
-          const float mu = m_new == -INFINITY ? 0.f : m_new;
-          const float a_m = exp2f(m[n][i] - mu);
-          l[n][i] *= a_m, lx[n][i] *= a_m;
-          float a_w = a_m, mwu = mu;
-          if constexpr (E4M3) {
-            const float mw_new = fmaxf(mw[n][i], max_over_g(topw));
-            mwu = mw_new == -INFINITY ? 0.f : mw_new;
-            a_w = exp2f(mw[n][i] - mwu);
-            mw[n][i] = mw_new;
-          } else {
-            mw[n][i] = m_new;
-          }
-          m[n][i] = m_new;
+          const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i];
+          const float mwu = (mw[n][i] == -INFINITY ? 0.f : mw[n][i]) - kShift;
 #pragma unroll
           for (int r = 0; r < 2 * RG; ++r) {
             if constexpr (E4M3) {
-              const float e = ex2_approx(x[r][i] - mu);
-              l[n][i] += e, lx[n][i] += e;
-              pw[r][i] = ex2_approx(x[r][i] + vexp[r] - mwu + kShift);
+              l[n][i] += ex2_approx(x[r][i] - mu);
+              pw[r][i] = ex2_approx(x[r][i] + vexp[r] - mwu);
             } else {
-              pw[r][i] = ex2_approx(x[r][i] - mwu + kShift);
-            }
-          }
-          if (__any_sync(0xffffffffu, a_w != 1.f)) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              acc[n][mt][i] *= a_w;
-              acc[n][mt][2 + i] *= a_w;
+              pw[r][i] = ex2_approx(x[r][i] - mwu);
             }
           }
         }
@@ -676,36 +652,117 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG))
       }
     }
 
-    // ---- join of the four warps
-    copy_async_wait<0>();
-    __syncthreads();  // no ring is read any more
+    // ---- the next piece's first groups, then the join of the four warps
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float ls = sum_over_g(l[n][i]), lxs = sum_over_g(lx[n][i]);
-        if (g == 0) {
-          const int h = n * 8 + 2 * t + i;
-          sh->m[warp][h] = m[n][i];
-          sh->mw[warp][h] = mw[n][i];
-          // 16-bit caches sum the weights as shifted for the product
-          sh->l[warp][h] = E4M3 ? ls : ls * exp2f(-kShift);
-          sh->lx[warp][h] = E4M3 ? lxs : lxs * exp2f(-kShift);
+        l[n][i] = sum_over_g(l[n][i]);
+        lx[n][i] = E4M3 ? l[n][i] : sum_over_g(lx[n][i]);
+      }
+    const Piece done = s;
+    const bool more = walker.next(p, &s);
+    if (more) begin();
+    auto put = [&](X& to) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          to.acc[n * MT + mt][lane] =
+              make_float4(acc[n][mt][0], acc[n][mt][1], acc[n][mt][2], acc[n][mt][3]);
+        if (g == 0)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            to.stat[n * 2 + i][t] = make_float4(m[n][i], mw[n][i], l[n][i], lx[n][i]);
+      }
+    };
+    // merge of another warp's state into this one's, each relative to its own
+    // maxima
+    auto take = [&](const X& from) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float own[2], oth[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 st = from.stat[n * 2 + i][t];
+          const float M = fmaxf(m[n][i], st.x), mu = M == -INFINITY ? 0.f : M;
+          const float a = exp2f(m[n][i] - mu), b = exp2f(st.x - mu);
+          l[n][i] = a * l[n][i] + b * st.z;
+          lx[n][i] = a * lx[n][i] + b * st.w;
+          m[n][i] = M;
+          const float W = fmaxf(mw[n][i], st.y), wu = W == -INFINITY ? 0.f : W;
+          own[i] = E4M3 ? exp2f(mw[n][i] - wu) : a;
+          oth[i] = E4M3 ? exp2f(st.y - wu) : b;
+          mw[n][i] = W;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const float4 o = from.acc[n * MT + mt][lane];
+          acc[n][mt][0] = own[0] * acc[n][mt][0] + oth[0] * o.x;
+          acc[n][mt][1] = own[1] * acc[n][mt][1] + oth[1] * o.y;
+          acc[n][mt][2] = own[0] * acc[n][mt][2] + oth[0] * o.z;
+          acc[n][mt][3] = own[1] * acc[n][mt][3] + oth[1] * o.w;
         }
       }
+    };
+    __syncthreads();  // the last join has been read
+    if (warp >= 2) put(xch[warp - 2]);
+    __syncthreads();
+    if (warp < 2) take(xch[warp]);
+    if (warp == 1) put(xch[1]);  // (only this warp read it)
+    __syncthreads();
+    if (warp == 0) {
+      take(xch[1]);
+      const int h0 = done.hk * p.group + done.hb * HPB;
+      const int nh = min(HPB, p.group - done.hb * HPB);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int d = E4M3 ? g * VE + 2 * mt : (g + 8 * (mt / 4)) * 8 + 2 * (mt % 4);
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc_sh[(warp * HPB + n * 8 + 2 * t + (i & 1)) * (DPAD + 1) + d + (i >> 1)] = acc[n][mt][i];
-      }
+        for (int i = 0; i < 2; ++i) {
+          const int h = n * 8 + 2 * t + i;
+          if (h >= nh) continue;
+          const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i];
+          // (l may be NaN: a NaN among the logits reaches every output of the
+          // row.  With a 16-bit cache l and the accumulator have the same
+          // exponent; mw - m is 0 there.)
+          float f = l[n][i] == 0.f ? 0.f : 1.f / l[n][i];
+          if (E4M3) f *= mw[n][i] == -INFINITY ? 0.f : exp2f(mw[n][i] - kShift - mu);
+          const float lse = lx[n][i] == 0.f ? -INFINITY : mu + log2f(lx[n][i]) - (E4M3 ? 0.f : kShift);
+          const long long ws = slot_row(p, blockIdx.x, done.slot, HPB, h);
+          if (g == 0) {
+            if (done.slot >= 0) p.ws_lse[ws] = lse;
+            else if (p.lse) p.lse[static_cast<long long>(done.b) * p.H + h0 + h] = lse * 0.6931471805599453f;
+          }
+#pragma unroll
+          for (int u = 0; u < MT / 4; ++u) {  // eight columns from d
+            const int d = E4M3 ? g * VE + 8 * u : (g + 8 * u) * 8;
+            if (d >= D) continue;
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = acc[n][4 * u + k][i] * f;
+              o[2 * k + 1] = acc[n][4 * u + k][2 + i] * f;
+            }
+            if (done.slot >= 0) {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + ws * DPAD + d);
+              dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+              dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+            } else {
+              TQ* dst = static_cast<TQ*>(p.o) + done.b * p.so.b + (h0 + h) * p.so.h + d;
+              if (p.o_vec) {
+                *reinterpret_cast<uint4*>(dst) =
+                    make_uint4(pack2(o[0], o[1], Elem<TQ>::kBF16), pack2(o[2], o[3], Elem<TQ>::kBF16),
+                               pack2(o[4], o[5], Elem<TQ>::kBF16), pack2(o[6], o[7], Elem<TQ>::kBF16));
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dst[k] = Elem<TQ>::put(o[k]);
+              }
+            }
+          }
+        }
     }
-    __syncthreads();
-    merge_stats(sh, kShift);
-    __syncthreads();
-    store_piece<TQ, HPB, DPAD>(p, sh, acc_sh, s, slot);
-  });
+    if (!more) break;
+  }
 }
 
 // ------------------------------------------------------------------ CUDA cores
@@ -743,15 +800,21 @@ __device__ __forceinline__ float4 load4(const T* row, int d, int D) {
   return f;
 }
 
+template <int HPB, int DPAD>
+struct SimtShared {
+  SplitShared split;
+  float m[kWarps][HPB], l[kWarps][HPB];
+  alignas(16) float q[HPB][DPAD];
+  alignas(16) float acc[kWarps][HPB][DPAD];
+};
+
 template <typename TQ, int DPAD, bool E4M3, int HPB, bool VEC>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParams p) {
   constexpr int NC = DPAD / 16;  // 4-column pieces per lane
   constexpr int TILE = kDecodeSimtTile, KT = TILE / kWarps;
   static_assert(KT == 16, "a warp takes two rounds of eight keys");
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto* sh = reinterpret_cast<Shared<HPB, DPAD>*>(smem_raw);
-  auto* sq = reinterpret_cast<float(*)[DPAD]>(smem_raw + shared_bytes<HPB, DPAD>());
-  float* acc_sh = reinterpret_cast<float*>(sq + HPB);
+  auto* sh = reinterpret_cast<SimtShared<HPB, DPAD>*>(smem_raw);
   const PagedCache& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int D = c.D;
@@ -760,13 +823,16 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
   const TC* vc = static_cast<const TC*>(c.v);
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  walk<TILE>(p, sh, [&](const Segment& s, int t0, int t1, int slot) {
+  Walker<TILE> walker;
+  if (!walker.start(p, &sh->split)) return;
+  Piece s;
+  while (walker.next(p, &s)) {
     const int h0 = s.hk * p.group + s.hb * HPB;
     const int nh = min(HPB, p.group - s.hb * HPB);
     __syncthreads();
     for (int e = threadIdx.x; e < HPB * DPAD; e += kThreads) {
       const int h = e / DPAD, d = e % DPAD;
-      sq[h][d] = (h < nh && d < D)
+      sh->q[h][d] = (h < nh && d < D)
                      ? Elem<TQ>::get(static_cast<const TQ*>(p.q)[s.b * p.sq.b + (h0 + h) * p.sq.h + d])
                      : 0.f;
     }
@@ -779,7 +845,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
 #pragma unroll
       for (int u = 0; u < NC; ++u) acc[h][u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int tile = t0; tile < t1; ++tile) {
+    for (int tile = s.t0; tile < s.t1; ++tile) {
       const int j0 = tile * TILE + warp * KT;
       if (j0 >= s.len) break;
 #pragma unroll 1
@@ -813,7 +879,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
           float dot = 0.f;
 #pragma unroll
           for (int u = 0; u < NC; ++u) {
-            const float4 q = *reinterpret_cast<const float4*>(&sq[h][4 * (t + 4 * u)]);
+            const float4 q = *reinterpret_cast<const float4*>(&sh->q[h][4 * (t + 4 * u)]);
             dot = fmaf(x[u].x, q.x, fmaf(x[u].y, q.y, fmaf(x[u].z, q.z, fmaf(x[u].w, q.w, dot))));
           }
           dot += __shfl_xor_sync(0xffffffffu, dot, 1);
@@ -845,35 +911,58 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
 #pragma unroll
     for (int h = 0; h < HPB; ++h) {
       const float ls = sum_over_g(l[h]);
-      if (lane == 0) sh->m[warp][h] = sh->mw[warp][h] = m[h], sh->l[warp][h] = sh->lx[warp][h] = ls;
+      if (lane == 0) sh->m[warp][h] = m[h], sh->l[warp][h] = ls;
 #pragma unroll
       for (int u = 0; u < NC; ++u) {
         const float4 a = make_float4(sum_over_g(acc[h][u].x), sum_over_g(acc[h][u].y),
                                      sum_over_g(acc[h][u].z), sum_over_g(acc[h][u].w));
-        if (g == 0) {
-          float* dst = acc_sh + (warp * HPB + h) * (DPAD + 1) + 4 * (t + 4 * u);
-          dst[0] = a.x, dst[1] = a.y, dst[2] = a.z, dst[3] = a.w;
-        }
+        if (g == 0) *reinterpret_cast<float4*>(&sh->acc[warp][h][4 * (t + 4 * u)]) = a;
       }
     }
     __syncthreads();
-    merge_stats(sh, 0.f);
-    __syncthreads();
-    store_piece<TQ, HPB, DPAD>(p, sh, acc_sh, s, slot);
-  });
+    for (int e = threadIdx.x; e < nh * DPAD; e += kThreads) {
+      const int h = e / DPAD, d = e % DPAD;
+      if (d >= D) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh->m[w][h]);
+      const float mu = M == -INFINITY ? 0.f : M;
+      float sum = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float a = exp2f(sh->m[w][h] - mu);
+        sum += a * sh->l[w][h];
+        o += a * sh->acc[w][h][d];
+      }
+      o *= sum == 0.f ? 0.f : 1.f / sum;
+      const float lse = sum == 0.f ? -INFINITY : mu + log2f(sum);
+      if (s.slot >= 0) {
+        const long long ws = slot_row(p, blockIdx.x, s.slot, HPB, h);
+        p.ws_o[ws * DPAD + d] = o;
+        if (d == 0) p.ws_lse[ws] = lse;
+      } else {
+        static_cast<TQ*>(p.o)[s.b * p.so.b + (h0 + h) * p.so.h + d] = Elem<TQ>::put(o);
+        if (d == 0 && p.lse)
+          p.lse[static_cast<long long>(s.b) * p.H + h0 + h] = lse * 0.6931471805599453f;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------ the join
-// One warp per (sequence, query head): outputs of the CTAs that share its
-// segment, weighted by their log-sum-exps, in CTA order.  Sequences without
-// keys get the empty row (0, -inf).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParams p, int hpb,
-                                                               int tile) {
+// One block per (sequence, query head): outputs of the CTAs that share its
+// segment, weighted by their log-sum-exps.  Warp w takes every eighth of them
+// from the w-th, a lane four columns; the warps' sums are added in order.
+// Sequences without keys get the empty row (0, -inf).
+constexpr int kJoinWarps = 8;
+template <typename T, int DPAD>
+__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p, int hpb,
+                                                                      int tile) {
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float weight[kJoinWarps];
   const PagedCache& c = p.c;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int b = static_cast<int>(item / p.H), h = static_cast<int>(item % p.H);
+  const int b = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool bad = false;
   long long before = 0, total = 0;
   for (int i = lane; i < c.B; i += 32) {
@@ -886,17 +975,16 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
-  if (bad && item == 0) atomicOr(c.status, kStatusIndex);
+  if (bad && blockIdx.x == 0) atomicOr(c.status, kStatusIndex);
   // This kernel may be placed while the attention kernel runs: from here on
-  // that one is complete and its partial states are visible.  (Every warp
+  // that one is complete and its partial states are visible.  (Every block
   // waits, so that this kernel never ends before it.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (b >= c.B) return;
   T* dst = static_cast<T*>(p.o) + b * p.so.b + h * p.so.h;
   const int nt = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), tile);
   if (nt == 0) {
-    for (int d = lane; d < c.D; d += 32) dst[d] = Elem<T>::put(0.f);
-    if (lane == 0 && p.lse) p.lse[static_cast<long long>(b) * p.H + h] = -INFINITY;
+    for (int d = threadIdx.x; d < c.D; d += kJoinWarps * 32) dst[d] = Elem<T>::put(0.f);
+    if (threadIdx.x == 0 && p.lse) p.lse[static_cast<long long>(b) * p.H + h] = -INFINITY;
     return;
   }
   const long long HH = static_cast<long long>(c.Hkv) * p.head_blocks;
@@ -907,34 +995,47 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   const long long c0 = ((first + 1) * G - 1) / W, c1 = ((first + nt) * G - 1) / W;
   if (c0 == c1) return;  // written by that CTA
   // the first CTA's piece begins the segment (slot 1), the others' continue it
-  auto slot = [&](long long cta) { return (cta * 2 + (cta == c0 ? 1 : 0)) * hpb + hi; };
+  auto row = [&](long long cta) { return slot_row(p, cta, cta == c0 ? 1 : 0, hpb, hi); };
   float M = -INFINITY;
-  for (long long cta = c0 + lane; cta <= c1; cta += 32) M = fmaxf(M, p.ws_lse[slot(cta)]);
+  for (long long cta = c0 + lane; cta <= c1; cta += 32) M = fmaxf(M, p.ws_lse[row(cta)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float mu = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (long long base = c0; base <= c1; base += 32) {
-    const long long cta = base + lane;
-    const float w = cta <= c1 ? exp2f(p.ws_lse[slot(cta)] - mu) : 0.f;
-    const int n = static_cast<int>(min(32ll, c1 - base + 1));
+  const bool on = 4 * lane < DPAD;
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.ws_o + slot(base + i) * c.D;
-      L += wi;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (lane + 32 * u < c.D) acc[u] = fmaf(wi, src[lane + 32 * u], acc[u]);
-    }
+  for (long long cta = c0 + warp; cta <= c1; cta += kJoinWarps) {
+    const long long r = row(cta);
+    const float w = exp2f(p.ws_lse[r] - mu);
+    // (columns past D of a row are not written: they are not used either)
+    const float4 x = on ? *reinterpret_cast<const float4*>(p.ws_o + r * DPAD + 4 * lane)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    L += w;
+    acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  sums[warp][lane] = acc;
+  if (lane == 0) weight[warp] = L;
+  __syncthreads();
+  if (warp == 0) {
+    L = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (lane + 32 * u < c.D) dst[lane + 32 * u] = Elem<T>::put(acc[u] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[static_cast<long long>(b) * p.H + h] =
-        L == 0.f ? -INFINITY : (mu + log2f(L)) * 0.6931471805599453f;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float4 x = sums[w][lane];
+      L += weight[w];
+      acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (4 * lane + k < c.D) dst[4 * lane + k] = Elem<T>::put(o[k]);
+    if (lane == 0 && p.lse)
+      p.lse[static_cast<long long>(b) * p.H + h] =
+          L == 0.f ? -INFINITY : (mu + log2f(L)) * 0.6931471805599453f;
+  }
 }
 
 // ------------------------------------------------------------------ launch
@@ -950,18 +1051,14 @@ cudaError_t launch_with_smem(K kern, int bytes, const DecodeParams& p, cudaStrea
 
 template <typename TQ, int DPAD, bool E4M3, int NG>
 cudaError_t launch_tc(const DecodeParams& p, cudaStream_t stream) {
-  using S = Shared<8 * NG, DPAD>;
-  constexpr int rings = kWarps * Ring<DPAD, E4M3>::WARP;
-  constexpr int bytes =
-      shared_bytes<8 * NG, DPAD>() + (rings > S::kAccBytes ? rings : S::kAccBytes);
-  static_assert(decode_ctas_per_sm(DPAD, NG) * (bytes + 1024) <= 228 * 1024, "resident CTAs");
+  constexpr int bytes = 128 + 2 * sizeof(Exchange<DPAD, NG>) + kWarps * Ring<DPAD, E4M3>::WARP;
+  static_assert(decode_ctas_per_sm(DPAD, NG, E4M3) * (bytes + 1024) <= 228 * 1024, "resident CTAs");
   return launch_with_smem(decode_tc_kernel<TQ, DPAD, E4M3, NG>, bytes, p, stream);
 }
 template <typename TQ, int DPAD, bool E4M3>
 cudaError_t launch_simt(bool vec, const DecodeParams& p, cudaStream_t stream) {
   constexpr int HPB = DPAD > 64 ? 2 : 4;
-  constexpr int bytes =
-      shared_bytes<HPB, DPAD>() + HPB * DPAD * 4 + Shared<HPB, DPAD>::kAccBytes;
+  constexpr int bytes = sizeof(SimtShared<HPB, DPAD>);
   return vec ? launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, true>, bytes, p, stream)
              : launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, false>, bytes, p, stream);
 }
@@ -989,19 +1086,18 @@ cudaError_t launch_typed(bool e4m3, bool tc, bool vec, const DecodeParams& p, cu
   }
   // The join may be placed on the GPU while the attention kernel still runs
   // (programmatic dependent launch); it waits for it before it reads.
-  const long long rows = static_cast<long long>(p.c.B) * p.H;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.c.B) * p.H));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.grid > 0 ? 1 : 0;
-  const int tile = decode_tile(tc, p.c.D, e4m3);
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ>, p,
-                            decode_heads_per_block(tc, p.c.D, p.group), tile);
+  const int hpb = decode_heads_per_block(tc, p.c.D, p.group), tile = decode_tile(tc, p.c.D, e4m3);
+  return wide ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, 128>, p, hpb, tile)
+              : cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, 64>, p, hpb, tile);
 }
 
 }  // namespace

@@ -161,7 +161,8 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
   d.head_blocks = (group + d.heads_per_block - 1) / d.heads_per_block;
   const int64_t most = c->max_pages * c->page_size;
   const int64_t wave =
-      static_cast<int64_t>(num_sms) * decode_ctas_per_sm(D, tc ? d.heads_per_block / 8 : 1);
+      static_cast<int64_t>(num_sms) *
+      (tc ? decode_ctas_per_sm(D, d.heads_per_block / 8, c->dtype == JVP_E4M3) : kDecodeSimtCtasPerSm);
   const int tile = decode_tile(tc, D, c->dtype == JVP_E4M3);
   const int64_t tiles = (most + tile - 1) / tile;
   // B * Hkv * head_blocks <= B * H <= 2^31 - 1 (checked by the caller), tiles < 2^31
@@ -172,7 +173,7 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
   }
   d.grid = static_cast<int>(std::min<int64_t>(wave, tiles ? (segments > wave ? wave : segments * tiles) : 0));
   const size_t slots = static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
-  d.bytes = ((slots * 4 + 255) & ~static_cast<size_t>(255)) + slots * D * 4;
+  d.bytes = ((slots * 4 + 255) & ~static_cast<size_t>(255)) + slots * (D > 64 ? 128 : 64) * 4;
   return d;
 }
 
@@ -393,6 +394,7 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
     return api_fail(JVP_ERR_WORKSPACE,
                     "workspace is NULL or smaller than jvp_attn_decode_workspace_size()");
   if (!aligned_to(workspace, 16)) return api_fail(JVP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  p.o_vec = aligned_to(o, 16) && multiple(p.so, 8);
   p.head_blocks = d.head_blocks, p.grid = d.grid, p.direct = d.direct;
   const size_t slots = d.direct ? 0 : static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
   p.ws_lse = static_cast<float*>(workspace);

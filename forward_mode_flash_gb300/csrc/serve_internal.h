@@ -59,7 +59,8 @@ struct DecodeParams {
   float* lse;          // [B, H] or nullptr
   float scale_log2;    // logit scale * log2(e)
   float* ws_lse;       // [grid][2][heads_per_block]
-  float* ws_o;         // [grid][2][heads_per_block][D]
+  float* ws_o;         // [grid][2][heads_per_block][64 or 128]
+  int o_vec;           // output rows are 16-byte aligned
 };
 
 // Which kernel a call takes: tensor cores (16-bit queries, 16-byte aligned
@@ -73,16 +74,16 @@ inline int decode_heads_per_block(bool tc, int D, int group) {
 // Tensor cores: keys of a warp's group of rows (K and V rows of 8 KB at most)
 // and groups in a warp's ring; four warps' groups are the split's tile.
 constexpr int decode_warp_keys(int D, bool e4m3) { return D > 64 && !e4m3 ? 16 : 32; }
-constexpr int kDecodeStages = 2;
+constexpr int decode_stages(bool e4m3) { return e4m3 ? 2 : 3; }
 constexpr int kDecodeSimtTile = 64;
+constexpr int kDecodeSimtCtasPerSm = 3;
 constexpr int decode_tile(bool tc, int D, bool e4m3) {
   return tc ? 4 * decode_warp_keys(D, e4m3) : kDecodeSimtTile;
 }
-// CTAs per SM that the split is made for: one resident wave (registers: 168 a
-// thread at three CTAs of 128; the widest variant, 16 heads of 128 columns,
-// spills there).
-constexpr int decode_ctas_per_sm(int D, int head_groups) {
-  return D > 64 && head_groups > 1 ? 2 : 3;
+// CTAs per SM that the split is made for: one resident wave (shared memory of
+// the rings, 64 or 96 KB; registers, 168 a thread at three CTAs of 128).
+constexpr int decode_ctas_per_sm(int D, int head_groups, bool e4m3) {
+  return !e4m3 || (D > 64 && head_groups > 1) ? 2 : 3;
 }
 // Where no sequence can have more tiles than this, a CTA takes a whole segment
 // and nothing is joined.
