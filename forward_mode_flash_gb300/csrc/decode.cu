@@ -175,12 +175,14 @@ struct SplitShared {
 // output goes (-1: it is the whole segment).
 struct Piece {
   int b, hk, hb, len, t0, t1, slot;
+  long long first;  // the segment's first tile in the list, and its tiles
+  int nt;
 };
 
 // This CTA's range of the list, segment by segment.
 template <int TILE>
 struct Walker {
-  long long at, hi, seq_first, HH;
+  long long at, hi, seq_first, HH, W, G;  // W tiles in all, on G CTAs
   int b, len, nt;
 
   // False: nothing to do here.  Executed by the whole block.
@@ -201,8 +203,8 @@ struct Walker {
     for (int i = b_lo; i < b_hi; ++i) mine += tiles_of(clamp_len(c, __ldg(p.lens + i), &bad), TILE);
     long long seq_total;
     const long long before = block_exclusive<kThreads>(mine, &seq_total, sh->scan);
-    const long long W = seq_total * HH;
-    const long long G = min(static_cast<long long>(p.grid), W);
+    W = seq_total * HH;
+    G = min(static_cast<long long>(p.grid), W);
     if (static_cast<long long>(blockIdx.x) >= G) return false;
     at = W * blockIdx.x / G, hi = W * (blockIdx.x + 1) / G;
     // the thread whose run of sequences holds tile `at` finds the sequence
@@ -245,8 +247,17 @@ struct Walker {
     s->t0 = static_cast<int>(at - first);
     s->t1 = static_cast<int>(min(hi - first, static_cast<long long>(nt)));
     s->slot = (s->t0 == 0 && s->t1 == nt) ? -1 : (s->t0 > 0 ? 0 : 1);
+    s->first = first, s->nt = nt;
     at = first + s->t1;
     return true;
+  }
+  // For the join, by the CTA that begins a segment: the CTAs that share it
+  // (CTA c holds tiles [W c / G, W (c + 1) / G); this one is the first).
+  __device__ __forceinline__ void note(const DecodeParams& p, const Piece& s) const {
+    if (p.direct || s.t0 > 0 || threadIdx.x != 0) return;
+    const int c1 = static_cast<int>(((s.first + s.nt) * G - 1) / W);
+    p.ws_cta[(static_cast<long long>(s.b) * p.c.Hkv + s.hk) * p.head_blocks + s.hb] =
+        make_int2(static_cast<int>(blockIdx.x), c1);
   }
 };
 
@@ -660,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
         l[n][i] = sum_over_g(l[n][i]);
         lx[n][i] = E4M3 ? l[n][i] : sum_over_g(lx[n][i]);
       }
+    walker.note(p, s);
     const Piece done = s;
     const bool more = walker.next(p, &s);
     if (more) begin();
@@ -919,6 +931,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
         if (g == 0) *reinterpret_cast<float4*>(&sh->acc[warp][h][4 * (t + 4 * u)]) = a;
       }
     }
+    walker.note(p, s);
     __syncthreads();
     for (int e = threadIdx.x; e < nh * DPAD; e += kThreads) {
       const int h = e / DPAD, d = e % DPAD;
@@ -951,91 +964,76 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
 
 // ------------------------------------------------------------------ the join
 // One block per (sequence, query head): outputs of the CTAs that share its
-// segment, weighted by their log-sum-exps.  Warp w takes every eighth of them
-// from the w-th, a lane four columns; the warps' sums are added in order.
-// Sequences without keys get the empty row (0, -inf).
-constexpr int kJoinWarps = 8;
+// segment, weighted by their log-sum-exps.  DPAD / 4 threads take a row of
+// partial output, the block several rows at once, which are added up in order
+// at the end.  Sequences without keys get the empty row (0, -inf).
+// (Latency: an empty kernel here costs 1 us, the chain lengths -> CTAs ->
+// partial outputs -> sum another 3 to 4; a block per segment, blocks of 64 to
+// 512 threads and a join by the last CTA of a segment to finish (counters
+// zeroed by a kernel in front) measured the same within 1 us, or slower where
+// a segment has many parts.)
+constexpr int kJoinThreads = 256;
 template <typename T, int DPAD>
-__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p, int hpb,
-                                                                      int tile) {
-  __shared__ float4 sums[kJoinWarps][32];
-  __shared__ float weight[kJoinWarps];
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeParams p, int hpb) {
+  constexpr int LPR = DPAD / 4, ROWS = kJoinThreads / LPR;  // threads of a row; rows at once
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ float2 stats[ROWS];  // maximum and weight
   const PagedCache& c = p.c;
   const int b = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = h / p.group, hb = (h - hk * p.group) / hpb, hi = (h - hk * p.group) % hpb;
   bool bad = false;
-  long long before = 0, total = 0;
-  for (int i = lane; i < c.B; i += 32) {
-    const int nt = tiles_of(clamp_len(c, __ldg(p.lens + i), &bad), tile);
-    total += nt;
-    if (i < b) before += nt;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (bad && blockIdx.x == 0) atomicOr(c.status, kStatusIndex);
+  const int len = clamp_len(c, __ldg(p.lens + b), &bad);
+  if (bad && h == 0 && threadIdx.x == 0) atomicOr(c.status, kStatusIndex);
   // This kernel may be placed while the attention kernel runs: from here on
   // that one is complete and its partial states are visible.  (Every block
   // waits, so that this kernel never ends before it.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  T* dst = static_cast<T*>(p.o) + b * p.so.b + h * p.so.h;
-  const int nt = tiles_of(clamp_len(c, __ldg(p.lens + b), &bad), tile);
-  if (nt == 0) {
-    for (int d = threadIdx.x; d < c.D; d += kJoinWarps * 32) dst[d] = Elem<T>::put(0.f);
-    if (threadIdx.x == 0 && p.lse) p.lse[static_cast<long long>(b) * p.H + h] = -INFINITY;
-    return;
-  }
-  const long long HH = static_cast<long long>(c.Hkv) * p.head_blocks;
-  const long long W = total * HH, G = min(static_cast<long long>(p.grid), W);
-  const int hk = h / p.group, hb = (h - hk * p.group) / hpb, hi = (h - hk * p.group) % hpb;
-  const long long first = before * HH + static_cast<long long>(hk * p.head_blocks + hb) * nt;
-  // CTA c holds tiles [W c / G, W (c + 1) / G): the one that holds tile x
-  const long long c0 = ((first + 1) * G - 1) / W, c1 = ((first + nt) * G - 1) / W;
-  if (c0 == c1) return;  // written by that CTA
-  // the first CTA's piece begins the segment (slot 1), the others' continue it
-  auto row = [&](long long cta) { return slot_row(p, cta, cta == c0 ? 1 : 0, hpb, hi); };
-  float M = -INFINITY;
-  for (long long cta = c0 + lane; cta <= c1; cta += 32) M = fmaxf(M, p.ws_lse[row(cta)]);
+  int2 ctas = make_int2(0, -1);
+  if (len > 0) ctas = p.ws_cta[(static_cast<long long>(b) * c.Hkv + hk) * p.head_blocks + hb];
+  if (ctas.x == ctas.y) return;  // written by that CTA
+  const int row = static_cast<int>(threadIdx.x) / LPR, d = 4 * (static_cast<int>(threadIdx.x) % LPR);
+  float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  auto merge = [&](float y, float weight, const float4& x) {
+    const float M_new = fmaxf(M, y), mu = M_new == -INFINITY ? 0.f : M_new;
+    const float a = exp2f(M - mu), w = exp2f(y - mu);
+    M = M_new;
+    L = L * a + weight * w;
+    acc[0] = fmaf(w, x.x, acc[0] * a), acc[1] = fmaf(w, x.y, acc[1] * a);
+    acc[2] = fmaf(w, x.z, acc[2] * a), acc[3] = fmaf(w, x.w, acc[3] * a);
+  };
+  constexpr int U = 4;  // rows in flight per thread
+  for (int cta = ctas.x + row; cta <= ctas.y; cta += U * ROWS) {
+    float y[U];
+    float4 x[U];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float mu = M == -INFINITY ? 0.f : M;
-  const bool on = 4 * lane < DPAD;
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (long long cta = c0 + warp; cta <= c1; cta += kJoinWarps) {
-    const long long r = row(cta);
-    const float w = exp2f(p.ws_lse[r] - mu);
-    // (columns past D of a row are not written: they are not used either)
-    const float4 x = on ? *reinterpret_cast<const float4*>(p.ws_o + r * DPAD + 4 * lane)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-    L += w;
-    acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y);
-    acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
-  }
-  sums[warp][lane] = acc;
-  if (lane == 0) weight[warp] = L;
-  __syncthreads();
-  if (warp == 0) {
-    L = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float4 x = sums[w][lane];
-      L += weight[w];
-      acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+    for (int u = 0; u < U; ++u) {
+      const int at = cta + u * ROWS;
+      y[u] = -INFINITY, x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (at <= ctas.y) {
+        // the first CTA's piece begins the segment (slot 1), the others' continue it
+        const long long r = slot_row(p, at, at == ctas.x ? 1 : 0, hpb, hi);
+        y[u] = p.ws_lse[r];
+        // (columns past D of a row are not written: they are not used either)
+        x[u] = *reinterpret_cast<const float4*>(p.ws_o + r * DPAD + d);
+      }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (4 * lane + k < c.D) dst[4 * lane + k] = Elem<T>::put(o[k]);
-    if (lane == 0 && p.lse)
-      p.lse[static_cast<long long>(b) * p.H + h] =
-          L == 0.f ? -INFINITY : (mu + log2f(L)) * 0.6931471805599453f;
+    for (int u = 0; u < U; ++u) merge(y[u], 1.f, x[u]);
   }
+  sums[threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  if (d == 0) stats[row] = make_float2(M, L);
+  __syncthreads();
+  if (row != 0) return;
+#pragma unroll
+  for (int i = 1; i < ROWS; ++i) merge(stats[i].x, stats[i].y, sums[threadIdx.x + i * LPR]);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  T* dst = static_cast<T*>(p.o) + b * p.so.b + h * p.so.h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (d + k < c.D) dst[d + k] = Elem<T>::put(acc[k] * inv);
+  if (d == 0 && p.lse)
+    p.lse[static_cast<long long>(b) * p.H + h] =
+        L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ launch
@@ -1087,17 +1085,17 @@ cudaError_t launch_typed(bool e4m3, bool tc, bool vec, const DecodeParams& p, cu
   // The join may be placed on the GPU while the attention kernel still runs
   // (programmatic dependent launch); it waits for it before it reads.
   cudaLaunchConfig_t cfg = {};
+  const int hpb = decode_heads_per_block(tc, p.c.D, p.group);
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.c.B) * p.H));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.grid > 0 ? 1 : 0;
-  const int hpb = decode_heads_per_block(tc, p.c.D, p.group), tile = decode_tile(tc, p.c.D, e4m3);
-  return wide ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, 128>, p, hpb, tile)
-              : cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, 64>, p, hpb, tile);
+  return wide ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, 128>, p, hpb)
+              : cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, 64>, p, hpb);
 }
 
 }  // namespace

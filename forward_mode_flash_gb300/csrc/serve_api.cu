@@ -152,7 +152,7 @@ jvp_status_t cache_rows(bool write, const jvp_cache_t* c, jvp_dtype_t dtype, int
 // CTAs of the single-token attention and the query heads each takes.
 struct DecodePlan {
   int heads_per_block = 0, head_blocks = 0, grid = 0, direct = 0;
-  size_t bytes = 0;
+  size_t bytes = 0, at_o = 0, at_cta = 0;  // workspace: lse, partial outputs, CTAs of segments
 };
 DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
   DecodePlan d;
@@ -173,7 +173,11 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
   }
   d.grid = static_cast<int>(std::min<int64_t>(wave, tiles ? (segments > wave ? wave : segments * tiles) : 0));
   const size_t slots = static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
-  d.bytes = ((slots * 4 + 255) & ~static_cast<size_t>(255)) + slots * (D > 64 ? 128 : 64) * 4;
+  if (d.grid > 0) {
+    d.at_o = (slots * 4 + 255) & ~static_cast<size_t>(255);
+    d.at_cta = d.at_o + slots * (D > 64 ? 128 : 64) * 4;
+    d.bytes = d.at_cta + static_cast<size_t>(segments) * 8;
+  }
   return d;
 }
 
@@ -396,9 +400,12 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
   if (!aligned_to(workspace, 16)) return api_fail(JVP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
   p.o_vec = aligned_to(o, 16) && multiple(p.so, 8);
   p.head_blocks = d.head_blocks, p.grid = d.grid, p.direct = d.direct;
-  const size_t slots = d.direct ? 0 : static_cast<size_t>(d.grid) * 2 * d.heads_per_block;
-  p.ws_lse = static_cast<float*>(workspace);
-  p.ws_o = p.ws_lse + ((slots * 4 + 255) & ~static_cast<size_t>(255)) / 4;
+  if (d.bytes > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.ws_lse = reinterpret_cast<float*>(ws);
+    p.ws_o = reinterpret_cast<float*>(ws + d.at_o);
+    p.ws_cta = reinterpret_cast<int2*>(ws + d.at_cta);
+  }
   const cudaError_t err = launch_decode(static_cast<DType>(dtype), e4m3, tc, vec, p,
                                         static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return api_cuda_fail(err);

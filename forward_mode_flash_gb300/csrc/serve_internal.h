@@ -60,6 +60,7 @@ struct DecodeParams {
   float scale_log2;    // logit scale * log2(e)
   float* ws_lse;       // [grid][2][heads_per_block]
   float* ws_o;         // [grid][2][heads_per_block][64 or 128]
+  int2* ws_cta;        // [B][Hkv][head_blocks] first and last CTA of a segment
   int o_vec;           // output rows are 16-byte aligned
 };
 

@@ -493,8 +493,8 @@ jvp_status_t jvp_attn_cache_read(const jvp_cache_t* cache, jvp_dtype_t dtype, in
  *                do not matter.  Calls that share one must not overlap.
  *
  * The keys of all sequences are split evenly over the GPU whatever their
- * lengths and joined by a second kernel, in an order that depends on the
- * lengths only (the same call gives the same bits).  Accumulation and softmax
+ * lengths, and the parts of one sequence are combined in an order that depends
+ * on the lengths only (the same call gives the same bits).  Accumulation and softmax
  * in fp32; fp16/bf16 queries with D a multiple of 8 (of 16 over e4m3),
  * 16-byte aligned cache rows and 8-byte aligned query rows use the tensor
  * cores with 16-bit weights, every other case CUDA cores in fp32.  Keys past
@@ -509,8 +509,9 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
                              size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of jvp_attn_decode on the current device: partial outputs of
- * at most one resident wave of CTAs, whatever the lengths (a few MiB); 0 for an
- * empty problem, an invalid description or no device. */
+ * at most one resident wave of CTAs, whatever the lengths (a few MiB), and 8
+ * bytes per sequence and block of heads; 0 for a block table so small that
+ * nothing is split, an empty problem, an invalid description or no device. */
 size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype);
 
 /*

@@ -475,3 +475,47 @@ def test_empty_problems():
     assert kc.eq(0).all()
     k, v = api.cache_read(kc, kc, i32([[0]]), None, i32([0, 0]), num_rows=0)
     assert k.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_split_decode_in_graphs_that_follow_the_lengths(e4m3):
+    """Long block tables, so that segments are split and combined: two captured
+    calls, replayed with other lengths, beside eager calls on another stream."""
+    B, most = 5, 9000
+    c = Cache([most] * B, 2, 64, 16, torch.bfloat16, e4m3, seed=13)
+    dev = c.cuda()
+    q = torch.randn(B, 4, 64, generator=torch.Generator().manual_seed(4)).bfloat16()
+    dq, dl = q.cuda(), i32([most] * B)
+
+    def call(lens, **kw):
+        return api.attention_decode(dq, dev["k_cache"], dev["v_cache"], dev["block_table"], lens,
+                                    k_scale=dev["k_scale"], v_scale=dev["v_scale"], return_lse=True, **kw)
+
+    want = {}
+    for lens in ([most, 0, 70, 1, 5000], [0, 0, 0, 0, most], [0] * 5, [most] * 5):
+        want[tuple(lens)] = call(i32(lens))
+        check_decode(c, q, *want[tuple(lens)], 0.125, True, lens=lens)
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(dl))
+        graphs.append(g)
+    fixed = i32([3000, 1, most, 0, 2])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        alone = call(fixed)
+    side.synchronize()
+    for lens, (o, lse) in want.items():
+        dl.copy_(i32(list(lens)))
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            with torch.cuda.stream(side):
+                o2, lse2 = call(fixed)
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, alone[0]) and torch.equal(lse2, alone[1])
+        for og, lg in outs:
+            assert torch.equal(og, o) and torch.equal(lg, lse)
