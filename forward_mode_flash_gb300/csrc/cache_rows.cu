@@ -12,16 +12,22 @@
 // Both directions are bound by memory: a row is read once and written once.
 // One warp takes one row (all heads of K and V), so its place in the cache
 // (a binary search in cu_seqlens and one block-table entry) is looked up once;
-// a group of lanes takes one head with 16 bytes per lane of the 16- or 32-bit
-// side, and the heads are unrolled so that several loads are in flight.
+// a group of lanes takes one head of K or V with 16 bytes per lane and access
+// of the 16- or 32-bit side, several heads at once so that their loads are in
+// flight together.  Writing e4m3 is near the issue rate too: the largest
+// magnitude of 16-bit rows is found on packed pairs (79 -> 67 us in the case
+// below) and a lane takes two pieces of a row where they fit (67 -> 56 us).
+// Measured, 56.8k rows of 12 sequences, 8 heads of 128, bf16 to and from e4m3:
+// 56 us written and 60 us read, 91 and 85 % of the copy rate over 350 MB.
 #include <cmath>
+#include <type_traits>
 
 #include "paged.cuh"
 
 namespace jvp {
 namespace {
 
-constexpr int kWarps = 8;  // rows per block
+constexpr int kWarps = 4;  // rows per block
 
 template <typename T>
 struct Rows;  // conversions of a row's element type
@@ -85,70 +91,164 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// ------------------------------------------------------------------ writing
-// VEC elements of type T are 16 bytes; D is a multiple of VEC.
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32, 4) cache_write_vec(const CacheRowsParams p, int lanes) {
+// Largest magnitude of a group of LANES lanes' PC 16-byte pieces of a row (NaN
+// not counted).
+template <int LANES, int PC>
+__device__ __forceinline__ float group_top(const float*, const uint4 (&x)[PC]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < PC; ++i)
+    top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(x[i].x)), fabsf(__uint_as_float(x[i].y))),
+                           fmaxf(fabsf(__uint_as_float(x[i].z)), fabsf(__uint_as_float(x[i].w)))));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top;
+}
+template <typename T2>
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+  const T2 m = __hmax2(*reinterpret_cast<const T2*>(&a), *reinterpret_cast<const T2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+template <typename T2, int LANES, int PC>
+__device__ __forceinline__ uint32_t packed_top(const uint4 (&x)[PC]) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < PC; ++i) {
+    m = pair_max<T2>(pair_max<T2>(m, x[i].x & kAbs), x[i].y & kAbs);
+    m = pair_max<T2>(m, pair_max<T2>(x[i].z & kAbs, x[i].w & kAbs));
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    m = pair_max<T2>(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return pair_max<T2>(m, m >> 16);  // low half
+}
+template <int LANES, int PC>
+__device__ __forceinline__ float group_top(const __half*, const uint4 (&x)[PC]) {
+  const uint32_t m = packed_top<__half2, LANES>(x);
+  return __low2float(*reinterpret_cast<const __half2*>(&m));
+}
+template <int LANES, int PC>
+__device__ __forceinline__ float group_top(const __nv_bfloat16*, const uint4 (&x)[PC]) {
+  return __uint_as_float(packed_top<__nv_bfloat162, LANES>(x) << 16);
+}
+
+// Codes of 16 bytes of a row (4 or 8 of them).
+template <typename T>
+__device__ __forceinline__ void encode(const uint4& x, float inv, uint32_t (&c)[4 / sizeof(T)]) {
+  const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(16 / sizeof(T)); i += 4)
+    c[i / 4] = to_e4m3x2(Rows<T>::get(e[i]) * inv, Rows<T>::get(e[i + 1]) * inv) |
+               (static_cast<uint32_t>(to_e4m3x2(Rows<T>::get(e[i + 2]) * inv,
+                                                Rows<T>::get(e[i + 3]) * inv))
+                << 16);
+}
+// 16 bytes of a row from their codes.
+template <typename T>
+__device__ __forceinline__ uint4 decode(const uint32_t (&c)[4 / sizeof(T)], float s) {
   constexpr int VEC = 16 / sizeof(T);
+  uint4 x;
+  T* e = reinterpret_cast<T*>(&x);
+#pragma unroll
+  for (int i = 0; i < VEC; i += 4) {
+    uint32_t h2[2];
+    e4m3x4_to_half2x2(c[i / 4], h2[0], h2[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[k]));
+      e[i + 2 * k] = Rows<T>::put(f.x * s);
+      e[i + 2 * k + 1] = Rows<T>::put(f.y * s);
+    }
+  }
+  return x;
+}
+// W 32-bit words of codes at a time, as one access.
+template <int W>
+__device__ __forceinline__ void put_words(uint8_t* dst, const uint32_t (&c)[W]) {
+  if constexpr (W == 1) *reinterpret_cast<uint32_t*>(dst) = c[0];
+  else if constexpr (W == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+  else *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
+}
+template <int W>
+__device__ __forceinline__ void get_words(const uint8_t* src, uint32_t (&c)[W]) {
+  if constexpr (W == 1) {
+    c[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  } else if constexpr (W == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+    c[0] = x.x, c[1] = x.y;
+  } else {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+    c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+  }
+}
+
+// What a lane group works on: rows of K heads 0 .. Hkv - 1, then of V heads.
+struct HeadRow {
+  int h;
+  bool v, on;
+};
+__device__ __forceinline__ HeadRow head_row(const PagedCache& c, int i, bool in_row) {
+  HeadRow r;
+  r.v = i >= c.Hkv;
+  r.h = r.v ? i - c.Hkv : i;
+  r.on = i < 2 * c.Hkv && in_row;
+  return r;
+}
+
+// ------------------------------------------------------------------ writing
+// A lane takes PC pieces of 16 bytes (D is a multiple of that many elements),
+// LANES lanes a row: the power of two that covers it (4 at least).
+template <typename T, bool E4M3, int LANES, int PC>
+__global__ void __launch_bounds__(kWarps * 32, 12) cache_write_vec(const CacheRowsParams p) {
+  constexpr int VEC = 16 / sizeof(T), EL = VEC * PC;  // elements of a piece, of a lane
+  using C = typename std::conditional<E4M3, uint8_t, T>::type;
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= p.T) return;
   int page, row;
   if (!locate(p, r, &page, &row)) return;
-  // group of `lanes` lanes (a power of two) per head, 32 / lanes heads at once
-  const int per = 32 / lanes, sub = lane / lanes, dl = (lane & (lanes - 1)) * VEC;
+  constexpr int per = 32 / LANES;  // heads at once
+  const int sub = lane / LANES, dl = lane % LANES * EL;
   const bool in_row = dl < p.c.D;
-  constexpr int UN = E4M3 ? 2 : 4;  // heads of one lane group in flight, for K and V each
-  for (int h0 = 0; h0 < p.c.Hkv; h0 += per * UN) {
-    uint4 x[2][UN];
+  const T* const ks = static_cast<const T*>(p.k) + r * p.srk.n + dl;
+  const T* const vs = static_cast<const T*>(p.v) + r * p.srv.n + dl;
+  C* const kd = static_cast<C*>(p.c.k) + page * p.c.sk.b + row * p.c.sk.n + dl;
+  C* const vd = static_cast<C*>(p.c.v) + page * p.c.sv.b + row * p.c.sv.n + dl;
+  const long long scale_at = static_cast<long long>(page) * p.c.Hkv * p.c.page_size + row;
+  constexpr int UN = 4 / PC;  // heads of one lane group in flight
+  for (int i0 = 0; i0 < 2 * p.c.Hkv; i0 += per * UN) {
+    uint4 x[UN][PC];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int h = h0 + u * per + sub;
-      const bool on = h < p.c.Hkv && in_row;
-      const T* ks = static_cast<const T*>(p.k) + r * p.srk.n + h * p.srk.h + dl;
-      const T* vs = static_cast<const T*>(p.v) + r * p.srv.n + h * p.srv.h + dl;
-      x[0][u] = on ? __ldg(reinterpret_cast<const uint4*>(ks)) : make_uint4(0, 0, 0, 0);
-      x[1][u] = on ? __ldg(reinterpret_cast<const uint4*>(vs)) : make_uint4(0, 0, 0, 0);
+      const HeadRow at = head_row(p.c, i0 + u * per + sub, in_row);
+      const T* src = at.v ? vs + at.h * p.srv.h : ks + at.h * p.srk.h;
+#pragma unroll
+      for (int i = 0; i < PC; ++i)
+        x[u][i] = at.on ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      if (h0 + u * per >= p.c.Hkv) break;  // uniform over the warp
-      const int h = h0 + u * per + sub;
-      const bool on = h < p.c.Hkv && in_row;
+      if (i0 + u * per >= 2 * p.c.Hkv) break;  // uniform over the warp
+      const HeadRow at = head_row(p.c, i0 + u * per + sub, in_row);
+      C* dst = at.v ? vd + at.h * p.c.sv.h : kd + at.h * p.c.sk.h;
+      if constexpr (!E4M3) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const Strides& sc = w ? p.c.sv : p.c.sk;
-        const long long at = page * sc.b + h * sc.h + row * sc.n + dl;
-        void* cache = w ? p.c.v : p.c.k;
-        if constexpr (!E4M3) {
-          if (on) *reinterpret_cast<uint4*>(static_cast<T*>(cache) + at) = x[w][u];
-        } else {
-          const T* e = reinterpret_cast<const T*>(&x[w][u]);
-          float f[VEC], top = 0.f;
+        for (int i = 0; i < PC; ++i)
+          if (at.on) reinterpret_cast<uint4*>(dst)[i] = x[u][i];
+      } else {
+        const unsigned sb = scale_byte(group_top<LANES>(ks, x[u]));
+        const float inv = __uint_as_float((254u - sb) << 23);  // 2^-e, e = sb - 127
+        constexpr int W = 4 / sizeof(T);
+        uint32_t c[PC * W];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            f[i] = Rows<T>::get(e[i]);
-            top = fmaxf(top, fabsf(f[i]));
-          }
-          for (int o = lanes >> 1; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const unsigned sb = scale_byte(top);
-          const float inv = __uint_as_float((254u - sb) << 23);  // 2^-e, e = sb - 127
-          if (on) {
-            uint32_t c[VEC / 4];
-#pragma unroll
-            for (int i = 0; i < VEC; i += 4)
-              c[i / 4] = to_e4m3x2(f[i] * inv, f[i + 1] * inv) |
-                         (static_cast<uint32_t>(to_e4m3x2(f[i + 2] * inv, f[i + 3] * inv)) << 16);
-            uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-            if constexpr (VEC == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
-            else *reinterpret_cast<uint32_t*>(dst) = c[0];
-            if (dl == 0) {
-              uint8_t* scale = w ? p.c.v_scale : p.c.k_scale;
-              scale[(static_cast<long long>(page) * p.c.Hkv + h) * p.c.page_size + row] =
-                  static_cast<uint8_t>(sb);
-            }
-          }
+        for (int i = 0; i < PC; ++i)
+          encode<T>(x[u][i], inv, *reinterpret_cast<uint32_t(*)[W]>(&c[i * W]));
+        if (at.on) {
+          put_words(dst, c);
+          if (dl == 0)
+            (at.v ? p.c.v_scale : p.c.k_scale)[scale_at + at.h * p.c.page_size] =
+                static_cast<uint8_t>(sb);
         }
       }
     }
@@ -190,71 +290,46 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_any(const CacheRowsPa
 }
 
 // ------------------------------------------------------------------ reading
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) cache_read_vec(const CacheRowsParams p, int lanes) {
+template <typename T, bool E4M3, int LANES>
+__global__ void __launch_bounds__(kWarps * 32) cache_read_vec(const CacheRowsParams p) {
   constexpr int VEC = 16 / sizeof(T);
+  using C = typename std::conditional<E4M3, uint8_t, T>::type;
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= p.T) return;
   int page, row;
   if (!locate(p, r, &page, &row)) return;
-  const int per = 32 / lanes, sub = lane / lanes, dl = (lane & (lanes - 1)) * VEC;
+  constexpr int per = 32 / LANES;
+  const int sub = lane / LANES, dl = lane % LANES * VEC;
   const bool in_row = dl < p.c.D;
+  const C* const ks = static_cast<const C*>(p.c.k) + page * p.c.sk.b + row * p.c.sk.n + dl;
+  const C* const vs = static_cast<const C*>(p.c.v) + page * p.c.sv.b + row * p.c.sv.n + dl;
+  T* const kd = const_cast<T*>(static_cast<const T*>(p.k)) + r * p.srk.n + dl;
+  T* const vd = const_cast<T*>(static_cast<const T*>(p.v)) + r * p.srv.n + dl;
+  const long long scale_at = static_cast<long long>(page) * p.c.Hkv * p.c.page_size + row;
   constexpr int UN = 4;
-  for (int h0 = 0; h0 < p.c.Hkv; h0 += per * UN) {
-    uint4 x[2][UN];
-    unsigned sb[2][UN];
+  constexpr int W = (E4M3 ? 4 : 16) / (E4M3 ? sizeof(T) : 4);  // 32-bit words of a lane's part
+  for (int i0 = 0; i0 < 2 * p.c.Hkv; i0 += per * UN) {
+    uint32_t x[UN][W];
+    unsigned sb[UN];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int h = h0 + u * per + sub;
-      const bool on = h < p.c.Hkv && in_row;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const Strides& sc = w ? p.c.sv : p.c.sk;
-        const void* cache = w ? p.c.v : p.c.k;
-        const long long at = page * sc.b + h * sc.h + row * sc.n + dl;
-        x[w][u] = make_uint4(0, 0, 0, 0);
-        if (on) {
-          if constexpr (!E4M3) {
-            x[w][u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(cache) + at));
-          } else {
-            const uint8_t* src = static_cast<const uint8_t*>(cache) + at;
-            if constexpr (VEC == 8) {
-              const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
-              x[w][u].x = c.x, x[w][u].y = c.y;
-            } else {
-              x[w][u].x = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
-            sb[w][u] = __ldg((w ? p.c.v_scale : p.c.k_scale) +
-                             (static_cast<long long>(page) * p.c.Hkv + h) * p.c.page_size + row);
-          }
-        }
-      }
+      const HeadRow at = head_row(p.c, i0 + u * per + sub, in_row);
+      if (!at.on) continue;
+      const C* src = at.v ? vs + at.h * p.c.sv.h : ks + at.h * p.c.sk.h;
+      get_words(reinterpret_cast<const uint8_t*>(src), x[u]);
+      if constexpr (E4M3)
+        sb[u] = __ldg((at.v ? p.c.v_scale : p.c.k_scale) + scale_at + at.h * p.c.page_size);
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int h = h0 + u * per + sub;
-      if (h >= p.c.Hkv || !in_row) continue;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const Strides& sr = w ? p.srv : p.srk;
-        T* dst = const_cast<T*>(static_cast<const T*>(w ? p.v : p.k)) + r * sr.n + h * sr.h + dl;
-        if constexpr (E4M3) {
-          const float s = scale_value(sb[w][u]);
-          const uint32_t c[2] = {x[w][u].x, x[w][u].y};
-          T e[VEC];
-#pragma unroll
-          for (int i = 0; i < VEC; i += 2) {
-            const uint32_t h2 = e4m3x2_to_half2((c[i / 4] >> (8 * (i & 2))) & 0xFFFFu);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-            e[i] = Rows<T>::put(f.x * s);
-            e[i + 1] = Rows<T>::put(f.y * s);
-          }
-          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(e);
-        } else {
-          *reinterpret_cast<uint4*>(dst) = x[w][u];
-        }
-      }
+      const HeadRow at = head_row(p.c, i0 + u * per + sub, in_row);
+      if (!at.on) continue;
+      T* dst = at.v ? vd + at.h * p.srv.h : kd + at.h * p.srk.h;
+      if constexpr (E4M3)
+        *reinterpret_cast<uint4*>(dst) = decode<T>(x[u], scale_value(sb[u]));
+      else
+        *reinterpret_cast<uint4*>(dst) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
     }
   }
 }
@@ -288,17 +363,31 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_any(const CacheRowsPar
   }
 }
 
+template <typename T, bool E4M3, bool WRITE, int LANES, int PC>
+void launch_vec(unsigned grid, const CacheRowsParams& p, cudaStream_t stream) {
+  if constexpr (LANES * PC < (sizeof(T) == 4 ? 32 : 16)) {  // D <= 128
+    if (p.c.D > LANES * PC * static_cast<int>(16 / sizeof(T)))
+      return launch_vec<T, E4M3, WRITE, LANES * 2, PC>(grid, p, stream);
+  }
+  if constexpr (WRITE) cache_write_vec<T, E4M3, LANES, PC><<<grid, kWarps * 32, 0, stream>>>(p);
+  else cache_read_vec<T, E4M3, LANES><<<grid, kWarps * 32, 0, stream>>>(p);
+}
+
 template <typename T, bool E4M3, bool WRITE>
 cudaError_t launch(const CacheRowsParams& p, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((p.T + kWarps - 1) / kWarps);
   if (p.vec) {
-    const int need = p.c.D / static_cast<int>(16 / sizeof(T));
-    int lanes = 1;
-    while (lanes < need) lanes *= 2;
-    if (WRITE) cache_write_vec<T, E4M3><<<grid, kWarps * 32, 0, stream>>>(p, lanes);
-    else cache_read_vec<T, E4M3><<<grid, kWarps * 32, 0, stream>>>(p, lanes);
+    // Two pieces a lane where the cost is instructions, in writing e4m3 rows,
+    // and they fit; reading them that way took 67.7 us against 60.7.
+    if constexpr (WRITE && E4M3) {
+      if (p.vec == 2) {
+        launch_vec<T, E4M3, WRITE, 4, 2>(grid, p, stream);
+        return cudaGetLastError();
+      }
+    }
+    launch_vec<T, E4M3, WRITE, 4, 1>(grid, p, stream);
   } else {
-    if (WRITE) cache_write_any<T, E4M3><<<grid, kWarps * 32, 0, stream>>>(p);
+    if constexpr (WRITE) cache_write_any<T, E4M3><<<grid, kWarps * 32, 0, stream>>>(p);
     else cache_read_any<T, E4M3><<<grid, kWarps * 32, 0, stream>>>(p);
   }
   return cudaGetLastError();

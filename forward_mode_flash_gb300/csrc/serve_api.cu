@@ -135,11 +135,18 @@ jvp_status_t cache_rows(bool write, const jvp_cache_t* c, jvp_dtype_t dtype, int
   p.cu = cu, p.start = start;
   p.k = k, p.v = v;
   p.srk = used(strides[0], 0, c->Hkv, T), p.srv = used(strides[1], 0, c->Hkv, T);
-  // 16 bytes of packed rows per access, and the same elements of the cache
-  const int64_t vec = 16 / e, ce = elem_bytes(c->dtype);
-  p.vec = c->D % vec == 0 && aligned_to(k, 16) && aligned_to(v, 16) && multiple(p.srk, vec) &&
-          multiple(p.srv, vec) && aligned_to(kc, vec * ce) && aligned_to(vc, vec * ce) &&
-          multiple(p.c.sk, vec) && multiple(p.c.sv, vec);
+  // 16 bytes of packed rows per access and the same elements of the cache, or
+  // (an e4m3 cache) two such pieces per lane and their elements of the cache
+  const int64_t ce = elem_bytes(c->dtype);
+  auto fits = [&](int64_t el) {
+    return c->D % el == 0 && aligned_to(kc, el * ce) && aligned_to(vc, el * ce) &&
+           multiple(p.c.sk, el) && multiple(p.c.sv, el);
+  };
+  const int64_t vec = 16 / e;
+  p.vec = aligned_to(k, 16) && aligned_to(v, 16) && multiple(p.srk, vec) && multiple(p.srv, vec) &&
+                  fits(vec)
+              ? (ce == 1 && fits(2 * vec) ? 2 : 1)
+              : 0;
   const bool e4m3 = c->dtype == JVP_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t err = write ? launch_cache_write(static_cast<DType>(dtype), e4m3, p, s)
