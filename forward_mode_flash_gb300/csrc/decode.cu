@@ -778,38 +778,65 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 }
 
 // ------------------------------------------------------------------ CUDA cores
-// Any type and alignment: fp32 arithmetic.  Four lanes share a key (lane t
-// takes the columns 4 (t + 4 i) .. + 3), a warp's 16 keys go in two rounds of
-// eight, and a CTA takes HPB query heads, each lane summing its own keys'
-// weighted values until the end of the piece.
+// Any type and alignment: fp32 arithmetic.  DPAD / 16 lanes share a key (lane t
+// of them takes the columns 4 (t + LK u) .. + 3), so a warp takes 8 or 4 keys at
+// once; it loads the next ones' rows before it works on these.  A CTA takes HPB
+// query heads, each lane summing its own keys' weighted values until the end of
+// the piece.  Measured, fp32 caches: 60000 keys of 8 ungrouped heads of 128 in
+// 78 us, 92 % of the copy rate (four CTAs per SM; three: 90 %); 16 sequences of
+// 500 to 4000 keys, 8 heads on 2 of 128, 28 us, 46 % (three; four, of 128
+// registers a thread: 36 us): grouped heads are bound by the arithmetic.
+template <typename T>
+struct Raw {  // four columns as stored
+  uint32_t w[sizeof(T)];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ float4 load4(const T* row, int d, int D) {
-  float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+__device__ __forceinline__ Raw<T> load4(const T* row, int d, int D) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) r.w[i] = 0u;
   if constexpr (VEC) {
     if (d < D) {
       if constexpr (sizeof(T) == 4) {
-        f = __ldg(reinterpret_cast<const float4*>(row + d));
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + d));
+        r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
       } else if constexpr (sizeof(T) == 2) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + d));
-        const float2 a = unpack2(w.x, Elem<T>::kBF16), b = unpack2(w.y, Elem<T>::kBF16);
-        f = make_float4(a.x, a.y, b.x, b.y);
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + d));
+        r.w[0] = x.x, r.w[1] = x.y;
       } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row + d));
-        const uint32_t a = e4m3x2_to_half2(w & 0xFFFFu), b = e4m3x2_to_half2(w >> 16);
-        const float2 fa = unpack2(a, false), fb = unpack2(b, false);
-        f = make_float4(fa.x, fa.y, fb.x, fb.y);
+        r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + d));
       }
     }
   } else {
-    float* e = &f.x;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (d + i < D) {
-        if constexpr (sizeof(T) == 1) e[i] = unpack2(e4m3x2_to_half2(row[d + i]), false).x;
-        else e[i] = Elem<T>::get(row[d + i]);
+        if constexpr (sizeof(T) == 4)
+          r.w[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + d + i);
+        else if constexpr (sizeof(T) == 2)
+          r.w[i / 2] |= static_cast<uint32_t>(
+                            __ldg(reinterpret_cast<const unsigned short*>(row) + d + i))
+                        << (16 * (i & 1));
+        else
+          r.w[0] |= static_cast<uint32_t>(__ldg(row + d + i)) << (8 * i);
       }
   }
-  return f;
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float4 value4(const Raw<T>& r) {
+  if constexpr (sizeof(T) == 4) {
+    return make_float4(__uint_as_float(r.w[0]), __uint_as_float(r.w[1]), __uint_as_float(r.w[2]),
+                       __uint_as_float(r.w[3]));
+  } else if constexpr (sizeof(T) == 2) {
+    const float2 a = unpack2(r.w[0], Elem<T>::kBF16), b = unpack2(r.w[1], Elem<T>::kBF16);
+    return make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    uint32_t a, b;
+    e4m3x4_to_half2x2(r.w[0], a, b);
+    const float2 fa = unpack2(a, false), fb = unpack2(b, false);
+    return make_float4(fa.x, fa.y, fb.x, fb.y);
+  }
 }
 
 template <int HPB, int DPAD>
@@ -821,18 +848,26 @@ struct SimtShared {
 };
 
 template <typename TQ, int DPAD, bool E4M3, int HPB, bool VEC>
-__global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParams p) {
-  constexpr int NC = DPAD / 16;  // 4-column pieces per lane
-  constexpr int TILE = kDecodeSimtTile, KT = TILE / kWarps;
-  static_assert(KT == 16, "a warp takes two rounds of eight keys");
+__global__ void __launch_bounds__(kThreads, decode_simt_ctas_per_sm(HPB))
+decode_simt_kernel(const DecodeParams p) {
+  constexpr int LK = DPAD / 16, NC = 4, KR = 32 / LK;  // lanes of a key, pieces of a lane, keys
+  constexpr int TILE = kDecodeSimtTile, KT = TILE / kWarps, R = KT / KR;
+  static_assert(KT == 16 && R * KR == KT, "rounds of a warp's part of a tile");
   extern __shared__ __align__(128) uint8_t smem_raw[];
   auto* sh = reinterpret_cast<SimtShared<HPB, DPAD>*>(smem_raw);
   const PagedCache& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / LK, t = lane % LK;
   const int D = c.D;
   using TC = typename std::conditional<E4M3, uint8_t, TQ>::type;
   const TC* kc = static_cast<const TC*>(c.k);
   const TC* vc = static_cast<const TC*>(c.v);
+  auto over_keys = [&](float x, auto op) {  // over the lanes with this t
+#pragma unroll
+    for (int o = LK; o < 32; o <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  };
+  auto add = [](float x, float y) { return x + y; };
+  auto larger = [](float x, float y) { return fmaxf(x, y); };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walker<TILE> walker;
@@ -857,78 +892,107 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(const DecodeParam
 #pragma unroll
       for (int u = 0; u < NC; ++u) acc[h][u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int tile = s.t0; tile < s.t1; ++tile) {
-      const int j0 = tile * TILE + warp * KT;
-      if (j0 >= s.len) break;
+    // Rounds i of the piece: a key's page is looked up a round before its rows
+    // are asked for, its K row during the second half of the round before (when
+    // the last one's scores are formed), its V row at the end of that round.
+    const int rounds = (s.t1 - s.t0) * R;
+    long long ko = 0, vo = 0, so = 0;  // of the next round's key
+    bool next_on = false;
+    auto look_up = [&](int i) {
+      next_on = false;
+      if (i >= rounds) return;
+      const int j = (s.t0 + i / R) * TILE + warp * KT + (i % R) * KR + g;
+      if (j >= s.len) return;
+      int entry, row;
+      split_position(c, j, &entry, &row);
+      const int page = page_of(c, s.b, entry);
+      if (page < 0) return;
+      next_on = true;
+      ko = page * c.sk.b + s.hk * c.sk.h + row * c.sk.n;
+      vo = page * c.sv.b + s.hk * c.sv.h + row * c.sv.n;
+      if (E4M3) so = (static_cast<long long>(page) * c.Hkv + s.hk) * c.page_size + row;
+    };
+    Raw<TC> k[NC], v[NC];
+    unsigned ke = 127u, ve = 127u;
+    auto fetch = [&](Raw<TC>(&x)[NC], const TC* row, const uint8_t* scale, unsigned* byte) {
+      const int width = next_on ? D : 0;
+#pragma unroll
+      for (int u = 0; u < NC; ++u) x[u] = load4<TC, VEC>(row, 4 * (t + LK * u), width);
+      if (E4M3) *byte = next_on ? __ldg(scale + so) : 127u;
+    };
+    look_up(0);
+    fetch(k, kc + ko, c.k_scale, &ke);
+    fetch(v, vc + vo, c.v_scale, &ve);
+    bool on = next_on;
+    look_up(1);
 #pragma unroll 1
-      for (int r = 0; r < 2; ++r) {
-        const int j = j0 + 8 * r + g;
-        bool on = j < s.len;
-        long long ko = 0, vo = 0, so = 0;
-        if (on) {
-          int entry, row;
-          split_position(c, j, &entry, &row);
-          const int page = page_of(c, s.b, entry);
-          on = page >= 0;
-          if (on) {
-            ko = page * c.sk.b + s.hk * c.sk.h + row * c.sk.n;
-            vo = page * c.sv.b + s.hk * c.sv.h + row * c.sv.n;
-            so = (static_cast<long long>(page) * c.Hkv + s.hk) * c.page_size + row;
-          }
-        }
-        float4 x[NC];
+    for (int i = 0; i < rounds; ++i) {
+      float w[HPB];
+      bool need = false;
+      const float ks = E4M3 ? p.scale_log2 * scale_value(ke) : p.scale_log2;
 #pragma unroll
-        for (int u = 0; u < NC; ++u)
-          x[u] = on ? load4<TC, VEC>(kc + ko, 4 * (t + 4 * u), D) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float ks = p.scale_log2, vs = 1.f;
-        if (E4M3 && on) {
-          ks *= scale_value(__ldg(c.k_scale + so));
-          vs = scale_value(__ldg(c.v_scale + so));
-        }
-        float w[HPB];
+      for (int h = 0; h < HPB; ++h) w[h] = 0.f;
+#pragma unroll
+      for (int u = 0; u < NC; ++u) {
+        const float4 x = value4<TC>(k[u]);
 #pragma unroll
         for (int h = 0; h < HPB; ++h) {
-          float dot = 0.f;
-#pragma unroll
-          for (int u = 0; u < NC; ++u) {
-            const float4 q = *reinterpret_cast<const float4*>(&sh->q[h][4 * (t + 4 * u)]);
-            dot = fmaf(x[u].x, q.x, fmaf(x[u].y, q.y, fmaf(x[u].z, q.z, fmaf(x[u].w, q.w, dot))));
-          }
-          dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-          dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-          w[h] = on ? dot * ks : -INFINITY;
-        }
-#pragma unroll
-        for (int u = 0; u < NC; ++u)
-          x[u] = on ? load4<TC, VEC>(vc + vo, 4 * (t + 4 * u), D) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int h = 0; h < HPB; ++h) {
-          const float m_new = fmaxf(m[h], max_over_g(w[h]));
-          const float mu = m_new == -INFINITY ? 0.f : m_new;
-          const float a = exp2f(m[h] - mu);
-          const float e = exp2f(w[h] - mu);
-          m[h] = m_new;
-          l[h] = l[h] * a + e;
-          const float ev = e * vs;
-#pragma unroll
-          for (int u = 0; u < NC; ++u) {
-            acc[h][u].x = fmaf(ev, x[u].x, acc[h][u].x * a);
-            acc[h][u].y = fmaf(ev, x[u].y, acc[h][u].y * a);
-            acc[h][u].z = fmaf(ev, x[u].z, acc[h][u].z * a);
-            acc[h][u].w = fmaf(ev, x[u].w, acc[h][u].w * a);
-          }
+          const float4 q = *reinterpret_cast<const float4*>(&sh->q[h][4 * (t + LK * u)]);
+          w[h] = fmaf(x.x, q.x, fmaf(x.y, q.y, fmaf(x.z, q.z, fmaf(x.w, q.w, w[h]))));
         }
       }
+      fetch(k, kc + ko, c.k_scale, &ke);
+#pragma unroll
+      for (int h = 0; h < HPB; ++h) {
+#pragma unroll
+        for (int o = 1; o < LK; o <<= 1) w[h] += __shfl_xor_sync(0xffffffffu, w[h], o);
+        w[h] = on ? w[h] * ks : -INFINITY;
+        need |= w[h] > m[h] + 8.f;
+      }
+      if (__any_sync(0xffffffffu, need)) {  // (as on the tensor cores)
+#pragma unroll
+        for (int h = 0; h < HPB; ++h) {
+          const float m_new = fmaxf(m[h], over_keys(w[h], larger));
+          const float a = m_new == m[h] ? 1.f : exp2f(m[h] - m_new);
+          m[h] = m_new;
+          l[h] *= a;
+#pragma unroll
+          for (int u = 0; u < NC; ++u)
+            acc[h][u].x *= a, acc[h][u].y *= a, acc[h][u].z *= a, acc[h][u].w *= a;
+        }
+      }
+      const float vs = E4M3 ? scale_value(ve) : 1.f;
+#pragma unroll
+      for (int h = 0; h < HPB; ++h) {
+        w[h] = exp2f(w[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+        l[h] += w[h];
+        if (E4M3) w[h] *= vs;
+      }
+#pragma unroll
+      for (int u = 0; u < NC; ++u) {
+        const float4 x = value4<TC>(v[u]);
+#pragma unroll
+        for (int h = 0; h < HPB; ++h) {
+          acc[h][u].x = fmaf(w[h], x.x, acc[h][u].x);
+          acc[h][u].y = fmaf(w[h], x.y, acc[h][u].y);
+          acc[h][u].z = fmaf(w[h], x.z, acc[h][u].z);
+          acc[h][u].w = fmaf(w[h], x.w, acc[h][u].w);
+        }
+      }
+      fetch(v, vc + vo, c.v_scale, &ve);
+      on = next_on;
+      look_up(i + 2);
     }
 #pragma unroll
     for (int h = 0; h < HPB; ++h) {
-      const float ls = sum_over_g(l[h]);
+      const float ls = over_keys(l[h], add);
       if (lane == 0) sh->m[warp][h] = m[h], sh->l[warp][h] = ls;
 #pragma unroll
       for (int u = 0; u < NC; ++u) {
-        const float4 a = make_float4(sum_over_g(acc[h][u].x), sum_over_g(acc[h][u].y),
-                                     sum_over_g(acc[h][u].z), sum_over_g(acc[h][u].w));
-        if (g == 0) *reinterpret_cast<float4*>(&sh->acc[warp][h][4 * (t + 4 * u)]) = a;
+        const float4 a =
+            make_float4(over_keys(acc[h][u].x, add), over_keys(acc[h][u].y, add),
+                        over_keys(acc[h][u].z, add), over_keys(acc[h][u].w, add));
+        if (g == 0) *reinterpret_cast<float4*>(&sh->acc[warp][h][4 * (t + LK * u)]) = a;
       }
     }
     walker.note(p, s);
@@ -1053,9 +1117,8 @@ cudaError_t launch_tc(const DecodeParams& p, cudaStream_t stream) {
   static_assert(decode_ctas_per_sm(DPAD, NG, E4M3) * (bytes + 1024) <= 228 * 1024, "resident CTAs");
   return launch_with_smem(decode_tc_kernel<TQ, DPAD, E4M3, NG>, bytes, p, stream);
 }
-template <typename TQ, int DPAD, bool E4M3>
+template <typename TQ, int DPAD, bool E4M3, int HPB>
 cudaError_t launch_simt(bool vec, const DecodeParams& p, cudaStream_t stream) {
-  constexpr int HPB = DPAD > 64 ? 2 : 4;
   constexpr int bytes = sizeof(SimtShared<HPB, DPAD>);
   return vec ? launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, true>, bytes, p, stream)
              : launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, false>, bytes, p, stream);
@@ -1068,7 +1131,8 @@ cudaError_t launch_attention(bool tc, bool vec, const DecodeParams& p, cudaStrea
       return p.group > 8 ? launch_tc<TQ, DPAD, E4M3, 2>(p, stream)
                          : launch_tc<TQ, DPAD, E4M3, 1>(p, stream);
   }
-  return launch_simt<TQ, DPAD, E4M3>(vec, p, stream);
+  return p.group == 1 ? launch_simt<TQ, DPAD, E4M3, 1>(vec, p, stream)
+                      : launch_simt<TQ, DPAD, E4M3, 4>(vec, p, stream);
 }
 
 template <typename TQ>
@@ -1085,7 +1149,7 @@ cudaError_t launch_typed(bool e4m3, bool tc, bool vec, const DecodeParams& p, cu
   // The join may be placed on the GPU while the attention kernel still runs
   // (programmatic dependent launch); it waits for it before it reads.
   cudaLaunchConfig_t cfg = {};
-  const int hpb = decode_heads_per_block(tc, p.c.D, p.group);
+  const int hpb = decode_heads_per_block(tc, p.group);
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.c.B) * p.H));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;

@@ -44,7 +44,7 @@ jvp_status_t check_cache(const jvp_cache_t* c, bool written) {
   if (c->pages > kMax || c->Hkv > kMax || c->B > kMax || c->max_pages > kMax ||
       c->page_size > kMax || c->max_pages * c->page_size > kMax)
     return api_fail(JVP_ERR_UNSUPPORTED,
-                    "a size of the cache, or max_pages * page_size, exceeds 2^31 - 1");
+                    "a size of the cache exceeds 2^31 - 1");
   if (c->B > 1 && c->table_stride < c->max_pages)
     return api_fail(JVP_ERR_INVALID_ARG, "table_stride is less than max_pages");
   for (const jvp_strides_t* s : {&c->k_strides, &c->v_strides}) {
@@ -164,12 +164,13 @@ struct DecodePlan {
 DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
   DecodePlan d;
   const int D = static_cast<int>(c->D), group = static_cast<int>(H / c->Hkv);
-  d.heads_per_block = decode_heads_per_block(tc, D, group);
+  d.heads_per_block = decode_heads_per_block(tc, group);
   d.head_blocks = (group + d.heads_per_block - 1) / d.heads_per_block;
   const int64_t most = c->max_pages * c->page_size;
   const int64_t wave =
       static_cast<int64_t>(num_sms) *
-      (tc ? decode_ctas_per_sm(D, d.heads_per_block / 8, c->dtype == JVP_E4M3) : kDecodeSimtCtasPerSm);
+      (tc ? decode_ctas_per_sm(D, d.heads_per_block / 8, c->dtype == JVP_E4M3)
+          : decode_simt_ctas_per_sm(d.heads_per_block));
   const int tile = decode_tile(tc, D, c->dtype == JVP_E4M3);
   const int64_t tiles = (most + tile - 1) / tile;
   // B * Hkv * head_blocks <= B * H <= 2^31 - 1 (checked by the caller), tiles < 2^31

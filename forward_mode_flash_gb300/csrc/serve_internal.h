@@ -67,17 +67,17 @@ struct DecodeParams {
 // Which kernel a call takes: tensor cores (16-bit queries, 16-byte aligned
 // rows, D a multiple of 8, of 16 for an e4m3 cache) or CUDA cores.
 // Query heads per CTA: 8 or 16 of a key/value head's group on the tensor
-// cores, 2 or 4 on the CUDA cores.
-inline int decode_heads_per_block(bool tc, int D, int group) {
+// cores, 1 (ungrouped heads) or 4 on the CUDA cores.
+inline int decode_heads_per_block(bool tc, int group) {
   if (tc) return group > 8 ? 16 : 8;
-  return D > 64 ? 2 : 4;
+  return group > 1 ? 4 : 1;
 }
 // Tensor cores: keys of a warp's group of rows (K and V rows of 8 KB at most)
 // and groups in a warp's ring; four warps' groups are the split's tile.
 constexpr int decode_warp_keys(int D, bool e4m3) { return D > 64 && !e4m3 ? 16 : 32; }
 constexpr int decode_stages(bool e4m3) { return e4m3 ? 2 : 3; }
 constexpr int kDecodeSimtTile = 64;
-constexpr int kDecodeSimtCtasPerSm = 3;
+constexpr int decode_simt_ctas_per_sm(int heads) { return heads > 1 ? 3 : 4; }
 constexpr int decode_tile(bool tc, int D, bool e4m3) {
   return tc ? 4 * decode_warp_keys(D, e4m3) : kDecodeSimtTile;
 }
