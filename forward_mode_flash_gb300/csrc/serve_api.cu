@@ -14,6 +14,8 @@ namespace jvp {
 namespace {
 
 constexpr int64_t kMax = (1ll << 31) - 1;
+// Positions and rows: below this a tile's end, too, is a 32-bit number.
+constexpr int64_t kMaxRows = (1ll << 31) - 1024;
 
 bool aligned_to(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 int64_t elem_bytes(int dt) { return dt == JVP_E4M3 ? 1 : dt == JVP_F32 ? 4 : 2; }
@@ -42,9 +44,9 @@ jvp_status_t check_cache(const jvp_cache_t* c, bool written) {
   if (!tensor_type(c->dtype) && c->dtype != JVP_E4M3)
     return api_fail(JVP_ERR_INVALID_ARG, "unknown cache dtype");
   if (c->pages > kMax || c->Hkv > kMax || c->B > kMax || c->max_pages > kMax ||
-      c->page_size > kMax || c->max_pages * c->page_size > kMax)
+      c->page_size > kMax || c->max_pages * c->page_size > kMaxRows)
     return api_fail(JVP_ERR_UNSUPPORTED,
-                    "a size of the cache exceeds 2^31 - 1");
+                    "a size of the cache exceeds 2^31 - 1, or max_pages * page_size 2^31 - 1024");
   if (c->B > 1 && c->table_stride < c->max_pages)
     return api_fail(JVP_ERR_INVALID_ARG, "table_stride is less than max_pages");
   for (const jvp_strides_t* s : {&c->k_strides, &c->v_strides}) {
@@ -251,7 +253,7 @@ jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dt
   if (H > 0 && H % Hkv != 0)
     return api_fail(JVP_ERR_INVALID_ARG, "H must be a multiple of Hkv (grouped-query attention)");
   // the largest grid: one block per (query head, 1-row sequence or tile)
-  if (T > kMax || B > kMax || H > kMax || T + B > kMax || (H > 0 && T + B > kMax / H))
+  if (T > kMax || B > kMax || H > kMax || T + B > kMaxRows || (H > 0 && T + B > kMax / H))
     return api_fail(JVP_ERR_UNSUPPORTED, "problem too large for one launch");
   for (int i = 0; i < 4; ++i) {
     const jvp_status_t st = check_strides(i < 3 ? in_strides[i] : *out_strides,

@@ -391,7 +391,8 @@ jvp_status_t jvp_attn_bwd_dual_noalloc(const jvp_shape_t* shape, jvp_dtype_t dty
  * fp16/bf16 with D a multiple of 8 up to 128, H / Hkv at most 128, a nonzero
  * scale and 16-byte aligned rows run on the tensor cores (weights rounded to
  * 16 bits, fp32 accumulation); every other case on the CUDA cores in fp32.
- * No workspace.
+ * No workspace.  T + B must be at most 2^31 - 1024, and H (T + B) at most
+ * 2^31 - 1 (else JVP_ERR_UNSUPPORTED).
  */
 typedef struct {
   int64_t T, B, H, Hkv, D;
@@ -422,7 +423,9 @@ jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dt
  * checked there: an entry that names no page, a position outside the block
  * table, or a length outside [0, max_pages * page_size] reaches no memory;
  * what it would have reached is skipped, and
- * jvp_attn_get_device_status() reports JVP_ERR_INDEX.
+ * jvp_attn_get_device_status() reports JVP_ERR_INDEX.  Sizes must be at most
+ * 2^31 - 1 and max_pages * page_size at most 2^31 - 1024 (else
+ * JVP_ERR_UNSUPPORTED).
  */
 typedef struct {
   int64_t pages, page_size, Hkv, D; /* D: 1..128 */

@@ -60,6 +60,8 @@ def test_cache_descriptions(lib, call):
     assert call(lib, cache(dtype=_abi.JVP_F16)) == BAD            # neither bf16 nor e4m3
     assert call(lib, cache(pages=1 << 31)) == UNS
     assert call(lib, cache(page=1 << 16, max_pages=1 << 15)) == UNS
+    assert call(lib, cache(page=(1 << 31) - 1023, max_pages=1)) == UNS  # a tile's end past 2^31
+    assert call(lib, cache(page=1, max_pages=(1 << 31) - 1, stride=1 << 31)) == UNS
     assert call(lib, cache(ks=_abi.Strides(2048, 1024, 64, 2))) == BAD
     assert call(lib, cache(vs=_abi.Strides(2048, -1024, 64, 1))) == BAD
     assert call(lib, kc=None) == BAD
@@ -145,7 +147,8 @@ def test_packed(lib):
                dict(outs=_abi.Strides(0, 0, 256, 1)), dict(outs=_abi.Strides(0, 64, -256, 1)),
                dict(ins=(_abi.Strides * 3)(*[_abi.Strides(0, 64, 256, 2)] * 3))):
         assert packed(lib, **kw) == BAD, kw
-    for kw in (dict(D=136), dict(T=1 << 31), dict(B=1 << 31), dict(T=1 << 30, H=4)):
+    for kw in (dict(D=136), dict(T=1 << 31), dict(B=1 << 31), dict(T=1 << 30, H=4),
+               dict(T=(1 << 31) - 1024, B=1, H=1, Hkv=1), dict(T=8, B=(1 << 31) - 1031, H=1, Hkv=1)):
         assert packed(lib, **kw) == UNS, kw
     for kw in (dict(ptr=ctypes.c_void_p(0x10001)), dict(cu=ctypes.c_void_p(0x10002)),
                dict(lse=ctypes.c_void_p(0x10002))):
