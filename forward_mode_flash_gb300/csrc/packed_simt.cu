@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "packed.cuh"
 
@@ -153,27 +154,34 @@ __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParam
     __syncthreads();  // P is written, V has landed, K has been read
     const bool more = j0 + BN < keys;
     if (more) load_rows(sK, L::LD, BN, k, p.sk.n, j0 + BN);
+    // acc += P V.  In a tile that the causal mask cuts, a masked key's weight
+    // is 0 and its values are left out (0 * NaN would not be 0).
+    auto values = [&](auto masked) {
 #pragma unroll 2
-    for (int j = 0; j < BN; j += 4) {
-      float4 a[4];
+      for (int j = 0; j < BN; j += 4) {
+        float4 a[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        a[i] = *reinterpret_cast<const float4*>(sP + (ty + TY * i) * L::LP + j);
+        for (int i = 0; i < 4; ++i)
+          a[i] = *reinterpret_cast<const float4*>(sP + (ty + TY * i) * L::LP + j);
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj)
+        for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-        for (int e = 0; e < DC; e += 4) {
-          const float4 b = *reinterpret_cast<const float4*>(sV + (j + jj) * DP + 4 * tx + 16 * e);
+          for (int e = 0; e < DC; e += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(sV + (j + jj) * DP + 4 * tx + 16 * e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float w = jj == 0 ? a[i].x : jj == 1 ? a[i].y : jj == 2 ? a[i].z : a[i].w;
-            acc[i][e] = fmaf(w, b.x, acc[i][e]);
-            acc[i][e + 1] = fmaf(w, b.y, acc[i][e + 1]);
-            acc[i][e + 2] = fmaf(w, b.z, acc[i][e + 2]);
-            acc[i][e + 3] = fmaf(w, b.w, acc[i][e + 3]);
+            for (int i = 0; i < 4; ++i) {
+              if (masked.value && j0 + j + jj > q0 + ty + TY * i) continue;
+              const float w = jj == 0 ? a[i].x : jj == 1 ? a[i].y : jj == 2 ? a[i].z : a[i].w;
+              acc[i][e] = fmaf(w, b.x, acc[i][e]);
+              acc[i][e + 1] = fmaf(w, b.y, acc[i][e + 1]);
+              acc[i][e + 2] = fmaf(w, b.z, acc[i][e + 2]);
+              acc[i][e + 3] = fmaf(w, b.w, acc[i][e + 3]);
+            }
           }
-        }
-    }
+      }
+    };
+    if (p.causal && j0 + BN - 1 > q0) values(std::true_type());
+    else values(std::false_type());
     __syncthreads();  // V and P have been read
     if (more) load_rows(sV, DP, BN, v, p.sv.n, j0 + BN);
   }

@@ -219,6 +219,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t saddr, uint32_t a, uint32_
                "r"(d)
                : "memory");
 }
+__device__ __forceinline__ void ld_shared_v4(uint32_t saddr, uint32_t (&x)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(saddr)
+               : "memory");
+}
 __device__ __forceinline__ float4 ld_shared_v4f(uint32_t saddr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"

@@ -381,13 +381,15 @@ jvp_status_t jvp_attn_bwd_dual_noalloc(const jvp_shape_t* shape, jvp_dtype_t dty
  *                between heads, .b unused, .d must be 1.
  *   cu_seqlens   int32 [B + 1] on the device, non-decreasing, within [0, T];
  *                read when the work runs.  Rows before the first and behind the
- *                last sequence are neither read nor written (a padded batch).
+ *                last sequence have no influence and are not written (a padded
+ *                batch).
  *                Offsets that break this rule reach no memory: their
  *                sequences are skipped (with none of their rows written) and
  *                jvp_attn_get_device_status() reports JVP_ERR_INDEX.
  *   lse          NULL or [H, T] contiguous float32.
  *
- * A sequence's results do not depend on the rows of others, whatever they hold.
+ * A sequence's results do not depend on the rows of others, nor (causal) a
+ * row's on later rows, whatever they hold.
  * fp16/bf16 with D a multiple of 8 up to 128, H / Hkv at most 128, a nonzero
  * scale and 16-byte aligned rows run on the tensor cores (weights rounded to
  * 16 bits, fp32 accumulation); every other case on the CUDA cores in fp32.

@@ -158,6 +158,42 @@ def test_rows_of_other_sequences_and_of_none_have_no_say(dt, D, causal, lens):
     assert torch.isnan(o[r]).all()
 
 
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2)])
+@pytest.mark.parametrize("lens", [[300, 5, 131], [1500, 1400]], ids=["short", "long"])
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64), ("f16", 40), ("f32", 64)])
+def test_values_behind_a_row_have_no_say(dt, D, lens, H, Hkv):
+    """Causal: infinities and NaN among later keys and values leave a row as it was; the rows
+    that see them have them in the same columns."""
+    q, k, v, cu = make(lens, H, Hkv, D, dt, seed=17)
+    want, wl = run(q, k, v, cu, True)
+    inf, nan = float("inf"), float("nan")
+    places = [(lens[0] - 1, 0, 3, nan), (lens[0] - 150, Hkv - 1, D - 1, inf),
+              (lens[0] // 2, 0, 0, -inf), (129, Hkv - 1, 17, inf), (130, Hkv - 1, 17, -inf),
+              (0, 0, 5, inf), (lens[0] + 1, 0, 8, inf), (sum(lens) - 1, 0, 9, nan)]
+    for row, h, d, x in places:
+        v[row, h, d] = x
+    o, lse = run(q, k, v, cu, True)
+    expect = want.float().clone()
+    ends = [int(e) for e in cu[1:]]
+    for row, h, d, x in places:
+        end = next(e for e in ends if row < e)
+        heads = slice(h * (H // Hkv), (h + 1) * (H // Hkv))
+        expect[row:end, heads, d] += x
+    bad = ~torch.isfinite(expect)
+    assert bad.any() and not bad.all()
+    assert torch.equal(o[~bad].float(), expect[~bad])
+    assert torch.equal(torch.nan_to_num(o[bad].float(), nan=7.0),
+                       torch.nan_to_num(expect[bad], nan=7.0))
+    assert torch.equal(lse, wl)
+    # keys too: the rows in front of a NaN key keep their bits
+    row = lens[0] - 20
+    k[row] = nan
+    o2, _ = run(q, k, v, cu, True)
+    same = o2[:row].eq(o[:row]) | (torch.isnan(o2[:row]) & torch.isnan(o[:row]))
+    assert same.all()
+    assert torch.isnan(o2[row:lens[0]]).all()
+
+
 @pytest.mark.parametrize("dt,D", [("bf16", 64), ("f16", 128), ("f32", 64)])
 def test_strides_of_a_joint_projection(dt, D):
     """q, k, v side by side in one tensor, the output into part of another."""
