@@ -1101,13 +1101,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
 }
 
 // ------------------------------------------------------------------ launch
-template <typename K>
-cudaError_t launch_with_smem(K kern, int bytes, const DecodeParams& p, cudaStream_t stream) {
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<p.grid, kThreads, bytes, stream>>>(p);
+template <auto KERN>
+cudaError_t launch_with_smem(int bytes, const DecodeParams& p, cudaStream_t stream) {
+  const cudaError_t e = allow_shared_memory<KERN>(bytes);
+  if (e != cudaSuccess) return e;
+  KERN<<<p.grid, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1115,13 +1113,13 @@ template <typename TQ, int DPAD, bool E4M3, int NG>
 cudaError_t launch_tc(const DecodeParams& p, cudaStream_t stream) {
   constexpr int bytes = 128 + 2 * sizeof(Exchange<DPAD, NG>) + kWarps * Ring<DPAD, E4M3>::WARP;
   static_assert(decode_ctas_per_sm(DPAD, NG, E4M3) * (bytes + 1024) <= 228 * 1024, "resident CTAs");
-  return launch_with_smem(decode_tc_kernel<TQ, DPAD, E4M3, NG>, bytes, p, stream);
+  return launch_with_smem<decode_tc_kernel<TQ, DPAD, E4M3, NG>>(bytes, p, stream);
 }
 template <typename TQ, int DPAD, bool E4M3, int HPB>
 cudaError_t launch_simt(bool vec, const DecodeParams& p, cudaStream_t stream) {
   constexpr int bytes = sizeof(SimtShared<HPB, DPAD>);
-  return vec ? launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, true>, bytes, p, stream)
-             : launch_with_smem(decode_simt_kernel<TQ, DPAD, E4M3, HPB, false>, bytes, p, stream);
+  return vec ? launch_with_smem<decode_simt_kernel<TQ, DPAD, E4M3, HPB, true>>(bytes, p, stream)
+             : launch_with_smem<decode_simt_kernel<TQ, DPAD, E4M3, HPB, false>>(bytes, p, stream);
 }
 
 template <typename TQ, int DPAD, bool E4M3>

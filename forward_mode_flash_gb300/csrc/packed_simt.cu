@@ -208,11 +208,10 @@ __global__ void __launch_bounds__(kThreads) packed_simt_kernel(const PackedParam
 template <typename T, int DP, bool VEC>
 cudaError_t launch_variant(const PackedParams& p, cudaStream_t stream) {
   constexpr int bytes = Smem<DP>::FLOATS * 4;
-  auto kern = packed_simt_kernel<T, DP, VEC>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_shared_memory<packed_simt_kernel<T, DP, VEC>>(bytes);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.tiles) * p.H;
-  kern<<<static_cast<unsigned>(grid), kThreads, bytes, stream>>>(p);
+  packed_simt_kernel<T, DP, VEC><<<static_cast<unsigned>(grid), kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 template <typename T, bool VEC>

@@ -54,8 +54,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <atomic>
-
 #include "debug_checks.cuh"
 #include "packed.cuh"
 #include "sm103_ptx.cuh"
@@ -680,19 +678,12 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
 template <typename T, int D, int NQ>
 cudaError_t launch_packed_tc_variant(const PackedMaps& maps, const PackedParams& p,
                                      cudaStream_t stream) {
-  auto kern = packed_tc_kernel<T, D, NQ>;
   constexpr int smem = PackedLayout<D, NQ>::SMEM_BYTES;
-  static std::atomic<unsigned long long> attr_done{0};  // per device; setting it twice is harmless
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_shared_memory<packed_tc_kernel<T, D, NQ>>(smem);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(attr_done.load(std::memory_order_relaxed) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   const long long grid = static_cast<long long>(p.tiles) * p.Hkv;
-  kern<<<static_cast<unsigned>(grid), packed_threads(NQ), smem, stream>>>(maps, p);
+  packed_tc_kernel<T, D, NQ>
+      <<<static_cast<unsigned>(grid), packed_threads(NQ), smem, stream>>>(maps, p);
   return cudaGetLastError();
 }
 

@@ -3,6 +3,7 @@
 // the public ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -122,6 +123,22 @@ constexpr int kPackedBlockN = 128;    // keys per tile
 // CUDA-core kernel (any type, any D up to 128).
 cudaError_t launch_packed_simt(DType dt, const PackedParams& p, cudaStream_t stream);
 constexpr int kPackedSimtRows = 32;
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device.
+// Once per kernel and device (the call costs 2 us of an eager call's host time;
+// making it twice is harmless).
+template <auto KERN>
+cudaError_t allow_shared_memory(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & (1ull << dev))) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // What the entry points of the other translation unit share with jvp_attn_api.cu.
 jvp_status_t api_fail(jvp_status_t s, const char* msg);
