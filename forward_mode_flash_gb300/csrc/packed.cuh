@@ -12,13 +12,46 @@ struct PackedTile {
 };
 
 // Query tile `u` of the list of all sequences' tiles (ceil(len / rows) each),
-// for each sequence last tile first where `last_first`.  Executed by a whole
+// for each sequence last tile first where `last_first`.  Otherwise a tile's work
+// goes with its sequence's length, and up to 32 sequences are taken longest
+// first (16 of 90 to 1024 tokens, 8 heads, D = 64: 37.1 against 39.6 us).  The
+// same over the tiles of causal sequences, last tiles of all first, is slower
+// (66.0 against 63.7 us, 4 of 2048 tokens, 16/4 heads, D = 128).  Executed by a whole
 // warp; false where the list has fewer tiles.  Offsets outside 0 <= cu[b] <=
 // cu[b + 1] <= T make an empty sequence and are recorded by the block u = 0.
 __device__ __forceinline__ bool find_packed_tile(const int* cu, int B, int T, int rows, int u,
                                                  bool last_first, unsigned int* status,
                                                  PackedTile* out) {
   const int lane = threadIdx.x & 31;
+  if (B <= 32 && !last_first) {  // longest sequences first
+    int r0 = lane < B ? __ldg(cu + lane) : 0, r1 = lane < B ? __ldg(cu + lane + 1) : 0;
+    const bool wrong = r0 < 0 || r1 < r0 || r1 > T;
+    if (wrong) r0 = r1 = 0;
+    if (u == 0 && __any_sync(0xffffffffu, wrong) && lane == 0) atomicOr(status, kStatusIndex);
+    const int nt = (r1 - r0 + rows - 1) / rows;
+    // x: the smallest number with at most u tiles in sequences of more than x
+    // tiles (`before` of them)
+    int lo = 0, x = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(nt)));
+    int before = 0;
+    while (x - lo > 1) {
+      const int mid = (lo + x) >> 1;
+      const int n = static_cast<int>(
+          __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nt > mid ? nt : 0)));
+      if (n > u) lo = mid;
+      else x = mid, before = n;
+    }
+    const unsigned of_x = __ballot_sync(0xffffffffu, nt == x);
+    const int k = u - before;
+    if (x == 0 || k >= __popc(of_x) * x) return false;
+    const int which = k / x;
+    const unsigned pick = __ballot_sync(
+        0xffffffffu, nt == x && __popc(of_x & ((1u << lane) - 1u)) == which);
+    const int src = __ffs(pick) - 1;
+    out->r0 = __shfl_sync(0xffffffffu, r0, src);
+    out->len = __shfl_sync(0xffffffffu, r1, src) - out->r0;
+    out->tile = k - which * x;
+    return true;
+  }
   int base = 0;
   bool bad = false, found = false;
   int next0 = lane < B ? __ldg(cu + lane) : 0, next1 = lane < B ? __ldg(cu + lane + 1) : 0;
