@@ -222,13 +222,14 @@ def test_strides_of_a_joint_projection(dt, D):
     check(q.cpu(), k[:1].expand(T, Hkv, D).cpu(), v.cpu(), cu, False, o4, l4, tensor_cores=False)
 
 
+@pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_bad_offsets_are_skipped_and_reported(dt):
+def test_bad_offsets_are_skipped_and_reported(dt, causal):
     q, k, v, cu = make([50, 60, 40], 4, 2, 64, dt, seed=7)
-    good, _ = run(q, k, v, cu, True)
+    good, _ = run(q, k, v, cu, causal)
     for bad in ([0, 50, 40, 40], [0, 50, 110, 151], [-1, 50, 110, 150]):
         out = torch.full(q.shape, 5.0, dtype=q.dtype, device="cuda")
-        run(q, k, v, torch.tensor(bad, dtype=torch.int32), True, out=out)
+        run(q, k, v, torch.tensor(bad, dtype=torch.int32), causal, out=out)
         assert api.device_status() == _abi.JVP_ERR_INDEX
         for b in range(3):
             r0, r1 = bad[b], bad[b + 1]
