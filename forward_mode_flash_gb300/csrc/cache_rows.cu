@@ -22,6 +22,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "debug_checks.cuh"
 #include "paged.cuh"
 
 namespace jvp {
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kWarps * 32, 12) cache_write_vec(const CacheRo
   if (!locate(p, r, &page, &row)) return;
   constexpr int per = 32 / LANES;  // heads at once
   const int sub = lane / LANES, dl = lane % LANES * EL;
-  const bool in_row = dl < p.c.D;
+  const bool in_row = dl < p.c.D && JVP_CHECK(dl + EL <= p.c.D, p.c.status, kChkGlobalCol);
   const T* const ks = static_cast<const T*>(p.k) + r * p.srk.n + dl;
   const T* const vs = static_cast<const T*>(p.v) + r * p.srv.n + dl;
   C* const kd = static_cast<C*>(p.c.k) + page * p.c.sk.b + row * p.c.sk.n + dl;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_vec(const CacheRowsPar
   if (!locate(p, r, &page, &row)) return;
   constexpr int per = 32 / LANES;
   const int sub = lane / LANES, dl = lane % LANES * VEC;
-  const bool in_row = dl < p.c.D;
+  const bool in_row = dl < p.c.D && JVP_CHECK(dl + VEC <= p.c.D, p.c.status, kChkGlobalCol);
   const C* const ks = static_cast<const C*>(p.c.k) + page * p.c.sk.b + row * p.c.sk.n + dl;
   const C* const vs = static_cast<const C*>(p.c.v) + page * p.c.sv.b + row * p.c.sv.n + dl;
   T* const kd = const_cast<T*>(static_cast<const T*>(p.k)) + r * p.srk.n + dl;

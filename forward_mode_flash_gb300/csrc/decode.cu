@@ -54,6 +54,7 @@
 // log-sum-exp uses the unrounded sum.
 #include <cmath>
 
+#include "debug_checks.cuh"
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
 
@@ -256,8 +257,10 @@ struct Walker {
   __device__ __forceinline__ void note(const DecodeParams& p, const Piece& s) const {
     if (p.direct || s.t0 > 0 || threadIdx.x != 0) return;
     const int c1 = static_cast<int>(((s.first + s.nt) * G - 1) / W);
-    p.ws_cta[(static_cast<long long>(s.b) * p.c.Hkv + s.hk) * p.head_blocks + s.hb] =
-        make_int2(static_cast<int>(blockIdx.x), c1);
+    if (JVP_CHECK(s.b < p.c.B && s.hk < p.c.Hkv && s.hb < p.head_blocks && c1 < p.grid, p.c.status,
+                  kChkGlobalRow))
+      p.ws_cta[(static_cast<long long>(s.b) * p.c.Hkv + s.hk) * p.head_blocks + s.hb] =
+          make_int2(static_cast<int>(blockIdx.x), c1);
   }
 };
 
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           for (int i = 0; i < 16 / RS; ++i) {
             const int r = 16 * h + i * RS + lr;
             const bool on = col_on && (keep == 0xFFFFu || ((keep >> (i * RS + lr)) & 1u));
+            if (!JVP_CHECK(R::v_at(r, x) + 16 <= R::STAGE, c.status, kChkSmem)) continue;
             copy_async16(dst + R::k_at(r, x), kr, on);
             copy_async16(dst + R::v_at(r, x), vr, on);
             kr += RS * c.sk.n, vr += RS * c.sv.n;
@@ -425,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           const TC* vr = reinterpret_cast<const TC*>(
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vp), r));
           const bool on = col_on && ((keep_next >> r) & 1u);
+          if (!JVP_CHECK(R::v_at(r, x) + 16 <= R::STAGE, c.status, kChkSmem)) continue;
           copy_async16(dst + R::k_at(r, x), kr + xcol, on);
           copy_async16(dst + R::v_at(r, x), vr + xcol, on);
         }
@@ -741,6 +746,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           if (E4M3) f *= mw[n][i] == -INFINITY ? 0.f : exp2f(mw[n][i] - kShift - mu);
           const float lse = lx[n][i] == 0.f ? -INFINITY : mu + log2f(lx[n][i]) - (E4M3 ? 0.f : kShift);
           const long long ws = slot_row(p, blockIdx.x, done.slot, HPB, h);
+          if (!JVP_CHECK(done.slot >= 0 ? ws < 2ll * p.grid * HPB : done.b < c.B && h0 + h < p.H,
+                         c.status, kChkGlobalRow))
+            continue;
           if (g == 0) {
             if (done.slot >= 0) p.ws_lse[ws] = lse;
             else if (p.lse) p.lse[static_cast<long long>(done.b) * p.H + h0 + h] = lse * 0.6931471805599453f;
@@ -748,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 #pragma unroll
           for (int u = 0; u < MT / 4; ++u) {  // eight columns from d
             const int d = E4M3 ? g * VE + 8 * u : (g + 8 * u) * 8;
-            if (d >= D) continue;
+            if (d >= D || !JVP_CHECK(d + 8 <= D, c.status, kChkGlobalCol)) continue;
             float o[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -1076,6 +1084,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
       if (at <= ctas.y) {
         // the first CTA's piece begins the segment (slot 1), the others' continue it
         const long long r = slot_row(p, at, at == ctas.x ? 1 : 0, hpb, hi);
+        if (!JVP_CHECK(at >= 0 && r < 2ll * p.grid * hpb, c.status, kChkGlobalRow)) continue;
         y[u] = p.ws_lse[r];
         // (columns past D of a row are not written: they are not used either)
         x[u] = *reinterpret_cast<const float4*>(p.ws_o + r * DPAD + d);

@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
         const int from = max(0, tok0 + 1 - t * BN);  // rows before: every token sees them
         for (int e = lane; e < (BN - rows) * KCH * 8; e += 32) {
           const int piece = e % 8, c = (e / 8) % KCH, row = rows + e / (8 * KCH);
-          st_shared_v4(v + c * BN * 128 + row * 128 + piece * 16, 0u, 0u, 0u, 0u);
+          if (JVP_CHECK(row < BN, p.status, kChkSmem))
+            st_shared_v4(v + c * BN * 128 + row * 128 + piece * 16, 0u, 0u, 0u, 0u);
         }
         if (p.causal && from < rows) {
           using E = PackedElem<T>;
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
             for (int c = 0; c < KCH; ++c)
               for (int e = from * 8 + lane; e < rows * 8; e += 32) {
                 uint32_t x[4];
+                if (!JVP_CHECK(e * 16 + 16 <= BN * 128, p.status, kChkSmem)) continue;
                 ld_shared_v4(v + c * BN * 128 + e * 16, x);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -532,6 +534,8 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
       if (!(ok = wait(&ctrl->s_full[x][bar_of(t)], phase_of(t)))) break;
       tc_fence_after();
       float s[BN];
+      const bool s_cols = JVP_CHECK(buffer_of(x, t) < NB && buffer_of(x, t) >= 0, p.status, kChkTmem);
+      if (!s_cols) continue;
 #pragma unroll
       for (int q = 0; q < BN; q += 64) {
         uint32_t a[32], b[32];
@@ -568,6 +572,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
           }
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
+            if (!JVP_CHECK(L::TM_O + x * D + col + 32 <= L::TM_COLS, p.status, kChkTmem)) continue;
             uint32_t o[32];
             tmem_ld32(o_tm + col, o);
 #pragma unroll
@@ -603,7 +608,9 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
     if (nx > 0 && ok && (ok = wait(&ctrl->o_full[x], 0))) {
       tc_fence_after();
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (NaN stays NaN)
-      if (row_ok && p.lse)
+      const bool in_t = JVP_CHECK(!row_ok || (r0 + i < p.T && hk * p.group + rh < p.H), p.status,
+                                  kChkGlobalRow);
+      if (row_ok && p.lse && in_t)
         p.lse[static_cast<long long>(hk * p.group + rh) * p.T + r0 + i] =
             l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
       // All tokens of the tile exist: through the (now idle) Q tile, 16-byte
@@ -646,10 +653,13 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
           for (int k = 0; k < 4; ++k)
             w[k] = PackedElem<T>::pack(__uint_as_float(o[e / 32][e % 32 + 2 * k]) * inv,
                                        __uint_as_float(o[e / 32][e % 32 + 2 * k + 1]) * inv);
+          if (!JVP_CHECK((col / 64) * BM * 128 + r * 128 + 128 <= L::Q_BYTES, p.status, kChkSmem))
+            continue;
           if (whole)
             st_shared_v4(stage + (col / 64) * BM * 128 + (((e / 8) ^ (r & 7)) << 4), w[0], w[1],
                          w[2], w[3]);
-          else if (row_ok && col + e < p.D)
+          else if (row_ok && in_t && col + e < p.D &&
+                   JVP_CHECK(col + e + 8 <= p.D, p.status, kChkGlobalCol))
             *reinterpret_cast<uint4*>(dst + col + e) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
