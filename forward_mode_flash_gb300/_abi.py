@@ -8,6 +8,8 @@ is missing or fails to load, importing the binding raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -179,8 +181,28 @@ def load(path: str | None = None):
         lib.jvp_attn_debug_last_path.restype = i32
         lib.jvp_attn_debug_set_cluster_split.argtypes = [i32]
         lib.jvp_attn_debug_set_cluster_split.restype = i32
+        # addresses of the entry points that the native part of the binding calls
+        lib.addresses = {n: ctypes.cast(getattr(lib, n), vp).value
+                         for n in ("jvp_attn_fwd_packed", "jvp_attn_cache_write",
+                                   "jvp_attn_cache_read", "jvp_attn_decode")}
         _libs[p] = lib
         return lib
+
+
+def load_bind():
+    """The native part of the binding (built by forward_mode_flash_gb300.build).
+    Needs PyTorch imported."""
+    from . import build
+
+    path = build.bind_path()
+    if not os.path.exists(path):
+        raise ImportError(
+            f"{path} is missing: build it with forward_mode_flash_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("_serve_bind", path)
+    spec = importlib.util.spec_from_file_location("_serve_bind", path, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    return module
 
 
 def check(status: int) -> None:

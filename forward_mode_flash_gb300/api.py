@@ -464,25 +464,16 @@ def fwd_dual_host(q, k, v, dq, dk, dv, attn_mask: Optional[torch.Tensor] = None,
 
 # ---- packed prompts, the paged key-value cache and the attention over it
 _E4M3 = torch.float8_e4m3fn
-_PLANS = {}
-_PLANS_MAX = 512
+_bind = None  # the binding's native part
 
 
-def _remember(key, plan):
-    """Keeps a validated call description (sizes, types, strides; no addresses)."""
-    if len(_PLANS) >= _PLANS_MAX:
-        _PLANS.clear()
-    _PLANS[key] = plan
-    return plan
-
-
-def _layout(t):
-    """What a call description depends on: all of a tensor but its address and values."""
-    return None if t is None else (t.dtype, t.get_device(), t.shape, t.stride())
-
-
-def _data(t):
-    return None if t is None else t.data_ptr()
+def _native(name):
+    """The native part of the binding, and the address of an entry point."""
+    global _bind
+    lib = _abi.load()
+    if _bind is None:
+        _bind = _abi.load_bind()
+    return _bind, lib.addresses[name]
 
 
 def _check_int32(t, name, shape, device):
@@ -492,11 +483,6 @@ def _check_int32(t, name, shape, device):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have a unit innermost stride")
-
-
-def _row_strides(t):
-    """Stride record of a packed [T, heads, D] tensor."""
-    return _abi.Strides(0, t.stride(1), t.stride(0), 1)
 
 
 def _check_packed(t, name, ref_dtype, device, shape):
@@ -541,22 +527,7 @@ def _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale):
                       _abi.Strides(sk[0], sk[1], sk[2], 1), _abi.Strides(sv[0], sv[1], sv[2], 1))
 
 
-def _call(index, entry, *args):
-    """Calls an entry point with a device current and its current stream as the
-    last argument, and raises on an error status."""
-    # the stream's handle without the object that torch.cuda.current_stream
-    # makes (1 us of a 10 us call)
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
-        st = entry(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            st = entry(*args, stream)
-    if st != _abi.JVP_OK:
-        _abi.check(st)
-
-
-def _packed_plan(q, k, v, cu_seqlens, out):
+def _check_packed_call(q, k, v, cu_seqlens, out):
     if q.dim() != 3:
         raise ValueError(f"q must be [T, H, D], got {tuple(q.shape)}")
     if q.dtype not in _DT:
@@ -576,10 +547,6 @@ def _packed_plan(q, k, v, cu_seqlens, out):
     _check_int32(cu_seqlens, "cu_seqlens", (B + 1,), q.device)
     if out is not None:
         _check_packed(out, "out", q.dtype, q.device, (T, H, D))
-    o_strides = _abi.Strides(0, D, H * D, 1) if out is None else _row_strides(out)
-    return (_abi.PackedShape(T, B, H, hkv, D), _DT[q.dtype],
-            (_abi.Strides * 3)(*[_row_strides(t) for t in (q, k, v)]), o_strides,
-            1.0 / math.sqrt(D) if D else 1.0)
 
 
 def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -595,23 +562,19 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     belong to no sequence are not written (give ``out`` to keep what it holds).
     Forward only, as ``attention``.
     """
-    key = ("packed", _layout(q), _layout(k), _layout(v), _layout(cu_seqlens), _layout(out))
-    plan = _PLANS.get(key)
-    if plan is None:
-        plan = _remember(key, _packed_plan(q, k, v, cu_seqlens, out))
-    shape, dt, strides, o_strides, default_scale = plan
-    device = q.device
-    o = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else out
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=device) \
-        if return_lse else None
-    _call(device.index, _abi.load().jvp_attn_fwd_packed, shape, dt, q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), strides, cu_seqlens.data_ptr(), 1 if is_causal else 0,
-          default_scale if scale is None else float(scale), o.data_ptr(), o_strides, _data(lse))
-    return (o, lse) if return_lse else o
+    bind, entry = _native("jvp_attn_fwd_packed")
+    r = bind.packed(entry, q, k, v, cu_seqlens, out, is_causal, scale, return_lse)
+    if r is None:  # a layout not seen before
+        _check_packed_call(q, k, v, cu_seqlens, out)
+        bind.remember(bind.PACKED, 0, q, k, v, cu_seqlens, out)
+        r = bind.packed(entry, q, k, v, cu_seqlens, out, is_causal, scale, return_lse)
+    if type(r) is int:
+        _abi.check(r)
+    return r
 
 
-def _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens, k_scale, v_scale, k, v):
-    """Description shared by cache_write and cache_read for packed rows k, v."""
+def _check_rows(k, v, k_cache, v_cache, block_table, start_pos, cu_seqlens, k_scale, v_scale):
+    """Checks of cache_write and cache_read, with packed rows k, v."""
     desc = _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale)
     dev = k_cache.device
     if k.dtype not in _DT:
@@ -627,7 +590,19 @@ def _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens, k_scale, v_
         _check_int32(cu_seqlens, "cu_seqlens", (desc.B + 1,), dev)
     elif shape[0] != desc.B:
         raise ValueError("without cu_seqlens there must be one row per sequence")
-    return desc, (_abi.Strides * 2)(_row_strides(k), _row_strides(v)), _DT[k.dtype]
+
+
+def _rows(write, name, *tensors):
+    """cache_write or cache_read: (k, v, k_cache, v_cache, block_table, start_pos,
+    cu_seqlens, k_scale, v_scale)."""
+    bind, entry = _native(name)
+    f = bind.write if write else bind.read
+    st = f(entry, *tensors)
+    if st is None:  # a layout not seen before
+        _check_rows(*tensors)
+        bind.remember(bind.WRITE if write else bind.READ, 0, *tensors)
+        st = f(entry, *tensors)
+    _abi.check(st)
 
 
 def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -649,18 +624,8 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     skipped and reported by ``device_status`` (JVP_ERR_INDEX).  No two rows of
     a call may have the same place.
     """
-    key = ("write", _layout(k), _layout(v), _layout(k_cache), _layout(v_cache),
-           _layout(block_table), _layout(start_pos), _layout(cu_seqlens), _layout(k_scale),
-           _layout(v_scale))
-    plan = _PLANS.get(key)
-    if plan is None:
-        plan = _remember(key, _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens,
-                                         k_scale, v_scale, k, v))
-    desc, strides, dt = plan
-    _call(k_cache.get_device(), _abi.load().jvp_attn_cache_write, desc, dt, k.shape[0],
-          k.data_ptr(), v.data_ptr(), strides, block_table.data_ptr(), _data(start_pos),
-          _data(cu_seqlens), k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale),
-          _data(v_scale))
+    _rows(True, "jvp_attn_cache_write", k, v, k_cache, v_cache, block_table, start_pos,
+          cu_seqlens, k_scale, v_scale)
 
 
 def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -692,22 +657,13 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         k, v = out
         if dtype is not None and k.dtype != dtype:
             raise ValueError(f"out has dtype {k.dtype}, not {dtype}")
-    key = ("read", _layout(k), _layout(v), _layout(k_cache), _layout(v_cache),
-           _layout(block_table), _layout(start_pos), _layout(cu_seqlens), _layout(k_scale),
-           _layout(v_scale))
-    plan = _PLANS.get(key)
-    if plan is None:
-        plan = _remember(key, _rows_plan(k_cache, v_cache, block_table, start_pos, cu_seqlens,
-                                         k_scale, v_scale, k, v))
-    desc, strides, dt = plan
-    _call(k_cache.get_device(), _abi.load().jvp_attn_cache_read, desc, dt, k.shape[0],
-          k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale), _data(v_scale),
-          block_table.data_ptr(), _data(start_pos), _data(cu_seqlens), k.data_ptr(), v.data_ptr(),
-          strides)
+    _rows(False, "jvp_attn_cache_read", k, v, k_cache, v_cache, block_table, start_pos,
+          cu_seqlens, k_scale, v_scale)
     return k, v
 
 
-def _decode_plan(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out):
+def _check_decode(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out):
+    """Checks of attention_decode; the workspace bytes of such a call."""
     desc = _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale)
     dev = k_cache.device
     if q.dtype not in _DT:
@@ -723,11 +679,7 @@ def _decode_plan(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, o
     if out is not None:
         _check_packed(out, "out", q.dtype, dev, shape)
     with torch.cuda.device(dev):
-        need = int(_abi.load().jvp_attn_decode_workspace_size(desc, H, _DT[q.dtype]))
-    o_strides = _abi.Strides(H * desc.D, desc.D, 0, 1) if out is None else \
-        _abi.Strides(out.stride(0), out.stride(1), 0, 1)
-    return (desc, H, _DT[q.dtype], _abi.Strides(q.stride(0), q.stride(1), 0, 1), o_strides, need,
-            1.0 / math.sqrt(desc.D) if desc.D else 1.0)
+        return int(_abi.load().jvp_attn_decode_workspace_size(desc, H, _DT[q.dtype]))
 
 
 def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -747,28 +699,18 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     (uint8, 16-byte aligned, ``decode_workspace_size`` bytes) is allocated here
     if not given; calls that share one must not overlap.
     """
-    key = ("decode", _layout(q), _layout(k_cache), _layout(v_cache), _layout(block_table),
-           _layout(seq_lens), _layout(k_scale), _layout(v_scale), _layout(out))
-    plan = _PLANS.get(key)
-    if plan is None:
-        plan = _remember(key, _decode_plan(q, k_cache, v_cache, block_table, seq_lens, k_scale,
-                                           v_scale, out))
-    desc, H, dt, q_strides, o_strides, need, default_scale = plan
-    device = k_cache.device
-    o = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else out
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if return_lse else None
-    if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        need = workspace.numel() * workspace.element_size()
-    elif need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _call(device.index, _abi.load().jvp_attn_decode, desc, H, dt, q.data_ptr(), q_strides,
-          k_cache.data_ptr(), v_cache.data_ptr(), _data(k_scale), _data(v_scale),
-          block_table.data_ptr(), seq_lens.data_ptr(),
-          default_scale if scale is None else float(scale), o.data_ptr(), o_strides, _data(lse),
-          _data(workspace), need)
-    return (o, lse) if return_lse else o
+    if workspace is not None and (workspace.device != k_cache.device
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {k_cache.device}")
+    bind, entry = _native("jvp_attn_decode")
+    layout = (q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out)
+    r = bind.decode(entry, *layout, workspace, scale, return_lse)
+    if r is None:  # a layout not seen before
+        bind.remember(bind.DECODE, _check_decode(*layout), *layout)
+        r = bind.decode(entry, *layout, workspace, scale, return_lse)
+    if type(r) is int:
+        _abi.check(r)
+    return r
 
 
 def decode_workspace_size(k_cache: torch.Tensor, block_table: torch.Tensor, H: int,

@@ -3,6 +3,8 @@
 Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then
 linked into one shared library exporting the C ABI of ``include/jvp_attn.h``.
 The CUDA runtime is linked statically, so the library loads without a GPU.
+``csrc/serve_bind.cpp``, the native part of the Python binding, becomes a
+Python module for the installed PyTorch beside it.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,6 +47,38 @@ def _deps():
                                       os.path.join(CSRC, "exports.map")]
 
 
+def bind_path() -> str:
+    """The binding's native module, by the PyTorch it is compiled for."""
+    import torch
+
+    return os.path.join(BUILD, f"_serve_bind.torch-{torch.__version__}.so")
+
+
+def build_bind() -> str:
+    """Compiles the binding's native module unless it is up to date."""
+    out = bind_path()
+    src = os.path.join(CSRC, "serve_bind.cpp")
+    deps = (src, os.path.join(ROOT, "include", "jvp_attn.h"))
+    if os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in deps):
+        return out
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = out + f".tmp{os.getpid()}"
+    os.makedirs(BUILD, exist_ok=True)
+    r = subprocess.run(
+        [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+         "-I", os.path.join(home, "include"), "-I", sysconfig.get_paths()["include"],
+         "-I", os.path.join(cuda, "include"), "-I", os.path.join(ROOT, "include"), src, "-o", tmp,
+         "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+        capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for serve_bind.cpp:\n" + r.stdout + r.stderr)
+    os.replace(tmp, out)
+    return out
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
@@ -58,6 +93,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     tensor-core kernels bounds-check their hand-computed indices."""
     lib, out_dir = (DEBUG_LIB, DEBUG_BUILD) if debug else (LIB, BUILD)
     if not force and up_to_date(lib):
+        build_bind()
         return lib
     os.makedirs(out_dir, exist_ok=True)
     cc = nvcc()
@@ -73,14 +109,16 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    workers = min(len(cmds), os.cpu_count() or 4)
+    workers = min(len(cmds) + 1, os.cpu_count() or 4)
     failed = []
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
+        bind = ex.submit(build_bind)
         for cmd, r in ex.map(run, cmds):
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
                 failed.append(cmd[-3])
+        bind.result()
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
     tmp = lib + f".tmp{os.getpid()}"
