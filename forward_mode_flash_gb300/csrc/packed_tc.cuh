@@ -11,7 +11,8 @@
 // [T, H, D] lays them out so), so grouped heads share each K/V tile in the same
 // product and a short prompt of few tokens still fills rows.  A CTA takes two
 // consecutive query tiles A and B of a sequence against the same K/V ring:
-// while one tile's softmax runs, the tensor core works for the other.
+// while one tile's softmax runs, the tensor core works for the other.  (NQ = 1,
+// for short prompts: one tile, and two CTAs per SM that do the same.)
 //   warp 0      TMA producer: Q of both tiles, then K and V tiles through two
 //               rings
 //   warp 1      TMEM allocator; issues every MMA
@@ -22,11 +23,11 @@
 // The scores of a step (query tile, key tile) are formed in a buffer in TMEM,
 // the softmax writes the weights P~ over their first half as 16-bit values, and
 // the second product O += P~ V reads them from there as its A operand.  Behind
-// the product, in the same warp and therefore
-// in order, go the next scores into that buffer: at D = 128 (two buffers; they
-// and both O fill the 512 columns) the same tile's, at D = 64 (three) those of
-// three steps on in the order A(0), B(0), A(1), B(1), ..., so that a softmax
-// warpgroup finds its next scores ready.
+// the product, in the same warp and therefore in order, go the next scores into
+// that buffer: at D = 128 (two buffers; they and both O fill the 512 columns)
+// the same tile's, at D = 64 (three) those of three steps on in the order A(0),
+// B(0), A(1), B(1), ..., so that a softmax warpgroup finds its next scores
+// ready.
 //
 // The row maximum in the exponent moves only when a tile's maximum exceeds it
 // by 2^8 (ratios are exact for any stale maximum), so O is rarely rescaled.
@@ -43,12 +44,16 @@
 // What bounds it: at D = 128 the tensor core's operand reads (one step's
 // products, 2 x 128 x 128 x 128, read 96 KB of shared memory for 1024 cycles of
 // tensor work at 128 bytes a cycle, and copies write 32 KB more); at D = 64 the
-// exponentials and the rest of the softmax.  Measured and not kept: a
-// persistent CTA that takes over blocks through the launch control (8 % slower
-// on long prompts: its item rings keep more warps polling; 20 % faster on
-// prompts of one tile); one issuing warp per query tile (the tiles' products
-// interleave and both scores come late: 1182 against 1154 us); waits with a
-// suspend-time hint (5 % slower).
+// exponentials and the rest of the softmax; prompts of a few tiles, a CTA's
+// beginning and end (about 3 us of set-up, first loads and stores).  Measured,
+// bf16, 16/2 heads of 128, causal, 16384 and 10101 tokens: 914 us, 1660 TFLOP/s
+// (tensor pipe 70 % active); fp16, 16/16 heads of 64, 8192 tokens: 290 us, 946
+// TFLOP/s; bf16, 16/4 heads of 128, causal, twelve of 166 to 2048 tokens: 88 us,
+// 896 TFLOP/s.  Measured and not kept: a persistent CTA that takes over blocks
+// through the launch control (8 % slower on long prompts: its item rings keep
+// more warps polling; 20 % faster on prompts of one tile); at D = 128, one
+// issuing warp per query tile (the tiles' products interleave and both scores
+// come late: 1182 against 1154 us); waits with a suspend-time hint (5 % slower).
 #pragma once
 
 #include <cuda_bf16.h>
