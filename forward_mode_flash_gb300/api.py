@@ -648,11 +648,7 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
             if cu_seqlens is not None:
                 raise ValueError("num_rows (or out) is needed with cu_seqlens")
             num_rows = block_table.shape[0]
-        if dtype is None:
-            dtype = torch.bfloat16 if k_cache.dtype == _E4M3 else k_cache.dtype
-        shape = (num_rows, k_cache.shape[1], k_cache.shape[-1])
-        k = torch.empty(shape, dtype=dtype, device=k_cache.device)
-        v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        k, v = _native("jvp_attn_cache_read")[0].empty_rows(k_cache, num_rows, dtype)
     else:
         k, v = out
         if dtype is not None and k.dtype != dtype:

@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -258,6 +259,25 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// empty_rows(k_cache, rows, dtype): new k, v [rows, Hkv, D] for read, of the
+// cache's type (bfloat16 for an e4m3 one) if dtype is None
+PyObject* empty_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const at::Tensor* c = tensor(a[0]);
+    const int64_t rows = PyLong_AsLongLong(a[1]);
+    if (rows == -1 && PyErr_Occurred()) throw BadArgument();
+    if (!c || c->dim() != 4 || (a[2] != Py_None && !THPDtype_Check(a[2]))) {
+      PyErr_SetString(PyExc_TypeError, "expected a cache [pages, Hkv, page_size, D] and a dtype");
+      throw BadArgument();
+    }
+    const at::ScalarType t = a[2] != Py_None ? reinterpret_cast<THPDtype*>(a[2])->scalar_type
+                             : c->scalar_type() == at::kFloat8_e4m3fn ? at::kBFloat16
+                                                                      : c->scalar_type();
+    const at::Tensor k = empty({rows, c->size(1), c->size(3)}, t, c->device());
+    return result(JVP_OK, k, empty(k.sizes(), t, c->device()), true);
+  });
+}
+
 // decode(entry, q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale,
 //        out, workspace, scale, return_lse)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -289,9 +309,11 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-#define JVP_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {JVP_METHOD(remember), JVP_METHOD(packed), JVP_METHOD(write),
-                         JVP_METHOD(read), JVP_METHOD(decode), {nullptr, nullptr, 0, nullptr}};
+#define JVP_METHOD(f) \
+  {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {JVP_METHOD(remember),   JVP_METHOD(packed), JVP_METHOD(write),
+                         JVP_METHOD(read),       JVP_METHOD(decode), JVP_METHOD(empty_rows),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
