@@ -306,7 +306,14 @@ jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dt
     // (causal 67.9 / 68.5), 1024 122.6 / 120.6 (90.5 / 88.2), 4096 382 / 357
     // (222 / 204); 16/16 heads D = 64: 128 62.2 / 85.2, 512 65.2 / 67.8
     // (57.5 / 67.8), 1024 101.8 / 96.8 (75.8 / 82.5), 4096 330 / 277 (182 / 178).
-    p.query_tiles = T <= (causal ? 768 : 512) * B ? 1 : 2;
+    // At D > 64 also where the pairs would leave SMs idle (one prompt, one
+    // against two: 2048 tokens, 8/8 heads, 64 pairs 26.2 / 28.7 us, causal 26.9
+    // / 29.5; 2142 tokens, 12/4 heads, 104 pairs, D = 80, 35.8 / 30.9, causal
+    // 28.8 / 30.9; 4096 tokens, 4/4 heads of 64, 64 pairs 40.1 / 39.4).
+    const int64_t pairs = (T + 2 * p.tok - 1) / (2 * p.tok) * Hkv;
+    p.query_tiles = T <= (causal ? 768 : 512) * B || (D > 64 && pairs <= (causal ? sms : sms / 2))
+                        ? 1
+                        : 2;
     // >= sum of ceil(length / tokens of a CTA)
     p.tiles = static_cast<int>(T / (p.query_tiles * p.tok) + B);
     // as many key/value heads side by side as keep their rows within 32 MB of L2

@@ -340,16 +340,17 @@ def test_a_prompt_and_the_tokens_after_it(e4m3):
 
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", [2, 40])  # (few heads: one query tile per CTA at D = 128)
 @pytest.mark.parametrize("n", [100, 300, 1000, 1290, 1700])
-def test_a_query_tile_on_its_own_keeps_its_running_maximum(n, D, causal):
+def test_a_query_tile_on_its_own_keeps_its_running_maximum(n, H, D, causal):
     """Lengths whose last work item has one query tile only (its steps run
     through the score buffers alone), with keys that grow so that most tiles
     rescale; and many such items side by side."""
-    q, k, v, cu = make([n, 128 * 5 + 1, n], 2, 2, D, "bf16", seed=n)
+    q, k, v, cu = make([n, 128 * 5 + 1, n], H, H, D, "bf16", seed=n)
     ramp = torch.cat([torch.linspace(0.2, 8.0, int(m)) for m in (cu[1:] - cu[:-1])])[:, None, None]
     q, k = (q.abs() * 2).bfloat16(), (k.abs() * ramp).bfloat16()
     o, lse = run(q, k, v, cu, causal)
-    check(q, k, v, cu, causal, o, lse)
+    check(q, k, v, cu, causal, o, lse, heads=[0, H - 1])
     for _ in range(5):
         o2, lse2 = run(q, k, v, cu, causal)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)

@@ -78,3 +78,40 @@ def test_threads_on_their_own_streams():
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_split_calls_on_two_streams_at_once():
+    """Each call has its own workspace, and so has each captured one."""
+    H, Hkv, D, page = 8, 2, 128, 16
+    g = torch.Generator().manual_seed(2)
+    kc, vc = (torch.randn(800, Hkv, page, D, generator=g).bfloat16().cuda() for _ in range(2))
+    qs = [torch.randn(2, H, D, generator=g).bfloat16().cuda() for _ in range(2)]
+    tables = [torch.randperm(800, generator=g)[:600].view(2, 300).int().cuda() for _ in range(2)]
+    lens = [torch.tensor(n, dtype=torch.int32).cuda() for n in ([4700, 800], [4800, 33])]
+    assert api.decode_workspace_size(kc, tables[0], H) > 0
+    calls = [lambda i=i: api.attention_decode(qs[i], kc, vc, tables[i], lens[i]) for i in range(2)]
+    want = [c().clone() for c in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(100):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(calls[i]())
+        graphs.append(graph)
+    for _ in range(50):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], want[i])
+    assert api.device_status() == 0
