@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 // the piece.  Measured, fp32 caches: 60000 keys of 8 ungrouped heads of 128 in
 // 78 us, 92 % of the copy rate (four CTAs per SM; three: 90 %); 16 sequences of
 // 500 to 4000 keys, 8 heads on 2 of 128, 28 us, 46 % (three; four, of 128
-// registers a thread: 36 us): grouped heads are bound by the arithmetic.
+// registers a thread: 34 us): grouped heads are bound by the arithmetic.
 template <typename T>
 struct Raw {  // four columns as stored
   uint32_t w[sizeof(T)];

@@ -76,8 +76,8 @@ inline int decode_heads_per_block(bool tc, int group) {
 // Tensor cores: keys of a warp's group of rows (K and V rows of 8 KB at most)
 // and groups in a warp's ring; four warps' groups are the split's tile.
 // (e4m3, 64 sequences, 16/2 heads of 128: 57.1 us as here; three stages at two
-// CTAs per SM 65.5; three of 16 keys at three CTAs 57.3, at four of 128 registers
-// a thread 71.5.)
+// CTAs per SM 64.4; groups of 16 keys in three stages at three CTAs 69.2, in two
+// stages at four CTAs 64.2.)
 constexpr int decode_warp_keys(int D, bool e4m3) { return D > 64 && !e4m3 ? 16 : 32; }
 constexpr int decode_stages(bool e4m3) { return e4m3 ? 2 : 3; }
 constexpr int kDecodeSimtTile = 64;
