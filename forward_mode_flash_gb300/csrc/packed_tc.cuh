@@ -32,6 +32,15 @@
 // The row maximum in the exponent moves only when a tile's maximum exceeds it
 // by 2^8 (ratios are exact for any stale maximum), so O is rarely rescaled.
 //
+// Rounding: the weights are rounded to 16 bits for the second product; the row
+// sum adds them unrounded.  bf16 keeps its 8 bits at any size, fp16 its 11 only
+// down to 2^-14, where one key far above thousands of others would leave those
+// with a few bits, or as zeros.  So fp16 weights are 2^(11 + x - m) and the
+// maximum moves past 2^4.9 already (61148 at most, fp16 holds 65504): a weight
+// keeps its 11 bits down to 2^-25 of the row's largest (17 nats) and becomes 0
+// below 2^-36.  (8192 tokens, 16/16 heads of 64: 295.5 us with the maximum moving
+// past 2^8 or 2^5, 297.3 past 2^4, 308.3 past 2^3.)
+//
 // The last key tile of a sequence may end inside the box: the rows behind it
 // are another sequence's.  Their scores are replaced before the maximum, and
 // their V rows, whose weights are 0, are overwritten with zeros in shared
@@ -70,6 +79,8 @@ struct PackedElem;
 template <>
 struct PackedElem<__half> {
   static constexpr bool kBF16 = false;
+  // weights are 2^(kShift + x - m), with logits x up to m + kStale
+  static constexpr float kShift = 11.f, kUnshift = 1.f / 2048.f, kStale = 4.9f;
   static constexpr uint32_t kExp = 0x7C00u;  // exponent bits, all set: infinity or NaN
   static __device__ __forceinline__ float get(uint32_t bits) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
@@ -87,6 +98,7 @@ struct PackedElem<__half> {
 template <>
 struct PackedElem<__nv_bfloat16> {
   static constexpr bool kBF16 = true;
+  static constexpr float kShift = 0.f, kUnshift = 1.f, kStale = 8.f;
   static constexpr uint32_t kExp = 0x7F80u;
   static __device__ __forceinline__ float get(uint32_t bits) { return __uint_as_float(bits << 16); }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
           if (j0 + e >= limit) s[e] = -INFINITY;
       }
       const float m_tile = packed_max(s) * c;
-      const bool need = m_tile > m_run + 8.f;
+      const bool need = m_tile > m_run + PackedElem<T>::kStale;
       if (__any_sync(0xffffffffu, need)) {
         const float m_new = need ? m_tile : m_run;
         const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
@@ -586,7 +598,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
           }
         }
       }
-      const float m_use = m_run == -INFINITY ? 0.f : m_run;
+      const float m_use = (m_run == -INFINITY ? 0.f : m_run) - PackedElem<T>::kShift;
       const float2 c2 = make_float2(c, c), nm2 = make_float2(-m_use, -m_use);
       float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -617,7 +629,8 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
                                   kChkGlobalRow);
       if (row_ok && p.lse && in_t)
         p.lse[static_cast<long long>(hk * p.group + rh) * p.T + r0 + i] =
-            l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
+            l_run == 0.f ? -INFINITY
+                         : (m_run + log2f(l_run * PackedElem<T>::kUnshift)) * 0.6931471805599453f;
       // All tokens of the tile exist: through the (now idle) Q tile, 16-byte
       // piece k of row r at position k ^ (r % 8), and a TMA store of the box.
       // Else the sequence ends inside the tile: each thread writes its row.

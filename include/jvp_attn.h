@@ -392,7 +392,9 @@ jvp_status_t jvp_attn_bwd_dual_noalloc(const jvp_shape_t* shape, jvp_dtype_t dty
  * row's on later rows, whatever they hold.
  * fp16/bf16 with D a multiple of 8 up to 128, H / Hkv at most 128, a nonzero
  * scale and 16-byte aligned rows run on the tensor cores (weights rounded to
- * 16 bits, fp32 accumulation); every other case on the CUDA cores in fp32.
+ * 16 bits, fp32 accumulation; fp16 weights keep 11 bits down to 2^-25 of the
+ * row's largest and are 0 below 2^-36); every other case on the CUDA cores in
+ * fp32.
  * No workspace.  T + B must be at most 2^31 - 1024, and H (T + B) at most
  * 2^31 - 1 (else JVP_ERR_UNSUPPORTED).
  */
