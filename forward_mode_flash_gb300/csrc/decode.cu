@@ -51,11 +51,13 @@
 // normalisation per head (their largest magnitude to [2^14, 2^15)), so bf16
 // queries of any magnitude keep their 8 bits.
 //
-// Rounding: the weights are rounded to 16 bits for the matrix product (fp16
-// ones scaled by 2^6, to keep small weights out of the subnormals and the
-// largest, 2^8 past a stale maximum, in range).  With a 16-bit cache the row sum
-// adds the same rounded weights, so the output is the exact average under
-// slightly perturbed weights; the log-sum-exp uses the unrounded sum.
+// Rounding: the weights are rounded to 16 bits for the matrix product, fp16 ones
+// scaled by 2^11 and with a maximum that moves past 2^4.9 (61148 at most): they
+// keep their 11 bits down to 2^-25 of a row's largest and become 0 below 2^-36.
+// (bf16 weights need no scale; their maximum moves past 2^8.)  With a 16-bit
+// cache the row sum adds the same rounded weights, so the output is the exact
+// average under slightly perturbed weights; the log-sum-exp uses the unrounded
+// sum.
 #include <cmath>
 
 #include "debug_checks.cuh"
@@ -331,7 +333,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
   constexpr int KT = R::KT, RG = KT / 16, TILE = kWarps * KT, ST = R::ST;
   static_assert(ST == 2 || !E4M3, "scale bytes are held for one group ahead");
   constexpr bool kBF16 = Elem<TQ>::kBF16 && !E4M3;  // operand type of the products
-  constexpr float kShift = kBF16 ? 0.f : 6.f;       // fp16 weights: at most 2^(6 + 8)
+  // weights are 2^(kShift + x - m), with logits x up to m + kStale
+  constexpr float kShift = kBF16 ? 0.f : 11.f, kUnshift = kBF16 ? 1.f : 1.f / 2048.f;
+  constexpr float kStale = kBF16 ? 8.f : 4.9f;
   constexpr int KS = DPAD / 16;                     // contraction steps of S^T
   constexpr int EPC = E4M3 ? 16 : 8;                // elements of a 16-byte piece
   constexpr int KSP = EPC / 4;                      // contraction steps per K piece
@@ -573,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
       for (int n = 0; n < NG; ++n) {
         float x[2 * RG][2], pw[2 * RG][2];  // [key g + 8 r][head 2t + i]
         // The maxima in the exponents move only where a logit exceeds them by
-        // 2^8 (ratios are exact for any stale maximum): one vote, and the
+        // 2^kStale (ratios are exact for any stale maximum): one vote, and the
         // reductions over the keys only then.
         bool need = false;
 #pragma unroll
@@ -582,8 +586,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           for (int i = 0; i < 2; ++i) {
             const float y = sc[r / 2][n][2 * (r & 1) + i] * (E4M3 ? kscale[r] * qs[n][i] : qs[n][i]);
             x[r][i] = kept(g + 8 * r) ? y : -INFINITY;
-            need |= x[r][i] > m[n][i] + 8.f;
-            if constexpr (E4M3) need |= x[r][i] + vexp[r] > mw[n][i] + 8.f;
+            need |= x[r][i] > m[n][i] + kStale;
+            if constexpr (E4M3) need |= x[r][i] + vexp[r] > mw[n][i] + kStale;
           }
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           // exponent; mw - m is 0 there.)
           float f = l[n][i] == 0.f ? 0.f : 1.f / l[n][i];
           if (E4M3) f *= mw[n][i] == -INFINITY ? 0.f : exp2f(mw[n][i] - kShift - mu);
-          const float lse = lx[n][i] == 0.f ? -INFINITY : mu + log2f(lx[n][i]) - (E4M3 ? 0.f : kShift);
+          const float lse = lx[n][i] == 0.f ? -INFINITY : mu + log2f(lx[n][i] * (E4M3 ? 1.f : kUnshift));
           const long long ws = slot_row(p, blockIdx.x, done.slot, HPB, h);
           if (!JVP_CHECK(done.slot >= 0 ? ws < 2ll * p.grid * HPB : done.b < c.B && h0 + h < p.H,
                          c.status, kChkGlobalRow))

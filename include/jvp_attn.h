@@ -504,7 +504,8 @@ jvp_status_t jvp_attn_cache_read(const jvp_cache_t* cache, jvp_dtype_t dtype, in
  * on the lengths only (the same call gives the same bits).  Accumulation and softmax
  * in fp32; fp16/bf16 queries with D a multiple of 8 (of 16 over e4m3),
  * 16-byte aligned cache rows and 8-byte aligned query rows use the tensor
- * cores with 16-bit weights, every other case CUDA cores in fp32.  Keys past
+ * cores with 16-bit weights (fp16 over e4m3; fp16 ones keep 11 bits down to
+ * 2^-25 of the largest), every other case CUDA cores in fp32.  Keys past
  * seq_lens and pages that are skipped are never multiplied, whatever they
  * hold.
  */

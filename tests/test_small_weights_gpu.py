@@ -70,3 +70,37 @@ def test_packed_prompts(dt, where, lens, D, causal):
             e = np.abs(f64(o[:n, h]) - ref[0])
             assert (e <= b_o).all(), (nats, h, (e / b_o).max())
             assert (np.abs(f64(lse[h, :n]) - ref[1]) <= b_lse).all(), (nats, h)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [250, 500, 3000])
+@pytest.mark.parametrize("H", [4, 24])  # one or two groups of 8 query heads
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("dt,e4m3", [("f16", False), ("bf16", False), ("f16", True), ("bf16", True)])
+def test_single_tokens(dt, e4m3, where, H, n, D):
+    """Many sequences, so that few parts of a sequence have the far key to themselves."""
+    B, Hkv, page = 300, 2, 16
+    far = {"first": 0, "middle": n // 2, "last": n - 1}[where]
+    q, k, v = rows(n, far, D, dt)
+    u = torch.finfo(DT[dt]).eps / 2
+    most = -(-n // page)
+    cache = torch.float8_e4m3fn if e4m3 else DT[dt]
+    kc, vc = (torch.zeros(most, Hkv, page, D, device="cuda").to(cache) for _ in range(2))
+    sc = [torch.zeros(kc.shape[:3], dtype=torch.uint8, device="cuda") if e4m3 else None
+          for _ in range(2)]
+    table = torch.arange(most, dtype=torch.int32, device="cuda")
+    api.cache_write(*(x[:, None].expand(n, Hkv, D).contiguous().cuda() for x in (k, v)), kc, vc,
+                    table[None], cu_seqlens=torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                    k_scale=sc[0], v_scale=sc[1])
+    tables = table.expand(B, most).contiguous()  # (sequences may share pages that are only read)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    qs = q[0].expand(B, H, D).contiguous().cuda()
+    for nats in NATS:
+        o, lse = api.attention_decode(qs, kc, vc, tables, lens, k_scale=sc[0], v_scale=sc[1],
+                                      scale=nats, return_lse=True)
+        assert api.last_path() == 1
+        ref = attend(f64(q[:1]), f64(k), f64(v), np.ones((1, n), bool), float(np.float32(nats)))
+        b_o, b_lse = bounds(*ref, n, D, u, 2.0 ** -11 if e4m3 else u, True)
+        e = np.abs(f64(o) - ref[0][0]).max((0, 1))
+        assert (e <= b_o[0]).all(), (nats, (e / b_o[0]).max())
+        assert (np.abs(f64(lse) - ref[1][0]) <= b_lse[0]).all(), nats
