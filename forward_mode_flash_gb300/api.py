@@ -620,9 +620,10 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     one scale byte per (page, head, row) in k_scale, v_scale (uint8 [pages,
     Hkv, page_size]): an entry is ``code * 2**(byte - 127)``, the scale the
     smallest power of two that fits the row's largest magnitude.  Rows that
-    belong to no sequence are ignored; rows whose place is out of range are
-    skipped and reported by ``device_status`` (JVP_ERR_INDEX).  No two rows of
-    a call may have the same place.
+    belong to no sequence are ignored; rows whose place is out of range, and
+    sequences whose offsets decrease or leave [0, T], are skipped
+    and reported by ``device_status`` (JVP_ERR_INDEX).  No two rows of a call
+    may have the same place.
     """
     _rows(True, "jvp_attn_cache_write", k, v, k_cache, v_cache, block_table, start_pos,
           cu_seqlens, k_scale, v_scale)
@@ -641,7 +642,7 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     the device); ``out`` = (k, v) gives preallocated ones instead.  Without
     cu_seqlens one row per sequence.  An e4m3 cache's entries become their
     values in ``dtype`` (default bfloat16).  Rows that belong to no sequence,
-    or whose place is out of range, are not written.
+    and those that ``cache_write`` would skip and report, are not written.
     """
     if out is None:
         if num_rows is None:

@@ -49,11 +49,17 @@ struct Rows<__nv_bfloat16> {
 };
 
 // Where row r of the packed tensors lives in the cache: false if it belongs to
-// no sequence, or (recorded in the status word) its place is out of range.
+// no sequence, or (recorded in the status word) its sequence's offsets or its
+// place are out of range.  Executed by a whole warp, one per row; together these
+// look through all offsets (32 for each of the first rows).
 __device__ __forceinline__ bool locate(const CacheRowsParams& p, long long r, int* page, int* row) {
   int b;
   long long first;
   if (p.cu) {
+    for (long long i = r * 32 + (threadIdx.x & 31); i < p.c.B; i += p.T * 32) {
+      const int r0 = __ldg(p.cu + i), r1 = __ldg(p.cu + i + 1);
+      if (r0 < 0 || r1 < r0 || r1 > p.T) atomicOr(p.c.status, kStatusIndex);
+    }
     // last b with cu[b] <= r
     int lo = -1, hi = p.c.B;  // cu[lo] <= r < cu[hi], the ends taken as given
     while (hi - lo > 1) {
@@ -62,9 +68,11 @@ __device__ __forceinline__ bool locate(const CacheRowsParams& p, long long r, in
       else hi = mid;
     }
     // rows before the first sequence and behind the last are in none
-    if (lo < 0 || __ldg(p.cu + p.c.B) <= r) return false;
+    if (lo < 0) return false;
     b = lo;
     first = __ldg(p.cu + b);
+    const int end = __ldg(p.cu + b + 1);
+    if (end <= r || first < 0 || end > p.T) return false;  // (what is wrong has been recorded)
   } else {
     b = static_cast<int>(r);
     first = r;

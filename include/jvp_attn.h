@@ -447,9 +447,12 @@ typedef struct {
  *   k, v         [T, Hkv, D] (in_strides: 2 records; .n is the distance between
  *                rows, .h between heads, .b unused): the new rows of all
  *                sequences, one sequence behind the other.
- *   cu_seqlens   int32 [B + 1], non-decreasing: sequence b's rows are
- *                cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows before the first
- *                and behind the last sequence are ignored (a padded batch).
+ *   cu_seqlens   int32 [B + 1], non-decreasing, within [0, T]: sequence b's
+ *                rows are cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows before
+ *                the first and behind the last sequence are ignored (a padded
+ *                batch).  Offsets that break this rule are reported
+ *                (JVP_ERR_INDEX) and their sequences skipped; a row within
+ *                several others then goes to one of these.
  *                NULL: one row per sequence (T = B), as for single tokens.
  *   start_pos    int32 [B]: position of the sequence's first new row; NULL: 0.
  *   k_cache, v_cache, k_scale, v_scale   written (the scales for e4m3 only).
@@ -472,7 +475,7 @@ jvp_status_t jvp_attn_cache_write(const jvp_cache_t* cache, jvp_dtype_t dtype, i
 /*
  * The reverse: copies rows out of the cache into packed k, v [T, Hkv, D]
  * (out_strides: 2 records), sequence b's positions start_pos[b] (NULL: 0) and
- * on, as many as cu_seqlens (NULL: one each) gives it.  An e4m3 cache's entries
+ * on, as many as cu_seqlens (NULL: one each; bad offsets as above) gives it.  An e4m3 cache's entries
  * become their values, rounded once to `dtype`; otherwise `dtype` is the
  * cache's.  Rows of k and v that belong to no sequence, or whose place is out
  * of range, are left as they are.
