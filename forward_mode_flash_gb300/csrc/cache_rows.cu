@@ -48,18 +48,21 @@ struct Rows<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
 };
 
+// Looks at the offsets of one sequence per thread of the grid (which has as many).
+__device__ __forceinline__ void check_offsets(const CacheRowsParams& p) {
+  const long long i = static_cast<long long>(blockIdx.x) * (kWarps * 32) + threadIdx.x;
+  if (!p.cu || i >= p.c.B) return;
+  const int r0 = __ldg(p.cu + i), r1 = __ldg(p.cu + i + 1);
+  if (r0 < 0 || r1 < r0 || r1 > p.T) atomicOr(p.c.status, kStatusIndex);
+}
+
 // Where row r of the packed tensors lives in the cache: false if it belongs to
 // no sequence, or (recorded in the status word) its sequence's offsets or its
-// place are out of range.  Executed by a whole warp, one per row; together these
-// look through all offsets (32 for each of the first rows).
+// place are out of range.
 __device__ __forceinline__ bool locate(const CacheRowsParams& p, long long r, int* page, int* row) {
   int b;
   long long first;
   if (p.cu) {
-    for (long long i = r * 32 + (threadIdx.x & 31); i < p.c.B; i += p.T * 32) {
-      const int r0 = __ldg(p.cu + i), r1 = __ldg(p.cu + i + 1);
-      if (r0 < 0 || r1 < r0 || r1 > p.T) atomicOr(p.c.status, kStatusIndex);
-    }
     // last b with cu[b] <= r
     int lo = -1, hi = p.c.B;  // cu[lo] <= r < cu[hi], the ends taken as given
     while (hi - lo > 1) {
@@ -72,7 +75,7 @@ __device__ __forceinline__ bool locate(const CacheRowsParams& p, long long r, in
     b = lo;
     first = __ldg(p.cu + b);
     const int end = __ldg(p.cu + b + 1);
-    if (end <= r || first < 0 || end > p.T) return false;  // (what is wrong has been recorded)
+    if (end <= r || first < 0 || end > p.T) return false;  // (check_offsets records what is wrong)
   } else {
     b = static_cast<int>(r);
     first = r;
@@ -214,6 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, 12) cache_write_vec(const CacheRo
   using C = typename std::conditional<E4M3, uint8_t, T>::type;
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  check_offsets(p);
   if (r >= p.T) return;
   int page, row;
   if (!locate(p, r, &page, &row)) return;
@@ -269,6 +273,7 @@ template <typename T, bool E4M3>
 __global__ void __launch_bounds__(kWarps * 32) cache_write_any(const CacheRowsParams p) {
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  check_offsets(p);
   if (r >= p.T) return;
   int page, row;
   if (!locate(p, r, &page, &row)) return;
@@ -305,6 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_vec(const CacheRowsPar
   using C = typename std::conditional<E4M3, uint8_t, T>::type;
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  check_offsets(p);
   if (r >= p.T) return;
   int page, row;
   if (!locate(p, r, &page, &row)) return;
@@ -347,6 +353,7 @@ template <typename T, bool E4M3>
 __global__ void __launch_bounds__(kWarps * 32) cache_read_any(const CacheRowsParams p) {
   const long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  check_offsets(p);
   if (r >= p.T) return;
   int page, row;
   if (!locate(p, r, &page, &row)) return;
@@ -384,7 +391,10 @@ void launch_vec(unsigned grid, const CacheRowsParams& p, cudaStream_t stream) {
 
 template <typename T, bool E4M3, bool WRITE>
 cudaError_t launch(const CacheRowsParams& p, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((p.T + kWarps - 1) / kWarps);
+  // a warp for each row, a thread for each sequence's offsets
+  const long long rows = (p.T + kWarps - 1) / kWarps;
+  const long long offsets = p.cu ? (p.c.B + kWarps * 32 - 1ll) / (kWarps * 32) : 0;
+  const unsigned grid = static_cast<unsigned>(rows > offsets ? rows : offsets);
   if (p.vec) {
     // Two pieces a lane where the cost is instructions, in writing e4m3 rows,
     // and they fit; reading them that way took 67.7 us against 60.7.

@@ -108,7 +108,7 @@ def test_too_few_rows_for_the_offsets_are_reported():
 @pytest.mark.parametrize("where", [1, 31, 32, 33, 500, 999])
 @pytest.mark.parametrize("rows", [1, 3, 400])
 def test_every_offset_is_looked_at(rows, where):
-    """More offsets than 32 per row: one in `where` is wrong, whoever reads it."""
+    """More sequences than the rows' threads (and fewer): one offset is wrong."""
     B = 1000
     kc = torch.zeros(2, 1, 16, 64, device="cuda", dtype=torch.bfloat16)
     x = torch.ones(rows, 1, 64, device="cuda", dtype=torch.bfloat16)
