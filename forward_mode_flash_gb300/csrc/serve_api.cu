@@ -145,8 +145,11 @@ jvp_status_t cache_rows(bool write, const jvp_cache_t* c, jvp_dtype_t dtype, int
            multiple(p.c.sk, el) && multiple(p.c.sv, el);
   };
   const int64_t vec = 16 / e;
-  p.vec = aligned_to(k, 16) && aligned_to(v, 16) && multiple(p.srk, vec) && multiple(p.srv, vec) &&
-                  fits(vec)
+  // (the kernel of 16-byte accesses has 32-bit offsets of the scales within a
+  // page: with 64-bit ones it took 3 to 5 % longer)
+  const bool scales_fit = c->dtype != JVP_E4M3 || c->page_size <= kMax / c->Hkv;
+  p.vec = scales_fit && aligned_to(k, 16) && aligned_to(v, 16) && multiple(p.srk, vec) &&
+                  multiple(p.srv, vec) && fits(vec)
               ? (ce == 1 && fits(2 * vec) ? 2 : 1)
               : 0;
   const bool e4m3 = c->dtype == JVP_E4M3;

@@ -39,7 +39,8 @@ struct CacheRowsParams {
   const int* start; // [B] position of each sequence's first row, or nullptr: 0
   const void *k, *v;  // rows to write (or, reading, outputs)
   Strides srk, srv;
-  int vec;          // 16-byte pieces per lane that alignment and D allow: 0, 1 or 2
+  int vec;          // 16-byte pieces per lane that alignment and D allow: 0, 1 or 2 (e4m3: 0
+                    // where the scales of a page are more than 2^31 - 1)
 };
 // Writes packed rows into the cache / reads them back.  dt: type of the packed
 // rows; e4m3: the cache holds codes and scales, else entries of type dt.
