@@ -66,7 +66,7 @@ __device__ __forceinline__ bool locate(const CacheRowsParams& p, long long r, in
     // last b with cu[b] <= r
     int lo = -1, hi = p.c.B;  // cu[lo] <= r < cu[hi], the ends taken as given
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
+      const int mid = lo + ((hi - lo) >> 1);  // (lo + hi may pass 2^31)
       if (__ldg(p.cu + mid) <= r) lo = mid;
       else hi = mid;
     }

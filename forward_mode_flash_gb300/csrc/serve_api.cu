@@ -14,7 +14,8 @@ namespace jvp {
 namespace {
 
 constexpr int64_t kMax = (1ll << 31) - 1;
-// Positions and rows: below this a tile's end, too, is a 32-bit number.
+// Positions, rows and sequences: below this the end of a tile, or of a thread's
+// share of them, is a 32-bit number too.
 constexpr int64_t kMaxRows = (1ll << 31) - 1024;
 
 bool aligned_to(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -43,10 +44,10 @@ jvp_status_t check_cache(const jvp_cache_t* c, bool written) {
   if (c->D > 128) return api_fail(JVP_ERR_UNSUPPORTED, "D > 128 is not supported");
   if (!tensor_type(c->dtype) && c->dtype != JVP_E4M3)
     return api_fail(JVP_ERR_INVALID_ARG, "unknown cache dtype");
-  if (c->pages > kMax || c->Hkv > kMax || c->B > kMax || c->max_pages > kMax ||
+  if (c->pages > kMax || c->Hkv > kMax || c->B > kMaxRows || c->max_pages > kMax ||
       c->page_size > kMax || c->max_pages * c->page_size > kMaxRows)
     return api_fail(JVP_ERR_UNSUPPORTED,
-                    "a size of the cache exceeds 2^31 - 1, or max_pages * page_size 2^31 - 1024");
+                    "a size of the cache exceeds 2^31 - 1, or B or max_pages * page_size 2^31 - 1024");
   if (c->B > 1 && c->table_stride < c->max_pages)
     return api_fail(JVP_ERR_INVALID_ARG, "table_stride is less than max_pages");
   for (const jvp_strides_t* s : {&c->k_strides, &c->v_strides}) {

@@ -428,7 +428,7 @@ jvp_status_t jvp_attn_fwd_packed(const jvp_packed_shape_t* shape, jvp_dtype_t dt
  * table, or a length outside [0, max_pages * page_size] reaches no memory;
  * what it would have reached is skipped, and
  * jvp_attn_get_device_status() reports JVP_ERR_INDEX.  Sizes must be at most
- * 2^31 - 1 and max_pages * page_size at most 2^31 - 1024 (else
+ * 2^31 - 1, B and max_pages * page_size at most 2^31 - 1024 (else
  * JVP_ERR_UNSUPPORTED).
  */
 typedef struct {

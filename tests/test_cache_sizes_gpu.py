@@ -48,3 +48,19 @@ def test_scales_of_a_page_past_31_bits(page, Hkv):
     for i in range(2):
         assert torch.equal(scales[i][:, :, at], ss[i][:, :, 0])
         assert torch.equal(got[i], want[i])
+
+
+def test_more_than_2_to_the_30_sequences():
+    """Nearly all of them empty."""
+    B, page, D = (1 << 30) + 40, 4, 8
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[B - 2:] = i32([1, 1, 5])  # sequence B - 3 has row 0, sequence B - 1 the others
+    table = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    table[B - 3], table[B - 1] = 2, 0
+    x = torch.randn(5, 1, D, device="cuda").bfloat16()
+    kc, vc = (torch.zeros(3, 1, page, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    api.cache_write(x, -x, kc, vc, table, None, cu)
+    assert torch.equal(kc[0], x[1:].transpose(0, 1)) and torch.equal(vc[0], -x[1:].transpose(0, 1))
+    assert torch.equal(kc[2, 0, 0], x[0, 0]) and kc[2, 0, 1:].eq(0).all() and kc[1].eq(0).all()
+    k, v = api.cache_read(kc, vc, table, None, cu, num_rows=5)
+    assert torch.equal(k, x) and torch.equal(v, -x)
