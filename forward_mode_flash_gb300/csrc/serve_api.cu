@@ -109,6 +109,8 @@ jvp_status_t cache_rows(bool write, const jvp_cache_t* c, jvp_dtype_t dtype, int
     return api_fail(JVP_ERR_INVALID_ARG, "the rows must have the cache's dtype (or the cache e4m3)");
   if (T < 0) return api_fail(JVP_ERR_INVALID_ARG, "negative T");
   if (T > kMax) return api_fail(JVP_ERR_UNSUPPORTED, "T exceeds 2^31 - 1");
+  // (the kernels walk the heads of K and V as one list, up to 32 at a time)
+  if (c->Hkv > kMax / 2 - 64) return api_fail(JVP_ERR_UNSUPPORTED, "Hkv exceeds 2^30 - 65");
   if (!cu && T != c->B)
     return api_fail(JVP_ERR_INVALID_ARG, "without cu_seqlens there must be one row per sequence");
   if (!strides) return api_fail(JVP_ERR_INVALID_ARG, "strides are NULL");

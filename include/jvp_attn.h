@@ -464,7 +464,8 @@ typedef struct {
  * back as an infinity.  Rows whose place is out of range are skipped (see
  * above).  No two rows of a call may have the same place: the pages that a
  * call writes belong to one sequence each (sequences may share pages that
- * hold a common prefix and are only read).
+ * hold a common prefix and are only read).  Hkv must be at most 2^30 - 65, here
+ * and for jvp_attn_cache_read (else JVP_ERR_UNSUPPORTED).
  */
 jvp_status_t jvp_attn_cache_write(const jvp_cache_t* cache, jvp_dtype_t dtype, int64_t T,
                                   const void* k, const void* v, const jvp_strides_t* in_strides,
