@@ -4,13 +4,15 @@ Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then
 linked into one shared library exporting the C ABI of ``include/jvp_attn.h``.
 The CUDA runtime is linked statically, so the library loads without a GPU.
 ``csrc/serve_bind.cpp``, the native part of the Python binding, becomes a
-Python module for the installed PyTorch beside it.
+Python module for the installed PyTorch beside it.  The library needs neither
+PyTorch nor Python's headers, and is built whether or not the module can be.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -54,8 +56,11 @@ def bind_path() -> str:
     return os.path.join(BUILD, f"_serve_bind.torch-{torch.__version__}.so")
 
 
-def build_bind() -> str:
-    """Compiles the binding's native module unless it is up to date."""
+def build_bind() -> str | None:
+    """Compiles the binding's native module unless it is up to date; None
+    without PyTorch, which the binding is for."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     out = bind_path()
     src = os.path.join(CSRC, "serve_bind.cpp")
     deps = (src, os.path.join(ROOT, "include", "jvp_attn.h"))
@@ -89,6 +94,9 @@ def up_to_date(lib: str = LIB) -> bool:
 def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = False) -> str:
     """Compile every translation unit and link the library; returns its path.
 
+    Also builds the binding's native module, beside the library's units; if that
+    fails, the library is finished before the error is raised.
+
     debug=True builds the separate debug library (DEBUG_LIB) whose
     tensor-core kernels bounds-check their hand-computed indices."""
     lib, out_dir = (DEBUG_LIB, DEBUG_BUILD) if debug else (LIB, BUILD)
@@ -118,7 +126,6 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
                 failed.append(cmd[-3])
-        bind.result()
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
     tmp = lib + f".tmp{os.getpid()}"
@@ -128,6 +135,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, lib)
+    bind.result()
     return lib
 
 
