@@ -50,10 +50,12 @@ def _deps():
 
 
 def bind_path() -> str:
-    """The binding's native module, by the PyTorch it is compiled for."""
+    """The binding's native module, by the PyTorch and the Python (its binary
+    interface) that it is compiled for."""
     import torch
 
-    return os.path.join(BUILD, f"_serve_bind.torch-{torch.__version__}.so")
+    return os.path.join(
+        BUILD, f"_serve_bind.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def build_bind() -> str | None:
@@ -63,7 +65,7 @@ def build_bind() -> str | None:
         return None
     out = bind_path()
     src = os.path.join(CSRC, "serve_bind.cpp")
-    deps = (src, os.path.join(ROOT, "include", "jvp_attn.h"))
+    deps = (src, os.path.join(ROOT, "include", "jvp_attn.h"), __file__)  # (its flags are here)
     if os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in deps):
         return out
     import torch

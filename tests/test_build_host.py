@@ -3,6 +3,7 @@
 import os
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
@@ -34,3 +35,29 @@ def test_the_library_is_built_though_the_binding_is_not(tmp_path, monkeypatch):
     with pytest.raises(RuntimeError, match="no headers"):
         build.build()
     assert os.path.exists(build.LIB)
+
+
+def test_the_binding_is_built_for_this_interpreter():
+    """(Another one with the same PyTorch must not load it.)"""
+    assert sysconfig.get_config_var("SOABI") in os.path.basename(build.bind_path())
+
+
+def test_the_binding_is_built_again_for_other_flags(tmp_path, monkeypatch):
+    out = build.build_bind()
+    before = os.path.getmtime(out)
+    recipe = tmp_path / "build.py"
+    recipe.write_text("")
+    os.utime(recipe, (before - 10, before - 10))
+    monkeypatch.setattr(build, "__file__", str(recipe))
+    calls = []
+
+    def compiler(cmd, **kw):
+        calls.append(cmd)
+        return subprocess.CompletedProcess(cmd, 1, "", "not run")
+
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    assert build.build_bind() == out and not calls
+    os.utime(recipe, (before + 10, before + 10))
+    with pytest.raises(RuntimeError, match="not run"):
+        build.build_bind()
+    assert len(calls) == 1
