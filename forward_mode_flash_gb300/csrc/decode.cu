@@ -53,7 +53,9 @@
 //
 // Rounding: the weights are rounded to 16 bits for the matrix product, fp16 ones
 // scaled by 2^11 and with a maximum that moves past 2^4.9 (61148 at most): they
-// keep their 11 bits down to 2^-25 of a row's largest and become 0 below 2^-36.
+// keep their 11 bits down to 2^-25 of a row's largest and become 0 below 2^-36. (The
+// base m - 11 of the exponents is kept as rounded, and compared by differences,
+// so that large logits take no weight past its range.)
 // (bf16 weights need no scale; their maximum moves past 2^8.)  With a 16-bit
 // cache the row sum adds the same rounded weights, so the output is the exact
 // average under slightly perturbed weights; the log-sum-exp uses the unrounded
@@ -333,9 +335,12 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
   constexpr int KT = R::KT, RG = KT / 16, TILE = kWarps * KT, ST = R::ST;
   static_assert(ST == 2 || !E4M3, "scale bytes are held for one group ahead");
   constexpr bool kBF16 = Elem<TQ>::kBF16 && !E4M3;  // operand type of the products
-  // weights are 2^(kShift + x - m), with logits x up to m + kStale
+  // weights are 2^(x - base), the base kShift below a maximum; it moves where they
+  // would pass 2^kTop
   constexpr float kShift = kBF16 ? 0.f : 11.f, kUnshift = kBF16 ? 1.f : 1.f / 2048.f;
-  constexpr float kStale = kBF16 ? 8.f : 4.9f;
+  constexpr float kTop = kBF16 ? 8.f : 15.9f;
+  // (the maximum itself where a step of fp32 is 16, so that m - 11 would be m - 16)
+  auto base = [&](float m) { return m - (m - kShift) > kTop ? m : m - kShift; };
   constexpr int KS = DPAD / 16;                     // contraction steps of S^T
   constexpr int EPC = E4M3 ? 16 : 8;                // elements of a 16-byte piece
   constexpr int KSP = EPC / 4;                      // contraction steps per K piece
@@ -576,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         float x[2 * RG][2], pw[2 * RG][2];  // [key g + 8 r][head 2t + i]
-        // The maxima in the exponents move only where a logit exceeds them by
-        // 2^kStale (ratios are exact for any stale maximum): one vote, and the
-        // reductions over the keys only then.
+        // The bases of the exponents move only where a weight would pass 2^kTop
+        // (ratios are exact for any base): one vote, and the reductions over
+        // the keys only then.  (Over e4m3 m is the base of the row sum, which
+        // is fp32, and mw that of the weights; else they are the same.)
         bool need = false;
 #pragma unroll
         for (int r = 0; r < 2 * RG; ++r)
@@ -586,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           for (int i = 0; i < 2; ++i) {
             const float y = sc[r / 2][n][2 * (r & 1) + i] * (E4M3 ? kscale[r] * qs[n][i] : qs[n][i]);
             x[r][i] = kept(g + 8 * r) ? y : -INFINITY;
-            need |= x[r][i] > m[n][i] + kStale;
-            if constexpr (E4M3) need |= x[r][i] + vexp[r] > mw[n][i] + kStale;
+            need |= x[r][i] - m[n][i] > (E4M3 ? 8.f : kTop);
+            if constexpr (E4M3) need |= x[r][i] + vexp[r] - mw[n][i] > kTop;
           }
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -598,12 +604,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
               top = fmaxf(top, x[r][i]);
               if constexpr (E4M3) topw = fmaxf(topw, x[r][i] + vexp[r]);
             }
-            const float m_new = fmaxf(m[n][i], max_over_g(top));
+            top = max_over_g(top);
+            const float m_new = fmaxf(m[n][i], E4M3 ? top : base(top));
             float a = m_new == m[n][i] ? 1.f : exp2f(m[n][i] - m_new);
             m[n][i] = m_new;
             l[n][i] *= a, lx[n][i] *= a;
             if constexpr (E4M3) {
-              const float mw_new = fmaxf(mw[n][i], max_over_g(topw));
+              const float mw_new = fmaxf(mw[n][i], base(max_over_g(topw)));
               a = mw_new == mw[n][i] ? 1.f : exp2f(mw[n][i] - mw_new);
               mw[n][i] = mw_new;
             } else {
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i];
-          const float mwu = (mw[n][i] == -INFINITY ? 0.f : mw[n][i]) - kShift;
+          const float mwu = mw[n][i] == -INFINITY ? 0.f : mw[n][i];
 #pragma unroll
           for (int r = 0; r < 2 * RG; ++r) {
             if constexpr (E4M3) {
@@ -751,8 +758,10 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           // row.  With a 16-bit cache l and the accumulator have the same
           // exponent; mw - m is 0 there.)
           float f = l[n][i] == 0.f ? 0.f : 1.f / l[n][i];
-          if (E4M3) f *= mw[n][i] == -INFINITY ? 0.f : exp2f(mw[n][i] - kShift - mu);
-          const float lse = lx[n][i] == 0.f ? -INFINITY : mu + log2f(lx[n][i] * (E4M3 ? 1.f : kUnshift));
+          if (E4M3) f *= mw[n][i] == -INFINITY ? 0.f : exp2f(mw[n][i] - mu);
+          const float lse = lx[n][i] == 0.f ? -INFINITY
+                            : E4M3          ? mu + log2f(lx[n][i])
+                                            : mu + kShift + log2f(lx[n][i] * kUnshift);
           const long long ws = slot_row(p, blockIdx.x, done.slot, HPB, h);
           if (!JVP_CHECK(done.slot >= 0 ? ws < 2ll * p.grid * HPB : done.b < c.B && h0 + h < p.H,
                          c.status, kChkGlobalRow))

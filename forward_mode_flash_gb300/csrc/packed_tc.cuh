@@ -39,7 +39,9 @@
 // maximum moves past 2^4.9 already (61148 at most, fp16 holds 65504): a weight
 // keeps its 11 bits down to 2^-25 of the row's largest (17 nats) and becomes 0
 // below 2^-36.  (8192 tokens, 16/16 heads of 64: 295.5 us with the maximum moving
-// past 2^8 or 2^5, 297.3 past 2^4, 308.3 past 2^3.)
+// past 2^8 or 2^5, 297.3 past 2^4, 308.3 past 2^3.)  What is kept is the base
+// m - 11 as rounded, and comparisons are of differences from it, so that large
+// logits, where fp32 has steps of 1 and more, do not take a weight past its range.
 //
 // The last key tile of a sequence may end inside the box: the rows behind it
 // are another sequence's.  Their scores are replaced before the maximum, and
@@ -79,8 +81,9 @@ struct PackedElem;
 template <>
 struct PackedElem<__half> {
   static constexpr bool kBF16 = false;
-  // weights are 2^(kShift + x - m), with logits x up to m + kStale
-  static constexpr float kShift = 11.f, kUnshift = 1.f / 2048.f, kStale = 4.9f;
+  // weights are 2^(x - base), the base kShift below a maximum; it moves where they
+  // would pass 2^kTop
+  static constexpr float kShift = 11.f, kUnshift = 1.f / 2048.f, kTop = 15.9f;
   static constexpr uint32_t kExp = 0x7C00u;  // exponent bits, all set: infinity or NaN
   static __device__ __forceinline__ float get(uint32_t bits) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
@@ -98,7 +101,7 @@ struct PackedElem<__half> {
 template <>
 struct PackedElem<__nv_bfloat16> {
   static constexpr bool kBF16 = true;
-  static constexpr float kShift = 0.f, kUnshift = 1.f, kStale = 8.f;
+  static constexpr float kShift = 0.f, kUnshift = 1.f, kTop = 8.f;
   static constexpr uint32_t kExp = 0x7F80u;
   static __device__ __forceinline__ float get(uint32_t bits) { return __uint_as_float(bits << 16); }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -188,6 +191,14 @@ __device__ __forceinline__ float packed_max(const float (&x)[N]) {
   y[0] = fmax3(y[0], x[N - 4], x[N - 3]);
   y[1] = fmax3(y[1], x[N - 2], x[N - 1]);
   return fmaxf(fmax3(y[0], y[1], y[2]), y[3]);
+}
+
+// Base of the exponents for a maximum m (m itself where a step of fp32 is 16, so
+// that m - 11 would be m - 16).
+template <typename T>
+__device__ __forceinline__ float packed_base(float m) {
+  const float b = m - PackedElem<T>::kShift;
+  return m - b > PackedElem<T>::kTop ? m : b;
 }
 
 template <typename T, int D, int NQ>
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
     const uint32_t o_tm = lane_base + L::TM_O + x * D;
     const float c = p.scale_log2;
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;  // the base of the exponents, the sum
     bool ok = true;
     for (int t = 0; t < nx; ++t) {
       const uint32_t s_tm = lane_base + L::TM_S + buffer_of(x, t) * BN;
@@ -570,9 +581,9 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
           if (j0 + e >= limit) s[e] = -INFINITY;
       }
       const float m_tile = packed_max(s) * c;
-      const bool need = m_tile > m_run + PackedElem<T>::kStale;
+      const bool need = m_tile - m_run > PackedElem<T>::kTop;
       if (__any_sync(0xffffffffu, need)) {
-        const float m_new = need ? m_tile : m_run;
+        const float m_new = need ? packed_base<T>(m_tile) : m_run;
         const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
         l_run *= alpha;
         m_run = m_new;
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
           }
         }
       }
-      const float m_use = (m_run == -INFINITY ? 0.f : m_run) - PackedElem<T>::kShift;
+      const float m_use = m_run == -INFINITY ? 0.f : m_run;
       const float2 c2 = make_float2(c, c), nm2 = make_float2(-m_use, -m_use);
       float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -630,7 +641,8 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
       if (row_ok && p.lse && in_t)
         p.lse[static_cast<long long>(hk * p.group + rh) * p.T + r0 + i] =
             l_run == 0.f ? -INFINITY
-                         : (m_run + log2f(l_run * PackedElem<T>::kUnshift)) * 0.6931471805599453f;
+                         : (m_run + PackedElem<T>::kShift + log2f(l_run * PackedElem<T>::kUnshift)) *
+                               0.6931471805599453f;
       // All tokens of the tile exist: through the (now idle) Q tile, 16-byte
       // piece k of row r at position k ^ (r % 8), and a TMA store of the box.
       // Else the sequence ends inside the tile: each thread writes its row.

@@ -104,3 +104,81 @@ def test_single_tokens(dt, e4m3, where, H, n, D):
         e = np.abs(f64(o) - ref[0][0]).max((0, 1))
         assert (e <= b_o[0]).all(), (nats, (e / b_o[0]).max())
         assert (np.abs(f64(lse) - ref[1][0]) <= b_lse[0]).all(), nats
+
+
+def unit_scale():
+    """The scale whose logits are exact in log2 units: scale * log2(e) rounds to 1."""
+    log2e = np.float32(1.4426950408889634)
+    near = np.float32(1.0) / log2e
+    for s in (near, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(1))):
+        if np.float32(s * log2e) == 1:
+            return float(s)
+    raise AssertionError("no such scale")
+
+
+def steps(power):
+    """Differences, in log2 units, that fp32 holds beside 2^power (and e4m3 beside
+    the rest of a row)."""
+    u = 2.0 ** (power - 23)
+    return sorted({max(1, int(np.ceil(x / u))) * u for x in (4.0, 4.5, 5.0, 8.0, 16.0)})
+
+
+def far_logits(n, power, step, at, D, dt):
+    """q, k, v: all logits are 2^power (log2 units), that of key `at` larger by step."""
+    q, k, v = torch.zeros(D), torch.zeros(n, D), torch.zeros(n, D)
+    q[0], q[1] = 2.0 ** 15, 1.0
+    k[:, 0], k[at, 1] = 2.0 ** (power - 15), step
+    v[:, 0], v[at, 0], v[at, 1] = 1.0, 0.0, 1.0
+    return [x.to(DT[dt]) for x in (q, k, v)]
+
+
+def far_bounds(q, k, v, u, w):
+    # (the logits are exact, products and sums too: no error of theirs)
+    n, D = k.shape
+    o, lse, mag, big = attend(f64(q)[None], f64(k), f64(v), np.ones((1, n), bool), np.log(2.0))
+    return (o[0], lse[0]), [b[0] for b in bounds(o, lse, mag, 0 * big, n, D, u, w, True)]
+
+
+@pytest.mark.parametrize("power", [12, 18, 20, 21, 22, 23, 24, 25, 26, 27])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_packed_prompts_with_large_logits(dt, D, power):
+    """Where fp32 has few or no bits behind the point of a logit, weights beside a
+    maximum that has not moved yet stay in range."""
+    n, at, u = 300, 200, torch.finfo(DT[dt]).eps / 2
+    for step in steps(power):
+        q, k, v = far_logits(n, power, step, at, D, dt)
+        for lens in ([n], [n] * 4 + [5 * n]):
+            x = [t.expand(n, D) if t.dim() == 1 else t for t in (q, k, v)]
+            x = [torch.cat([t] * (sum(lens) // n))[:, None].contiguous().cuda() for t in x]
+            cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+            o, lse = api.attention_packed(*x, cu, scale=unit_scale(), return_lse=True)
+            assert api.last_path() == 1
+            want, tol = far_bounds(q, k, v, u, u)
+            assert (np.abs(f64(o[:n, 0]) - want[0]) <= tol[0]).all(), (step, lens)
+            assert (np.abs(f64(lse[0, :n]) - want[1]) <= tol[1]).all(), (step, lens)
+
+
+@pytest.mark.parametrize("power", [12, 18, 20, 21, 22, 23, 24, 25, 26, 27])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", [2, 12])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_single_tokens_with_large_logits(dt, H, D, power):
+    """(Few keys, so that a CTA has a whole sequence: log-sum-exps of parts, by which
+    they are joined, would be rounded to the steps of fp32 here.)"""
+    n, at, page, B, u = 250, 201, 16, 3, torch.finfo(DT[dt]).eps / 2
+    most = -(-n // page)
+    for step in steps(power):
+        q, k, v = far_logits(n, power, step, at, D, dt)
+        kc, vc = (torch.zeros(most, 1, page, D, device="cuda", dtype=DT[dt]) for _ in range(2))
+        table = torch.arange(most, dtype=torch.int32, device="cuda")
+        api.cache_write(k[:, None].cuda(), v[:, None].cuda(), kc, vc, table[None],
+                        cu_seqlens=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+        o, lse = api.attention_decode(q.expand(B, H, D).contiguous().cuda(), kc, vc,
+                                      table.expand(B, most).contiguous(),
+                                      torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                                      scale=unit_scale(), return_lse=True)
+        assert api.last_path() == 1
+        want, tol = far_bounds(q, k, v, u, u)
+        assert (np.abs(f64(o) - want[0]) <= tol[0]).all(), step
+        assert (np.abs(f64(lse) - want[1]) <= tol[1]).all(), step
