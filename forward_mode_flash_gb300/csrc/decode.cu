@@ -45,21 +45,20 @@
 //
 // e4m3 caches: codes are converted to fp16 exactly.  The key scale 2^(ek-127)
 // multiplies the logit.  The value scale goes into the exponent of the weight,
-// w_j = 2^(x_j + ev_j - 127 - mw) with its own running maximum mw (x_j the
+// w_j = 2^((x_j - m) + ev_j - 127 - mw) with its own running base mw (x_j the
 // logit in log2 units), so no range of scales over- or underflows; the output
-// is 2^(mw - m) sum w_j vc_j / l.  Queries become fp16 after a power-of-two
+// is 2^mw sum w_j vc_j / l.  Queries become fp16 after a power-of-two
 // normalisation per head (their largest magnitude to [2^14, 2^15)), so bf16
 // queries of any magnitude keep their 8 bits.
 //
 // Rounding: the weights are rounded to 16 bits for the matrix product, fp16 ones
 // scaled by 2^11 and with a maximum that moves past 2^4.9 (61148 at most): they
-// keep their 11 bits down to 2^-25 of a row's largest and become 0 below 2^-36. (The
-// base m - 11 of the exponents is kept as rounded, and compared by differences,
-// so that large logits take no weight past its range.)
-// (bf16 weights need no scale; their maximum moves past 2^8.)  With a 16-bit
-// cache the row sum adds the same rounded weights, so the output is the exact
-// average under slightly perturbed weights; the log-sum-exp uses the unrounded
-// sum.
+// keep their 11 bits down to 2^-25 of a row's largest and become 0 below 2^-36.
+// (The base m - 11 of the exponents is kept as rounded, and compared by
+// differences, so that large logits take no weight past its range.  bf16 weights
+// need no scale; their maximum moves past 2^8.)  With a 16-bit cache the row sum
+// adds the same rounded weights, so the output is the exact average under
+// slightly perturbed weights; the log-sum-exp uses the unrounded sum.
 #include <cmath>
 
 #include "debug_checks.cuh"
@@ -584,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
         // The bases of the exponents move only where a weight would pass 2^kTop
         // (ratios are exact for any base): one vote, and the reductions over
         // the keys only then.  (Over e4m3 m is the base of the row sum, which
-        // is fp32, and mw that of the weights; else they are the same.)
+        // is fp32, and mw that of the weights, relative to m: beside a large
+        // logit fp32 would not hold a value's exponent.  Else m is both.)
         bool need = false;
 #pragma unroll
         for (int r = 0; r < 2 * RG; ++r)
@@ -592,29 +592,30 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           for (int i = 0; i < 2; ++i) {
             const float y = sc[r / 2][n][2 * (r & 1) + i] * (E4M3 ? kscale[r] * qs[n][i] : qs[n][i]);
             x[r][i] = kept(g + 8 * r) ? y : -INFINITY;
-            need |= x[r][i] - m[n][i] > (E4M3 ? 8.f : kTop);
-            if constexpr (E4M3) need |= x[r][i] + vexp[r] - mw[n][i] > kTop;
+            const float above = x[r][i] - m[n][i];
+            need |= above > (E4M3 ? 8.f : kTop);
+            if constexpr (E4M3) need |= above + (vexp[r] - mw[n][i]) > kTop;
           }
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = -INFINITY, topw = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < 2 * RG; ++r) {
-              top = fmaxf(top, x[r][i]);
-              if constexpr (E4M3) topw = fmaxf(topw, x[r][i] + vexp[r]);
-            }
+            for (int r = 0; r < 2 * RG; ++r) top = fmaxf(top, x[r][i]);
             top = max_over_g(top);
             const float m_new = fmaxf(m[n][i], E4M3 ? top : base(top));
-            float a = m_new == m[n][i] ? 1.f : exp2f(m[n][i] - m_new);
+            const float move = m_new == m[n][i] ? 0.f : m[n][i] - m_new;
+            float a = exp2f(move);
             m[n][i] = m_new;
             l[n][i] *= a, lx[n][i] *= a;
             if constexpr (E4M3) {
-              const float mw_new = fmaxf(mw[n][i], base(max_over_g(topw)));
-              a = mw_new == mw[n][i] ? 1.f : exp2f(mw[n][i] - mw_new);
+              float topw = -INFINITY;
+#pragma unroll
+              for (int r = 0; r < 2 * RG; ++r) topw = fmaxf(topw, (x[r][i] - m_new) + vexp[r]);
+              const float mw_old = mw[n][i] + move;
+              const float mw_new = fmaxf(mw_old, base(max_over_g(topw)));
+              a = mw_new == mw_old ? 1.f : exp2f(mw_old - mw_new);
               mw[n][i] = mw_new;
-            } else {
-              mw[n][i] = m_new;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -631,9 +632,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           for (int r = 0; r < 2 * RG; ++r) {
             if constexpr (E4M3) {
               l[n][i] += ex2_approx(x[r][i] - mu);
-              pw[r][i] = ex2_approx(x[r][i] + vexp[r] - mwu);
+              pw[r][i] = ex2_approx((x[r][i] - mu) + (vexp[r] - mwu));
             } else {
-              pw[r][i] = ex2_approx(x[r][i] - mwu);
+              pw[r][i] = ex2_approx(x[r][i] - mu);
             }
           }
         }
@@ -717,15 +718,18 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float4 st = from.stat[n * 2 + i][t];
-          const float M = fmaxf(m[n][i], st.x), mu = M == -INFINITY ? 0.f : M;
-          const float a = exp2f(m[n][i] - mu), b = exp2f(st.x - mu);
+          const float mine = m[n][i], M = fmaxf(mine, st.x), mu = M == -INFINITY ? 0.f : M;
+          const float a = exp2f(mine - mu), b = exp2f(st.x - mu);
           l[n][i] = a * l[n][i] + b * st.z;
           lx[n][i] = a * lx[n][i] + b * st.w;
           m[n][i] = M;
-          const float W = fmaxf(mw[n][i], st.y), wu = W == -INFINITY ? 0.f : W;
-          own[i] = E4M3 ? exp2f(mw[n][i] - wu) : a;
-          oth[i] = E4M3 ? exp2f(st.y - wu) : b;
-          mw[n][i] = W;
+          own[i] = a, oth[i] = b;
+          if constexpr (E4M3) {
+            const float u = mw[n][i] + (mine - mu), v = st.y + (st.x - mu);
+            const float W = fmaxf(u, v), wu = W == -INFINITY ? 0.f : W;
+            own[i] = exp2f(u - wu), oth[i] = exp2f(v - wu);
+            mw[n][i] = W;
+          }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -756,9 +760,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
           const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i];
           // (l may be NaN: a NaN among the logits reaches every output of the
           // row.  With a 16-bit cache l and the accumulator have the same
-          // exponent; mw - m is 0 there.)
+          // base.)
           float f = l[n][i] == 0.f ? 0.f : 1.f / l[n][i];
-          if (E4M3) f *= mw[n][i] == -INFINITY ? 0.f : exp2f(mw[n][i] - mu);
+          if (E4M3) f *= exp2f(mw[n][i]);  // (0 without keys)
           const float lse = lx[n][i] == 0.f ? -INFINITY
                             : E4M3          ? mu + log2f(lx[n][i])
                                             : mu + kShift + log2f(lx[n][i] * kUnshift);

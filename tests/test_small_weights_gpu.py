@@ -182,3 +182,30 @@ def test_single_tokens_with_large_logits(dt, H, D, power):
         want, tol = far_bounds(q, k, v, u, u)
         assert (np.abs(f64(o) - want[0]) <= tol[0]).all(), step
         assert (np.abs(f64(lse) - want[1]) <= tol[1]).all(), step
+
+
+@pytest.mark.parametrize("power", [12, 20, 23, 24, 25, 26, 27])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 250])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_value_scales_beside_large_logits(dt, n, D, power):
+    """An e4m3 cache whose rows of values have scales of their own."""
+    at, page, B, H, u = n * 4 // 5, 16, 3, 2, torch.finfo(DT[dt]).eps / 2
+    most = -(-n // page)
+    for step in steps(power):
+        q, k, v = far_logits(n, power, step, at, D, dt)
+        v *= torch.exp2(torch.arange(n) * 7 % 9 - 4.0)[:, None]
+        kc, vc = (torch.zeros(most, 1, page, D, device="cuda").to(torch.float8_e4m3fn)
+                  for _ in range(2))
+        ks, vs = (torch.zeros(kc.shape[:3], dtype=torch.uint8, device="cuda") for _ in range(2))
+        table = torch.arange(most, dtype=torch.int32, device="cuda")
+        api.cache_write(k[:, None].cuda(), v[:, None].cuda(), kc, vc, table[None], k_scale=ks, v_scale=vs,
+                        cu_seqlens=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+        o, lse = api.attention_decode(q.expand(B, H, D).contiguous().cuda(), kc, vc,
+                                      table.expand(B, most).contiguous(),
+                                      torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                                      k_scale=ks, v_scale=vs, scale=unit_scale(), return_lse=True)
+        assert api.last_path() == 1
+        want, tol = far_bounds(q, k, v, u, 2.0 ** -11)
+        assert (np.abs(f64(o) - want[0]) <= tol[0]).all(), step
+        assert (np.abs(f64(lse) - want[1]) <= tol[1]).all(), step
