@@ -285,6 +285,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensors<8> t(kDecode, a + 1);
     const Plan* plan = t.plan();
     if (!plan) return none();
+    // (by value: an allocation may run Python code, which may remember layouts)
+    const int64_t need = plan->workspace;
     auto* f = entry<decltype(jvp_attn_decode)>(a[0]);
     const at::Tensor* given = tensor(a[9]);
     const bool want_lse = truth(a[11]);
@@ -295,7 +297,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor lse, ws;
     if (want_lse) lse = empty({q.size(0), q.size(1)}, at::kFloat, q.device());
     if (given) ws = *given;
-    else if (plan->workspace > 0) ws = empty({plan->workspace}, at::kByte, q.device());
+    else if (need > 0) ws = empty({need}, at::kByte, q.device());
     const size_t bytes = ws.defined() ? ws.nbytes() : 0;
     const jvp_strides_t qs = token_strides(q), os = token_strides(o);
     const int st = call(q.device(), [&](void* stream) {
