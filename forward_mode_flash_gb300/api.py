@@ -560,7 +560,7 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     attend to each other only (``is_causal``: row i to rows j <= i).  Returns o
     [T, H, D], or (o, lse) with ``return_lse`` (float32 [H, T]).  Rows that
     belong to no sequence are not written (give ``out`` to keep what it holds).
-    Forward only, as ``attention``.
+    Forward only, as ``attention``: no gradient or tangent passes through.
     """
     bind, entry = _native("jvp_attn_fwd_packed")
     r = bind.packed(entry, q, k, v, cu_seqlens, out, is_causal, scale, return_lse)
@@ -694,7 +694,8 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     attention).  Returns o [B, H, D], or (o, lse) with ``return_lse`` (float32
     [B, H]); a sequence without keys gets o = 0 and lse = -inf.  ``workspace``
     (uint8, 16-byte aligned, ``decode_workspace_size`` bytes) is allocated here
-    if not given; calls that share one must not overlap.
+    if not given; calls that share one must not overlap.  Forward only, as
+    ``attention_packed``.
     """
     if workspace is not None and (workspace.device != k_cache.device
                                   or not workspace.is_contiguous()):

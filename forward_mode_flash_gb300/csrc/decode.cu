@@ -5,15 +5,16 @@
 //   s_j = scale q . k_j,  o = sum_j exp(s_j - m) v_j / l,  lse = m + log l,
 // with the running maximum m and sum l of an online softmax (fp32).
 //
-// Bound: memory.  Every cached row is read once by the query heads of its
-// group; nothing is reused beyond that, so what counts is bytes in flight: each
-// warp keeps its own ring of row groups in shared memory, filled by 16-byte
-// asynchronous copies some groups ahead, and no warp waits for another until
-// the end of a segment.  Measured with the join: fp16, sequences of 131072 and
-// 78806 keys, 8 heads of 64: 70 us, 90 % of the copy rate; bf16, 48 of 18 to 4096
-// keys, 16/4 heads of 128: 43 us, 72 %; e4m3, 64 of 334 to 16384 keys, 16/2
-// heads of 128: 57.5 us, 70 % (5 us of the latter two are the join's latency,
-// 2 to 3 the lookups in front of the first copies).
+// Bound: memory.  Every cached row is read once by each block of query heads of
+// its group (up to 16 on the tensor cores, 4 on the CUDA cores); nothing is
+// reused beyond that, so what counts is bytes in flight: each warp keeps its own
+// ring of row groups in shared memory, filled by 16-byte asynchronous copies some
+// groups ahead, and no warp waits for another until the end of a segment.
+// Measured with the join, in a CUDA graph: fp16, sequences of 131072 and 78806
+// keys, 8 heads of 64: 68 us, 93 % of the copy rate; bf16, 48 of 18 to 4096 keys,
+// 16/4 heads of 128: 41 us, 74 %; e4m3, 64 of 334 to 16384 keys, 16/2 heads of
+// 128: 57.6 us, 70 % (5 us of the latter two are the join's latency, 2 to 3 the
+// lookups in front of the first copies).
 //
 // Split: the work is the list of key tiles of all (sequence, key/value head,
 // block of query heads) segments, in that order, and CTA c takes the c-th of
@@ -25,7 +26,10 @@
 // slots per CTA, and the join kernel combines them in a fixed order (no
 // atomics: results do not depend on timing).  Where no sequence can have more
 // than a few tiles (a small block table), a CTA takes a whole segment and there
-// is no second kernel.
+// is no second kernel.  (The host knows the table's width, not the lengths: 130
+// keys, bf16, 16/4 heads of 128, take 5.2 us in a graph with a table of up to 16
+// pages of 16, 6.8 us with any wider one.)  Parts are joined by log-sum-exps in
+// fp32, so their shares are as exact as fp32 logits are.
 //
 // Tensor-core path (mma.sync m16n8k16): the products are formed transposed,
 // S^T = K Q^T and O^T = V^T P^T, so that the 16 rows of the instruction are
@@ -811,10 +815,13 @@ __global__ void __launch_bounds__(kThreads, decode_ctas_per_sm(DPAD, NG, E4M3))
 // of them takes the columns 4 (t + LK u) .. + 3), so a warp takes 8 or 4 keys at
 // once; it loads the next ones' rows before it works on these.  A CTA takes HPB
 // query heads, each lane summing its own keys' weighted values until the end of
-// the piece.  Measured, fp32 caches: 60000 keys of 8 ungrouped heads of 128 in
-// 78 us, 92 % of the copy rate (four CTAs per SM; three: 90 %); 16 sequences of
-// 500 to 4000 keys, 8 heads on 2 of 128, 28 us, 46 % (three; four, of 128
-// registers a thread: 34 us): grouped heads are bound by the arithmetic.
+// the piece.  Measured in a CUDA graph, fp32 caches: 60000 keys of 8 ungrouped
+// heads of 128 in 79 us, 91 % of the copy rate (four CTAs per SM; three: 90 %); 16
+// sequences of 500 to 4000 keys, 8 heads on 2 of 128, 28 us, 46 % (three; four, of
+// 128 registers a thread: 34 us).  The latter has some ten rounds a warp, each
+// waiting for rows that were asked for one round ahead, and a start and a join;
+// its FMAs are 2 us.  bf16, 48 of 4000 keys, 16/4 heads: rows of 100, 115 us, 39 %;
+// rows of 128 off their 16-byte alignment (single loads), 277 us, 21 %.
 template <typename T>
 struct Raw {  // four columns as stored
   uint32_t w[sizeof(T)];

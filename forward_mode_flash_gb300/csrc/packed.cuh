@@ -16,8 +16,10 @@ struct PackedTile {
 // goes with its sequence's length, and up to 32 sequences are taken longest
 // first (16 of 90 to 1024 tokens, 8 heads, D = 64: 37.1 against 39.6 us).  The
 // same over the tiles of causal sequences, last tiles of all first, is slower
-// (66.0 against 63.7 us, 4 of 2048 tokens, 16/4 heads, D = 128).  Executed by a whole
-// warp; false where the list has fewer tiles.  Offsets outside 0 <= cu[b] <=
+// (66.0 against 63.7 us, 4 of 2048 tokens, 16/4 heads, D = 128).  Beyond 32
+// sequences, and for causal ones, the offsets before the tile's sequence are
+// walked, 32 at a time: every block's start takes longer with many sequences.
+// Executed by a whole warp; false where the list has fewer tiles.  Offsets outside 0 <= cu[b] <=
 // cu[b + 1] <= T make an empty sequence and are recorded by the block u = 0.
 __device__ __forceinline__ bool find_packed_tile(const int* cu, int B, int T, int rows, int u,
                                                  bool last_first, unsigned int* status,

@@ -9,12 +9,15 @@
 // padded by 4 floats so that 16 lanes' rows hit distinct banks) and then a
 // 4 x D/16 piece of O.  Either product reads 8 x 16 bytes of shared memory for
 // 64 FMAs, issued as pairs (10 % less time: the rest of the loop wants the issue
-// slots).  Bound by fp32 FMA issue.  float32 tiles are copied asynchronously,
+// slots).  Bound by those reads (on long prompts the shared-memory pipe is 69 %
+// active, the FMA pipe 55 %).  float32 tiles are copied asynchronously,
 // K's next tile during the softmax and the second product, V's during the next
 // scores.  Measured, causal: eight prompts of about 1000 tokens, 8/8 heads of
 // 64: 273 us, 31 TFLOP/s of counted products (those of tiles that the mask cuts
 // are formed whole); four of 125 to 700 tokens, 8/2 heads of 64: 55 us, where
-// the FMAs alone take 13 (the last wave is short).
+// the FMAs alone take 13 (the last wave is short).  16-bit rows that the tensor
+// cores cannot take (converted while they are loaded, not copied): bf16, eight of
+// 1024 tokens, 8/8 heads of 60: 355 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

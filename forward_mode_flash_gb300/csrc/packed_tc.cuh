@@ -57,10 +57,11 @@
 // tensor work at 128 bytes a cycle, and copies write 32 KB more); at D = 64 the
 // exponentials and the rest of the softmax; prompts of a few tiles, a CTA's
 // beginning and end (about 3 us of set-up, first loads and stores).  Measured,
-// bf16, 16/2 heads of 128, causal, 16384 and 10101 tokens: 914 us, 1660 TFLOP/s
-// (tensor pipe 70 % active); fp16, 16/16 heads of 64, 8192 tokens: 290 us, 946
-// TFLOP/s; bf16, 16/4 heads of 128, causal, twelve of 166 to 2048 tokens: 88 us,
-// 896 TFLOP/s.  Measured and not kept: a persistent CTA that takes over blocks
+// bf16, 16/2 heads of 128, causal, 16384 and 10101 tokens: 914 us in short runs,
+// 1660 TFLOP/s (tensor pipe 70 % active), 980 us after a second, under the power
+// cap; fp16, 16/16 heads of 64, 8192 tokens: 293 us, 938 TFLOP/s; bf16, 16/4
+// heads of 128, causal, twelve of 166 to 2048 tokens: 88 us, 896 TFLOP/s.
+// Measured and not kept: a persistent CTA that takes over blocks
 // through the launch control (8 % slower on long prompts: its item rings keep
 // more warps polling; 20 % faster on prompts of one tile); at D = 128, one
 // issuing warp per query tile (the tiles' products interleave and both scores

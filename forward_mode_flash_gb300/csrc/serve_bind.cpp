@@ -2,10 +2,14 @@
 // prompts, paged cache, single-token attention) as a native module.
 //
 // These calls are short: through ctypes one took 10 to 19 us of host time for
-// 3 to 5 us on the GPU, from here 4 to 7.  This module reads the tensors' layouts, allocates the
-// outputs and calls the C ABI in one step.  It checks nothing itself: a call is
-// made only for layouts (types, devices, sizes, strides) that were `remember`ed
-// after Python has checked them; for any other it returns None.
+// 3 to 5 us on the GPU, from here 4 to 7.  This module reads the tensors' layouts,
+// allocates the outputs and calls the C ABI in one step.  It checks nothing
+// itself: a call is made only for layouts (types, devices, sizes, strides) that
+// were `remember`ed after Python has checked them; for any other it returns None.
+// So these times are of layouts that recur.  A call with another number of rows
+// or another width of the block table than before is checked in full: 12 us
+// (packed prompts), 14 (rows written), 27 (single tokens).  At 512 layouts all are
+// forgotten.
 //
 // Entry points are passed as addresses, since a process may have two builds of
 // the library loaded.

@@ -461,7 +461,8 @@ typedef struct {
  * of two 2^e, -127 <= e <= 120, with top <= 448 * 2^e, and each entry is
  * x / 2^e (exact) rounded to the nearest e4m3 value, ties to even.  A NaN
  * stays NaN and is not counted in top; an infinity takes e = 120 and reads
- * back as an infinity.  Rows whose place is out of range are skipped (see
+ * back as an infinity (as do magnitudes from 31/32 of 2^128 on, which the nearest
+ * e4m3 value takes to 2^128).  Rows whose place is out of range are skipped (see
  * above).  No two rows of a call may have the same place: the pages that a
  * call writes belong to one sequence each (sequences may share pages that
  * hold a common prefix and are only read).  Hkv must be at most 2^30 - 65, here
