@@ -43,6 +43,10 @@ EXPORTS = (
     "jvp_attn_cache_read",
     "jvp_attn_decode",
     "jvp_attn_decode_workspace_size",
+    "jvp_attn_norm_rope",
+    "jvp_attn_norm_rope_bwd",
+    "jvp_attn_norm_rope_bwd_workspace_size",
+    "jvp_attn_cache_append",
     "jvp_attn_get_device_status",
     "jvp_attn_status_string",
     "jvp_attn_last_error",
@@ -82,6 +86,14 @@ class Cache(ctypes.Structure):
                 ("D", ctypes.c_int64), ("B", ctypes.c_int64), ("max_pages", ctypes.c_int64),
                 ("table_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("k_strides", Strides), ("v_strides", Strides)]
+
+
+class Rope(ctypes.Structure):
+    # angles and norm weights of queries and keys (jvp_rope_t)
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("interleaved", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -167,6 +179,24 @@ def load(path: str | None = None):
         lib.jvp_attn_decode.restype = i32
         lib.jvp_attn_decode_workspace_size.argtypes = [CP, i64, i32]
         lib.jvp_attn_decode_workspace_size.restype = ctypes.c_size_t
+        RP = ctypes.POINTER(Rope)
+        # shape, dtype, rope, positions, their stride, q k dq dk, in_strides, outputs,
+        # out_strides, stream
+        lib.jvp_attn_norm_rope.argtypes = [SP, i32, RP, vp, i64] + [vp] * 4 + [STP] + [vp] * 4 + \
+            [STP, vp]
+        lib.jvp_attn_norm_rope.restype = i32
+        # ..., q k dq dk g_q g_k g_dq g_dk, in_strides, gradients, out_strides,
+        # g_q_weight, g_k_weight, workspace, bytes, stream
+        lib.jvp_attn_norm_rope_bwd.argtypes = [SP, i32, RP, vp, i64] + [vp] * 8 + [STP] + \
+            [vp] * 4 + [STP, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.jvp_attn_norm_rope_bwd.restype = i32
+        lib.jvp_attn_norm_rope_bwd_workspace_size.argtypes = [i64]
+        lib.jvp_attn_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+        # cache, H, dtype, T, q, k, v, in_strides, rope, block_table, start_pos,
+        # cu_seqlens, q_out, its strides, k_cache, v_cache, k_scale, v_scale, stream
+        lib.jvp_attn_cache_append.argtypes = [CP, i64, i32, i64, vp, vp, vp, STP, RP] + [vp] * 4 + \
+            [STP] + [vp] * 5
+        lib.jvp_attn_cache_append.restype = i32
         lib.jvp_attn_get_device_status.argtypes = [vp]
         lib.jvp_attn_get_device_status.restype = i32
         lib.jvp_attn_status_string.argtypes = [i32]
@@ -184,7 +214,8 @@ def load(path: str | None = None):
         # addresses of the entry points that the native part of the binding calls
         lib.addresses = {n: ctypes.cast(getattr(lib, n), vp).value
                          for n in ("jvp_attn_fwd_packed", "jvp_attn_cache_write",
-                                   "jvp_attn_cache_read", "jvp_attn_decode")}
+                                   "jvp_attn_cache_read", "jvp_attn_decode", "jvp_attn_norm_rope",
+                                   "jvp_attn_norm_rope_bwd", "jvp_attn_cache_append")}
         _libs[p] = lib
         return lib
 

@@ -728,6 +728,204 @@ def decode_workspace_size(k_cache: torch.Tensor, block_table: torch.Tensor, H: i
         return int(_abi.load().jvp_attn_decode_workspace_size(desc, int(H), _DT[dtype]))
 
 
+# ---- norms of queries and keys per head, and rotation by position
+def rope_table(num_positions: int, dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """Angles for ``norm_rope`` and ``cache_append``: float32 [num_positions, dim].
+
+    Row p holds the cosines, then the sines, of p * base**(-2 i / dim), i < dim / 2,
+    computed in 64 bits.  Any other table of this layout will do (scaled
+    frequencies, positions with several axes).
+    """
+    if dim < 2 or dim % 2:
+        raise ValueError(f"dim must be even and positive, got {dim}")
+    i = torch.arange(dim // 2, dtype=torch.float64, device=device)
+    p = torch.arange(num_positions, dtype=torch.float64, device=device)
+    a = p[:, None] * torch.exp(i * (-2.0 * math.log(base) / dim))
+    return torch.cat((a.cos(), a.sin()), 1).float()
+
+
+def _check_rope(rope, q_weight, k_weight, D, device):
+    if rope is None and q_weight is None and k_weight is None:
+        raise ValueError("neither rope nor norm weights are given")
+    if rope is not None:
+        if (rope.dim() != 2 or rope.dtype != torch.float32 or rope.device != device
+                or not rope.is_contiguous()):
+            raise ValueError(f"rope must be a contiguous float32 [positions, dim] tensor on {device}")
+        if rope.shape[1] % 2 or not 0 < rope.shape[1] <= D:
+            raise ValueError(f"rope must have an even number of columns of at most {D}, got "
+                             f"{rope.shape[1]}")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if q_weight is not None:
+        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if tuple(t.shape) != (D,) or t.device != device or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous [{D}] tensor on {device}")
+            if t.dtype not in _DT or t.dtype != q_weight.dtype:
+                raise TypeError("q_weight and k_weight must be float32, float16 or bfloat16, both alike")
+
+
+def _check_norm_rope(q, k, dq, dk, rope, positions, q_weight, k_weight, cotangents=()):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, H, N, D]")
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if q.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    B, _, N, D = q.shape
+    if k.shape[0] != B or k.shape[2] != N or k.shape[3] != D:
+        raise ValueError(f"k must be [{B}, heads, {N}, {D}], got {tuple(k.shape)}")
+    if (dq is None) != (dk is None):
+        raise ValueError("dq and dk go together")
+    named = [("q", q, q), ("k", k, k)]
+    if dq is not None:
+        named += [("dq", dq, q), ("dk", dk, k)]
+    named += list(cotangents)
+    for n, t, like in named:
+        if t is None or t.shape != like.shape or t.dtype != q.dtype or t.device != q.device:
+            raise ValueError(f"{n} must be a {q.dtype} tensor {tuple(like.shape)} on {q.device}")
+        if t.stride(3) != 1 and t.numel() > 0 and D > 1:
+            raise ValueError(f"{n} must have a unit innermost stride")
+    _check_rope(rope, q_weight, k_weight, D, q.device)
+    if positions is not None:
+        if positions.dim() == 1:
+            raise ValueError(f"positions must be [{B}, {N}] (expand those that are shared)")
+        _check_int32(positions, "positions", (B, N), q.device)
+
+
+def _positions(positions, q):
+    """[N] as [B, N]."""
+    if positions is not None and positions.dim() == 1 and q.dim() == 4:
+        return positions.expand(q.shape[0], -1)
+    return positions
+
+
+def _rope_call(dq_dk, q, k, rope, positions, q_weight, k_weight, eps, interleaved):
+    bind, entry = _native("jvp_attn_norm_rope")
+    layout = (q, k, *dq_dk, rope, _positions(positions, q), q_weight, k_weight)
+    r = bind.rope(entry, *layout, eps, interleaved)
+    if r is None:  # a layout not seen before
+        _check_norm_rope(*layout)
+        bind.remember(bind.ROPE, 0, *layout)
+        r = bind.rope(entry, *layout, eps, interleaved)
+    if type(r) is int:
+        _abi.check(r)
+    return r
+
+
+def _rope_bwd_call(tensors, g, rope, positions, q_weight, k_weight, eps, interleaved):
+    bind, entry = _native("jvp_attn_norm_rope_bwd")
+    rest = (rope, _positions(positions, tensors[0]), q_weight, k_weight)
+    r = bind.rope_bwd(entry, *tensors, *g, *rest, eps, interleaved)
+    if r is None:  # a layout not seen before
+        q, k, dq, _ = tensors
+        names = (("g_q", g[0], q), ("g_k", g[1], k), ("g_dq", g[2], q), ("g_dk", g[3], k))
+        _check_norm_rope(*tensors, *rest, cotangents=names if dq is not None else names[:2])
+        with torch.cuda.device(q.device):
+            need = int(_abi.load().jvp_attn_norm_rope_bwd_workspace_size(q.shape[3]))
+        bind.remember(bind.ROPE_BWD, need, *tensors, *g, *rest)
+        r = bind.rope_bwd(entry, *tensors, *g, *rest, eps, interleaved)
+    if type(r) is int:
+        _abi.check(r)
+    return r
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+              k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+              interleaved: bool = False):
+    """Queries [B, H, N, D] and keys [B, Hkv, N, D] normalised per head and rotated by position.
+
+    Per row: x * rsqrt(mean(x**2) + eps) * weight over the head dimension (without
+    weights no norm), then the first ``rope.shape[1]`` columns rotated in pairs by the
+    angles of the row's position: ``rope`` is float32 [positions, dim], cosines then
+    sines (``rope_table``; None: no rotation); pairs are columns (i, i + dim / 2), or
+    (2 i, 2 i + 1) with ``interleaved``.  ``positions`` (int32 [N] or [B, N], on the
+    device) defaults to 0 .. N - 1; one that is no row of the table is reported by
+    ``device_status`` (JVP_ERR_INDEX), and the outputs' rows of its token are not
+    written.  Computed in float32; returns (q, k) in q's dtype.  ``autograd.norm_rope``
+    is the differentiable form.
+    """
+    return _rope_call((None, None), q, k, rope, positions, q_weight, k_weight, eps, interleaved)
+
+
+def norm_rope_dual(q: torch.Tensor, k: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor,
+                   rope: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                   q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   interleaved: bool = False):
+    """``norm_rope`` with tangents dq, dk of q and k: (q, k, dq, dk) from one pass."""
+    return _rope_call((dq, dk), q, k, rope, positions, q_weight, k_weight, eps, interleaved)
+
+
+def norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, g_q: torch.Tensor, g_k: torch.Tensor,
+                  rope: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                  q_weight: Optional[torch.Tensor] = None,
+                  k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  interleaved: bool = False):
+    """Gradients (q, k, q_weight, k_weight) of ``norm_rope`` for cotangents g_q, g_k.
+
+    Those of the weights are float32 (None without norms), summed in a fixed order.
+    """
+    return _rope_bwd_call((q, k, None, None), (g_q, g_k, None, None), rope, positions, q_weight,
+                          k_weight, eps, interleaved)
+
+
+def norm_rope_bwd_dual(q: torch.Tensor, k: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor,
+                       g_q: torch.Tensor, g_k: torch.Tensor, g_dq: torch.Tensor,
+                       g_dk: torch.Tensor, rope: Optional[torch.Tensor] = None,
+                       positions: Optional[torch.Tensor] = None,
+                       q_weight: Optional[torch.Tensor] = None,
+                       k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       interleaved: bool = False):
+    """Gradients (q, k, dq, dk, q_weight, k_weight) of ``norm_rope_dual``."""
+    return _rope_bwd_call((q, k, dq, dk), (g_q, g_k, g_dq, g_dk), rope, positions, q_weight,
+                          k_weight, eps, interleaved)
+
+
+def _check_append(q, k, v, k_cache, v_cache, block_table, rope, start_pos, cu_seqlens, q_weight,
+                  k_weight, k_scale, v_scale, out):
+    _check_rows(k, v, k_cache, v_cache, block_table, start_pos, cu_seqlens, k_scale, v_scale)
+    T, D, dev = k.shape[0], k_cache.shape[3], k_cache.device
+    H = q.shape[1] if q.dim() == 3 else -1
+    _check_packed(q, "q", k.dtype, dev, (T, H, D))
+    if out is not None:
+        _check_packed(out, "out", k.dtype, dev, (T, H, D))
+    _check_rope(rope, q_weight, k_weight, D, dev)
+
+
+def cache_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, block_table: torch.Tensor,
+                 rope: Optional[torch.Tensor] = None, start_pos: Optional[torch.Tensor] = None,
+                 cu_seqlens: Optional[torch.Tensor] = None,
+                 q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """``cache_write`` of keys that are normalised and rotated on the way, with the queries.
+
+    q is [T, H, D], k and v [T, Hkv, D]: the new rows as they leave their projections.
+    A row's position in its sequence (``start_pos[b]`` + its place among the sequence's
+    rows) is its row of ``rope``; rope, weights, eps and interleaved are those of
+    ``norm_rope``, and the rest of the arguments those of ``cache_write``.  Returns the
+    normalised and rotated queries [T, H, D] (``out`` if given), for
+    ``attention_chunk`` or ``attention_decode``.  The cache holds what ``norm_rope``
+    and ``cache_write`` would leave there.  Tokens whose place is out of range, or
+    whose position is no row of rope, are skipped whole and reported by
+    ``device_status`` (JVP_ERR_INDEX); rows that belong to no sequence are ignored.
+    """
+    bind, entry = _native("jvp_attn_cache_append")
+    layout = (q, k, v, k_cache, v_cache, block_table, rope, start_pos, cu_seqlens, q_weight,
+              k_weight, k_scale, v_scale, out)
+    r = bind.append(entry, *layout, eps, interleaved)
+    if r is None:  # a layout not seen before
+        _check_append(*layout)
+        bind.remember(bind.APPEND, 0, *layout)
+        r = bind.append(entry, *layout, eps, interleaved)
+    if type(r) is int:
+        _abi.check(r)
+    return r
+
+
 def device_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     """Synchronise the stream and return (and clear) the library's device status."""
     lib = _abi.load()

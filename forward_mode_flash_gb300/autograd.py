@@ -17,6 +17,11 @@ Mirrors the "JVP Flash Attention" project page (Usage section):
   forward-mode rule calls ``fwd_dual`` and whose backward calls the
   primal-only ``bwd`` (no tangent terms).
 
+* ``norm_rope(q, k, rope, ...)`` is what comes before attention: norms of
+  queries and keys per head and their rotation by position.  Under
+  torch.func.jvp one ``norm_rope_dual`` launch gives values and tangents, both
+  differentiable; elsewhere it back-propagates through ``norm_rope_bwd``.
+
 All arithmetic runs in the library's kernels; this module only wires them
 into autograd.
 """
@@ -84,6 +89,21 @@ class _FwdDual(torch.autograd.Function):
         return (*grads, None, None, None)
 
 
+def _record(function, *args):
+    """Applies an autograd.Function at the enclosing level of torch.func.
+
+    functorch's dispatch is off, and the single-level Function is applied
+    directly (torch.func would otherwise insist on handling the Function at this
+    level itself)."""
+    prev = _ft.get_single_level_autograd_function_allowed()
+    _ft.set_single_level_autograd_function_allowed(True)
+    try:
+        with torch._C._DisableFuncTorch():
+            return super(torch.autograd.Function, function).apply(*args)
+    finally:
+        _ft.set_single_level_autograd_function_allowed(prev)
+
+
 def _fused_under_jvp(q, k, v, attn_mask, is_causal, scale):
     """O as a forward-mode dual (O, tO) from one fused call, or None.
 
@@ -114,17 +134,7 @@ def _fused_under_jvp(q, k, v, attn_mask, is_causal, scale):
     mask = None if attn_mask is None else one_level(attn_mask)
     if any(_ft.is_functorch_wrapped_tensor(t) for t in (*ps, *ts) + ((mask,) if mask is not None else ())):
         return None  # nested transforms: the generic forward-mode rule handles them
-    # Record the node at the enclosing level: functorch's dispatch is off, and
-    # the single-level Function is applied directly (torch.func would otherwise
-    # insist on handling the Function at this level itself).
-    prev = _ft.get_single_level_autograd_function_allowed()
-    _ft.set_single_level_autograd_function_allowed(True)
-    try:
-        with torch._C._DisableFuncTorch():
-            o, t_o = super(torch.autograd.Function, _FwdDual).apply(
-                *ps, *ts, mask, is_causal, scale)
-    finally:
-        _ft.set_single_level_autograd_function_allowed(prev)
+    o, t_o = _record(_FwdDual, *ps, *ts, mask, is_causal, scale)
     return fwAD.make_dual(_ft._wrap_for_grad(o, level), _ft._wrap_for_grad(t_o, level))
 
 
@@ -196,3 +206,111 @@ def jvp_attention(q, k, v, attn_mask: Optional[torch.Tensor] = None, is_causal: 
         return fused
     o, _ = JVPAttn.apply(q, k, v, attn_mask, is_causal, scale)
     return o
+
+
+# ---- norms of queries and keys, and rotation
+def _weight_grads(g, weights):
+    return tuple(None if w is None else x.to(w.dtype) for x, w in zip(g, weights))
+
+
+class _NormRopeDual(torch.autograd.Function):
+    """(q, k, dq, dk) of one norm_rope_dual call; backward = reverse mode of the dual map."""
+
+    @staticmethod
+    def forward(ctx, q, k, dq, dk, q_weight, k_weight, rope, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, dq, dk, q_weight, k_weight, rope, positions)
+        ctx.options = eps, interleaved
+        return api.norm_rope_dual(q, k, dq, dk, rope, positions, q_weight, k_weight, eps,
+                                  interleaved)
+
+    @staticmethod
+    def backward(ctx, *g):
+        q, k, dq, dk, q_weight, k_weight, rope, positions = ctx.saved_tensors
+        g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k, q, k))]
+        out = api.norm_rope_bwd_dual(q, k, dq, dk, *g, rope, positions, q_weight, k_weight,
+                                     *ctx.options)
+        return (*out[:4], *_weight_grads(out[4:], (q_weight, k_weight)), None, None, None, None)
+
+
+class _NormRope(torch.autograd.Function):
+    """norm_rope with a forward-mode rule backed by norm_rope_dual."""
+
+    @staticmethod
+    def forward(q, k, q_weight, k_weight, rope, positions, eps, interleaved):
+        return api.norm_rope(q, k, rope, positions, q_weight, k_weight, eps, interleaved)
+
+    @staticmethod
+    def setup_context(ctx, inputs, output):
+        ctx.save_for_forward(*inputs[:6])
+        ctx.save_for_backward(*inputs[:6])
+        ctx.options = inputs[6:]
+
+    @staticmethod
+    def jvp(ctx, dq, dk, dqw, dkw, *_):
+        with torch._C._DisableFuncTorch():  # (as in JVPAttn.jvp)
+            q, k, q_weight, k_weight, rope, positions = (_plain(t) for t in ctx.saved_tensors)
+            dq, dk = (_zeros_if_none(_plain(t), x) for t, x in ((dq, q), (dk, k)))
+            t = api.norm_rope_dual(q, k, dq, dk, rope, positions, q_weight, k_weight,
+                                   *ctx.options)[2:]
+            if dqw is not None or dkw is not None:  # the outputs are linear in the weights
+                dw = [_zeros_if_none(_plain(x), w) for x, w in ((dqw, q_weight), (dkw, k_weight))]
+                more = api.norm_rope(q, k, rope, positions, *dw, *ctx.options)
+                t = tuple(x + y for x, y in zip(t, more))
+        return t
+
+    @staticmethod
+    def backward(ctx, *g):
+        q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
+        g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k))]
+        out = api.norm_rope_bwd(q, k, *g, rope, positions, q_weight, k_weight, *ctx.options)
+        return (*out[:2], *_weight_grads(out[2:], (q_weight, k_weight)), None, None, None, None)
+
+
+def _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved):
+    """(q, k) as forward-mode duals from one fused call, or None (see _fused_under_jvp)."""
+    level = _ft.maybe_current_level()
+    if level is None:
+        return None
+
+    def here(x):
+        return _ft.is_functorch_wrapped_tensor(x) and _ft.maybe_get_level(x) == level
+
+    def one_level(t):
+        return _ft.get_unwrapped(t) if t is not None and _ft.is_functorch_wrapped_tensor(t) else t
+
+    if not here(q) or not here(k):
+        return None
+    xs = (q, k, q_weight, k_weight)
+    pairs = [fwAD.unpack_dual(x) if x is not None and here(x) else (x, None) for x in xs]
+    if all(t is None for _, t in pairs):
+        return None
+    ps, ts = ([one_level(x[i]) for x in pairs] for i in (0, 1))
+    rest = (one_level(rope), one_level(positions))
+    if any(t is not None and _ft.is_functorch_wrapped_tensor(t) for t in (*ps, *ts, *rest)):
+        return None  # nested transforms: the generic forward-mode rule handles them
+    with torch._C._DisableFuncTorch():
+        d = [_zeros_if_none(t, p) for t, p in zip(ts[:2], ps[:2])]
+    y = _record(_NormRopeDual, *ps[:2], *d, *ps[2:], *rest, eps, interleaved)
+    out, tangents = y[:2], y[2:]
+    if ts[2] is not None or ts[3] is not None:  # the outputs are linear in the weights
+        with torch._C._DisableFuncTorch():
+            dw = [_zeros_if_none(t, w) for t, w in zip(ts[2:], ps[2:])]
+        more = _record(_NormRope, *ps[:2], *dw, *rest, eps, interleaved)
+        with torch._C._DisableFuncTorch():
+            tangents = tuple(x + z for x, z in zip(tangents, more))
+    return tuple(fwAD.make_dual(_ft._wrap_for_grad(o, level), _ft._wrap_for_grad(t, level))
+                 for o, t in zip(out, tangents))
+
+
+def norm_rope(q, k, rope: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, interleaved: bool = False):
+    """Differentiable ``api.norm_rope``: (q, k), for ``jvp_attention``.
+
+    Inside torch.func.jvp the outputs carry their tangents, from one fused pass, and
+    values and tangents are differentiable with respect to q, k, their tangents and
+    the norm weights (rope and positions are constants)."""
+    fused = _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
+    if fused is not None:
+        return fused
+    return _NormRope.apply(q, k, q_weight, k_weight, rope, positions, eps, interleaved)

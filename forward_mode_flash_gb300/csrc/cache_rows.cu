@@ -27,83 +27,21 @@
 
 #include "debug_checks.cuh"
 #include "paged.cuh"
+#include "rows.cuh"
 
 namespace jvp {
 namespace {
 
 constexpr int kWarps = 4;  // rows per block
 
-template <typename T>
-struct Rows;  // conversions of a row's element type
-template <>
-struct Rows<float> {
-  static __device__ __forceinline__ float get(float x) { return x; }
-  static __device__ __forceinline__ float put(float x) { return x; }
-};
-template <>
-struct Rows<__half> {
-  static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
-  static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
-};
-template <>
-struct Rows<__nv_bfloat16> {
-  static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-};
-
 // Looks at the offsets of one sequence per thread of the grid (which has as many).
 __device__ __forceinline__ void check_offsets(const CacheRowsParams& p) {
-  const long long i = static_cast<long long>(blockIdx.x) * (kWarps * 32) + threadIdx.x;
-  if (!p.cu || i >= p.c.B) return;
-  const int r0 = __ldg(p.cu + i), r1 = __ldg(p.cu + i + 1);
-  if (r0 < 0 || r1 < r0 || r1 > p.T) atomicOr(p.c.status, kStatusIndex);
+  check_sequence_offsets(p.c, p.cu, p.T,
+                         static_cast<long long>(blockIdx.x) * (kWarps * 32) + threadIdx.x);
 }
-
-// Where row r of the packed tensors lives in the cache: false if it belongs to
-// no sequence, or (recorded in the status word) its sequence's offsets or its
-// place are out of range.
 __device__ __forceinline__ bool locate(const CacheRowsParams& p, long long r, int* page, int* row) {
-  int b;
-  long long first;
-  if (p.cu) {
-    // last b with cu[b] <= r
-    int lo = -1, hi = p.c.B;  // cu[lo] <= r < cu[hi], the ends taken as given
-    while (hi - lo > 1) {
-      const int mid = lo + ((hi - lo) >> 1);  // (lo + hi may pass 2^31)
-      if (__ldg(p.cu + mid) <= r) lo = mid;
-      else hi = mid;
-    }
-    // rows before the first sequence and behind the last are in none
-    if (lo < 0) return false;
-    b = lo;
-    first = __ldg(p.cu + b);
-    const int end = __ldg(p.cu + b + 1);
-    if (end <= r || first < 0 || end > p.T) return false;  // (check_offsets records what is wrong)
-  } else {
-    b = static_cast<int>(r);
-    first = r;
-  }
-  const long long pos = (p.start ? static_cast<long long>(__ldg(p.start + b)) : 0ll) + (r - first);
-  const long long most = static_cast<long long>(p.c.max_pages) * p.c.page_size;
-  if (pos < 0 || pos >= most) {
-    atomicOr(p.c.status, kStatusIndex);
-    return false;
-  }
-  int entry;
-  split_position(p.c, static_cast<int>(pos), &entry, row);
-  *page = page_of(p.c, b, entry);
-  return *page >= 0;
-}
-
-// Biased exponent (the scale byte) for a row whose largest magnitude is top.
-__device__ __forceinline__ unsigned scale_byte(float top) {
-  const unsigned bits = __float_as_uint(top);
-  const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return e < 0 ? 0u : static_cast<unsigned>(e);
-}
-
-__device__ __forceinline__ uint16_t to_e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  int pos;
+  return locate_row(p.c, p.cu, p.start, p.T, r, page, row, &pos);
 }
 
 // Largest magnitude of a group of LANES lanes' PC 16-byte pieces of a row (NaN

@@ -186,7 +186,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
   return nullptr;
 }
 
-enum Op : int64_t { kPacked, kWrite, kRead, kDecode };
+enum Op : int64_t { kPacked, kWrite, kRead, kDecode, kRope, kRopeBwd, kAppend };
 
 // remember(op, workspace bytes, tensors ...): the layouts of these arguments
 // have been checked.
@@ -315,10 +315,134 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The angles and norm weights of a call: tensors (or none) and numbers.
+jvp_rope_t rope_of(const at::Tensor* table, const at::Tensor* qw, const at::Tensor* kw, PyObject* eps,
+                   PyObject* interleaved) {
+  jvp_rope_t r{};
+  if (table) r.table = data<float>(table), r.rows = table->size(0), r.dim = table->size(1);
+  r.interleaved = truth(interleaved) ? 1 : 0;
+  r.q_weight = data(qw), r.k_weight = data(kw);
+  if (qw) r.weight_dtype = dtype_code(qw->scalar_type());
+  const double e = PyFloat_AsDouble(eps);
+  if (e == -1.0 && PyErr_Occurred()) throw BadArgument();
+  r.eps = static_cast<float>(e);
+  return r;
+}
+jvp_strides_t strides_of(const at::Tensor* t) {
+  if (!t) return {0, 0, 0, 1};
+  return {t->stride(0), t->stride(1), t->stride(2), 1};
+}
+jvp_shape_t dense_shape(const at::Tensor& q, const at::Tensor& k) {
+  return {q.size(0), q.size(1), q.size(2), q.size(2), q.size(3), k.size(1)};
+}
+PyObject* results(int status, const std::vector<at::Tensor>& out) {
+  if (status != JVP_OK) return PyLong_FromLong(status);
+  PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(out.size()));
+  for (size_t i = 0; t && i < out.size(); ++i) {
+    PyObject* x = out[i].defined() ? THPVariable_Wrap(out[i]) : none();
+    if (!x) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(t, static_cast<Py_ssize_t>(i), x);
+  }
+  return t;
+}
+
+// rope(entry, q, k, dq, dk, table, positions, q_weight, k_weight, eps, interleaved):
+// the outputs for q and k (and, given dq and dk, for these)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const Tensors<8> t(kRope, a + 1);
+    if (!t.plan()) return none();
+    auto* f = entry<decltype(jvp_attn_norm_rope)>(a[0]);
+    const at::Tensor &q = t[0], &k = t[1];
+    const jvp_rope_t r = rope_of(t.t[4], t.t[6], t.t[7], a[9], a[10]);
+    const jvp_shape_t shape = dense_shape(q, k);
+    std::vector<at::Tensor> out;
+    jvp_strides_t in[4], os[4];
+    void* y[4] = {};
+    for (int i = 0; i < (t.t[2] ? 4 : 2); ++i)
+      out.push_back(empty(t[i].sizes(), q.scalar_type(), q.device()));
+    for (size_t i = 0; i < 4; ++i) {
+      const bool on = i < out.size();
+      os[i] = strides_of(on ? &out[i] : nullptr), y[i] = on ? data(&out[i]) : nullptr;
+      in[i] = strides_of(t.t[i]);
+    }
+    const at::Tensor* at = t.t[5];
+    return results(call(q.device(), [&](void* stream) {
+      return f(&shape, static_cast<jvp_dtype_t>(dtype_code(q.scalar_type())), &r, data<int32_t>(at),
+               at ? at->stride(0) : 0, data(&q), data(&k), data(t.t[2]), data(t.t[3]), in, y[0],
+               y[1], y[2], y[3], os, stream);
+    }), out);
+  });
+}
+
+// rope_bwd(entry, q, k, dq, dk, g_q, g_k, g_dq, g_dk, table, positions, q_weight,
+//          k_weight, eps, interleaved): gradients of q, k (, dq, dk), the weights
+PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    const Tensors<12> t(kRopeBwd, a + 1);
+    const Plan* plan = t.plan();
+    if (!plan) return none();
+    const int64_t need = plan->workspace;  // (by value, as in decode)
+    auto* f = entry<decltype(jvp_attn_norm_rope_bwd)>(a[0]);
+    const at::Tensor &q = t[0], &k = t[1];
+    const jvp_rope_t r = rope_of(t.t[8], t.t[10], t.t[11], a[13], a[14]);
+    const jvp_shape_t shape = dense_shape(q, k);
+    const size_t rows = t.t[2] ? 4 : 2;
+    std::vector<at::Tensor> out;
+    for (size_t i = 0; i < rows; ++i)
+      out.push_back(empty(t[static_cast<int>(i)].sizes(), q.scalar_type(), q.device()));
+    at::Tensor ws;
+    for (int i = 0; i < 2; ++i)
+      out.push_back(t.t[10] ? empty({shape.D}, at::kFloat, q.device()) : at::Tensor());
+    if (t.t[10]) ws = empty({need}, at::kByte, q.device());
+    jvp_strides_t in[8], os[4];
+    void* y[4] = {};
+    for (int i = 0; i < 8; ++i) in[i] = strides_of(t.t[i]);
+    for (size_t i = 0; i < 4; ++i)
+      os[i] = strides_of(i < rows ? &out[i] : nullptr), y[i] = i < rows ? data(&out[i]) : nullptr;
+    float* gw[2] = {};
+    for (int i = 0; i < 2; ++i) gw[i] = out[rows + i].defined() ? data<float>(&out[rows + i]) : nullptr;
+    const at::Tensor* at = t.t[9];
+    return results(call(q.device(), [&](void* stream) {
+      return f(&shape, static_cast<jvp_dtype_t>(dtype_code(q.scalar_type())), &r, data<int32_t>(at),
+               at ? at->stride(0) : 0, data(&q), data(&k), data(t.t[2]), data(t.t[3]), data(t.t[4]),
+               data(t.t[5]), data(t.t[6]), data(t.t[7]), in, y[0], y[1], y[2], y[3], os, gw[0],
+               gw[1], ws.defined() ? data(&ws) : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+    }), out);
+  });
+}
+
+// append(entry, q, k, v, k_cache, v_cache, block_table, table, start_pos, cu_seqlens,
+//        q_weight, k_weight, k_scale, v_scale, out, eps, interleaved): the queries
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const Tensors<14> t(kAppend, a + 1);
+    if (!t.plan()) return none();
+    auto* f = entry<decltype(jvp_attn_cache_append)>(a[0]);
+    const at::Tensor &q = t[0], &k = t[1], &v = t[2];
+    const jvp_cache_t c = cache(t[3], t[4], t[5]);
+    const jvp_rope_t r = rope_of(t.t[6], t.t[9], t.t[10], a[15], a[16]);
+    const at::Tensor o = t.t[13] ? t[13] : empty(q.sizes(), q.scalar_type(), q.device());
+    const jvp_strides_t in[3] = {row_strides(q), row_strides(k), row_strides(v)};
+    const jvp_strides_t os = row_strides(o);
+    const int st = call(q.device(), [&](void* stream) {
+      return f(&c, q.size(1), static_cast<jvp_dtype_t>(dtype_code(q.scalar_type())), q.size(0),
+               data(&q), data(&k), data(&v), in, &r, data<int32_t>(&t[5]), data<int32_t>(t.t[7]),
+               data<int32_t>(t.t[8]), data(&o), &os, data(&t[3]), data(&t[4]),
+               data<uint8_t>(t.t[11]), data<uint8_t>(t.t[12]), stream);
+    });
+    return result(st, o, o, false);
+  });
+}
+
 #define JVP_METHOD(f) \
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {JVP_METHOD(remember),   JVP_METHOD(packed), JVP_METHOD(write),
                          JVP_METHOD(read),       JVP_METHOD(decode), JVP_METHOD(empty_rows),
+                         JVP_METHOD(rope),       JVP_METHOD(rope_bwd), JVP_METHOD(append),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
@@ -327,8 +451,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_bind", nullptr, -1, methods
 
 PyMODINIT_FUNC PyInit__serve_bind() {
   PyObject* m = PyModule_Create(&module);
-  if (m && (PyModule_AddIntConstant(m, "PACKED", kPacked) || PyModule_AddIntConstant(m, "WRITE", kWrite) ||
-            PyModule_AddIntConstant(m, "READ", kRead) || PyModule_AddIntConstant(m, "DECODE", kDecode)))
-    Py_CLEAR(m);
+  const struct { const char* name; Op op; } ops[] = {
+      {"PACKED", kPacked}, {"WRITE", kWrite}, {"READ", kRead}, {"DECODE", kDecode},
+      {"ROPE", kRope}, {"ROPE_BWD", kRopeBwd}, {"APPEND", kAppend}};
+  for (const auto& o : ops)
+    if (m && PyModule_AddIntConstant(m, o.name, o.op))
+      Py_CLEAR(m);
   return m;
 }

@@ -47,6 +47,56 @@ struct CacheRowsParams {
 cudaError_t launch_cache_write(DType dt, bool e4m3, const CacheRowsParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(DType dt, bool e4m3, const CacheRowsParams& p, cudaStream_t stream);
 
+// Norms per head and rotation by position.
+struct RopeParams {
+  int D, rot;           // rot: rotated columns (even, at most D; 0: none)
+  int interleaved;      // pairs are neighbours, else half a rotation apart
+  int table_rows;
+  const float* table;   // [table_rows][rot]: cosines, then sines, of the pairs
+  const void *wq, *wk;  // [D] each, or nullptr both: no norms
+  int weight_type;      // DType of the weights
+  float eps, inv_d;
+  unsigned int* status;
+};
+// Dense rows [B, H, N, D].  Tensors by index: queries and keys (0, 1), their
+// tangents (2, 3), backward also cotangents (4, 5) and those of the tangents (6, 7).
+struct RopeDense {
+  RopeParams r;
+  long long tokens;  // B * N
+  int N, H, Hkv;
+  const int* positions;  // [B, N], or nullptr: 0 .. N - 1
+  long long positions_stride;
+  const void* x[8];
+  Strides in[8];
+  void* y[4];
+  Strides out[4];
+  int back;          // without norms: rotate back
+  float* ws;         // [blocks][2][D] sums of the weights' gradients
+  float *gwq, *gwk;  // [D]
+  long long units;   // set by the launch: warps' work
+  int heads_per_unit, head_chunks;
+};
+constexpr int rope_blocks_per_sm() { return 4; }  // at most, where blocks leave sums
+// vec: 16-byte aligned rows of whole pieces; bwd: the gradients.
+cudaError_t launch_norm_rope(DType dt, bool vec, bool bwd, RopeDense d, int num_sms,
+                             cudaStream_t stream);
+
+struct AppendParams {
+  RopeParams r;
+  PagedCache c;
+  long long T;
+  int H;
+  const int *cu, *start;
+  const void* x[3];  // q, k, v
+  Strides in[3];
+  void* q_out;
+  Strides sq_out;
+  long long units;
+  int heads_per_unit, head_chunks;
+};
+cudaError_t launch_cache_append(DType dt, bool e4m3, bool vec, AppendParams a, int num_sms,
+                                cudaStream_t stream);
+
 struct DecodeParams {
   PagedCache c;
   int H, group;        // query heads, and query heads per key/value head

@@ -528,6 +528,104 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
 size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype);
 
 /*
+ * Norms of queries and keys per head, and rotation by position, before
+ * attention.  Per row x (one head of one token):
+ *   y = R (w n),  n = x (mean x^2 + eps)^(-1/2)
+ * with w the side's norm weights (without norms y = R x), and R the rotation of
+ * `dim` columns in pairs (a, b) -> (a cos - b sin, a sin + b cos) by the row
+ * `position` of the table; columns from dim on are not rotated.  Pair i is
+ * columns (i, i + dim / 2), or with `interleaved` (2 i, 2 i + 1).
+ *
+ *   table        float32 [rows, dim], contiguous: the cosines of the dim / 2
+ *                pairs, then their sines (any angles: scaled, of several axes).
+ *   dim          even, at most D; 0: no rotation (rows are then not looked up).
+ *   q_weight, k_weight   [D] of weight_dtype (F32, F16 or BF16), or NULL both: no
+ *                norms (dim must then be positive, eps is not used).
+ */
+typedef struct {
+  const float* table;
+  int64_t rows, dim;
+  int32_t interleaved; /* 0 or 1 */
+  int32_t weight_dtype;
+  const void *q_weight, *k_weight;
+  float eps;
+} jvp_rope_t;
+
+/*
+ * The norms and rotation of dense queries [B, H, Nq, D] and keys [B, Hkv, Nq, D]
+ * (shape->Nk must equal Nq; Hkv is the number of key heads, 0: none), and with
+ * tangents dq, dk (NULL both: none) those of the result:
+ *   dy = R (w dn),  dn = r (dx - n mean(n dx)),  r = (mean x^2 + eps)^(-1/2).
+ * In fp32, each output rounded once to `dtype`.
+ *
+ *   positions    int32 [B, Nq] on the device (positions_stride elements between
+ *                its rows; may be 0), or NULL: token n has position n.  A position
+ *                that is no row of the table is reported by
+ *                jvp_attn_get_device_status() (JVP_ERR_INDEX) and its token's rows
+ *                are not written.
+ *   in_strides, out_strides   4 records: queries, keys, their tangents (the last
+ *                two unused without tangents).
+ */
+jvp_status_t jvp_attn_norm_rope(const jvp_shape_t* shape, jvp_dtype_t dtype, const jvp_rope_t* rope,
+                                const int32_t* positions, int64_t positions_stride, const void* q,
+                                const void* k, const void* dq, const void* dk,
+                                const jvp_strides_t* in_strides, void* q_out, void* k_out,
+                                void* dq_out, void* dk_out, const jvp_strides_t* out_strides,
+                                void* stream);
+
+/*
+ * Gradients of <g_q, q_out> + <g_k, k_out> (+ <g_dq, dq_out> + <g_dk, dk_out> with
+ * tangents) with respect to q, k (dq, dk) and the norm weights.
+ *
+ *   q, k, dq, dk   the inputs of jvp_attn_norm_rope (dq, dk NULL without tangents)
+ *   in_strides     8 records: q, k, dq, dk, g_q, g_k, g_dq, g_dk
+ *   g_q_weight, g_k_weight   float32 [D]; sums over all rows in fp32, in an order
+ *                that depends on the sizes only (the same call gives the same
+ *                bits).  Unused without norms, as are q, k and the workspace.
+ *   workspace    device scratch of at least jvp_attn_norm_rope_bwd_workspace_size()
+ *                bytes, 4-byte aligned; its contents on entry do not matter.
+ *
+ * A token whose position is no row of the table is skipped (reported as above)
+ * and adds nothing to the weights' gradients.
+ */
+jvp_status_t jvp_attn_norm_rope_bwd(const jvp_shape_t* shape, jvp_dtype_t dtype,
+                                    const jvp_rope_t* rope, const int32_t* positions,
+                                    int64_t positions_stride, const void* q, const void* k,
+                                    const void* dq, const void* dk, const void* g_q,
+                                    const void* g_k, const void* g_dq, const void* g_dk,
+                                    const jvp_strides_t* in_strides, void* gq_out, void* gk_out,
+                                    void* gdq_out, void* gdk_out, const jvp_strides_t* out_strides,
+                                    float* g_q_weight, float* g_k_weight, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of jvp_attn_norm_rope_bwd on the current device, whatever the
+ * number of rows (some 600 KiB at D = 128); 0 for a bad D or no device. */
+size_t jvp_attn_norm_rope_bwd_workspace_size(int64_t D);
+
+/*
+ * jvp_attn_cache_write with the norms and rotation on the way: k becomes its row
+ * of the cache normalised and rotated, v its row as it is, and q [T, H, D] the
+ * normalised and rotated q_out.  A row's position in its sequence is its row of
+ * the table.  What is cached is what jvp_attn_norm_rope followed by
+ * jvp_attn_cache_write would leave there (computed in fp32, rounded to `dtype`,
+ * then quantised where the cache is e4m3).
+ *
+ *   H            query heads (any number, 0: none).
+ *   in_strides   3 records: q, k, v.
+ *
+ * The other arguments, and what is skipped and reported, are those of
+ * jvp_attn_cache_write; a token whose position is no row of the table, or whose
+ * place is out of range, is skipped whole (its row of q_out is not written).
+ */
+jvp_status_t jvp_attn_cache_append(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, int64_t T,
+                                   const void* q, const void* k, const void* v,
+                                   const jvp_strides_t* in_strides, const jvp_rope_t* rope,
+                                   const int32_t* block_table, const int32_t* start_pos,
+                                   const int32_t* cu_seqlens, void* q_out,
+                                   const jvp_strides_t* q_out_strides, void* k_cache, void* v_cache,
+                                   uint8_t* k_scale, uint8_t* v_scale, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side status word:
  * JVP_ERR_BOUNDS if a kernel of a debug build of the library found an index
  * out of its bounds (and skipped that access), else JVP_ERR_DEVICE_TIMEOUT if
