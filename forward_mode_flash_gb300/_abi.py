@@ -43,6 +43,7 @@ EXPORTS = (
     "jvp_attn_cache_read",
     "jvp_attn_decode",
     "jvp_attn_decode_workspace_size",
+    "jvp_attn_decode_window",
     "jvp_attn_norm_rope",
     "jvp_attn_norm_rope_bwd",
     "jvp_attn_norm_rope_bwd_workspace_size",
@@ -177,6 +178,10 @@ def load(path: str | None = None):
         lib.jvp_attn_decode.argtypes = [CP, i64, i32, vp, STP] + [vp] * 6 + \
             [f32, vp, STP, vp, vp, ctypes.c_size_t, vp]
         lib.jvp_attn_decode.restype = i32
+        # (window, sinks between seq_lens and scale)
+        lib.jvp_attn_decode_window.argtypes = [CP, i64, i32, vp, STP] + [vp] * 6 + \
+            [i64, i64, f32, vp, STP, vp, vp, ctypes.c_size_t, vp]
+        lib.jvp_attn_decode_window.restype = i32
         lib.jvp_attn_decode_workspace_size.argtypes = [CP, i64, i32]
         lib.jvp_attn_decode_workspace_size.restype = ctypes.c_size_t
         RP = ctypes.POINTER(Rope)
@@ -215,6 +220,7 @@ def load(path: str | None = None):
         lib.addresses = {n: ctypes.cast(getattr(lib, n), vp).value
                          for n in ("jvp_attn_fwd_packed", "jvp_attn_cache_write",
                                    "jvp_attn_cache_read", "jvp_attn_decode", "jvp_attn_norm_rope",
+                                   "jvp_attn_decode_window",
                                    "jvp_attn_norm_rope_bwd", "jvp_attn_cache_append")}
         _libs[p] = lib
         return lib

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 from typing import Optional, Tuple
 
 import torch
@@ -659,6 +660,17 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     return k, v
 
 
+_NO_WINDOW = (1 << 31) - 1  # as wide as any sequence
+
+
+def _window(window, sinks):
+    """Checked window and sinks, as whole numbers."""
+    window, sinks = _NO_WINDOW if window is None else operator.index(window), operator.index(sinks)
+    if window <= 0 or sinks < 0:
+        raise ValueError(f"window must be positive and sinks not negative, got {window} and {sinks}")
+    return min(window, _NO_WINDOW), min(sinks, _NO_WINDOW)
+
+
 def _check_decode(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out):
     """Checks of attention_decode; the workspace bytes of such a call."""
     desc = _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale)
@@ -684,7 +696,8 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      k_scale: Optional[torch.Tensor] = None,
                      v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                      return_lse: bool = False, out: Optional[torch.Tensor] = None,
-                     workspace: Optional[torch.Tensor] = None):
+                     workspace: Optional[torch.Tensor] = None, window: Optional[int] = None,
+                     sinks: int = 0):
     """Attention of one new token per sequence over its cached keys and values.
 
     q is [B, H, D]; the cache and block_table are as for ``cache_write`` (which
@@ -694,18 +707,25 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     attention).  Returns o [B, H, D], or (o, lse) with ``return_lse`` (float32
     [B, H]); a sequence without keys gets o = 0 and lse = -inf.  ``workspace``
     (uint8, 16-byte aligned, ``decode_workspace_size`` bytes) is allocated here
-    if not given; calls that share one must not overlap.  Forward only, as
+    if not given; calls that share one must not overlap.  With ``window`` only the
+    last ``window`` positions and the first ``sinks`` are attended to, and only these
+    are read (block-table entries of others may hold anything).  Forward only, as
     ``attention_packed``.
     """
     if workspace is not None and (workspace.device != k_cache.device
                                   or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {k_cache.device}")
-    bind, entry = _native("jvp_attn_decode")
     layout = (q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out)
-    r = bind.decode(entry, *layout, workspace, scale, return_lse)
+    if window is None and sinks == 0:
+        bind, entry = _native("jvp_attn_decode")
+        call, rest = bind.decode, (workspace, scale, return_lse)
+    else:
+        bind, entry = _native("jvp_attn_decode_window")
+        call, rest = bind.decode_window, (workspace, *_window(window, sinks), scale, return_lse)
+    r = call(entry, *layout, *rest)
     if r is None:  # a layout not seen before
         bind.remember(bind.DECODE, _check_decode(*layout), *layout)
-        r = bind.decode(entry, *layout, workspace, scale, return_lse)
+        r = call(entry, *layout, *rest)
     if type(r) is int:
         _abi.check(r)
     return r

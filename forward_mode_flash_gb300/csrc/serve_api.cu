@@ -85,7 +85,9 @@ struct DecodePlan {
   int heads_per_block = 0, head_blocks = 0, grid = 0, direct = 0;
   size_t bytes = 0, at_o = 0, at_cta = 0;  // workspace: lse, partial outputs, CTAs of segments
 };
-DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
+// window: 0 for none.
+DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms, int64_t window,
+                       int64_t sinks) {
   DecodePlan d;
   const int D = static_cast<int>(c->D), group = static_cast<int>(H / c->Hkv);
   d.heads_per_block = decode_heads_per_block(tc, group);
@@ -96,7 +98,9 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms) {
       (tc ? decode_ctas_per_sm(D, d.heads_per_block / 8, c->dtype == JVP_E4M3)
           : decode_simt_ctas_per_sm(d.heads_per_block));
   const int tile = decode_tile(tc, D, c->dtype == JVP_E4M3);
-  const int64_t tiles = (most + tile - 1) / tile;
+  int64_t tiles = (most + tile - 1) / tile;
+  // (a window's keys begin anywhere in a tile)
+  if (window > 0) tiles = std::min(tiles, (window + tile - 2) / tile + 1 + (sinks + tile - 1) / tile);
   // B * Hkv * head_blocks <= B * H <= 2^31 - 1 (checked by the caller), tiles < 2^31
   const int64_t segments = c->B * c->Hkv * d.head_blocks;
   if (tiles > 0 && tiles <= kDecodeDirectTiles) {
@@ -125,6 +129,74 @@ jvp_status_t check_decode(const jvp_cache_t* c, int64_t H, int dtype) {
   if (c->Hkv == 0 ? H > 0 : H % c->Hkv != 0)
     return api_fail(JVP_ERR_INVALID_ARG, "H must be a multiple of Hkv (grouped-query attention)");
   return JVP_OK;
+}
+
+// window: 0 for none.
+jvp_status_t decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, const void* q,
+                             const jvp_strides_t* q_strides, const void* k_cache,
+                             const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                             const int32_t* block_table, const int32_t* seq_lens, int64_t window,
+                    int64_t sinks, float scale,                             void* o, const jvp_strides_t* o_strides, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  api_set_path(0);
+  jvp_status_t st = check_decode(cache, H, dtype);
+  if (st != JVP_OK) return st;
+  if (!std::isfinite(scale)) return api_fail(JVP_ERR_INVALID_ARG, "scale is not finite");
+  if (!q_strides || !o_strides) return api_fail(JVP_ERR_INVALID_ARG, "strides are NULL");
+  const int64_t B = cache->B, D = cache->D;
+  for (const jvp_strides_t* s : {q_strides, o_strides}) {
+    st = check_strides(*s, "innermost (d) stride must be 1", "negative stride");
+    if (st != JVP_OK) return st;
+  }
+  if ((B > 1 && o_strides->b == 0) || (H > 1 && o_strides->h == 0))
+    return api_fail(JVP_ERR_INVALID_ARG, "an output must not have a stride of 0");
+  if (B == 0 || H == 0) return api_ok();
+  if (!q || !o || !seq_lens) return api_fail(JVP_ERR_INVALID_ARG, "q, o or seq_lens is NULL");
+  const int64_t e = elem_bytes(dtype), ce = elem_bytes(cache->dtype);
+  if (!aligned_to(q, e) || !aligned_to(o, e))
+    return api_fail(JVP_ERR_ALIGNMENT, "q or o not aligned to its element size");
+  if (!aligned_to(lse, 4) || !aligned_to(seq_lens, 4))
+    return api_fail(JVP_ERR_ALIGNMENT, "lse or seq_lens not 4-byte aligned");
+  st = check_cache_ptrs(cache, k_cache, v_cache, k_scale, v_scale, block_table);
+  if (st != JVP_OK) return st;
+  int sms = 0;
+  unsigned int* status = nullptr;
+  st = api_device(&sms, &status);
+  if (st != JVP_OK) return st;
+
+  DecodeParams p{};
+  p.c = describe(cache, k_cache, v_cache, k_scale, v_scale, block_table, status);
+  p.H = static_cast<int>(H), p.group = static_cast<int>(H / cache->Hkv);
+  p.lens = seq_lens;
+  p.q = q, p.sq = used(*q_strides, B, H, 0);
+  p.o = o, p.so = used(*o_strides, B, H, 0);
+  p.lse = lse;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const bool e4m3 = cache->dtype == JVP_E4M3;
+  const bool tc = e == 2 && D % (e4m3 ? 16 : 8) == 0 && aligned_to(q, 8) && multiple(p.sq, 4) &&
+                  aligned_to(k_cache, 16) && aligned_to(v_cache, 16) &&
+                  multiple(p.c.sk, 16 / ce) && multiple(p.c.sv, 16 / ce);
+  const bool vec = D % 4 == 0 && aligned_to(k_cache, 4 * ce) && aligned_to(v_cache, 4 * ce) &&
+                   multiple(p.c.sk, 4) && multiple(p.c.sv, 4);
+  const DecodePlan d = plan_decode(cache, H, tc, sms, window, sinks);
+  if (d.bytes > 0 && (!workspace || workspace_bytes < d.bytes))
+    return api_fail(JVP_ERR_WORKSPACE,
+                    "workspace is NULL or smaller than jvp_attn_decode_workspace_size()");
+  if (!aligned_to(workspace, 16)) return api_fail(JVP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  p.o_vec = aligned_to(o, 16) && multiple(p.so, 8);
+  p.head_blocks = d.head_blocks, p.grid = d.grid, p.direct = d.direct;
+  if (d.bytes > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.ws_lse = reinterpret_cast<float*>(ws);
+    p.ws_o = reinterpret_cast<float*>(ws + d.at_o);
+    p.ws_cta = reinterpret_cast<int2*>(ws + d.at_cta);
+  }
+  p.window = static_cast<int>(window), p.sinks = static_cast<int>(sinks);
+  const cudaError_t err = (window > 0 ? launch_decode_window : launch_decode)(
+      static_cast<DType>(dtype), e4m3, tc, vec, p, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return api_cuda_fail(err);
+  api_set_path(tc ? 1 : 2);
+  return api_ok();
 }
 
 }  // namespace
@@ -257,8 +329,8 @@ size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_d
   unsigned int* status = nullptr;
   if (jvp::api_device(&sms, &status) != JVP_OK) return 0;
   // enough for either path (which one runs depends on the pointers too)
-  return std::max(jvp::plan_decode(cache, H, true, sms).bytes,
-                  jvp::plan_decode(cache, H, false, sms).bytes);
+  return std::max(jvp::plan_decode(cache, H, true, sms, 0, 0).bytes,
+                  jvp::plan_decode(cache, H, false, sms, 0, 0).bytes);
 }
 
 jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, const void* q,
@@ -267,65 +339,25 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
                              const int32_t* block_table, const int32_t* seq_lens, float scale,
                              void* o, const jvp_strides_t* o_strides, float* lse, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  using namespace jvp;
-  api_set_path(0);
-  jvp_status_t st = check_decode(cache, H, dtype);
-  if (st != JVP_OK) return st;
-  if (!std::isfinite(scale)) return api_fail(JVP_ERR_INVALID_ARG, "scale is not finite");
-  if (!q_strides || !o_strides) return api_fail(JVP_ERR_INVALID_ARG, "strides are NULL");
-  const int64_t B = cache->B, D = cache->D;
-  for (const jvp_strides_t* s : {q_strides, o_strides}) {
-    st = check_strides(*s, "innermost (d) stride must be 1", "negative stride");
-    if (st != JVP_OK) return st;
-  }
-  if ((B > 1 && o_strides->b == 0) || (H > 1 && o_strides->h == 0))
-    return api_fail(JVP_ERR_INVALID_ARG, "an output must not have a stride of 0");
-  if (B == 0 || H == 0) return api_ok();
-  if (!q || !o || !seq_lens) return api_fail(JVP_ERR_INVALID_ARG, "q, o or seq_lens is NULL");
-  const int64_t e = elem_bytes(dtype), ce = elem_bytes(cache->dtype);
-  if (!aligned_to(q, e) || !aligned_to(o, e))
-    return api_fail(JVP_ERR_ALIGNMENT, "q or o not aligned to its element size");
-  if (!aligned_to(lse, 4) || !aligned_to(seq_lens, 4))
-    return api_fail(JVP_ERR_ALIGNMENT, "lse or seq_lens not 4-byte aligned");
-  st = check_cache_ptrs(cache, k_cache, v_cache, k_scale, v_scale, block_table);
-  if (st != JVP_OK) return st;
-  int sms = 0;
-  unsigned int* status = nullptr;
-  st = api_device(&sms, &status);
-  if (st != JVP_OK) return st;
+  return jvp::decode(cache, H, dtype, q, q_strides, k_cache, v_cache, k_scale, v_scale, block_table,
+                     seq_lens, 0, 0, scale, o, o_strides, lse, workspace, workspace_bytes, stream);
+}
 
-  DecodeParams p{};
-  p.c = describe(cache, k_cache, v_cache, k_scale, v_scale, block_table, status);
-  p.H = static_cast<int>(H), p.group = static_cast<int>(H / cache->Hkv);
-  p.lens = seq_lens;
-  p.q = q, p.sq = used(*q_strides, B, H, 0);
-  p.o = o, p.so = used(*o_strides, B, H, 0);
-  p.lse = lse;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  const bool e4m3 = cache->dtype == JVP_E4M3;
-  const bool tc = e == 2 && D % (e4m3 ? 16 : 8) == 0 && aligned_to(q, 8) && multiple(p.sq, 4) &&
-                  aligned_to(k_cache, 16) && aligned_to(v_cache, 16) &&
-                  multiple(p.c.sk, 16 / ce) && multiple(p.c.sv, 16 / ce);
-  const bool vec = D % 4 == 0 && aligned_to(k_cache, 4 * ce) && aligned_to(v_cache, 4 * ce) &&
-                   multiple(p.c.sk, 4) && multiple(p.c.sv, 4);
-  const DecodePlan d = plan_decode(cache, H, tc, sms);
-  if (d.bytes > 0 && (!workspace || workspace_bytes < d.bytes))
-    return api_fail(JVP_ERR_WORKSPACE,
-                    "workspace is NULL or smaller than jvp_attn_decode_workspace_size()");
-  if (!aligned_to(workspace, 16)) return api_fail(JVP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-  p.o_vec = aligned_to(o, 16) && multiple(p.so, 8);
-  p.head_blocks = d.head_blocks, p.grid = d.grid, p.direct = d.direct;
-  if (d.bytes > 0) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.ws_lse = reinterpret_cast<float*>(ws);
-    p.ws_o = reinterpret_cast<float*>(ws + d.at_o);
-    p.ws_cta = reinterpret_cast<int2*>(ws + d.at_cta);
+jvp_status_t jvp_attn_decode_window(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype,
+                                    const void* q, const jvp_strides_t* q_strides,
+                                    const void* k_cache, const void* v_cache,
+                                    const uint8_t* k_scale, const uint8_t* v_scale,
+                                    const int32_t* block_table, const int32_t* seq_lens,
+                                    int64_t window, int64_t sinks, float scale, void* o,
+                                    const jvp_strides_t* o_strides, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  if (const char* why = jvp::bad_window(window, sinks)) {
+    jvp::api_set_path(0);
+    return jvp::api_fail(JVP_ERR_INVALID_ARG, why);
   }
-  const cudaError_t err = launch_decode(static_cast<DType>(dtype), e4m3, tc, vec, p,
-                                        static_cast<cudaStream_t>(stream));
-  if (err != cudaSuccess) return api_cuda_fail(err);
-  api_set_path(tc ? 1 : 2);
-  return api_ok();
+  return jvp::decode(cache, H, dtype, q, q_strides, k_cache, v_cache, k_scale, v_scale, block_table,
+                     seq_lens, std::min(window, jvp::kMax), std::min(sinks, jvp::kMax), scale, o,
+                     o_strides, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

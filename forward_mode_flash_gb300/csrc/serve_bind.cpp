@@ -282,36 +282,57 @@ PyObject* empty_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A single-token call through an entry point of type F; more: its window and sinks.
+template <typename F, typename... More>
+PyObject* decode_call(PyObject* const* a, PyObject* workspace, PyObject* scale_arg, PyObject* lse_arg,
+                      More... more) {
+  const Tensors<8> t(kDecode, a + 1);
+  const Plan* plan = t.plan();
+  if (!plan) return none();
+  // (by value: an allocation may run Python code, which may remember layouts)
+  const int64_t need = plan->workspace;
+  auto* f = entry<F>(a[0]);
+  const at::Tensor* given = tensor(workspace);
+  const bool want_lse = truth(lse_arg);
+  const at::Tensor &q = t[0], &kc = t[1], &vc = t[2], &table = t[3], &lens = t[4];
+  const jvp_cache_t c = cache(kc, vc, table);
+  const float scale = scale_of(scale_arg, c.D);
+  const at::Tensor o = t.t[7] ? t[7] : empty(q.sizes(), q.scalar_type(), q.device());
+  at::Tensor lse, ws;
+  if (want_lse) lse = empty({q.size(0), q.size(1)}, at::kFloat, q.device());
+  if (given) ws = *given;
+  else if (need > 0) ws = empty({need}, at::kByte, q.device());
+  const size_t bytes = ws.defined() ? ws.nbytes() : 0;
+  const jvp_strides_t qs = token_strides(q), os = token_strides(o);
+  const int st = call(q.device(), [&](void* stream) {
+    return f(&c, q.size(1), static_cast<jvp_dtype_t>(dtype_code(q.scalar_type())), data(&q), &qs,
+             data(&kc), data(&vc), data<uint8_t>(t.t[5]), data<uint8_t>(t.t[6]),
+             data<int32_t>(&table), data<int32_t>(&lens), more..., scale, data(&o), &os,
+             want_lse ? data<float>(&lse) : nullptr, ws.defined() ? data(&ws) : nullptr, bytes,
+             stream);
+  });
+  return result(st, o, lse, want_lse);
+}
+
 // decode(entry, q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale,
 //        out, workspace, scale, return_lse)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject* {
-    const Tensors<8> t(kDecode, a + 1);
-    const Plan* plan = t.plan();
-    if (!plan) return none();
-    // (by value: an allocation may run Python code, which may remember layouts)
-    const int64_t need = plan->workspace;
-    auto* f = entry<decltype(jvp_attn_decode)>(a[0]);
-    const at::Tensor* given = tensor(a[9]);
-    const bool want_lse = truth(a[11]);
-    const at::Tensor &q = t[0], &kc = t[1], &vc = t[2], &table = t[3], &lens = t[4];
-    const jvp_cache_t c = cache(kc, vc, table);
-    const float scale = scale_of(a[10], c.D);
-    const at::Tensor o = t.t[7] ? t[7] : empty(q.sizes(), q.scalar_type(), q.device());
-    at::Tensor lse, ws;
-    if (want_lse) lse = empty({q.size(0), q.size(1)}, at::kFloat, q.device());
-    if (given) ws = *given;
-    else if (need > 0) ws = empty({need}, at::kByte, q.device());
-    const size_t bytes = ws.defined() ? ws.nbytes() : 0;
-    const jvp_strides_t qs = token_strides(q), os = token_strides(o);
-    const int st = call(q.device(), [&](void* stream) {
-      return f(&c, q.size(1), static_cast<jvp_dtype_t>(dtype_code(q.scalar_type())), data(&q), &qs,
-               data(&kc), data(&vc), data<uint8_t>(t.t[5]), data<uint8_t>(t.t[6]),
-               data<int32_t>(&table), data<int32_t>(&lens), scale, data(&o), &os,
-               want_lse ? data<float>(&lse) : nullptr, ws.defined() ? data(&ws) : nullptr, bytes,
-               stream);
-    });
-    return result(st, o, lse, want_lse);
+    return decode_call<decltype(jvp_attn_decode)>(a, a[9], a[10], a[11]);
+  });
+}
+
+int64_t integer(PyObject* o) {
+  const int64_t x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw BadArgument();
+  return x;
+}
+
+// decode_window(entry, q, ... out, workspace as decode, window, sinks, scale, return_lse)
+PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    return decode_call<decltype(jvp_attn_decode_window)>(a, a[9], a[12], a[13], integer(a[10]),
+                                                         integer(a[11]));
   });
 }
 
@@ -443,6 +464,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {JVP_METHOD(remember),   JVP_METHOD(packed), JVP_METHOD(write),
                          JVP_METHOD(read),       JVP_METHOD(decode), JVP_METHOD(empty_rows),
                          JVP_METHOD(rope),       JVP_METHOD(rope_bwd), JVP_METHOD(append),
+                         JVP_METHOD(decode_window),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

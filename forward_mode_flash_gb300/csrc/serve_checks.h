@@ -29,6 +29,11 @@ inline jvp_status_t check_strides(const jvp_strides_t& s, const char* what_d, co
   return JVP_OK;
 }
 
+// Why a window and its sinks are refused, or nullptr.
+inline const char* bad_window(int64_t window, int64_t sinks) {
+  return window <= 0 ? "window must be positive" : sinks < 0 ? "negative number of sinks" : nullptr;
+}
+
 // Sizes, types and strides of a cache description (no pointers).
 inline jvp_status_t check_cache(const jvp_cache_t* c, bool written) {
   if (!c) return api_fail(JVP_ERR_INVALID_ARG, "cache is NULL");

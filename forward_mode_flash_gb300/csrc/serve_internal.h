@@ -114,6 +114,7 @@ struct DecodeParams {
   float* ws_o;         // [grid][2][heads_per_block][64 or 128]
   int2* ws_cta;        // [B][Hkv][head_blocks] first and last CTA of a segment
   int o_vec;           // output rows are 16-byte aligned
+  int window, sinks;   // (launch_decode_window) keys j >= lens[b] - window or j < sinks are visible
 };
 
 // Which kernel a call takes: tensor cores (16-bit queries, 16-byte aligned
@@ -147,6 +148,8 @@ constexpr int kDecodeDirectTiles = 4;
 
 cudaError_t launch_decode(DType dt, bool e4m3, bool tc, bool vec, const DecodeParams& p,
                           cudaStream_t stream);
+cudaError_t launch_decode_window(DType dt, bool e4m3, bool tc, bool vec, const DecodeParams& p,
+                                 cudaStream_t stream);
 
 struct PackedParams {
   int T, B, H, Hkv, D, group;

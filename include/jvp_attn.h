@@ -521,6 +521,23 @@ jvp_status_t jvp_attn_decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dt
                              void* o, const jvp_strides_t* o_strides, float* lse, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/*
+ * jvp_attn_decode with a sliding window and sinks: of positions j < n, n =
+ * seq_lens[b], the token attends to those with j >= n - window or j < sinks.
+ * window must be positive and sinks not negative.  Other positions are neither
+ * read nor looked up (their block-table entries may hold anything), and the work
+ * is that of the visible ones.  The other arguments are those of
+ * jvp_attn_decode, jvp_attn_decode_workspace_size() among them.
+ */
+jvp_status_t jvp_attn_decode_window(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype,
+                                    const void* q, const jvp_strides_t* q_strides,
+                                    const void* k_cache, const void* v_cache,
+                                    const uint8_t* k_scale, const uint8_t* v_scale,
+                                    const int32_t* block_table, const int32_t* seq_lens,
+                                    int64_t window, int64_t sinks, float scale, void* o,
+                                    const jvp_strides_t* o_strides, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Workspace bytes of jvp_attn_decode on the current device: partial outputs of
  * at most one resident wave of CTAs, whatever the lengths (a few MiB), and 8
  * bytes per sequence and block of heads; 0 for a block table so small that
