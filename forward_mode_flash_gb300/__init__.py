@@ -7,8 +7,10 @@ this package holds the ctypes binding (``attention``), work/traffic counts
 does, and raises if it has not been built.
 """
 
-from .api import (attention, attention_decode, attention_packed, cache_append,  # noqa: F401
-                  cache_read, cache_write, device_status, fwd_dual, last_path, norm_rope, rope_table)
+from .api import (attention, attention_chunk, attention_decode, attention_packed,  # noqa: F401
+                  cache_append, cache_read, cache_write, device_status, fwd_dual, last_path,
+                  norm_rope, rope_table)
 
-__all__ = ["attention", "attention_decode", "attention_packed", "cache_append", "cache_read",
-           "cache_write", "fwd_dual", "device_status", "last_path", "norm_rope", "rope_table"]
+__all__ = ["attention", "attention_chunk", "attention_decode", "attention_packed", "cache_append",
+           "cache_read", "cache_write", "fwd_dual", "device_status", "last_path", "norm_rope",
+           "rope_table"]

@@ -44,6 +44,8 @@ EXPORTS = (
     "jvp_attn_decode",
     "jvp_attn_decode_workspace_size",
     "jvp_attn_decode_window",
+    "jvp_attn_chunk",
+    "jvp_attn_chunk_workspace_size",
     "jvp_attn_norm_rope",
     "jvp_attn_norm_rope_bwd",
     "jvp_attn_norm_rope_bwd_workspace_size",
@@ -184,6 +186,13 @@ def load(path: str | None = None):
         lib.jvp_attn_decode_window.restype = i32
         lib.jvp_attn_decode_workspace_size.argtypes = [CP, i64, i32]
         lib.jvp_attn_decode_workspace_size.restype = ctypes.c_size_t
+        # cache, H, dtype, T, q, q_strides, k_cache, v_cache, k_scale, v_scale, block_table,
+        # seq_lens, cu_seqlens, window, sinks, scale, o, o_strides, lse, workspace, bytes, stream
+        lib.jvp_attn_chunk.argtypes = [CP, i64, i32, i64, vp, STP] + [vp] * 7 + \
+            [i64, i64, f32, vp, STP, vp, vp, ctypes.c_size_t, vp]
+        lib.jvp_attn_chunk.restype = i32
+        lib.jvp_attn_chunk_workspace_size.argtypes = [CP, i64, i32, i64]
+        lib.jvp_attn_chunk_workspace_size.restype = ctypes.c_size_t
         RP = ctypes.POINTER(Rope)
         # shape, dtype, rope, positions, their stride, q k dq dk, in_strides, outputs,
         # out_strides, stream
@@ -220,7 +229,7 @@ def load(path: str | None = None):
         lib.addresses = {n: ctypes.cast(getattr(lib, n), vp).value
                          for n in ("jvp_attn_fwd_packed", "jvp_attn_cache_write",
                                    "jvp_attn_cache_read", "jvp_attn_decode", "jvp_attn_norm_rope",
-                                   "jvp_attn_decode_window",
+                                   "jvp_attn_decode_window", "jvp_attn_chunk",
                                    "jvp_attn_norm_rope_bwd", "jvp_attn_cache_append")}
         _libs[p] = lib
         return lib

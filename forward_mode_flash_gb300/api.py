@@ -731,21 +731,93 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     return r
 
 
+def _cache_like(k_cache, block_table):
+    """Description of a cache whose values lie as its keys, unchecked."""
+    sk = k_cache.stride()
+    strides = _abi.Strides(sk[0], sk[1], sk[2], 1)
+    pages, hkv, page, D = k_cache.shape
+    return _abi.Cache(pages, page, hkv, D, block_table.shape[0], block_table.shape[1],
+                      block_table.stride(0),
+                      _abi.JVP_E4M3 if k_cache.dtype == _E4M3 else _DT[k_cache.dtype], strides,
+                      strides)
+
+
 def decode_workspace_size(k_cache: torch.Tensor, block_table: torch.Tensor, H: int,
                           dtype: Optional[torch.dtype] = None) -> int:
     """Bytes of scratch that attention_decode needs for H query heads over this
     cache (``dtype``: of the queries; default the cache's, bfloat16 over e4m3)."""
-    sk = k_cache.stride()
-    strides = _abi.Strides(sk[0], sk[1], sk[2], 1)
-    e4m3 = k_cache.dtype == _E4M3
     if dtype is None:
-        dtype = torch.bfloat16 if e4m3 else k_cache.dtype
-    pages, hkv, page, D = k_cache.shape
-    desc = _abi.Cache(pages, page, hkv, D, block_table.shape[0], block_table.shape[1],
-                      block_table.stride(0), _abi.JVP_E4M3 if e4m3 else _DT[k_cache.dtype],
-                      strides, strides)
+        dtype = torch.bfloat16 if k_cache.dtype == _E4M3 else k_cache.dtype
+    desc = _cache_like(k_cache, block_table)
     with torch.cuda.device(k_cache.device):
         return int(_abi.load().jvp_attn_decode_workspace_size(desc, int(H), _DT[dtype]))
+
+
+def _check_chunk(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, k_scale, v_scale, out):
+    """Checks of attention_chunk; the workspace bytes of such a call."""
+    desc = _cache_desc(k_cache, v_cache, block_table, k_scale, v_scale)
+    dev = k_cache.device
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if k_cache.dtype != _E4M3 and q.dtype != k_cache.dtype:
+        raise ValueError("q must have the cache's dtype (unless the cache is e4m3)")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H, D], got {tuple(q.shape)}")
+    T, H = q.shape[:2]
+    _check_packed(q, "q", q.dtype, dev, (T, H, desc.D))
+    if desc.Hkv <= 0 and H > 0 or desc.Hkv > 0 and H % desc.Hkv != 0:
+        raise ValueError(f"query heads ({H}) must be a multiple of key/value heads ({desc.Hkv})")
+    _check_int32(seq_lens, "seq_lens", (desc.B,), dev)
+    _check_int32(cu_seqlens, "cu_seqlens", (desc.B + 1,), dev)
+    if out is not None:
+        _check_packed(out, "out", q.dtype, dev, (T, H, desc.D))
+    with torch.cuda.device(dev):
+        return int(_abi.load().jvp_attn_chunk_workspace_size(desc, H, _DT[q.dtype], T))
+
+
+def attention_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: torch.Tensor,
+                    window: Optional[int] = None, sinks: int = 0,
+                    k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Attention of some new tokens of each sequence over its cached keys and values.
+
+    q is [T, H, D]; sequence b's new tokens are its rows ``cu_seqlens[b]:cu_seqlens[b +
+    1]`` (int32 [B + 1], on the device) and the last of its ``seq_lens[b]`` positions
+    (int32 [B], on the device, the new ones included); their keys and values are in the
+    cache already (``cache_append`` or ``cache_write``, which also describe the cache
+    and block_table).  The token at position x attends to positions j <= x; with
+    ``window``, of these to j > x - window and to j < sinks (positions that no new token
+    of a sequence attends to are not read, and their block-table entries may hold
+    anything).  H is a multiple of the cache's heads (grouped-query attention).
+    Returns o [T, H, D], or (o, lse) with ``return_lse`` (float32 [H, T]); a token that
+    sees nothing gets o = 0 and lse = -inf, and rows that belong to no sequence are not
+    written.  ``workspace`` as in ``attention_decode`` (``chunk_workspace_size`` bytes).
+    Forward only, as ``attention_packed``.
+    """
+    if workspace is not None and (workspace.device != k_cache.device
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {k_cache.device}")
+    bind, entry = _native("jvp_attn_chunk")
+    layout = (q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, k_scale, v_scale, out)
+    rest = (workspace, *_window(window, sinks), scale, return_lse)
+    r = bind.chunk(entry, *layout, *rest)
+    if r is None:  # a layout not seen before
+        bind.remember(bind.CHUNK, _check_chunk(*layout), *layout)
+        r = bind.chunk(entry, *layout, *rest)
+    if type(r) is int:
+        _abi.check(r)
+    return r
+
+
+def chunk_workspace_size(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor) -> int:
+    """Bytes of scratch that attention_chunk needs for queries like q over this cache."""
+    desc = _cache_like(k_cache, block_table)
+    with torch.cuda.device(k_cache.device):
+        return int(_abi.load().jvp_attn_chunk_workspace_size(desc, q.shape[1], _DT[q.dtype],
+                                                             q.shape[0]))
 
 
 # ---- norms of queries and keys per head, and rotation by position

@@ -186,7 +186,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
   return nullptr;
 }
 
-enum Op : int64_t { kPacked, kWrite, kRead, kDecode, kRope, kRopeBwd, kAppend };
+enum Op : int64_t { kPacked, kWrite, kRead, kDecode, kRope, kRopeBwd, kAppend, kChunk };
 
 // remember(op, workspace bytes, tensors ...): the layouts of these arguments
 // have been checked.
@@ -336,6 +336,39 @@ PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// chunk(entry, q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, k_scale,
+//       v_scale, out, workspace, window, sinks, scale, return_lse)
+PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    const Tensors<9> t(kChunk, a + 1);
+    const Plan* plan = t.plan();
+    if (!plan) return none();
+    const int64_t need = plan->workspace;  // (by value, as in decode)
+    auto* f = entry<decltype(jvp_attn_chunk)>(a[0]);
+    const at::Tensor* given = tensor(a[10]);
+    const int64_t window = integer(a[11]), sinks = integer(a[12]);
+    const bool want_lse = truth(a[14]);
+    const at::Tensor &q = t[0], &kc = t[1], &vc = t[2], &table = t[3];
+    const jvp_cache_t c = cache(kc, vc, table);
+    const float scale = scale_of(a[13], c.D);
+    const at::Tensor o = t.t[8] ? t[8] : empty(q.sizes(), q.scalar_type(), q.device());
+    at::Tensor lse, ws;
+    if (want_lse) lse = empty({q.size(1), q.size(0)}, at::kFloat, q.device());
+    if (given) ws = *given;
+    else if (need > 0) ws = empty({need}, at::kByte, q.device());
+    const size_t bytes = ws.defined() ? ws.nbytes() : 0;
+    const jvp_strides_t qs = row_strides(q), os = row_strides(o);
+    const int st = call(q.device(), [&](void* stream) {
+      return f(&c, q.size(1), static_cast<jvp_dtype_t>(dtype_code(q.scalar_type())), q.size(0),
+               data(&q), &qs, data(&kc), data(&vc), data<uint8_t>(t.t[6]), data<uint8_t>(t.t[7]),
+               data<int32_t>(&table), data<int32_t>(t.t[4]), data<int32_t>(t.t[5]), window, sinks,
+               scale, data(&o), &os, want_lse ? data<float>(&lse) : nullptr,
+               ws.defined() ? data(&ws) : nullptr, bytes, stream);
+    });
+    return result(st, o, lse, want_lse);
+  });
+}
+
 // The angles and norm weights of a call: tensors (or none) and numbers.
 jvp_rope_t rope_of(const at::Tensor* table, const at::Tensor* qw, const at::Tensor* kw, PyObject* eps,
                    PyObject* interleaved) {
@@ -464,7 +497,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {JVP_METHOD(remember),   JVP_METHOD(packed), JVP_METHOD(write),
                          JVP_METHOD(read),       JVP_METHOD(decode), JVP_METHOD(empty_rows),
                          JVP_METHOD(rope),       JVP_METHOD(rope_bwd), JVP_METHOD(append),
-                         JVP_METHOD(decode_window),
+                         JVP_METHOD(decode_window), JVP_METHOD(chunk),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_bind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
@@ -475,7 +508,7 @@ PyMODINIT_FUNC PyInit__serve_bind() {
   PyObject* m = PyModule_Create(&module);
   const struct { const char* name; Op op; } ops[] = {
       {"PACKED", kPacked}, {"WRITE", kWrite}, {"READ", kRead}, {"DECODE", kDecode},
-      {"ROPE", kRope}, {"ROPE_BWD", kRopeBwd}, {"APPEND", kAppend}};
+      {"ROPE", kRope}, {"ROPE_BWD", kRopeBwd}, {"APPEND", kAppend}, {"CHUNK", kChunk}};
   for (const auto& o : ops)
     if (m && PyModule_AddIntConstant(m, o.name, o.op))
       Py_CLEAR(m);

@@ -181,6 +181,55 @@ constexpr int kPackedBlockN = 128;    // keys per tile
 cudaError_t launch_packed_simt(DType dt, const PackedParams& p, cudaStream_t stream);
 constexpr int kPackedSimtRows = 32;
 
+// Attention of chunks of new tokens over a paged cache.  Token i of a sequence's
+// len has position lens[b] - len + i and sees the keys at positions up to its own
+// (with a window: of these the last `window`, and the first `sinks`).
+struct ChunkParams {
+  PagedCache c;
+  int T, H, group;
+  int tok;           // query tokens of a tile of rows
+  int query_tiles;   // tensor cores: tiles of rows of a CTA (1 or 2)
+  int head_blocks;   // CUDA cores: blocks of `group_rows` query heads per key/value head
+  int group_rows;    // query heads of a tile's rows
+  int window, sinks; // window 0: none
+  float scale_log2;
+  int neg_scores;    // scale < 0: the score products are formed negated, |scale| applied
+  const int *cu, *lens;
+  const void* q;
+  Strides sq;
+  void* o;
+  Strides so;
+  float* lse;        // [H, T] or nullptr
+  // The split of long key ranges: an item's (tile of rows, head) key tiles are cut
+  // into pieces of at most max(least, all / target) tiles each.  least 0: no split.
+  int least;
+  int target;
+  int heads;         // key/value heads (times head_blocks): items of a tile of tokens
+  int slots;         // pieces of split items, at most
+  float* ws_o;       // [slots][rows of an item][64 or 128] normalised partial outputs
+  float* ws_lse;     // [slots][rows of an item], log2 units
+  int4* ws_item;     // [slots] pieces, first row, tokens, head; pieces 0: not an item's first
+  int* ws_count;     // slots in use
+  int units;         // blocks of the grid per head: an upper bound of all pieces
+  int box_rows;      // tensor cores: keys of a copied box, a divisor of 128 and the page size
+  int vec;           // CUDA cores: 16-byte aligned rows of whole 16-byte pieces
+};
+struct ChunkMaps {
+  CUtensorMap q, o, k, v;
+};
+// Keys per tile, fewest key tiles of a piece, join blocks.
+constexpr int kChunkTile = 128, kChunkSimtTile = 64, kChunkSimtRows = 32;
+constexpr int kChunkLeast = 4;
+// source of the key tiles: boxes of whole pages' parts by TMA, rows gathered by
+// threads, or e4m3 rows gathered and converted
+enum ChunkSource { kChunkBoxes, kChunkRows, kChunkE4M3 };
+cudaError_t launch_chunk_tc(DType dt, int kernel_d, ChunkSource source, const ChunkMaps& maps,
+                            const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_simt(DType dt, bool e4m3, const ChunkParams& p, cudaStream_t stream);
+// Joins the pieces of split items (rows: of an item; kernel_d: 64 or 128).
+cudaError_t launch_chunk_join(DType dt, int kernel_d, int rows, const ChunkParams& p, int num_sms,
+                              cudaStream_t stream);
+
 // Lets a kernel use `bytes` of dynamic shared memory on the current device.
 // Once per kernel and device (the call costs 2 us of an eager call's host time;
 // making it twice is harmless).

@@ -545,6 +545,56 @@ jvp_status_t jvp_attn_decode_window(const jvp_cache_t* cache, int64_t H, jvp_dty
 size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype);
 
 /*
+ * Attention of chunks of new tokens over a paged cache that holds their keys and
+ * values already (jvp_attn_cache_write or jvp_attn_cache_append): the next piece of
+ * a long prompt, drafted tokens to verify, or a batch that mixes them with single
+ * tokens.  Sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of
+ * q, the last of its n = seq_lens[b] positions: token i of len has position x = n -
+ * len + i and attends to positions j <= x; with a window, of these to j > x - window
+ * and to j < sinks:
+ *   s_j = scale q . k_j,  o = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j).
+ * Query head h reads key/value head h / (H / Hkv).
+ *
+ *   H            query heads, a multiple of the cache's Hkv.
+ *   dtype        element type of q and o; the cache's entries have it too, or
+ *                are e4m3.
+ *   q, o         [T, H, D] (one stride record each: .n, .h; .b unused).
+ *   seq_lens     int32 [B]: positions of each sequence, its new tokens included.  A
+ *                token whose position is negative (n < len) sees nothing.
+ *   cu_seqlens   int32 [B + 1] as in jvp_attn_fwd_packed: rows of no sequence are
+ *                not written, bad offsets are reported and their sequences skipped.
+ *   window       0: none.  Positions that no token of a sequence's chunk sees are not
+ *                read, and their block-table entries may hold anything.
+ *   sinks        not negative; without a window of no effect.
+ *   lse          NULL or [H, T] contiguous float32.
+ *   workspace    device scratch of at least jvp_attn_chunk_workspace_size() bytes,
+ *                16-byte aligned; contents on entry do not matter.  Calls that share
+ *                one must not overlap.
+ *
+ * A row that sees no key gets o = 0, lse = -inf.  Results do not depend on keys that
+ * a row does not see, whatever they hold.  Long key ranges with few tokens are split
+ * over the GPU, and their parts combined in an order that depends on the lengths only
+ * (the same call gives the same bits).  fp16/bf16 with D a multiple of 8, H / Hkv at
+ * most 128, a nonzero scale, 16-byte aligned rows and pages of a multiple of 8 rows
+ * run on the tensor cores (weights rounded to 16 bits as in jvp_attn_fwd_packed);
+ * every other case on the CUDA cores in fp32.
+ */
+jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, int64_t T,
+                            const void* q, const jvp_strides_t* q_strides, const void* k_cache,
+                            const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* cu_seqlens, int64_t window, int64_t sinks, float scale,
+                            void* o, const jvp_strides_t* o_strides, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of jvp_attn_chunk on the current device, for any window: partial
+ * outputs of a few waves of CTAs, whatever the lengths (40 MiB at most at D = 128);
+ * 0 for a block table so small that nothing is split, an empty problem, an invalid
+ * description or no device. */
+size_t jvp_attn_chunk_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype,
+                                     int64_t T);
+
+/*
  * Norms of queries and keys per head, and rotation by position, before
  * attention.  Per row x (one head of one token):
  *   y = R (w n),  n = x (mean x^2 + eps)^(-1/2)
