@@ -19,15 +19,17 @@ struct ChunkPlan {
   int least = 0, target = 0, slots = 0;
   size_t bytes = 0, at_lse = 0, at_item = 0, at_count = 0;
 };
-ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, bool tc, int num_sms,
+// Kernels: CUDA cores, tensor cores with copied boxes or with gathered rows.
+enum ChunkKernel { kSimt, kBoxes, kGathered };
+ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, ChunkKernel kernel, int num_sms,
                      int64_t window, int64_t sinks) {
   ChunkPlan d;
   const int64_t group = H / c->Hkv;
   int64_t tile;
-  if (tc) {
+  if (kernel != kSimt) {
     // Two query tiles per CTA share each K/V tile; a chunk that fills no more than
     // two tiles is better off with one per CTA and two CTAs per SM.
-    d.query_tiles = T * group <= 2 * kPackedTileRows * c->B ? 1 : 2;
+    d.query_tiles = kernel == kBoxes && T * group <= 2 * kPackedTileRows * c->B ? 1 : 2;
     d.group_rows = static_cast<int>(group);
     d.tok = static_cast<int>(kPackedTileRows / group);
     d.rows = d.query_tiles * kPackedTileRows;
@@ -111,10 +113,11 @@ size_t jvp_attn_chunk_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dt
   unsigned int* status = nullptr;
   if (api_device(&sms, &status) != JVP_OK) return 0;
   // enough for either path (which one runs depends on the pointers too) and any window
-  const size_t simt = plan_chunk(cache, H, T, false, sms, 0, 0).bytes;
-  return H / cache->Hkv > kPackedTileRows
-             ? simt
-             : std::max(simt, plan_chunk(cache, H, T, true, sms, 0, 0).bytes);
+  size_t most = plan_chunk(cache, H, T, kSimt, sms, 0, 0).bytes;
+  if (H / cache->Hkv <= kPackedTileRows)
+    for (const ChunkKernel k : {kBoxes, kGathered})
+      most = std::max(most, plan_chunk(cache, H, T, k, sms, 0, 0).bytes);
+  return most;
 }
 
 jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, int64_t T,
@@ -167,19 +170,25 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
   p.lse = lse;
   p.scale_log2 = scale * 1.4426950408889634f;
   const bool e4m3 = cache->dtype == JVP_E4M3;
-  bool tc = e == 2 && D % 8 == 0 && p.group <= kPackedTileRows && scale != 0.f && !e4m3 &&
-            cache->page_size % 8 == 0 && aligned_to(o, 16) && multiple(p.so, 8);
-  ChunkMaps maps;
+  bool tc = e == 2 && D % 8 == 0 && p.group <= kPackedTileRows && scale != 0.f &&
+            aligned_to(o, 16) && multiple(p.so, 8) && aligned_to(k_cache, 8 * ce) &&
+            aligned_to(v_cache, 8 * ce) && multiple(p.c.sk, 8) && multiple(p.c.sv, 8);
+  ChunkSource source = e4m3 ? kChunkE4M3 : kChunkRows;
+  ChunkMaps maps{};
   if (tc) {
-    p.box_rows = 8;
-    while (p.box_rows < kChunkTile && cache->page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
     const int tok = kPackedTileRows / p.group;
     tc = encode_packed(&maps.q, dtype, q, D, H, p.sq.h, T, p.sq.n, p.group, tok) &&
-         encode_packed(&maps.o, dtype, o, D, H, p.so.h, T, p.so.n, p.group, tok) &&
-         encode_cache(&maps.k, dtype, k_cache, p.c, p.c.sk, p.box_rows) &&
-         encode_cache(&maps.v, dtype, v_cache, p.c, p.c.sv, p.box_rows);
+         encode_packed(&maps.o, dtype, o, D, H, p.so.h, T, p.so.n, p.group, tok);
   }
-  const ChunkPlan d = plan_chunk(cache, H, T, tc, sms, p.window, p.sinks);
+  if (tc && !e4m3 && cache->page_size % 8 == 0) {
+    p.box_rows = 8;
+    while (p.box_rows < kChunkTile && cache->page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+    if (encode_cache(&maps.k, dtype, k_cache, p.c, p.c.sk, p.box_rows) &&
+        encode_cache(&maps.v, dtype, v_cache, p.c, p.c.sv, p.box_rows))
+      source = kChunkBoxes;
+  }
+  const ChunkPlan d = plan_chunk(cache, H, T, !tc ? kSimt : source == kChunkBoxes ? kBoxes : kGathered,
+                                 sms, p.window, p.sinks);
   if (d.bytes > 0 && (!workspace || workspace_bytes < d.bytes))
     return api_fail(JVP_ERR_WORKSPACE,
                     "workspace is NULL or smaller than jvp_attn_chunk_workspace_size()");
@@ -200,7 +209,7 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
   cudaError_t err;
   if (tc) {
     if (scale < 0.f) p.neg_scores = 1, p.scale_log2 = -p.scale_log2;
-    err = launch_chunk_tc(static_cast<DType>(dtype), kernel_d, kChunkBoxes, maps, p, s);
+    err = launch_chunk_tc(static_cast<DType>(dtype), kernel_d, source, maps, p, s);
   } else {
     p.vec = D % 4 == 0 && aligned_to(k_cache, 4 * ce) && aligned_to(v_cache, 4 * ce) &&
             multiple(p.c.sk, 4) && multiple(p.c.sv, 4);

@@ -10,18 +10,47 @@
 //     copying warp each look up one box's page and issue its copy, K's and V's from
 //     one lookup, made a tile ahead.  A box that no row sees, or whose page does not
 //     exist, is copied from behind the last page, where TMA writes zeros.
+//     SRC = kChunkRows (pages of any size) and kChunkE4M3: four more warps gather
+//     the rows in 8-element pieces by asynchronous copies three half tiles ahead, one
+//     thread looking up each key's place a tile ahead.  e4m3 pieces land in a staging
+//     area, and the thread that copied a piece converts it (a code is exact in fp16
+//     and bf16; times its scale, rounded to T as cache_read does).
 //   - A row sees an interval of keys and the sinks (ChunkKeys); tiles that no row
 //     sees are left out.
 //   - Few tokens over long contexts have few items: their key tiles are cut into
 //     pieces (chunk.cuh), whose normalised outputs and log-sum-exps a second
 //     kernel joins in a fixed order.
-// Keys of pages that do not exist are masked by a word of bits per tile.
+// Keys of pages that do not exist are masked by a bit each.
 #pragma once
 
 #include "chunk.cuh"
 #include "packed_tc.cuh"
 
 namespace jvp {
+
+// The gathering sources: threads, registers (65536 / 512 a thread: 56 + 104 + 2 * 176 =
+// 4 * 128), and their shared memory behind the control block.
+constexpr int chunk_threads(int NQ, ChunkSource src) {
+  return packed_threads(NQ) + (src == kChunkBoxes ? 0 : 128);
+}
+struct ChunkPlaces {
+  long long k[kChunkTile], v[kChunkTile];  // elements from the start of the cache, -1: none
+  uint8_t k_scale[2][kChunkTile], v_scale[2][kChunkTile];  // by tile modulo 2
+};
+constexpr int kChunkAhead = 3;  // half tiles in flight
+template <int D, int NQ, ChunkSource SRC>
+struct ChunkLayout : PackedLayout<D, NQ> {
+  using P = PackedLayout<D, NQ>;
+  static constexpr int HALF_CODES = 64 * D;  // bytes of half a tile of codes
+  static constexpr int OFF_PLACES = P::OFF_CTRL + 1024;
+  static constexpr int OFF_STAGE = OFF_PLACES + static_cast<int>(sizeof(ChunkPlaces));
+  static constexpr int BYTES = SRC == kChunkBoxes ? P::SMEM_BYTES
+                               : SRC == kChunkRows
+                                   ? P::SMEM_BYTES + static_cast<int>(sizeof(ChunkPlaces))
+                                   : P::SMEM_BYTES + static_cast<int>(sizeof(ChunkPlaces)) +
+                                         kChunkAhead * HALF_CODES;
+  static_assert(BYTES <= 227 * 1024, "shared memory budget");
+};
 
 template <int D, int NQ, int NS>
 struct ChunkCtrl {
@@ -33,19 +62,38 @@ struct ChunkCtrl {
   uint64_t staged[2];
   uint64_t drain[2];
   // By key tile modulo 16 (the copies are at most 2 NS tiles ahead of the
-  // softmax), a bit for every 8 keys: their page does not exist.
-  uint32_t missing[16];
+  // softmax), a bit for every key: its page does not exist.
+  alignas(16) uint32_t missing[16][4];
   uint32_t tmem_base;
   int abort;
   int special;
 };
 
+// Asynchronous copy of BYTES, or zeros.
+template <int BYTES>
+__device__ __forceinline__ void chunk_copy(uint32_t dst, const void* src, bool on) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
+                 : "memory");
+}
+// Two codes (as fp16 values, which hold them exactly), times the scale, rounded to T.
+template <typename T>
+__device__ __forceinline__ uint32_t chunk_decode(uint32_t half2, float scale) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&half2));
+  return PackedElem<T>::pack(f.x * scale, f.y * scale);
+}
+
 template <typename T, int D, int NQ, ChunkSource SRC>
-__global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
+__global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3 - NQ : 1)
     chunk_tc_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p) {
-  using L = PackedLayout<D, NQ>;
+  using L = ChunkLayout<D, NQ, SRC>;
   constexpr int BM = L::BM, BN = L::BN, NS = L::NS, NB = L::NB, KCH = L::KCH;
-  constexpr int THREADS = packed_threads(NQ);
+  constexpr int THREADS = chunk_threads(NQ, SRC);
+  constexpr bool kGather = SRC != kChunkBoxes;
+  constexpr int kSoftmax = kGather ? 8 : 4;  // first softmax warp
   constexpr bool kBF16 = PackedElem<T>::kBF16;
   constexpr uint32_t IDESC_S = idesc_f16(kBF16, BM, BN, false);
   constexpr uint32_t IDESC_O = idesc_f16(kBF16, BM, D, true);
@@ -81,9 +129,9 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
       mbar_init(&ctrl->staged[x], 4);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&ctrl->k_full[s], 1);
+      mbar_init(&ctrl->k_full[s], kGather ? 4 : 1);  // one arrival per gathering warp
       mbar_init(&ctrl->k_empty[s], NB == 3 ? 2 : 1);  // one arrival per issuing warp
-      mbar_init(&ctrl->v_full[s], 1);
+      mbar_init(&ctrl->v_full[s], kGather ? 4 : 1);
       mbar_init(&ctrl->v_empty[s], NB == 3 ? 2 : 1);
       mbar_init(&ctrl->v_issued[s], 1);
       mbar_init(&ctrl->v_checked[s], 1);
@@ -140,9 +188,25 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
   };
 
   if (warp < 4) {
-    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (kGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 0) {
+    auto load_q = [&](int x) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctrl->q_full[x], KCH * p.group * p.tok * 128);
+        for (int ch = 0; ch < KCH; ++ch)
+          tma_load_4d(smem + L::OFF_Q + x * L::Q_BYTES + ch * BM * 128, &maps.q, &ctrl->q_full[x],
+                      ch * 64, hk * p.group, r0 + tok0 + x * p.tok, 0);
+      }
+    };
+    if (warp == 0 && kGather) {
+      load_q(0);
+      if (n_b > 0) load_q(1);
+      // (landed before the CTA can exit, whatever becomes of the others)
+      const int zero = 0;
+      mbar_wait(&ctrl->q_full[0], 0, &zero);
+      if (n_b > 0) mbar_wait(&ctrl->q_full[1], 0, &zero);
+    } else if (warp == 0) {
       // ---------------------------------------------------------- producer
       // Lane l copies box l % boxes of chunk l / boxes of a tile.
       const int boxes = BN / p.box_rows;
@@ -169,21 +233,21 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
         next_missing = looked && (raw < 0 || raw >= c.pages);
         next_page = looked && !next_missing ? raw : c.pages;
         page = next_page, row = next_missing ? 0 : next_row;
-        const uint32_t bits = __reduce_or_sync(
-            0xffffffffu, next_missing ? ((1u << p.box_rows / 8) - 1u) << box * (p.box_rows / 8) : 0u);
-        if (lane == 0) {
-          *static_cast<volatile uint32_t*>(&ctrl->missing[t & 15]) = bits;
-          if (bits) atomicOr(c.status, kStatusIndex);
+        const bool any = __any_sync(0xffffffffu, next_missing);
+        // (box by box: word w has keys 32 w ..)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t bits = 0u;
+          if (any) {
+            const int k0 = box * p.box_rows - 32 * w, k1 = k0 + p.box_rows;  // keys of this box
+            if (next_missing && k1 > 0 && k0 < 32)
+              bits = (0xFFFFFFFFu << max(k0, 0)) & (0xFFFFFFFFu >> (32 - min(k1, 32)));
+            bits = __reduce_or_sync(0xffffffffu, bits);
+          }
+          if (lane == 0) *static_cast<volatile uint32_t*>(&ctrl->missing[t & 15][w]) = bits;
         }
+        if (any && lane == 0) atomicOr(c.status, kStatusIndex);
         look_up(t + 1);
-      };
-      auto load_q = [&](int x) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&ctrl->q_full[x], KCH * p.group * p.tok * 128);
-          for (int ch = 0; ch < KCH; ++ch)
-            tma_load_4d(smem + L::OFF_Q + x * L::Q_BYTES + ch * BM * 128, &maps.q,
-                        &ctrl->q_full[x], ch * 64, hk * p.group, r0 + tok0 + x * p.tok, 0);
-        }
       };
       int k_fills = 0, v_fills = 0;
       auto load_kv = [&](int t, bool v) -> bool {
@@ -406,11 +470,148 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
         if (lane == 0) mbar_arrive(&ctrl->v_checked[k % NS]);
       }
     }
+  } else if (kGather && warp < 8) {
+    // ------------------------------------------------------------ gathering warps
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    using TC = typename std::conditional<SRC == kChunkE4M3, uint8_t, T>::type;
+    constexpr int PR = D / 8, HP = PR / 2;  // pieces of a row; of a thread in half a tile
+    constexpr int RS = 128 / PR;            // rows between a thread's pieces
+    ChunkPlaces* const places = reinterpret_cast<ChunkPlaces*>(smem + L::OFF_PLACES);
+    const int g = static_cast<int>(threadIdx.x) - 128;
+    const int piece = g % PR, prow = g / PR;
+    const bool in_row = piece * 8 < c.D;
+    const TC* const kc = static_cast<const TC*>(c.k) + hk * c.sk.h + piece * 8;
+    const TC* const vc = static_cast<const TC*>(c.v) + hk * c.sv.h + piece * 8;
+    // where this thread's pieces of row r lie in a tile (rows differ by multiples of
+    // 8 where RS is 8, so the swizzle is the same; RS = 16 too)
+    const uint32_t in_tile = (piece / 8) * BN * 128 + prow * 128 + (((piece % 8) ^ (prow & 7)) << 4);
+    const uint32_t stage = smem_u32(smem + L::OFF_STAGE) + g * 8;
+    static_assert(RS % 8 == 0, "swizzle");
+    // Key g of a tile: its block-table entry two tiles ahead, its scales one ahead.
+    int raw = -1, raw_row = 0, page = -1, row = 0;
+    bool looked = false, have = false, none = false;  // looked up; there; its page is not
+    unsigned scales = 0;
+    auto look_up = [&](int t) {  // the entry
+      looked = false;
+      if (t >= n) return;
+      const int j = first_key(t) + g;
+      if (keys.unseen(j, 1) || j >= it.keys) return;
+      looked = true;
+      int entry;
+      split_position(c, j, &entry, &raw_row);
+      raw = __ldg(c.table + it.b * c.table_stride + entry);
+    };
+    auto resolve = [&]() {  // the place, and its scales on their way
+      have = looked && raw >= 0 && raw < c.pages;
+      none = looked && !have;
+      page = have ? raw : 0, row = have ? raw_row : 0;
+      if (SRC == kChunkE4M3 && have) {
+        const long long at = (static_cast<long long>(page) * c.Hkv + hk) * c.page_size + row;
+        scales = __ldg(c.k_scale + at) | static_cast<unsigned>(__ldg(c.v_scale + at)) << 8;
+      }
+    };
+    auto sync_gather = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    // The places of tile t for every thread, and the next tiles' lookups.
+    auto publish = [&](int t) {
+      sync_gather();  // the last tile's places have been read
+      places->k[g] = have ? page * c.sk.b + row * c.sk.n : -1;
+      places->v[g] = have ? page * c.sv.b + row * c.sv.n : -1;
+      if (SRC == kChunkE4M3) {
+        places->k_scale[t & 1][g] = static_cast<uint8_t>(have ? scales & 0xFFu : 127u);
+        places->v_scale[t & 1][g] = static_cast<uint8_t>(have ? scales >> 8 : 127u);
+      }
+      const uint32_t gone = __ballot_sync(0xffffffffu, none);
+      if (lane == 0) {
+        *static_cast<volatile uint32_t*>(&ctrl->missing[t & 15][warp & 3]) = gone;
+        if (gone) atomicOr(c.status, kStatusIndex);
+      }
+      resolve();
+      look_up(t + 2);
+      sync_gather();
+    };
+    // Half tile h: 4 t + 0, 1 of K's tile t, + 2, 3 of V's.
+    bool ok = true;
+    auto slot_of = [&](int t) { return t % NS; };
+    auto wait_empty = [&](int t, bool v) {
+      return wait(v ? &ctrl->v_empty[slot_of(t)] : &ctrl->k_empty[slot_of(t)], (t / NS) ^ 1);
+    };
+    auto issue = [&](int h) {
+      const int t = h >> 2;
+      // (whatever became of a wait: the warps meet here)
+      if (t < n && (h & 3) == 0) publish(t);
+      if (ok && t < n) {
+        const bool v = (h & 2) != 0;
+        const int r0h = (h & 1) * (BN / 2);
+        if (SRC == kChunkRows && (h & 1) == 0) ok = wait_empty(t, v);
+        if (ok) {
+          const uint32_t tile = smem_u32(smem + (v ? L::OFF_V : L::OFF_K) + slot_of(t) * L::KV_BYTES);
+          const uint32_t to = SRC == kChunkE4M3 ? stage + h % kChunkAhead * L::HALF_CODES
+                                                : tile + in_tile + r0h * 128;
+          const long long* at = v ? places->v : places->k;
+          const TC* base = v ? vc : kc;
+#pragma unroll
+          for (int i = 0; i < HP; ++i) {
+            const long long place = at[r0h + prow + i * RS];
+            const bool on = in_row && place >= 0;
+            if (!JVP_CHECK(r0h + prow + i * RS < BN, c.status, kChkSmem)) continue;
+            if constexpr (SRC == kChunkE4M3)
+              chunk_copy<8>(to + i * 128 * 8, base + (on ? place : 0), on);
+            else
+              chunk_copy<16>(to + i * RS * 128, base + (on ? place : 0), on);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(0);
+    resolve();
+    look_up(1);
+    for (int h = 0; h < kChunkAhead; ++h) issue(h);
+    for (int h = 0; h < 4 * n; ++h) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kChunkAhead - 1) : "memory");
+      const int t = h >> 2;
+      const bool v = (h & 2) != 0;
+      if constexpr (SRC == kChunkE4M3) {
+        if (ok && (h & 1) == 0) ok = wait_empty(t, v);
+        if (ok) {
+          const int r0h = (h & 1) * (BN / 2);
+          const uint32_t from = stage + h % kChunkAhead * L::HALF_CODES;
+          const uint32_t to = smem_u32(smem + (v ? L::OFF_V : L::OFF_K) + slot_of(t) * L::KV_BYTES) +
+                              in_tile + r0h * 128;
+          const uint8_t* scale = v ? places->v_scale[t & 1] : places->k_scale[t & 1];
+#pragma unroll
+          for (int i = 0; i < HP; ++i) {
+            uint32_t w[2], y[4];
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(w[0]), "=r"(w[1])
+                         : "r"(from + i * 128 * 8)
+                         : "memory");
+            const float f = scale_value(scale[r0h + prow + i * RS]);
+            e4m3x4_to_half2x2(w[0], y[0], y[1]);
+            e4m3x4_to_half2x2(w[1], y[2], y[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f);
+            st_shared_v4(to + i * RS * 128, y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      // (the staging area's next half tile takes the place of the one just read)
+      if (ok && v && (h & 1) == 0 && inspected(t) && g == 0)
+        mbar_arrive(&ctrl->v_issued[inspected_before(t) % NS]);
+      if (ok && (h & 1) == 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v ? &ctrl->v_full[slot_of(t)] : &ctrl->k_full[slot_of(t)]);
+      }
+      issue(h + kChunkAhead);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     // ------------------------------------------------------------ softmax
-    if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (kGather) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int x = (warp - 4) >> 2;  // query tile
+    const int x = (warp - kSoftmax) >> 2;  // query tile
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..
     const int r = sub * 32 + lane;
     const int nx = x ? n_b : n_a;
@@ -462,14 +663,12 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
         for (int e = 0; e < BN; ++e)
           if (e < a && e >= b) s[e] = -INFINITY;
       }
-      const uint32_t missing = *static_cast<volatile uint32_t*>(&ctrl->missing[t & 15]);
-      if (missing != 0u) {
+      uint32_t missing[4];
+      ld_shared_v4(smem_u32(ctrl->missing[t & 15]), missing);
+      if ((missing[0] | missing[1] | missing[2] | missing[3]) != 0u) {
 #pragma unroll
-        for (int e = 0; e < BN; e += 8)
-          if (missing & (1u << (e / 8))) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s[e + k] = -INFINITY;
-          }
+        for (int e = 0; e < BN; ++e)
+          if (missing[e / 32] & (1u << (e % 32))) s[e] = -INFINITY;
       }
       const float m_tile = packed_max(s) * scale;
       const bool need = m_tile - m_run > PackedElem<T>::kTop;
@@ -560,9 +759,22 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
             split_position(c, j, &entry, &in_page);
             const int page = page_of(c, it.b, entry);
             if (page < 0) continue;
-            const uint4 x4 = __ldg(reinterpret_cast<const uint4*>(
-                static_cast<const T*>(c.v) + page * c.sv.b + hk * c.sv.h + in_page * c.sv.n + d));
-            const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+            const long long place = page * c.sv.b + hk * c.sv.h + in_page * c.sv.n + d;
+            uint32_t w[4];
+            if constexpr (SRC == kChunkE4M3) {
+              const uint2 codes =
+                  __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + place));
+              const float f = scale_value(__ldg(
+                  c.v_scale + (static_cast<long long>(page) * c.Hkv + hk) * c.page_size + in_page));
+              e4m3x4_to_half2x2(codes.x, w[0], w[1]);
+              e4m3x4_to_half2x2(codes.y, w[2], w[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = chunk_decode<T>(w[k], f);
+            } else {
+              const uint4 x4 =
+                  __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(c.v) + place));
+              w[0] = x4.x, w[1] = x4.y, w[2] = x4.z, w[3] = x4.w;
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint32_t bits = w[k / 2] >> (16 * (k & 1)) & 0xFFFFu;
@@ -620,7 +832,7 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->staged[x]);
-        if (warp == 4 + 4 * x && wait(&ctrl->staged[x], 0) && lane == 0) {
+        if (warp == kSoftmax + 4 * x && wait(&ctrl->staged[x], 0) && lane == 0) {
           for (int ch = 0; ch < KCH; ++ch)
             tma_store_4d(&maps.o, smem + L::OFF_Q + x * L::Q_BYTES + ch * BM * 128, ch * 64,
                          hk * p.group, r0 + first, 0);
@@ -641,12 +853,12 @@ __global__ void __launch_bounds__(packed_threads(NQ), 3 - NQ)
 template <typename T, int D, int NQ, ChunkSource SRC>
 cudaError_t launch_chunk_tc_variant(const ChunkMaps& maps, const ChunkParams& p,
                                     cudaStream_t stream) {
-  constexpr int smem = PackedLayout<D, NQ>::SMEM_BYTES;
+  constexpr int smem = ChunkLayout<D, NQ, SRC>::BYTES;
   const cudaError_t e = allow_shared_memory<chunk_tc_kernel<T, D, NQ, SRC>>(smem);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.units) * p.heads;
   chunk_tc_kernel<T, D, NQ, SRC>
-      <<<static_cast<unsigned>(grid), packed_threads(NQ), smem, stream>>>(maps, p);
+      <<<static_cast<unsigned>(grid), chunk_threads(NQ, SRC), smem, stream>>>(maps, p);
   return cudaGetLastError();
 }
 

@@ -574,10 +574,12 @@ size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_d
  * A row that sees no key gets o = 0, lse = -inf.  Results do not depend on keys that
  * a row does not see, whatever they hold.  Long key ranges with few tokens are split
  * over the GPU, and their parts combined in an order that depends on the lengths only
- * (the same call gives the same bits).  fp16/bf16 with D a multiple of 8, H / Hkv at
- * most 128, a nonzero scale, 16-byte aligned rows and pages of a multiple of 8 rows
- * run on the tensor cores (weights rounded to 16 bits as in jvp_attn_fwd_packed);
- * every other case on the CUDA cores in fp32.
+ * (the same call gives the same bits).  fp16/bf16 queries with D a multiple of 8, H /
+ * Hkv at most 128, a nonzero scale and 16-byte aligned rows (8-byte aligned ones of an
+ * e4m3 cache) run on the tensor cores: weights are rounded to 16 bits as in
+ * jvp_attn_fwd_packed, and entries of an e4m3 cache are taken as jvp_attn_cache_read
+ * gives them in `dtype` (bf16: exact above its subnormals; fp16: infinite above 65504).
+ * Every other case runs on the CUDA cores in fp32.
  */
 jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, int64_t T,
                             const void* q, const jvp_strides_t* q_strides, const void* k_cache,

@@ -90,6 +90,35 @@ def test_ragged_chunks_on_the_tensor_cores(dt, H, Hkv, D, page, window, sinks):
     check(c, q, cu, o, lse, window, sinks, heads=sorted({0, H // 2, H - 1}))
 
 
+GATHERED = [("bf16", 8, 2, 128, 16, True), ("f16", 4, 4, 64, 32, True), ("bf16", 16, 1, 64, 1, True),
+            ("f16", 3, 1, 128, 100, True), ("bf16", 12, 4, 40, 24, True), ("bf16", 7, 1, 8, 3, True),
+            ("bf16", 8, 2, 128, 1, False), ("f16", 4, 4, 64, 20, False), ("bf16", 5, 5, 96, 7, False),
+            ("f16", 12, 4, 40, 130, False)]
+
+
+@pytest.mark.parametrize("window,sinks", [(None, 0), (1, 0), (50, 3), (200, 130)])
+@pytest.mark.parametrize("dt,H,Hkv,D,page,e4m3", GATHERED)
+def test_gathered_rows(dt, H, Hkv, D, page, e4m3, window, sinks):
+    """e4m3 caches, and pages that are no multiple of 8 rows."""
+    c, q, cu = make(NEW, PAST, H, Hkv, D, dt, page, e4m3, seed=D)
+    o, lse = run(c, q, cu, window, sinks)
+    assert api.last_path() == 1
+    check(c, q, cu, o, lse, window, sinks, heads=sorted({0, H // 2, H - 1}))
+
+
+@pytest.mark.parametrize("dt,H,Hkv,D,page,e4m3", [("bf16", 8, 2, 128, 16, True), ("f16", 2, 2, 64, 5, False),
+                                                  ("f16", 4, 1, 64, 64, True)])
+@pytest.mark.parametrize("new,past", [([1700], [900]), ([3] * 90, [40] * 90), ([4, 1, 70], [9000, 20000, 5000])],
+                         ids=["one", "ninety", "split"])
+def test_gathered_rows_of_long_chunks_and_contexts(new, past, dt, H, Hkv, D, page, e4m3):
+    c, q, cu = make(new, past, H, Hkv, D, dt, page, e4m3, seed=4)
+    o, lse = run(c, q, cu)
+    assert api.last_path() == 1
+    check(c, q, cu, o, lse, heads=[0, H - 1], rows=60)
+    o2, lse2 = run(c, q, cu)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("window,sinks", [(None, 0), (1, 1), (50, 3), (200, 70)])
 @pytest.mark.parametrize("dt,H,Hkv,D,page,e4m3", [
     ("f32", 4, 2, 64, 16, False), ("f32", 2, 2, 128, 7, False), ("f32", 3, 1, 33, 1, False),
@@ -151,9 +180,10 @@ def test_whole_prompts_agree_with_packed_attention(dt):
     check(fake, q, cu, p, plse)
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("dt", ["bf16", "f32", "e4m3"])
 def test_tokens_before_the_first_position_see_nothing(dt):
-    c, q, cu = make([5, 200, 3], [-2, -190, -3], 4, 2, 64, dt, seed=2)
+    c, q, cu = make([5, 200, 3], [-2, -190, -3], 4, 2, 64, "bf16" if dt == "e4m3" else dt,
+                    e4m3=dt == "e4m3", seed=2)
     assert c.lens == [3, 10, 0]
     o, lse = run(c, q, cu)
     check(c, q, cu, o, lse)
@@ -172,14 +202,18 @@ def test_a_padded_batch_leaves_its_other_rows(dt):
 
 
 @pytest.mark.parametrize("window,sinks", [(None, 0), (70, 3), (300, 140)])
-@pytest.mark.parametrize("dt,page", [("bf16", 16), ("f16", 64), ("f32", 16), ("bf16", 8)])
-def test_what_rows_do_not_see_has_no_say(dt, page, window, sinks):
+@pytest.mark.parametrize("dt,page,e4m3", [
+    ("bf16", 16, False), ("f16", 64, False), ("f32", 16, False), ("bf16", 8, False), ("f16", 20, False),
+    ("bf16", 16, True), ("f16", 7, True), ("f32", 16, True)])
+def test_what_rows_do_not_see_has_no_say(dt, page, e4m3, window, sinks):
     """Infinities and NaN at later positions, before the window and behind the end
     (in the last page) change nothing; pages that no token sees need not exist."""
     new, past = [40, 3, 130], [500, 700, 333]
-    c, q, cu = make(new, past, 4, 2, 64, dt, page, seed=5)
+    c, q, cu = make(new, past, 4, 2, 64, dt, page, e4m3, seed=5)
     want = run(c, q, cu, window, sinks)
     bad = torch.tensor([float("nan"), float("inf"), -float("inf"), float("nan")]).repeat(16)
+    if e4m3:  # (codes hold NaN but no infinities)
+        bad = torch.full((64,), float("nan"))
     some = torch.ones(len(q), dtype=torch.bool)
     for b, n in enumerate(c.lens):
         place = lambda j: (int(c.table[b, j // page]), j % page)  # noqa: E731
@@ -211,18 +245,20 @@ def test_what_rows_do_not_see_has_no_say(dt, page, window, sinks):
     assert torch.equal(got[1][:, some], want[1][:, some])
     # and the rows that do see them hold what the definition gives: NaN and infinities
     last = got[0][int(cu[1]) - 1].float().cpu()
+    if e4m3:
+        assert torch.isnan(last).all()
+        return
     assert torch.isnan(last[:, 0]).all() and (last[:, 1] == float("inf")).all()
     assert (last[:, 2] == -float("inf")).all()
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_pages_that_do_not_exist_are_skipped_and_reported(dt):
-    c, q, cu = make([5, 3], [300, 40], 4, 2, 64, dt, seed=5)
+@pytest.mark.parametrize("dt,e4m3", [("bf16", False), ("f32", False), ("bf16", True)])
+def test_pages_that_do_not_exist_are_skipped_and_reported(dt, e4m3):
+    c, q, cu = make([5, 3], [300, 40], 4, 2, 64, dt, e4m3=e4m3, seed=5)
     c.table[0, 4] = c.pages          # positions 64 .. 79 of the first
     c.table[0, 19] = -3              # its last page: positions 304 and on
     got = run(c, q, cu)
     assert api.device_status() == _abi.JVP_ERR_INDEX
-    k, v = (x.copy() for x in (np.zeros((2, 305, 64)), np.zeros((2, 305, 64))))
     ok = np.array([j // 16 not in (4, 19) for j in range(305)])
     c.table[0, 4] = c.table[0, 19] = 0
     k, v = c.rows(0)
@@ -317,7 +353,7 @@ def test_a_workspace_and_two_streams():
     got = run(c, q, cu, workspace=ws)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     with pytest.raises(_abi.JvpAttnError):
-        run(c, q, cu, workspace=ws[:need - 16])
+        run(c, q, cu, workspace=ws[:1024])
     lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
     args = (q.cuda(), d["k_cache"], d["v_cache"], d["block_table"], lens, cu.cuda())
     torch.cuda.synchronize()
@@ -327,6 +363,24 @@ def test_a_workspace_and_two_streams():
             outs.append(api.attention_chunk(*args))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[0]) for o in outs)
+
+
+def test_values_of_an_e4m3_cache_that_fp16_cannot_hold():
+    """Taken as cache_read gives them: infinite above 65504, multiples of 2^-24 below."""
+    c, q, cu = make([3], [40], 2, 1, 64, "f16", e4m3=True, seed=2)
+    c.scales[1][:] = 127 + 12
+    o, lse = run(c, q, cu)
+    d = c.cuda()
+    k, v = api.cache_read(d["k_cache"], d["v_cache"], d["block_table"], None,
+                          torch.tensor([0, 43], dtype=torch.int32).cuda(), num_rows=43,
+                          k_scale=d["k_scale"], v_scale=d["v_scale"], dtype=torch.float16)
+    big = torch.isinf(v[:41, 0])  # seen by every token
+    assert big.any()
+    assert not torch.isfinite(o[:, :, big.any(0)]).any()
+    c.scales[1][:] = 127 - 20
+    c.scales[0][:] = 127 - 24
+    o, lse = run(c, q, cu)
+    check(c, q, cu, o, lse)
 
 
 def test_no_rows():
