@@ -1,14 +1,17 @@
-// chunk.cuh -- which work a block of the attention of chunks over a paged cache
-// takes, and which keys its rows see.  Lengths live on the device, so each block
-// finds its own.
+// chunk.cuh -- which work a CTA of the attention of chunks over a paged cache takes,
+// and which keys its rows see.
 //
-// An item is a tile of a sequence's new tokens (ROWS tokens) and a head; its keys
-// are cut into pieces where that keeps the GPU busy.  With n_b key tiles of a
-// sequence's items (a bound) and t_b items per head, W = heads sum t_b n_b and
-// L = max(least, ceil(W / target)), each of its items is cut into S_b =
-// ceil(n_b / L) pieces: equal parts, so pieces are of about L tiles however the
-// lengths are spread, and nothing is cut where there are items enough.  Pieces of
-// cut items number at most 2 target: S_b <= 2 n_b / L where S_b > 1.
+// An item is a tile of a sequence's new tokens and a head; its cost is its key
+// tiles and kChunkStart for its beginning and end.  The items of all sequences form
+// a list, heads innermost, and CTA c takes the c-th of `count` equal parts of the
+// list's cost: it continues an item that others began, takes whole ones, and begins
+// one that others end.  So CTAs are equally loaded whatever the lengths, which only
+// the device knows, and an item is cut only where a CTA's part ends (and not within
+// kChunkSnap tiles of its ends).  Each CTA finds its part by itself: the costs of all
+// items are summed by its threads, an item each, some 2 us (a kernel of one block in
+// front that did it for all, its successor's set-up beside it, took 5.5).  Parts of
+// cut items leave normalised outputs and log-sum-exps in the workspace, two slots
+// per CTA, for the join.
 #pragma once
 
 #include "debug_checks.cuh"
@@ -16,21 +19,10 @@
 
 namespace jvp {
 
-struct ChunkItem {
-  int b, r0, len, past;  // sequence, its first row, new tokens, positions before them
-  int keys;              // positions of the sequence
-  int tok0;              // the item's first token
-  int piece, pieces;     // pieces as the sequence's items are cut (S_b)
-  long long slot;        // of the item's first piece for head 0, or -1: not cut
-};
-
 struct ChunkSequence {
-  int r0, len, keys;
-  long long items;  // tiles of tokens
-  int tiles;        // key tiles of an item, at most
+  int r0, len, keys;  // first row, new tokens, positions
+  int items;          // tiles of tokens
 };
-
-template <int TILE>
 __device__ __forceinline__ ChunkSequence chunk_sequence(const ChunkParams& p, int rows, int b,
                                                         bool* bad) {
   ChunkSequence s;
@@ -41,132 +33,8 @@ __device__ __forceinline__ ChunkSequence chunk_sequence(const ChunkParams& p, in
     *bad = true;
     s.r0 = s.len = 0;
   }
-  s.items = (s.len + static_cast<long long>(rows) - 1) / rows;
-  long long n = (s.keys + static_cast<long long>(TILE) - 1) / TILE;
-  if (p.window > 0) {  // the window's keys of `rows` tokens begin anywhere in a tile
-    const long long span = static_cast<long long>(p.window) + rows - 2;
-    const long long most = (span + TILE - 1) / TILE + 1 + (p.sinks + TILE - 1ll) / TILE;
-    n = n < most ? n : most;
-  }
-  s.tiles = n < 1 ? 1 : static_cast<int>(n);
+  s.items = static_cast<int>((static_cast<unsigned>(s.len) + rows - 1u) / rows);
   return s;
-}
-// Largest number of tiles of a piece, of W tiles in all.
-__device__ __forceinline__ long long chunk_piece_tiles(const ChunkParams& p, long long W) {
-  if (p.least == 0) return 1ll << 40;
-  const long long even = (W + p.target - 1) / p.target;
-  return even > p.least ? even : p.least;
-}
-
-template <typename T>
-__device__ __forceinline__ T warp_inclusive(T x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-
-struct ChunkScan {
-  long long part[32], part2[32];
-  ChunkItem item;
-  int found;
-};
-
-// Unit u of the list of all sequences' (tile of tokens, piece) pairs, a
-// sequence's last tokens (the longest key ranges) first.  Executed by the whole
-// block; false where the list is shorter.  `first`: of the blocks with u = 0 the
-// one that reports bad offsets and lengths and records the slots in use.
-template <int TILE, int THREADS>
-__device__ __forceinline__ bool find_chunk_item(const ChunkParams& p, int rows, int u, bool first,
-                                                ChunkScan* sh, ChunkItem* out) {
-  const int lane = threadIdx.x & 31;
-  const int B = p.c.B;
-  bool bad = false;
-  // (each thread a run of sequences; up to 32 sequences: each warp for itself)
-  const bool small = B <= 32;
-  const int threads = small ? 32 : THREADS, me = small ? lane : static_cast<int>(threadIdx.x);
-  const int per = (B + threads - 1) / threads;
-  const int b_lo = min(B, me * per), b_hi = min(B, b_lo + per);
-  auto block_inclusive = [&](long long x, long long* part, long long* total) {
-    long long incl = warp_inclusive(x);
-    if (small) {
-      *total = __shfl_sync(0xffffffffu, incl, 31);
-      return incl;
-    }
-    if (lane == 31) part[threadIdx.x >> 5] = incl;
-    __syncthreads();
-    long long before = 0, all = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < static_cast<int>(threadIdx.x >> 5)) before += part[w];
-      all += part[w];
-    }
-    __syncthreads();
-    *total = all;
-    return before + incl;
-  };
-  long long w = 0;
-  ChunkSequence s{};
-  for (int b = b_lo; b < b_hi; ++b) {
-    s = chunk_sequence<TILE>(p, rows, b, &bad);
-    w += s.items * s.tiles;
-  }
-  long long W;
-  block_inclusive(w, sh->part, &W);
-  const long long L = chunk_piece_tiles(p, W * p.heads);
-  long long units = 0, cut = 0;  // of this thread's sequences: pieces, those of cut items
-  for (int b = b_lo; b < b_hi; ++b) {
-    if (per > 1) s = chunk_sequence<TILE>(p, rows, b, &bad);
-    const long long S = (s.tiles + L - 1) / L, n = s.items * S;
-    units += n;
-    if (S > 1) cut += n;
-  }
-  long long all_units, all_cut;
-  long long before = block_inclusive(units, sh->part, &all_units) - units;
-  long long cut_before = block_inclusive(cut, sh->part2, &all_cut) - cut;
-  if (first && u == 0) {
-    if (bad) atomicOr(p.c.status, kStatusIndex);
-    if (threadIdx.x == 0 && p.least > 0) *p.ws_count = static_cast<int>(all_cut * p.heads);
-  }
-  if (u >= all_units) return false;
-  ChunkItem item{};
-  const bool mine = u >= before && u < before + units;
-  if (mine) {
-    int b = b_lo;
-    long long n = 0, S = 1;
-    for (; b < b_hi; ++b) {
-      if (per > 1) s = chunk_sequence<TILE>(p, rows, b, &bad);
-      S = (s.tiles + L - 1) / L, n = s.items * S;
-      if (u < before + n) break;
-      before += n;
-      if (S > 1) cut_before += n;
-    }
-    const long long at = u - before, back = at / S;
-    item.b = b, item.r0 = s.r0, item.len = s.len, item.keys = s.keys;
-    item.past = s.keys - s.len;
-    item.tok0 = static_cast<int>((s.items - 1 - back) * rows);
-    item.piece = static_cast<int>(at - back * S), item.pieces = static_cast<int>(S);
-    item.slot = S > 1 ? (cut_before + back * S) * p.heads : -1;
-  }
-  if (small) {
-    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-    out->b = __shfl_sync(0xffffffffu, item.b, src);
-    out->r0 = __shfl_sync(0xffffffffu, item.r0, src);
-    out->len = __shfl_sync(0xffffffffu, item.len, src);
-    out->past = __shfl_sync(0xffffffffu, item.past, src);
-    out->keys = __shfl_sync(0xffffffffu, item.keys, src);
-    out->tok0 = __shfl_sync(0xffffffffu, item.tok0, src);
-    out->piece = __shfl_sync(0xffffffffu, item.piece, src);
-    out->pieces = __shfl_sync(0xffffffffu, item.pieces, src);
-    out->slot = __shfl_sync(0xffffffffu, item.slot, src);
-  } else {
-    if (mine) sh->item = item;
-    __syncthreads();
-    *out = sh->item;
-  }
-  return true;
 }
 
 // The keys that the rows of an item see.  A row at position x sees [lo(x), x] and,
@@ -179,6 +47,7 @@ struct ChunkKeys {
   int end;                // keys of its last row
   int front, skip;
   __device__ __forceinline__ int lo(int x) const { return window > 0 ? max(0, x - window + 1) : 0; }
+  __device__ __forceinline__ ChunkKeys() {}
   // rows at positions first .. last (either may be negative: no keys)
   __device__ __forceinline__ ChunkKeys(const ChunkParams& p, int first, int last) {
     window = p.window, sinks = p.sinks;
@@ -196,6 +65,252 @@ struct ChunkKeys {
   }
   __device__ __forceinline__ bool sees(int x, int j) const {
     return j <= x && (j >= lo(x) || j < sinks);
+  }
+};
+// Tokens of an item: up to query_tiles tiles of rows of tok tokens.
+__device__ __forceinline__ int chunk_step(const ChunkParams& p) { return p.query_tiles * p.tok; }
+// Key tiles by which an item is cut: those of its first tile of rows (a second one
+// may have one more, which goes with the last part).
+template <int TILE>
+__device__ __forceinline__ int chunk_tiles(const ChunkParams& p, const ChunkSequence& s, int item,
+                                           ChunkKeys<TILE>* keys) {
+  const int past = s.keys - s.len, tok0 = item * chunk_step(p);
+  const int toks = min(s.len - tok0, chunk_step(p));
+  *keys = ChunkKeys<TILE>(p, past + tok0, past + tok0 + toks - 1);
+  return keys->tiles(past + tok0 + min(toks, p.tok) - 1);
+}
+
+// Shared memory of the division (the tiles' space, before they are copied).
+constexpr int kChunkSeqs = 2048;  // sequences at a time
+struct ChunkScratch {
+  long long part[32];
+  int4 plan[2];         // where the CTA's part begins and ends
+  long long cut_first;  // of the item in which it ends: its first position of the list
+  int cut_cost;
+  int first[kChunkSeqs + 1], r0[kChunkSeqs], len[kChunkSeqs], keys[kChunkSeqs];
+};
+// Exclusive sum over the block, and the total.
+template <int THREADS>
+__device__ __forceinline__ long long chunk_block_sum(long long x, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += part[w];
+    all += part[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + incl - x;
+}
+
+// Where the part of CTA blockIdx.x begins and ends (sequence, item, head, key tile);
+// false if it has none.  Executed by the whole block.  Also names for the join the
+// item that the CTA begins and others end, and (CTA 0) reports bad offsets and lengths.
+template <int TILE, int THREADS>
+__device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch* sh, int4* start,
+                                             int4* end) {
+  const int tid = static_cast<int>(threadIdx.x), B = p.c.B, step = chunk_step(p);
+  bool bad = false;
+  int b0 = 0, nb = 0;  // sequences in shared memory
+  auto load_round = [&](int from) {  // their items
+    b0 = from, nb = min(B - from, kChunkSeqs);
+    long long items = 0;
+    for (int i0 = 0; i0 < nb; i0 += THREADS) {
+      const int i = i0 + tid;
+      ChunkSequence s{};
+      if (i < nb) s = chunk_sequence(p, step, b0 + i, &bad);
+      long long total;
+      const long long before = items + chunk_block_sum<THREADS>(s.items, sh->part, &total);
+      if (i < nb)
+        sh->first[i] = static_cast<int>(before), sh->r0[i] = s.r0, sh->len[i] = s.len,
+        sh->keys[i] = s.keys;
+      items += total;
+    }
+    if (tid == 0) sh->first[nb] = static_cast<int>(items);
+    __syncthreads();
+    return static_cast<int>(items);
+  };
+  auto cost_of = [&](int i, int* b, int* in_seq) {  // of item i of the round
+    int lo = 0, hi = nb;  // the last sequence with first <= i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sh->first[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    *b = b0 + lo, *in_seq = i - sh->first[lo];
+    ChunkSequence s;
+    s.r0 = sh->r0[lo], s.len = sh->len[lo], s.keys = sh->keys[lo];
+    ChunkKeys<TILE> keys;
+    return kChunkStart + chunk_tiles(p, s, *in_seq, &keys);
+  };
+  // ---- all costs
+  long long all = 0, before = 0;
+  int cost = 0, b = 0, in_seq = 0, steps = 0;  // (kept where one step covers the items)
+  for (int from = 0; from < B; from += kChunkSeqs) {
+    const int I = load_round(from);
+    for (int i0 = 0; i0 < I; i0 += THREADS, ++steps) {
+      cost = i0 + tid < I ? cost_of(i0 + tid, &b, &in_seq) : 0;
+      long long total;
+      before = all + chunk_block_sum<THREADS>(cost, sh->part, &total);
+      all += total;
+    }
+  }
+  const int c = static_cast<int>(blockIdx.x);
+  const long long W = all * p.heads;
+  long long parts = W / kChunkLeast;
+  parts = parts < 1 ? 1 : parts > p.grid ? p.grid : parts;
+  const int count = W == 0 ? 0 : static_cast<int>(parts);
+  if (c == 0) {
+    if (bad) atomicOr(p.c.status, kStatusIndex);
+    if (tid == 0) *p.ws_count = count;
+  }
+  if (c >= count) return false;
+  // 32-bit arithmetic where it does: a 64-bit division takes a fifth of a microsecond
+  const bool narrow = W < (1ll << 31);
+  auto position = [&](int k) -> long long {
+    if (narrow) {
+      const unsigned w = static_cast<unsigned>(W), n = static_cast<unsigned>(count);
+      return w / n * k + w % n * k / n;
+    }
+    return W / count * k + W % count * k / count;
+  };
+  const long long x0 = position(c), x1 = position(c + 1);
+  // ---- the items in which the part begins and ends
+  auto place = [&](long long x, int which) {  // by the thread whose item holds position x
+    const long long from = x - before * p.heads;
+    const int h = narrow ? static_cast<int>(static_cast<unsigned>(from) / static_cast<unsigned>(cost))
+                         : static_cast<int>(from / cost);
+    const int d = static_cast<int>(from - static_cast<long long>(h) * cost);
+    int4 y;
+    if (d < kChunkStart + (p.cut ? kChunkSnap : 0) && (p.cut || d == 0)) {
+      y = make_int4(b, in_seq, h, 0);
+    } else if (p.cut && cost - d >= kChunkSnap) {
+      y = make_int4(b, in_seq, h, d - kChunkStart);
+      if (which) sh->cut_first = x - d, sh->cut_cost = cost;
+    } else if (h + 1 < p.heads) {  // the next item is the first of the next part
+      y = make_int4(b, in_seq, h + 1, 0);
+    } else {
+      bool ignore = false;
+      ChunkSequence s = chunk_sequence(p, step, b, &ignore);
+      y = make_int4(b, in_seq + 1, 0, 0);
+      while (y.y == s.items) {
+        y.x += 1, y.y = 0, s.items = 0;
+        if (y.x == B) break;
+        s = chunk_sequence(p, step, y.x, &ignore);
+      }
+    }
+    sh->plan[which] = y;
+  };
+  if (tid == 0 && c + 1 == count) sh->plan[1] = make_int4(B, 0, 0, 0);
+  auto look = [&]() {
+    const long long lo = before * p.heads, hi = lo + static_cast<long long>(cost) * p.heads;
+    if (x0 >= lo && x0 < hi) place(x0, 0);
+    if (c + 1 < count && x1 >= lo && x1 < hi) place(x1, 1);
+  };
+  if (steps == 1) {
+    look();
+  } else {
+    all = 0;
+    for (int from = 0; from < B; from += kChunkSeqs) {
+      const int I = B > kChunkSeqs ? load_round(from) : sh->first[nb];
+      for (int i0 = 0; i0 < I; i0 += THREADS) {
+        cost = i0 + tid < I ? cost_of(i0 + tid, &b, &in_seq) : 0;
+        long long total;
+        before = all + chunk_block_sum<THREADS>(cost, sh->part, &total);
+        all += total;
+        look();
+      }
+    }
+  }
+  __syncthreads();
+  *start = sh->plan[0], *end = sh->plan[1];
+  if (tid == 0) {
+    int4 item = make_int4(0, 0, 0, 0);
+    const bool goes_on =
+        start->x == end->x && start->y == end->y && start->z == end->z && start->w > 0;
+    if (end->w > 0 && !goes_on) {
+      // the CTA in whose part its last unit lies, unless that part begins so near the
+      // item's end that it leaves it to the one before
+      const long long last = sh->cut_first + sh->cut_cost - 1;
+      int c1 = static_cast<int>(min((last + 1) * count / W, static_cast<long long>(count - 1)));
+      while (position(c1) > last) --c1;
+      while (c1 + 1 < count && position(c1 + 1) <= last) ++c1;
+      if (last + 1 - position(c1) < kChunkSnap) --c1;
+      bool ignore = false;
+      const ChunkSequence s = chunk_sequence(p, step, end->x, &ignore);
+      const int tok0 = end->y * step;
+      item = make_int4(c1 - c + 1, s.r0 + tok0, min(s.len - tok0, step), end->z);
+    }
+    p.ws_item[c] = item;
+  }
+  __syncthreads();  // the scratch has been read
+  return true;
+}
+
+// A CTA's part of one item: key tiles [t0, t1) of `all`, in slot `slot` of the
+// workspace (-1: it is the whole item).
+template <int TILE>
+struct ChunkPart {
+  int b, r0, len, past, keys;  // as in the sequence; past: positions before its new tokens
+  int tok0, toks, head;
+  int t0, t1, all, slot;
+  ChunkKeys<TILE> see;
+};
+
+// The parts of CTA blockIdx.x, one after the other.  Every warp walks for itself.
+template <int TILE>
+struct ChunkWalk {
+  int b, item, head, t;
+  int4 end;
+  ChunkSequence s;
+  bool more;
+  __device__ __forceinline__ ChunkWalk(const ChunkParams& p, const int4& a, const int4& e) {
+    end = e;
+    b = a.x, item = a.y, head = a.z, t = a.w;
+    more = b < p.c.B;
+    bool bad = false;
+    if (more) s = chunk_sequence(p, chunk_step(p), b, &bad);
+  }
+  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPart<TILE>* part) {
+    while (more) {
+      const bool last = b == end.x && item == end.y && head == end.z;
+      part->all = chunk_tiles(p, s, item, &part->see);
+      part->b = b, part->r0 = s.r0, part->len = s.len, part->keys = s.keys;
+      part->past = s.keys - s.len;
+      part->tok0 = item * chunk_step(p), part->toks = min(s.len - part->tok0, chunk_step(p));
+      part->head = head;
+      part->t0 = t, part->t1 = last ? end.w : part->all;
+      part->slot = t > 0 ? 2 * static_cast<int>(blockIdx.x)
+                         : (part->t1 < part->all ? 2 * static_cast<int>(blockIdx.x) + 1 : -1);
+      if (last) {
+        more = false;
+      } else {
+        t = 0;
+        if (++head == p.heads) {
+          head = 0;
+          if (++item == s.items) {
+            item = 0;
+            bool bad = false;
+            do {
+              ++b;
+              if (b < p.c.B) s = chunk_sequence(p, chunk_step(p), b, &bad);
+            } while (b < p.c.B && s.items == 0);
+            more = b < p.c.B;
+          }
+        }
+      }
+      if (part->t0 < part->t1) return true;
+    }
+    return false;
   }
 };
 

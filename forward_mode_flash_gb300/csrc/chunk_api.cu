@@ -11,56 +11,69 @@
 namespace jvp {
 namespace {
 
-// How a call's work is cut up (see chunk.cuh).
+// How a call's work is divided (see chunk.cuh), and its workspace.
 struct ChunkPlan {
   int tok = 0, query_tiles = 1, head_blocks = 1, group_rows = 1;
   int rows = 0;  // of an item
-  int64_t units = 0, heads = 0;
-  int least = 0, target = 0, slots = 0;
-  size_t bytes = 0, at_lse = 0, at_item = 0, at_count = 0;
+  int64_t heads = 0;
+  int tile = 0, grid = 0, cut = 0;
+  size_t bytes = 0, at_count = 0, at_lse = 0, at_o = 0;  // workspace: items, ...
 };
-// Kernels: CUDA cores, tensor cores with copied boxes or with gathered rows.
-enum ChunkKernel { kSimt, kBoxes, kGathered };
-ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, ChunkKernel kernel, int num_sms,
+// Query tiles of a CTA; 0: the CUDA cores' kernel.  Two share each K/V tile; a chunk that
+// fills no more than two tiles is better off with one per CTA and two CTAs per SM, and
+// so is one whose window is so narrow that a second tile's tokens see much else.
+// Gathered rows leave room for one CTA per SM.  (One against two, us: @@NQFIG@@)
+int chunk_query_tiles(const jvp_cache_t* c, int64_t H, int64_t T, bool boxes, int64_t window) {
+  const int64_t group = H / c->Hkv, tok = kPackedTileRows / group;
+  const bool narrow = window > 0 && tok * (c->D > 64 ? 4 : 8) >= window;
+  return boxes && (narrow || T * group <= 2 * kPackedTileRows * c->B) ? 1 : 2;
+}
+ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, int query_tiles, int num_sms,
                      int64_t window, int64_t sinks) {
   ChunkPlan d;
   const int64_t group = H / c->Hkv;
-  int64_t tile;
-  if (kernel != kSimt) {
-    // Two query tiles per CTA share each K/V tile; a chunk that fills no more than
-    // two tiles is better off with one per CTA and two CTAs per SM.
-    d.query_tiles = kernel == kBoxes && T * group <= 2 * kPackedTileRows * c->B ? 1 : 2;
+  int ctas;  // resident
+  if (query_tiles > 0) {
+    d.query_tiles = query_tiles;
     d.group_rows = static_cast<int>(group);
     d.tok = static_cast<int>(kPackedTileRows / group);
     d.rows = d.query_tiles * kPackedTileRows;
-    d.target = num_sms * (3 - d.query_tiles);
-    tile = kChunkTile;
+    d.tile = kChunkTile;
+    ctas = num_sms * (3 - d.query_tiles);
   } else {
     d.group_rows = static_cast<int>(std::min<int64_t>(group, kChunkSimtRows));
     d.head_blocks = static_cast<int>((group + d.group_rows - 1) / d.group_rows);
     d.tok = kChunkSimtRows / d.group_rows;
     d.rows = kChunkSimtRows;
-    d.target = 2 * num_sms;
-    tile = kChunkSimtTile;
+    d.tile = kChunkSimtTile;
+    ctas = num_sms * (c->D > 64 ? 2 : 3);
   }
   d.heads = c->Hkv * d.head_blocks;
   const int64_t step = static_cast<int64_t>(d.tok) * d.query_tiles;
   const int64_t items = T / step + std::min(c->B, T);  // >= sum of ceil(len / step)
-  int64_t tiles = (c->max_pages * c->page_size + tile - 1) / tile;
-  if (window > 0)  // (chunk_sequence's bound)
-    tiles = std::min(tiles, (window + step - 2 + tile - 1) / tile + 1 + (sinks + tile - 1) / tile);
-  d.units = items;
-  if (tiles <= kChunkLeast) return d;
-  d.least = kChunkLeast;
-  const int64_t most = (tiles + kChunkLeast - 1) / kChunkLeast;  // pieces of an item
-  // items * heads <= 2^31 - 1 (checked by the caller), most < 2^31
-  d.units = items + std::min(d.target / d.heads + 1, items * (most - 1));
-  d.slots = static_cast<int>(std::min<int64_t>(2ll * d.target, items * d.heads * most));
-  const size_t rows = static_cast<size_t>(d.slots) * d.rows;
-  d.at_lse = rows * (c->D > 64 ? 128 : 64) * 4;
-  d.at_item = d.at_lse + rows * 4;
-  d.at_count = d.at_item + static_cast<size_t>(d.slots) * 16;
-  d.bytes = d.at_count + 16;
+  int64_t tiles = (c->max_pages * c->page_size + d.tile - 1) / d.tile;
+  if (window > 0)  // the window's keys of `step` tokens begin anywhere in a tile
+    tiles = std::min(tiles, (window + step - 2 + d.tile - 1) / d.tile + 1 +
+                                (sinks + d.tile - 1) / d.tile);
+  tiles = std::max<int64_t>(tiles, 1);
+  // (items of so few tiles are not worth a join; items * heads <= 2^31 - 1, checked by the
+  // caller, tiles < 2^31)
+  d.cut = tiles >= 2 * kChunkSnap ? 1 : 0;
+  d.grid = static_cast<int>(
+      std::min<int64_t>(ctas, items * d.heads * (tiles + kChunkStart) / kChunkLeast + 1));
+  auto place = [&](size_t* at, size_t bytes) {
+    *at = d.bytes;
+    d.bytes += (bytes + 255) & ~static_cast<size_t>(255);
+  };
+  const size_t grid = static_cast<size_t>(d.grid);
+  size_t at_item;
+  place(&at_item, grid * 16);
+  place(&d.at_count, 4);
+  if (d.cut) {
+    const size_t rows = 2 * grid * d.rows;
+    place(&d.at_lse, rows * 4);
+    place(&d.at_o, rows * (c->D > 64 ? 128 : 64) * 4);
+  }
   return d;
 }
 
@@ -79,24 +92,31 @@ jvp_status_t check_chunk(const jvp_cache_t* c, int64_t H, int dtype, int64_t T) 
   return JVP_OK;
 }
 
-// Map of a 16-bit cache [pages, Hkv, page_size, D], boxes of {64, rows} of one head.
+// Map of a cache [pages, Hkv, page_size, D], boxes of `rows` rows of one head: 64 columns
+// of 16 bits with a swizzle of 128 bytes, or all columns (64 or 128) of 8 bits.
 bool encode_cache(CUtensorMap* map, int dt, const void* ptr, const PagedCache& c, const Strides& s,
                   int rows) {
+  const bool codes = dt == JVP_E4M3;
+  const cuuint64_t e = codes ? 1 : 2;
   auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(api_tensor_map_encoder());
   if (!enc || !aligned_to(ptr, 16)) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page_size),
                         static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.pages)};
   // a size-1 dimension's stride is never used; give it a well-formed value
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.page_size > 1 ? s.n : c.D) * 2,
-                           static_cast<cuuint64_t>(c.Hkv > 1 ? s.h : c.D) * 2,
-                           static_cast<cuuint64_t>(c.pages > 1 ? s.b : c.D) * 2};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.page_size > 1 ? s.n : c.D) * e,
+                           static_cast<cuuint64_t>(c.Hkv > 1 ? s.h : c.D) * e,
+                           static_cast<cuuint64_t>(c.pages > 1 ? s.b : c.D) * e};
   for (auto x : strides)
     if (x == 0 || x % 16 != 0 || x >= (1ull << 40)) return false;
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+  cuuint32_t box[4] = {codes && c.D > 64 ? 128u : 64u, static_cast<cuuint32_t>(rows), 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, dt == JVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+  return enc(map,
+             codes            ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+             : dt == JVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              4, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -112,11 +132,10 @@ size_t jvp_attn_chunk_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dt
   int sms = 0;
   unsigned int* status = nullptr;
   if (api_device(&sms, &status) != JVP_OK) return 0;
-  // enough for either path (which one runs depends on the pointers too) and any window
-  size_t most = plan_chunk(cache, H, T, kSimt, sms, 0, 0).bytes;
-  if (H / cache->Hkv <= kPackedTileRows)
-    for (const ChunkKernel k : {kBoxes, kGathered})
-      most = std::max(most, plan_chunk(cache, H, T, k, sms, 0, 0).bytes);
+  // enough for each kernel (which one runs depends on the pointers too) and any window
+  size_t most = 0;
+  for (int tiles = 0; tiles <= (H / cache->Hkv <= kPackedTileRows ? 2 : 0); ++tiles)
+    most = std::max(most, plan_chunk(cache, H, T, tiles, sms, 0, 0).bytes);
   return most;
 }
 
@@ -180,43 +199,41 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
     tc = encode_packed(&maps.q, dtype, q, D, H, p.sq.h, T, p.sq.n, p.group, tok) &&
          encode_packed(&maps.o, dtype, o, D, H, p.so.h, T, p.so.n, p.group, tok);
   }
-  if (tc && !e4m3 && cache->page_size % 8 == 0) {
-    p.box_rows = 8;
-    while (p.box_rows < kChunkTile && cache->page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
-    if (encode_cache(&maps.k, dtype, k_cache, p.c, p.c.sk, p.box_rows) &&
-        encode_cache(&maps.v, dtype, v_cache, p.c, p.c.sv, p.box_rows))
-      source = kChunkBoxes;
+  if (tc && cache->page_size % 8 == 0) {  // (of e4m3 rows, half a tile at most)
+    int rows = 8;
+    while (rows < kChunkTile / (e4m3 ? 2 : 1) && cache->page_size % (2 * rows) == 0) rows *= 2;
+    if (encode_cache(&maps.k, cache->dtype, k_cache, p.c, p.c.sk, rows) &&
+        encode_cache(&maps.v, cache->dtype, v_cache, p.c, p.c.sv, rows)) {
+      p.box_rows = rows;
+      if (!e4m3) source = kChunkBoxes;
+    }
   }
-  const ChunkPlan d = plan_chunk(cache, H, T, !tc ? kSimt : source == kChunkBoxes ? kBoxes : kGathered,
-                                 sms, p.window, p.sinks);
-  if (d.bytes > 0 && (!workspace || workspace_bytes < d.bytes))
+  const int query_tiles =
+      tc ? chunk_query_tiles(cache, H, T, source == kChunkBoxes, p.window) : 0;
+  const ChunkPlan d = plan_chunk(cache, H, T, query_tiles, sms, p.window, p.sinks);
+  if (!workspace || workspace_bytes < d.bytes)
     return api_fail(JVP_ERR_WORKSPACE,
                     "workspace is NULL or smaller than jvp_attn_chunk_workspace_size()");
   if (!aligned_to(workspace, 16)) return api_fail(JVP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
   p.tok = d.tok, p.query_tiles = d.query_tiles;
   p.head_blocks = d.head_blocks, p.group_rows = d.group_rows;
-  p.least = d.least, p.target = d.target, p.slots = d.slots;
-  p.heads = static_cast<int>(d.heads), p.units = static_cast<int>(d.units);
-  if (d.bytes > 0) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.ws_o = reinterpret_cast<float*>(ws);
-    p.ws_lse = reinterpret_cast<float*>(ws + d.at_lse);
-    p.ws_item = reinterpret_cast<int4*>(ws + d.at_item);
-    p.ws_count = reinterpret_cast<int*>(ws + d.at_count);
-  }
+  p.heads = static_cast<int>(d.heads);
+  p.grid = d.grid, p.cut = d.cut;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws_item = reinterpret_cast<int4*>(ws);
+  p.ws_count = reinterpret_cast<int*>(ws + d.at_count);
+  p.ws_lse = reinterpret_cast<float*>(ws + d.at_lse);
+  p.ws_o = reinterpret_cast<float*>(ws + d.at_o);
   const int kernel_d = D <= 64 ? 64 : 128;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t err;
-  if (tc) {
-    if (scale < 0.f) p.neg_scores = 1, p.scale_log2 = -p.scale_log2;
-    err = launch_chunk_tc(static_cast<DType>(dtype), kernel_d, source, maps, p, s);
-  } else {
+  if (tc && scale < 0.f) p.neg_scores = 1, p.scale_log2 = -p.scale_log2;
+  if (!tc)
     p.vec = D % 4 == 0 && aligned_to(k_cache, 4 * ce) && aligned_to(v_cache, 4 * ce) &&
             multiple(p.c.sk, 4) && multiple(p.c.sv, 4);
-    err = launch_chunk_simt(static_cast<DType>(dtype), e4m3, p, s);
-  }
-  if (err == cudaSuccess && d.least > 0)
-    err = launch_chunk_join(static_cast<DType>(dtype), kernel_d, d.rows, p, sms, s);
+  cudaError_t err = tc ? launch_chunk_tc(static_cast<DType>(dtype), kernel_d, source, maps, p, s)
+                       : launch_chunk_simt(static_cast<DType>(dtype), e4m3, p, s);
+  if (err == cudaSuccess && d.cut)
+    err = launch_chunk_join(static_cast<DType>(dtype), kernel_d, d.rows, p, s);
   if (err != cudaSuccess) return api_cuda_fail(err);
   api_set_path(tc ? 1 : 2);
   return api_ok();

@@ -200,26 +200,25 @@ struct ChunkParams {
   void* o;
   Strides so;
   float* lse;        // [H, T] or nullptr
-  // The split of long key ranges: an item's (tile of rows, head) key tiles are cut
-  // into pieces of at most max(least, all / target) tiles each.  least 0: no split.
-  int least;
-  int target;
-  int heads;         // key/value heads (times head_blocks): items of a tile of tokens
-  int slots;         // pieces of split items, at most
-  float* ws_o;       // [slots][rows of an item][64 or 128] normalised partial outputs
-  float* ws_lse;     // [slots][rows of an item], log2 units
-  int4* ws_item;     // [slots] pieces, first row, tokens, head; pieces 0: not an item's first
-  int* ws_count;     // slots in use
-  int units;         // blocks of the grid per head: an upper bound of all pieces
+  int heads;         // key/value heads times head_blocks: items of a tile of tokens
+  // The division among CTAs (chunk.cuh)
+  int grid;
+  int cut;           // 0: items are not cut (their key tiles are few)
+  int4* ws_item;     // [grid] the item that a CTA begins and others end: CTAs, first row,
+                     // tokens, head (CTAs 0: none)
+  int* ws_count;     // CTAs with work
+  float* ws_o;       // [grid][2][rows of an item][64 or 128] normalised partial outputs
+  float* ws_lse;     // [grid][2][rows of an item], log2 units
   int box_rows;      // tensor cores: keys of a copied box, a divisor of 128 and the page size
   int vec;           // CUDA cores: 16-byte aligned rows of whole 16-byte pieces
 };
 struct ChunkMaps {
   CUtensorMap q, o, k, v;
 };
-// Keys per tile, fewest key tiles of a piece, join blocks.
-constexpr int kChunkTile = 128, kChunkSimtTile = 64, kChunkSimtRows = 32;
-constexpr int kChunkLeast = 4;
+constexpr int kChunkTile = 128, kChunkSimtTile = 64, kChunkSimtRows = 32;  // keys per tile, rows
+// Cost of an item beside its key tiles, in tiles, and the least cost for a CTA.
+constexpr int kChunkStart = 4, kChunkLeast = 9;
+constexpr int kChunkSnap = 4;  // fewest tiles of a part of a cut item
 // source of the key tiles: boxes of whole pages' parts by TMA, rows gathered by
 // threads, or e4m3 rows gathered and converted
 enum ChunkSource { kChunkBoxes, kChunkRows, kChunkE4M3 };
@@ -227,8 +226,24 @@ cudaError_t launch_chunk_tc(DType dt, int kernel_d, ChunkSource source, const Ch
                             const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_simt(DType dt, bool e4m3, const ChunkParams& p, cudaStream_t stream);
 // Joins the pieces of split items (rows: of an item; kernel_d: 64 or 128).
-cudaError_t launch_chunk_join(DType dt, int kernel_d, int rows, const ChunkParams& p, int num_sms,
+cudaError_t launch_chunk_join(DType dt, int kernel_d, int rows, const ChunkParams& p,
                               cudaStream_t stream);
+// Launches a kernel that may be placed while the one before it on the stream runs,
+// and waits for it by itself (griddepcontrol.wait).
+template <typename... P>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, int smem,
+                             cudaStream_t stream, const P&... params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
 
 // Lets a kernel use `bytes` of dynamic shared memory on the current device.
 // Once per kernel and device (the call costs 2 us of an eager call's host time;

@@ -590,9 +590,9 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
                             size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of jvp_attn_chunk on the current device, for any window: partial
- * outputs of a few waves of CTAs, whatever the lengths (40 MiB at most at D = 128);
- * 0 for a block table so small that nothing is split, an empty problem, an invalid
- * description or no device. */
+ * outputs of one resident wave of CTAs, whatever the lengths (40 MiB at most at D =
+ * 128), and some bytes per sequence and tile of new tokens; 0 for an empty problem, an
+ * invalid description or no device. */
 size_t jvp_attn_chunk_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype,
                                      int64_t T);
 

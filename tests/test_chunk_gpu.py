@@ -280,7 +280,7 @@ def test_bad_offsets_and_lengths_are_reported(dt):
     out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
     run(c, q, torch.tensor([0, 5, 3, 12], dtype=torch.int32), out=out)
     assert api.device_status() == _abi.JVP_ERR_INDEX
-    assert torch.equal(out[:5], good[0][:5])
+    assert torch.equal(out[:3], good[0][:3])  # (rows 3 and 4 are in the third sequence too)
     out.fill_(7.0)
     run(c, q, torch.tensor([0, 5, 8, 13], dtype=torch.int32), out=out)
     assert api.device_status() == _abi.JVP_ERR_INDEX
