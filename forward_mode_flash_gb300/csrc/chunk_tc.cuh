@@ -688,23 +688,23 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           }
         }
         const int j0 = first_key(w, t);
-        if (j0 + BN > warp_limit) {
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (j0 + e >= limit) s[e] = -INFINITY;
-        }
-        if (j0 < warp_lo && j0 + BN > w.see.sinks) {
-          const int a = lo - j0, b = w.see.sinks - j0;  // hidden: b <= e < a
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (e < a && e >= b) s[e] = -INFINITY;
-        }
         uint32_t missing[4];
         ld_shared_v4(smem_u32(ctrl->missing[(base + t) & 15]), missing);
-        if ((missing[0] | missing[1] | missing[2] | missing[3]) != 0u) {
+        if (j0 + BN > warp_limit || (j0 < warp_lo && j0 + BN > w.see.sinks) ||
+            (missing[0] | missing[1] | missing[2] | missing[3]) != 0u) {
+          // (as bits: one run over the scores for every kind of mask, since the loop
+          // must stay in the instruction cache)
 #pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (missing[e / 32] & (1u << (e % 32))) s[e] = -INFINITY;
+          for (int q = 0; q < BN; q += 32) {
+            const int here = limit - (j0 + q);  // keys that are not later than the row's
+            uint32_t bits = here >= 32 ? 0xFFFFFFFFu : here <= 0 ? 0u : (1u << here) - 1u;
+            const int h0 = max(w.see.sinks - (j0 + q), 0), h1 = min(lo - (j0 + q), 32);
+            if (h0 < h1) bits &= ~((0xFFFFFFFFu << h0) & (0xFFFFFFFFu >> (32 - h1)));
+            bits &= ~missing[q / 32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits & (1u << e))) s[q + e] = -INFINITY;
+          }
         }
         const float m_tile = packed_max(s) * scale;
         const bool need = m_tile - m_run > PackedElem<T>::kTop;
@@ -816,21 +816,18 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
             }
           }
         };
-#pragma unroll
+#pragma unroll 1
         for (int col = 0; col < D; col += 64) {
           uint32_t o[2][32];
           tmem_ld32x2(o_tm + col, o_tm + col + 32, o[0], o[1]);
-          if (special && row_ok) {
+          if (special && row_ok) {  // (rare: through local memory, to stay short)
+            float sums[64];
+#pragma unroll 1
+            for (int e = 0; e < 64; e += 8)
+              add_special(col + e, *reinterpret_cast<float(*)[8]>(&sums[e]));
 #pragma unroll
-            for (int e = 0; e < 64; e += 8) {
-              float y[8];
-              add_special(col + e, y);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                uint32_t& to = o[(e + k) / 32][(e + k) % 32];
-                to = __float_as_uint(__uint_as_float(to) + y[k]);
-              }
-            }
+            for (int e = 0; e < 64; ++e)
+              o[e / 32][e % 32] = __float_as_uint(__uint_as_float(o[e / 32][e % 32]) + sums[e]);
           }
           if (w.slot >= 0) {
             if (row_ok && JVP_CHECK(w.slot < 2 * p.grid, c.status, kChkGlobalRow)) {
