@@ -205,7 +205,7 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
     if (encode_cache(&maps.k, cache->dtype, k_cache, p.c, p.c.sk, rows) &&
         encode_cache(&maps.v, cache->dtype, v_cache, p.c, p.c.sv, rows)) {
       p.box_rows = rows;
-      if (!e4m3) source = kChunkBoxes;
+      source = e4m3 ? kChunkStaged : kChunkBoxes;
     }
   }
   const int query_tiles =

@@ -23,6 +23,7 @@ static cudaError_t launch_source(int kernel_d, ChunkSource source, const ChunkMa
     case kChunkBoxes: return launch_typed<T, kChunkBoxes>(kernel_d, maps, p, stream);
     case kChunkRows: return launch_typed<T, kChunkRows>(kernel_d, maps, p, stream);
     case kChunkE4M3: return launch_typed<T, kChunkE4M3>(kernel_d, maps, p, stream);
+    case kChunkStaged: return launch_typed<T, kChunkStaged>(kernel_d, maps, p, stream);
   }
   return cudaErrorInvalidValue;
 }

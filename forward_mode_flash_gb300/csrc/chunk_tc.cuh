@@ -28,34 +28,54 @@
 
 namespace jvp {
 
-// The gathering sources: threads, registers (65536 / 512 a thread: 56 + 104 + 2 * 176 =
-// 4 * 128), and their shared memory behind the control block.
+// The gathering sources: threads, and registers (65536 / 640 a thread, 96: 48 + 2 * 72 +
+// 2 * 144 = 5 * 96); their staging area lies behind the control block.
+constexpr int kGatherWarps = 8;
 constexpr int chunk_threads(int NQ, ChunkSource src) {
-  return packed_threads(NQ) + (src == kChunkBoxes ? 0 : 128);
+  return packed_threads(NQ) + (src == kChunkBoxes ? 0 : 32 * kGatherWarps);
 }
-struct ChunkPlaces {
-  long long k[kChunkTile], v[kChunkTile];  // elements from the start of the cache, -1: none
-  uint8_t k_scale[2][kChunkTile], v_scale[2][kChunkTile];  // by tile modulo 2
-};
-constexpr int kChunkAhead = 3;  // half tiles in flight
+constexpr int kChunkAhead = 3;  // half tiles that the gathering warps copy ahead
+// Half tiles of codes in flight by TMA: what the shared memory left holds.
+constexpr int chunk_ahead(int D) { return D > 64 ? 4 : 8; }
 template <int D, int NQ, ChunkSource SRC>
 struct ChunkLayout : PackedLayout<D, NQ> {
   using P = PackedLayout<D, NQ>;
+  static constexpr int AHEAD = chunk_ahead(D);
   static constexpr int NB = NQ;  // score buffers: one for each query tile
   static constexpr uint32_t TM_O = NB * P::BN;
   static_assert(NB * P::BN + NQ * D <= P::TM_COLS, "TMEM columns");
   static constexpr int HALF_CODES = 64 * D;  // bytes of half a tile of codes
-  static constexpr int OFF_PLACES = P::OFF_CTRL + 1024;
-  static constexpr int OFF_STAGE = OFF_PLACES + static_cast<int>(sizeof(ChunkPlaces));
-  static constexpr int BYTES = SRC == kChunkBoxes ? P::SMEM_BYTES
-                               : SRC == kChunkRows
-                                   ? P::SMEM_BYTES + static_cast<int>(sizeof(ChunkPlaces))
-                                   : P::SMEM_BYTES + static_cast<int>(sizeof(ChunkPlaces)) +
-                                         kChunkAhead * HALF_CODES;
+  static constexpr int CTRL = 2048;  // control block
+  static constexpr int OFF_STAGE = P::OFF_CTRL + CTRL;
+  // (and 1024 for alignment)
+  static constexpr int BYTES = OFF_STAGE + 1024 + (SRC == kChunkE4M3 || SRC == kChunkStaged ? AHEAD * HALF_CODES : 0);
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(SRC != kChunkBoxes || (3 - NQ) * (BYTES + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
-template <int NS>
+// A CTA's part as its roles see it: key tiles of the query tiles (n: the larger; 0: no
+// more parts); V tiles [0, low) and [cut, n) are inspected.
+struct ChunkJob : ChunkPart<kChunkTile> {
+  int n_a, n_b, n, low, cut;
+  __device__ __forceinline__ void shape(const ChunkParams& p) {
+    // A's key tiles are cut; where B has more they go with the last part
+    const int all_b = toks > p.tok ? see.tiles(past + tok0 + toks - 1) : 0;
+    n_a = t1 - t0;
+    n_b = all_b == 0 ? 0 : (t1 == all ? all_b : t1) - t0;
+    n = max(n_a, n_b);
+    // a window or the causal mask hides some of their keys from some rows, or the
+    // sequence ends inside
+    low = see.lo_last > 0 ? max(0, min(n, see.lo_last / kChunkTile + 1 - see.skip - t0)) : 0;
+    cut = max(low, min(n, max(0, past + tok0 + 1) / kChunkTile - see.skip - t0));
+  }
+  __device__ __forceinline__ bool inspected(int t) const { return t < low || t >= cut; }
+  // inspected tiles before tile t
+  __device__ __forceinline__ int before(int t) const { return t < low ? t : low + max(0, t - cut); }
+  __device__ __forceinline__ int first_key(int t) const { return see.tile(t0 + t) * kChunkTile; }
+};
+constexpr int kChunkJobs = 4;  // parts in shared memory
+
+template <int NS, int AHEAD>
 struct ChunkCtrl {
   uint64_t q_full[2];
   uint64_t done[2];  // a part's epilogue of the query tile has ended
@@ -64,10 +84,14 @@ struct ChunkCtrl {
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t staged[2];
   uint64_t drain;
-  uint64_t stage_full[kChunkAhead], stage_empty[kChunkAhead];  // half tiles of codes
-  // By key tile modulo 16 (the copies are at most 2 NS tiles ahead of the
-  // softmax), a bit for every key: its page does not exist.
-  alignas(16) uint32_t missing[16][4];
+  uint64_t stage_full[AHEAD], stage_empty[AHEAD];  // half tiles of codes
+  // Parts, written by one warp and read by the others, which hold little else of them
+  // in registers: what spills goes through an L1 of the 28 KB that shared memory leaves.
+  uint64_t job_full[kChunkJobs], job_empty[kChunkJobs];
+  ChunkJob job[kChunkJobs];
+  // By key tile modulo 8 (lookups are at most NS + 1 tiles ahead of the softmax), a bit
+  // for every key: its page does not exist.
+  alignas(16) uint32_t missing[8][4];
   // By part modulo 8 (copies are at most NS parts ahead): the number of the part,
   // counted from 1, if V entries were infinite or NaN where the window ([0]) or the
   // causal mask ([1]) cuts a tile.
@@ -93,6 +117,42 @@ __device__ __forceinline__ uint32_t chunk_decode(uint32_t half2, float scale) {
   return PackedElem<T>::pack(f.x * scale, f.y * scale);
 }
 
+// The same by shifts, for pairs of codes in the high bytes of 16-bit halves: sign,
+// exponent and fraction moved to T's places are the code times 2^-120 (bf16) or 2^-8
+// (fp16), subnormal codes too, and one product with the scale's power of two, 2^E,
+// gives the value, rounded once.  For factors that T holds as normal numbers, and no
+// NaN among the codes (which would become 480).  (Conversions by the dedicated
+// instruction and through fp32 are the slower half of the converting warps' time:
+// @@CVTFIG@@)
+template <typename T>
+struct ChunkShift;
+template <>
+struct ChunkShift<__nv_bfloat16> {
+  static constexpr int kExp = 120, kMin = -126, kMax = 127;
+  static __device__ __forceinline__ uint32_t place(uint32_t w) {
+    return (w >> 4 & 0x07F007F0u) | (w & 0x80008000u);
+  }
+  static __device__ __forceinline__ uint32_t factor(int e) { return (e + 127) * 0x00800080u; }
+  static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
+template <>
+struct ChunkShift<__half> {
+  static constexpr int kExp = 8, kMin = -14, kMax = 15;
+  static __device__ __forceinline__ uint32_t place(uint32_t w) {
+    return (w >> 1 & 0x3F803F80u) | (w & 0x80008000u);
+  }
+  static __device__ __forceinline__ uint32_t factor(int e) { return (e + 15) * 0x04000400u; }
+  static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                              *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
+
 template <typename T, int D, int NQ, ChunkSource SRC>
 __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3 - NQ : 1)
     chunk_tc_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p) {
@@ -100,7 +160,8 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
   constexpr int BM = L::BM, BN = L::BN, NS = L::NS, KCH = L::KCH;
   constexpr int THREADS = chunk_threads(NQ, SRC);
   constexpr bool kGather = SRC != kChunkBoxes;
-  constexpr int kSoftmax = kGather ? 8 : 4;  // first softmax warp
+  constexpr bool kCodes = SRC == kChunkE4M3 || SRC == kChunkStaged;
+  constexpr int kSoftmax = kGather ? 4 + kGatherWarps : 4;  // first softmax warp
   constexpr bool kBF16 = PackedElem<T>::kBF16;
   constexpr uint32_t IDESC_S = idesc_f16(kBF16, BM, BN, false);
   constexpr uint32_t IDESC_O = idesc_f16(kBF16, BM, D, true);
@@ -109,8 +170,8 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  using Ctrl = ChunkCtrl<NS>;
-  static_assert(sizeof(Ctrl) <= 1024, "control block budget");
+  using Ctrl = ChunkCtrl<NS, L::AHEAD>;
+  static_assert(sizeof(Ctrl) <= L::CTRL && NS <= 6, "control block budget");
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + L::OFF_CTRL);
   volatile int* abort = &ctrl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,16 +196,21 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       }
       mbar_init(&ctrl->drain, 1);
       for (int s = 0; s < NS; ++s) {
-        mbar_init(&ctrl->k_full[s], kGather ? 4 : 1);  // one arrival per gathering warp
+        mbar_init(&ctrl->k_full[s], kGather ? kGatherWarps : 1);
         mbar_init(&ctrl->k_empty[s], 1);
-        mbar_init(&ctrl->v_full[s], kGather ? 4 : 1);
+        mbar_init(&ctrl->v_full[s], kGather ? kGatherWarps : 1);
         mbar_init(&ctrl->v_empty[s], 1);
         mbar_init(&ctrl->v_issued[s], 1);
         mbar_init(&ctrl->v_checked[s], 1);
       }
-      for (int s = 0; s < kChunkAhead; ++s) {
+      for (int s = 0; s < kChunkJobs; ++s) {
+        mbar_init(&ctrl->job_full[s], 1);
+        // a warp each: copies, products, inspection, softmax, gathering
+        mbar_init(&ctrl->job_empty[s], 4 + 4 * NQ + (kGather ? kGatherWarps : 0));
+      }
+      for (int s = 0; s < L::AHEAD; ++s) {
         mbar_init(&ctrl->stage_full[s], 1);
-        mbar_init(&ctrl->stage_empty[s], 4);
+        mbar_init(&ctrl->stage_empty[s], kGatherWarps);
       }
       ctrl->abort = 0;
       fence_barrier_init();
@@ -163,53 +229,48 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return packed_warp_wait(bar, parity & 1, c.status, abort);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // (as packed_warp_wait)
+    const bool got = mbar_wait<false>(bar, parity & 1, abort);
+    if (!got) packed_timeout(c.status, abort);
+    return __all_sync(0xffffffffu, got);
   };
-  // Every role walks the CTA's parts by itself; barriers go on from part to part,
-  // so each role counts what came before: `base` key tiles, `seen` inspected V tiles,
-  // `uses` of each query tile and, in `steps`, its key tiles.
-  using Part = ChunkPart<BN>;
-  using Walk = ChunkWalk<BN>;
-  struct Geometry {  // key tiles of the query tiles; V tiles [0, low) and [cut, n) are inspected
-    int n_a, n_b, n, low, cut;
-    __device__ __forceinline__ Geometry(const ChunkParams& p, const Part& w) {
-      // A's key tiles are cut; where B has more they go with the last part
-      const int all_b = w.toks > p.tok ? w.see.tiles(w.past + w.tok0 + w.toks - 1) : 0;
-      n_a = w.t1 - w.t0;
-      n_b = all_b == 0 ? 0 : (w.t1 == w.all ? all_b : w.t1) - w.t0;
-      n = max(n_a, n_b);
-      // a window or the causal mask hides some of their keys from some rows, or the
-      // sequence ends inside
-      low = w.see.lo_last > 0 ? max(0, min(n, w.see.lo_last / BN + 1 - w.see.skip - w.t0)) : 0;
-      cut = max(low, min(n, max(0, w.past + w.tok0 + 1) / BN - w.see.skip - w.t0));
-    }
-    __device__ __forceinline__ bool inspected(int t) const { return t < low || t >= cut; }
-    // inspected tiles before tile t
-    __device__ __forceinline__ int before(int t) const { return t < low ? t : low + max(0, t - cut); }
+  // One warp walks the CTA's parts; the others take them from shared memory.  Barriers
+  // go on from part to part, so each role counts what came before: `base` key tiles,
+  // `seen` inspected V tiles, `uses` of each query tile and, in `steps`, its key tiles.
+  auto take_job = [&](int k) -> const ChunkJob* {  // nullptr: there is none
+    if (!wait(&ctrl->job_full[k % kChunkJobs], k / kChunkJobs)) return nullptr;
+    const ChunkJob* j = &ctrl->job[k % kChunkJobs];
+    return *static_cast<const volatile int*>(&j->n) > 0 ? j : nullptr;
   };
-  auto first_key = [&](const Part& w, int t) { return w.see.tile(w.t0 + t) * BN; };
+  auto leave_job = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctrl->job_empty[k % kChunkJobs]);
+  };
 
   if (warp < 4) {
-    if (kGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (kGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
-      // Copied boxes: lane l copies box l % boxes of chunk l / boxes of a tile; of
-      // codes (one chunk), to the staging area, half a tile at a time.
-      const bool copies = !kGather || (SRC == kChunkE4M3 && p.box_rows > 0);
+    if (warp == 0 || warp == 2) {
+      // ---------------------------------------------------------- copies
+      // Warp 0 copies query tiles and K, warp 2 V (a copy's issue takes some 40 cycles, and
+      // pages of 16 rows need 32 of them for a tile of K at D = 128; one warp for both: 1.8
+      // to 1.9 us a tile, 1.5 with pages of 64).  Boxes: lane l copies box l % boxes of
+      // chunk l / boxes of a tile.  Of codes (one chunk) warp 0 copies K and V to the
+      // staging area, half a tile at a time.
+      const bool values = warp == 2;
+      const bool copies = SRC == kChunkBoxes || (SRC == kChunkStaged && !values);
       const int boxes = copies ? BN / p.box_rows : 1;
       const int box = lane % boxes, chunk = lane / boxes;
       const bool mine = copies && chunk < (kGather ? 1 : KCH);
       int base = 0, seen = 0, halves = 0;
       int uses[2] = {0, 0};
-      int k_fills = 0, v_fills = 0;
+      int fills = 0;
       bool ok = true;
-      Walk walk(p, begin, end);
-      Part w;
-      while (ok && walk.next(p, &w)) {
-        const Geometry g(p, w);
+      for (int k = 0; ok; ++k) {
+        const ChunkJob* const job = take_job(k);
+        if (!job) break;
+        const ChunkJob &w = *job, &g = *job;
         auto load_q = [&](int x) -> bool {
           if (uses[x] > 0 && !wait(&ctrl->done[x], uses[x] - 1)) return false;
           ++uses[x];
@@ -228,7 +289,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
         auto look_up = [&](int t) {
           looked = false;
           if (t >= g.n || !mine) return;
-          const int j = first_key(w, t) + box * p.box_rows;
+          const int j = g.first_key(t) + box * p.box_rows;
           if (w.see.unseen(j, p.box_rows) || j >= w.keys) return;
           looked = true;
           int entry;
@@ -239,7 +300,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           const bool none = looked && (raw < 0 || raw >= c.pages);
           const bool have = looked && !none;
           page = have ? raw : c.pages, row = have ? raw_row : 0;
-          if (!kGather) {
+          if (!kGather && !values) {
             const bool any = __any_sync(0xffffffffu, none);
             // (box by box: word i has keys 32 i ..)
 #pragma unroll
@@ -252,17 +313,17 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
                 bits = __reduce_or_sync(0xffffffffu, bits);
               }
               if (lane == 0)
-                *static_cast<volatile uint32_t*>(&ctrl->missing[(base + t) & 15][i]) = bits;
+                *static_cast<volatile uint32_t*>(&ctrl->missing[(base + t) & 7][i]) = bits;
             }
             if (any && lane == 0) atomicOr(c.status, kStatusIndex);
           }
           look_up(t + 1);
         };
         auto load_kv = [&](int t, bool v) -> bool {
-          if constexpr (SRC == kChunkE4M3) {
+          if constexpr (SRC == kChunkStaged) {
             for (int i = 0; i < 2; ++i) {
-              const int s = halves % kChunkAhead;
-              if (!wait(&ctrl->stage_empty[s], (halves / kChunkAhead) ^ 1)) return false;
+              const int s = halves % L::AHEAD;
+              if (!wait(&ctrl->stage_empty[s], (halves / L::AHEAD) ^ 1)) return false;
               if (lane == 0) mbar_arrive_expect_tx(&ctrl->stage_full[s], L::HALF_CODES);
               __syncwarp();
               const int b0 = box - i * boxes / 2;  // box of this half
@@ -286,7 +347,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
                           full, chunk * 64, row, w.head, page);
             if (v && g.inspected(t) && lane == 0)
               mbar_arrive(&ctrl->v_issued[(seen + g.before(t)) % NS]);
-            ++(v ? v_fills : k_fills);
+            ++fills;
             return true;
           }
         };
@@ -294,29 +355,26 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           look_up(0);
           take(0);
         }
-        // the first copies of the next part do not wait for this one's epilogues
-        const bool q_first = base == 0;
-        if (q_first) ok = load_q(0) && (g.n_b == 0 || load_q(1));
-        if (ok && copies) ok = load_kv(0, false);
-        if (ok && copies) ok = load_kv(0, true);
-        if (ok && !q_first) ok = load_q(0) && (g.n_b == 0 || load_q(1));
+        // (the first copy of the next part does not wait for this one's epilogues)
+        if (!values && base == 0) ok = load_q(0) && (g.n_b == 0 || load_q(1));
+        if (ok && copies) ok = load_kv(0, values) && (!kGather || load_kv(0, true));
+        if (ok && !values && base > 0) ok = load_q(0) && (g.n_b == 0 || load_q(1));
         for (int t = 1; ok && copies && t < g.n; ++t) {
           take(t);
-          ok = load_kv(t, false) && load_kv(t, true);
+          ok = load_kv(t, values) && (!kGather || load_kv(t, true));
         }
         base += g.n, seen += g.before(g.n);
+        leave_job(k);
       }
       // Every copy issued lands before the CTA can exit.
       const int zero = 0;
       for (int x = 0; x < 2; ++x)
         if (uses[x] > 0) mbar_wait(&ctrl->q_full[x], (uses[x] - 1) & 1, &zero);
       if (!ok) {
-        for (int t = max(0, k_fills - NS); t < k_fills; ++t)
-          mbar_wait(&ctrl->k_full[t % NS], (t / NS) & 1, &zero);
-        for (int t = max(0, v_fills - NS); t < v_fills; ++t)
-          mbar_wait(&ctrl->v_full[t % NS], (t / NS) & 1, &zero);
-        for (int h = max(0, halves - kChunkAhead); h < halves; ++h)
-          mbar_wait(&ctrl->stage_full[h % kChunkAhead], (h / kChunkAhead) & 1, &zero);
+        for (int t = max(0, fills - NS); t < fills; ++t)
+          mbar_wait(values ? &ctrl->v_full[t % NS] : &ctrl->k_full[t % NS], (t / NS) & 1, &zero);
+        for (int h = max(0, halves - L::AHEAD); h < halves; ++h)
+          mbar_wait(&ctrl->stage_full[h % L::AHEAD], (h / L::AHEAD) & 1, &zero);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMAs
@@ -329,10 +387,10 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       int uses[2] = {0, 0};
       int steps[2] = {0, 0};
       bool ok = true;
-      Walk walk(p, begin, end);
-      Part part;
-      while (ok && walk.next(p, &part)) {
-        const Geometry g(p, part);
+      for (int k = 0; ok; ++k) {
+        const ChunkJob* const job = take_job(k);
+        if (!job) break;
+        const ChunkJob& g = *job;
         const int n_a = g.n_a, n_b = g.n_b, n = g.n;
         auto scores = [&](int x, int t) {
           const uint64_t qd = q_desc + x * (L::Q_BYTES >> 4);
@@ -400,25 +458,42 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
         base += n, seen += g.before(n);
         steps[0] += n_a, steps[1] += n_b;
         ++uses[0], uses[1] += n_b > 0;
+        leave_job(k);
       }
       if (!ok) packed_timeout(c.status, abort);
       mma_commit_warp(&ctrl->drain);
       const int zero = 0;
       mbar_wait(&ctrl->drain, 0, &zero);
     } else if (warp == 3) {
-      // ---------------------------------------------------------- V inspector
+      // ---------------------------------------------------------- the parts, V's inspection
+      ChunkWalk<BN> walk(p, begin, end);
+      bool more = true;
+      auto publish = [&](int k) {  // part k for all, n = 0 behind the last
+        if (!more) return true;
+        ChunkJob job;
+        more = walk.next(p, &job);
+        if (more) job.shape(p);
+        else job.n = 0;
+        if (!wait(&ctrl->job_empty[k % kChunkJobs], (k / kChunkJobs) ^ 1)) return false;
+        if (lane == 0) {
+          ctrl->job[k % kChunkJobs] = job;
+          mbar_arrive(&ctrl->job_full[k % kChunkJobs]);
+        }
+        return true;
+      };
       int base = 0, seen = 0, number = 0;
-      bool ok = true;
-      Walk walk(p, begin, end);
-      Part w;
-      while (ok && walk.next(p, &w)) {
-        const Geometry g(p, w);
+      bool ok = publish(0) && publish(1);
+      for (int job_k = 0; ok; ++job_k) {
+        if (!(ok = publish(job_k + 2))) break;
+        const ChunkJob* const job = take_job(job_k);
+        if (!job) break;
+        const ChunkJob &w = *job, &g = *job;
         ++number;
         for (int t = g.low > 0 ? 0 : g.cut; ok && t < g.n; t = t + 1 < g.low ? t + 1 : max(t + 1, g.cut)) {
           const int k = seen + g.before(t), s = (base + t) % NS;
           ok = wait(&ctrl->v_issued[k % NS], k / NS) && wait(&ctrl->v_full[s], (base + t) / NS);
           if (!ok) break;
-          const int j0 = first_key(w, t);
+          const int j0 = g.first_key(t);
           const uint32_t v = smem_u32(smem + L::OFF_V + s * L::KV_BYTES);
           const int rows = max(0, min(BN, w.keys - j0));
           for (int e = lane; e < (BN - rows) * KCH * 8; e += 32) {
@@ -465,108 +540,108 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           if (lane == 0) mbar_arrive(&ctrl->v_checked[k % NS]);
         }
         base += g.n, seen += g.before(g.n);
+        leave_job(job_k);
       }
     }
-  } else if (kGather && warp < 8) {
+  } else if (kGather && warp < kSoftmax) {
     // ------------------------------------------------------------ gathering warps
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    using TC = typename std::conditional<SRC == kChunkE4M3, uint8_t, T>::type;
-    constexpr int PR = D / 8, HP = PR / 2;  // pieces of a row; of a thread in half a tile
-    constexpr int RS = 128 / PR;            // rows between a thread's pieces
-    ChunkPlaces* const places = reinterpret_cast<ChunkPlaces*>(smem + L::OFF_PLACES);
-    const bool staged_by_tma = SRC == kChunkE4M3 && p.box_rows > 0;
-    const int gt = static_cast<int>(threadIdx.x) - 128;
-    const int piece = gt % PR, prow = gt / PR;
+    // Of each half of a tile a warp takes 8 rows, PR lanes a row, RI rows at once: keys
+    // 64 half + 8 gw + RI i + lane / PR.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    using TC = typename std::conditional<kCodes, uint8_t, T>::type;
+    constexpr int PR = D / 8, RI = 32 / PR, HP = 8 / RI;  // HP: pieces of a lane in half a tile
+    const int gw = warp - 4, piece = lane % PR, sub = lane / PR;
     const bool in_row = piece * 8 < c.D;
-    // where this thread's pieces of row prow lie in a tile (its rows differ by
-    // multiples of 8, so the swizzle is the same)
-    const uint32_t in_tile = (piece / 8) * BN * 128 + prow * 128 + (((piece % 8) ^ (prow & 7)) << 4);
-    const uint32_t stage = smem_u32(smem + L::OFF_STAGE) + gt * 8;
-    static_assert(RS % 8 == 0, "swizzle");
-    auto sync_gather = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    // a piece's place in its half of a tile (16 bytes, swizzled by the row modulo 8) and
+    // in the staging area (8 bytes)
+    const uint32_t in_tile = (piece / 8) * BN * 128 + (gw * 8 + sub) * 128;
+    auto tile_at = [&](int i) { return in_tile + RI * i * 128 + (((piece % 8) ^ sub ^ (RI * i)) << 4); };
+    const uint32_t stage = smem_u32(smem + L::OFF_STAGE) + (gw * 8 + sub) * D + piece * 8;
     int base = 0, seen = 0, halves = 0;
     bool ok = true;
-    Walk walk(p, begin, end);
-    Part w;
-    // (whatever becomes of a wait, the warps walk all parts: they meet in publish)
-    while (walk.next(p, &w)) {
-      const Geometry g(p, w);
+    for (int job_k = 0; ok; ++job_k) {
+      const ChunkJob* const job = take_job(job_k);
+      if (!job) break;
+      const ChunkJob &w = *job, &g = *job;
       const int n = g.n;
       const TC* const kc = static_cast<const TC*>(c.k) + w.head * c.sk.h + piece * 8;
       const TC* const vc = static_cast<const TC*>(c.v) + w.head * c.sv.h + piece * 8;
-      // Key gt of a tile: its block-table entry two tiles ahead, its scales one ahead.
+      // Lane l looks up key l % 16 of the warp's 16 of a tile (8 of each half), for K (l <
+      // 16) and V alike: the block-table entry two tiles ahead, the scale one ahead.
       int raw = -1, raw_row = 0, page = 0, row = 0;
       bool looked = false, have = false, none = false;  // looked up; there; its page is not
-      unsigned scales = 0;
+      unsigned next_scale = 127, scale = 127, tile_gone = 0;
+      long long place = -1;  // of the current tile, in elements from the start of the cache
       auto look_up = [&](int t) {  // the entry
         looked = false;
         if (t >= n) return;
-        const int j = first_key(w, t) + gt;
+        const int j = g.first_key(t) + (lane & 8) * 8 + gw * 8 + (lane & 7);
         if (w.see.unseen(j, 1) || j >= w.keys) return;
         looked = true;
         int entry;
         split_position(c, j, &entry, &raw_row);
         raw = __ldg(c.table + w.b * c.table_stride + entry);
       };
-      auto resolve = [&]() {  // the place, and its scales on their way
+      auto resolve = [&]() {  // the place, and its scale on its way
         have = looked && raw >= 0 && raw < c.pages;
         none = looked && !have;
         page = have ? raw : 0, row = have ? raw_row : 0;
-        if (SRC == kChunkE4M3 && have) {
-          const long long at = (static_cast<long long>(page) * c.Hkv + w.head) * c.page_size + row;
-          scales = __ldg(c.k_scale + at) | static_cast<unsigned>(__ldg(c.v_scale + at)) << 8;
+        if (kCodes) {
+          next_scale = 127;
+          if (have)
+            next_scale = __ldg((lane < 16 ? c.k_scale : c.v_scale) +
+                               (static_cast<long long>(page) * c.Hkv + w.head) * c.page_size + row);
         }
       };
-      // The places and scales of tile t for every thread, and the next tiles' lookups.
-      auto publish = [&](int t) {
-        sync_gather();  // the last tile's places have been read
-        if (!staged_by_tma) {
-          places->k[gt] = have ? page * c.sk.b + row * c.sk.n : -1;
-          places->v[gt] = have ? page * c.sv.b + row * c.sv.n : -1;
-        }
-        if (SRC == kChunkE4M3) {
-          places->k_scale[(base + t) & 1][gt] = static_cast<uint8_t>(have ? scales & 0xFFu : 127u);
-          places->v_scale[(base + t) & 1][gt] = static_cast<uint8_t>(have ? scales >> 8 : 127u);
-        }
+      auto take = [&](int t) {  // tile t becomes the current one; the next tiles' lookups
+        const Strides& s = lane < 16 ? c.sk : c.sv;
+        if (SRC != kChunkStaged) place = have ? page * s.b + row * s.n : -1;
+        scale = next_scale;
         const uint32_t gone = __ballot_sync(0xffffffffu, none);
         if (lane == 0) {
-          *static_cast<volatile uint32_t*>(&ctrl->missing[(base + t) & 15][warp & 3]) = gone;
+          volatile uint8_t* bytes = reinterpret_cast<uint8_t*>(ctrl->missing[(base + t) & 7]);
+          bytes[gw] = static_cast<uint8_t>(gone), bytes[8 + gw] = static_cast<uint8_t>(gone >> 8);
           if (gone) atomicOr(c.status, kStatusIndex);
         }
         resolve();
         look_up(t + 2);
-        sync_gather();
       };
+      // the lane that has looked up the key of piece i of half h (4 t + 0, 1 of K's tile t,
+      // + 2, 3 of V's)
+      auto lane_of = [&](int h, int i) { return (h & 2) * 8 + (h & 1) * 8 + RI * i + sub; };
       auto wait_empty = [&](int t, bool v) {
         const int s = (base + t) % NS;
         return wait(v ? &ctrl->v_empty[s] : &ctrl->k_empty[s], ((base + t) / NS) ^ 1);
       };
-      // Half tile h: 4 t + 0, 1 of K's tile t, + 2, 3 of V's.
+      auto half_of = [&](int h) {  // half tile h in the ring
+        return smem_u32(smem + ((h & 2) ? L::OFF_V : L::OFF_K)) +
+               (base + (h >> 2)) % NS * L::KV_BYTES + (h & 1) * (BN / 2) * 128;
+      };
+      unsigned scales_behind = 127;  // of the tile before the current one
       auto issue = [&](int h) {
         const int t = h >> 2;
-        if (t < n && (h & 3) == 0) publish(t);
+        if ((h & 3) == 0) {
+          scales_behind = scale;
+          if (t < n) take(t);
+        }
         if (ok && t < n) {
           const bool v = (h & 2) != 0;
-          const int r0h = (h & 1) * (BN / 2);
           if (SRC == kChunkRows && (h & 1) == 0) ok = wait_empty(t, v);
           if (ok) {
-            const uint32_t tile =
-                smem_u32(smem + (v ? L::OFF_V : L::OFF_K) + (base + t) % NS * L::KV_BYTES);
-            const uint32_t to = SRC == kChunkE4M3 ? stage + h % kChunkAhead * L::HALF_CODES
-                                                  : tile + in_tile + r0h * 128;
-            const long long* at = v ? places->v : places->k;
+            const uint32_t to =
+                SRC == kChunkE4M3 ? stage + h % kChunkAhead * L::HALF_CODES : half_of(h);
             const TC* from = v ? vc : kc;
-            long long place[HP];  // (all read first: the copies may not be reordered with reads)
+            long long at[HP];
 #pragma unroll
-            for (int i = 0; i < HP; ++i) place[i] = at[r0h + prow + i * RS];
+            for (int i = 0; i < HP; ++i) at[i] = __shfl_sync(0xffffffffu, place, lane_of(h, i));
 #pragma unroll
             for (int i = 0; i < HP; ++i) {
-              const bool on = in_row && place[i] >= 0;
-              if (!JVP_CHECK(r0h + prow + i * RS < BN, c.status, kChkSmem)) continue;
+              const bool on = in_row && at[i] >= 0;
+              if (!JVP_CHECK(tile_at(i) + 16 <= L::KV_BYTES, c.status, kChkSmem)) continue;
               if constexpr (SRC == kChunkE4M3)
-                chunk_copy<8>(to + i * 128 * 8, from + (on ? place[i] : 0), on);
+                chunk_copy<8>(to + i * RI * D, from + (on ? at[i] : 0), on);
               else
-                chunk_copy<16>(to + i * RS * 128, from + (on ? place[i] : 0), on);
+                chunk_copy<16>(to + tile_at(i), from + (on ? at[i] : 0), on);
             }
           }
         }
@@ -575,71 +650,81 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       look_up(0);
       resolve();
       look_up(1);
-      if (!staged_by_tma)
+      if constexpr (SRC != kChunkStaged)
         for (int h = 0; h < kChunkAhead; ++h) issue(h);
       for (int h = 0; h < 4 * n; ++h) {
         const int t = h >> 2;
         const bool v = (h & 2) != 0;
         int slot = h % kChunkAhead;
-        if (staged_by_tma) {
-          if ((h & 3) == 0) publish(t);
-          slot = halves % kChunkAhead;
-          ok = ok && wait(&ctrl->stage_full[slot], halves / kChunkAhead);
+        if constexpr (SRC == kChunkStaged) {
+          if ((h & 3) == 0) take(t);
+          slot = halves % L::AHEAD;
+          ok = ok && wait(&ctrl->stage_full[slot], halves / L::AHEAD);
         } else {
           asm volatile("cp.async.wait_group %0;" ::"n"(kChunkAhead - 1) : "memory");
+          __syncwarp();
         }
-        if constexpr (SRC == kChunkE4M3) {
+        if constexpr (kCodes) {
           if (ok && (h & 1) == 0) ok = wait_empty(t, v);
           if (ok) {
-            const int r0h = (h & 1) * (BN / 2);
-            const uint32_t from = stage + slot * L::HALF_CODES;
-            const uint32_t to =
-                smem_u32(smem + (v ? L::OFF_V : L::OFF_K) + (base + t) % NS * L::KV_BYTES) + in_tile +
-                r0h * 128;
-            const uint8_t* scale =
-                v ? places->v_scale[(base + t) & 1] : places->k_scale[(base + t) & 1];
-            uint32_t x[HP][2];
-            float f[HP];
-#pragma unroll
-            for (int i = 0; i < HP; ++i) {  // (all read first, as above)
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                           : "=r"(x[i][0]), "=r"(x[i][1])
-                           : "r"(from + i * 128 * 8)
-                           : "memory");
-              f[i] = scale_value(scale[r0h + prow + i * RS]);
-            }
-#pragma unroll
+            const uint32_t from = stage + slot * L::HALF_CODES, to = half_of(h);
+            // (the warp's own copies are three halves ahead: those of tile t + 1 begin behind
+            // K's second half of tile t)
+            const unsigned mine = SRC == kChunkStaged || !v ? scale : scales_behind;
+            // (a loop: what counts here is the instruction cache, which 20 warps at six
+            // different places share; unrolled, half a tile took 900 cycles, not @@LOOPFIG@@)
+#pragma unroll 1
             for (int i = 0; i < HP; ++i) {
-              uint32_t y[4];
-              e4m3x4_to_half2x2(x[i][0], y[0], y[1]);
-              e4m3x4_to_half2x2(x[i][1], y[2], y[3]);
+              uint32_t x[2], y[4];
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                           : "=r"(x[0]), "=r"(x[1])
+                           : "r"(from + i * RI * D)
+                           : "memory");
+              const unsigned byte = __shfl_sync(0xffffffffu, mine, lane_of(h, i));
+              using S = ChunkShift<T>;
+              const int e = static_cast<int>(byte) + S::kExp - 127;
+              // NaN among the codes
+              const uint32_t nan = (((x[0] & 0x7F7F7F7Fu) + 0x01010101u) |
+                                    ((x[1] & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+              if (nan == 0u && e >= S::kMin && e <= S::kMax) {
+                const uint32_t f = S::factor(e);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f[i]);
-              st_shared_v4(to + i * RS * 128, y[0], y[1], y[2], y[3]);
+                for (int k = 0; k < 4; ++k)
+                  y[k] = S::times(S::place(__byte_perm(x[k / 2], 0, k & 1 ? 0x3424 : 0x1404)), f);
+              } else {
+                const float f = scale_value(byte);
+                e4m3x4_to_half2x2(x[0], y[0], y[1]);
+                e4m3x4_to_half2x2(x[1], y[2], y[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f);
+              }
+              st_shared_v4(to + tile_at(i), y[0], y[1], y[2], y[3]);
             }
-          }
-          if (staged_by_tma) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctrl->stage_empty[slot]);
+          }
+          if constexpr (SRC == kChunkStaged) {
+            if (ok && lane == 0) mbar_arrive(&ctrl->stage_empty[slot]);
             ++halves;
           }
         }
         // (the staging area's next half tile takes the place of the one just read)
-        if (ok && v && (h & 1) == 0 && g.inspected(t) && gt == 0)
+        if (ok && v && (h & 1) == 0 && g.inspected(t) && gw == 0 && lane == 0)
           mbar_arrive(&ctrl->v_issued[(seen + g.before(t)) % NS]);
         if (ok && (h & 1) == 1) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(v ? &ctrl->v_full[(base + t) % NS] : &ctrl->k_full[(base + t) % NS]);
         }
-        if (!staged_by_tma) issue(h + kChunkAhead);
+        if constexpr (SRC != kChunkStaged) issue(h + kChunkAhead);
+        if (!ok) break;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       base += n, seen += g.before(n);
+      leave_job(job_k);
     }
   } else {
     // ------------------------------------------------------------ softmax
-    if (kGather) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if (kGather) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     else if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int x = (warp - kSoftmax) >> 2;  // query tile
@@ -652,10 +737,10 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
     const uint32_t s_tm = lane_base + L::TM_S + x * BN;
     int base = 0, number = 0, uses = 0, stores = 0, steps = 0;
     bool ok = true;
-    Walk walk(p, begin, end);
-    Part w;
-    while (ok && walk.next(p, &w)) {
-      const Geometry g(p, w);
+    for (int job_k = 0; ok; ++job_k) {
+      const ChunkJob* const job = take_job(job_k);
+      if (!job) break;
+      const ChunkJob &w = *job, &g = *job;
       ++number;
       const int nx = x ? g.n_b : g.n_a;
       const int first = w.tok0 + x * p.tok;  // first token of the tile
@@ -675,38 +760,60 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       for (int t = 0; t < nx; ++t) {
         if (!(ok = wait(&ctrl->s_full[x], steps + t))) break;
         tc_fence_after();
-        float s[BN];
-        if (!JVP_CHECK(L::TM_S + x * BN + BN <= L::TM_O, c.status, kChkTmem)) continue;
-#pragma unroll
-        for (int q = 0; q < BN; q += 64) {
-          uint32_t a[32], b[32];
-          tmem_ld32x2(s_tm + q, s_tm + q + 32, a, b);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            s[q + e] = __uint_as_float(a[e]);
-            s[q + 32 + e] = __uint_as_float(b[e]);
-          }
-        }
-        const int j0 = first_key(w, t);
+        // The row's visible keys of the tile as bits, where any are hidden: one kind of
+        // mask for all reasons, since the loop must stay in the instruction cache.
+        const int j0 = g.first_key(t);
         uint32_t missing[4];
-        ld_shared_v4(smem_u32(ctrl->missing[(base + t) & 15]), missing);
-        if (j0 + BN > warp_limit || (j0 < warp_lo && j0 + BN > w.see.sinks) ||
-            (missing[0] | missing[1] | missing[2] | missing[3]) != 0u) {
-          // (as bits: one run over the scores for every kind of mask, since the loop
-          // must stay in the instruction cache)
-#pragma unroll
+        ld_shared_v4(smem_u32(ctrl->missing[(base + t) & 7]), missing);
+        const bool masked = j0 + BN > warp_limit || (j0 < warp_lo && j0 + BN > w.see.sinks) ||
+                            (missing[0] | missing[1] | missing[2] | missing[3]) != 0u;
+        auto visible = [&](int q) {  // keys q .. q + 31
+          const int here = limit - (j0 + q);  // keys that are not later than the row's
+          uint32_t bits = here >= 32 ? 0xFFFFFFFFu : here <= 0 ? 0u : (1u << here) - 1u;
+          const int h0 = max(w.see.sinks - (j0 + q), 0), h1 = min(lo - (j0 + q), 32);
+          if (h0 < h1) bits &= ~((0xFFFFFFFFu << h0) & (0xFFFFFFFFu >> (32 - h1)));
+          return bits & ~ctrl->missing[(base + t) & 7][q / 32];
+        };
+        // (Gathering leaves the softmax 72 registers fewer: it reads the scores twice,
+        // for the maximum and for the weights, in loops that are short for the
+        // instruction cache, instead of holding the row.)
+        float s[kGather ? 1 : BN], m_tile;
+        if constexpr (kGather) {
+          m_tile = -INFINITY;
+#pragma unroll 1
           for (int q = 0; q < BN; q += 32) {
-            const int here = limit - (j0 + q);  // keys that are not later than the row's
-            uint32_t bits = here >= 32 ? 0xFFFFFFFFu : here <= 0 ? 0u : (1u << here) - 1u;
-            const int h0 = max(w.see.sinks - (j0 + q), 0), h1 = min(lo - (j0 + q), 32);
-            if (h0 < h1) bits &= ~((0xFFFFFFFFu << h0) & (0xFFFFFFFFu >> (32 - h1)));
-            bits &= ~missing[q / 32];
+            uint32_t a[32];
+            tmem_ld32(s_tm + q, a);
+            const uint32_t bits = masked ? visible(q) : 0xFFFFFFFFu;
+            float y[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(bits & (1u << e))) s[q + e] = -INFINITY;
+              y[e] = bits & (1u << e) ? __uint_as_float(a[e]) : -INFINITY;
+            m_tile = fmaxf(m_tile, packed_max(y));
           }
+        } else {
+#pragma unroll
+          for (int q = 0; q < BN; q += 64) {
+            uint32_t a[32], b[32];
+            tmem_ld32x2(s_tm + q, s_tm + q + 32, a, b);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              s[q + e] = __uint_as_float(a[e]);
+              s[q + 32 + e] = __uint_as_float(b[e]);
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int q = 0; q < BN; q += 32) {
+              const uint32_t bits = visible(q);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(bits & (1u << e))) s[q + e] = -INFINITY;
+            }
+          }
+          m_tile = packed_max(s);
         }
-        const float m_tile = packed_max(s) * scale;
+        m_tile *= scale;
         const bool need = m_tile - m_run > PackedElem<T>::kTop;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? packed_base<T>(m_tile) : m_run;
@@ -729,18 +836,33 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
         const float m_use = m_run == -INFINITY ? 0.f : m_run;
         const float2 c2 = make_float2(scale, scale), nm2 = make_float2(-m_use, -m_use);
         float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-        for (int q = 0; q < BN; q += 32) {
+        auto weights = [&](const float (&y)[32], int q) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float2 e2 = fma2(make_float2(s[q + e], s[q + e + 1]), c2, nm2);
+            float2 e2 = fma2(make_float2(y[e], y[e + 1]), c2, nm2);
             e2.x = ex2_approx(e2.x);
             e2.y = ex2_approx(e2.y);
             sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], e2);
             pk[e >> 1] = PackedElem<T>::pack(e2.x, e2.y);
           }
           tmem_st16(s_tm + q / 2, pk);
+        };
+        if constexpr (kGather) {
+#pragma unroll 1
+          for (int q = 0; q < BN; q += 32) {
+            uint32_t a[32];
+            tmem_ld32(s_tm + q, a);
+            const uint32_t bits = masked ? visible(q) : 0xFFFFFFFFu;
+            float y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              y[e] = bits & (1u << e) ? __uint_as_float(a[e]) : -INFINITY;
+            weights(y, q);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < BN; q += 32) weights(*reinterpret_cast<float(*)[32]>(&s[q]), q);
         }
         l_run += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
                  ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
@@ -784,9 +906,9 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
 #pragma unroll 1
           for (int t = 0; t < nx; ++t) {
             if (!g.inspected(t) || !(special & (t < g.low ? 1 : 2))) continue;
-            const int j1 = min(first_key(w, t) + BN, w.keys);
+            const int j1 = min(g.first_key(t) + BN, w.keys);
 #pragma unroll 1
-            for (int j = first_key(w, t); j < j1; ++j) {
+            for (int j = g.first_key(t); j < j1; ++j) {
               if (!w.see.sees(at, j)) continue;
               int entry, in_page;
               split_position(c, j, &entry, &in_page);
@@ -794,7 +916,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
               if (page < 0) continue;
               const long long place = page * c.sv.b + w.head * c.sv.h + in_page * c.sv.n + d;
               uint32_t y4[4];
-              if constexpr (SRC == kChunkE4M3) {
+              if constexpr (kCodes) {
                 const uint2 codes =
                     __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + place));
                 const float f = scale_value(__ldg(
@@ -881,6 +1003,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       }
       steps += nx;
       base += g.n;
+      leave_job(job_k);
     }
     tc_fence_before();
   }

@@ -219,9 +219,9 @@ constexpr int kChunkTile = 128, kChunkSimtTile = 64, kChunkSimtRows = 32;  // ke
 // Cost of an item beside its key tiles, in tiles, and the least cost for a CTA.
 constexpr int kChunkStart = 4, kChunkLeast = 9;
 constexpr int kChunkSnap = 4;  // fewest tiles of a part of a cut item
-// source of the key tiles: boxes of whole pages' parts by TMA, rows gathered by
-// threads, or e4m3 rows gathered and converted
-enum ChunkSource { kChunkBoxes, kChunkRows, kChunkE4M3 };
+// source of the key tiles: boxes of parts of pages by TMA, rows gathered by threads,
+// e4m3 rows gathered and converted, or copied by TMA and converted
+enum ChunkSource { kChunkBoxes, kChunkRows, kChunkE4M3, kChunkStaged };
 cudaError_t launch_chunk_tc(DType dt, int kernel_d, ChunkSource source, const ChunkMaps& maps,
                             const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_simt(DType dt, bool e4m3, const ChunkParams& p, cudaStream_t stream);

@@ -406,3 +406,25 @@ def test_refusals():
             run(c, q, bad)
     with pytest.raises(_abi.JvpAttnError):
         run(c, q, cu, scale=float("nan"))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("page", [16, 5])
+def test_every_code_of_an_e4m3_cache(dt, page):
+    """A sequence of one key returns its values: all 256 codes under scales from the
+    smallest to the largest, as cache_read gives them (NaN included)."""
+    D, n = 128, 254
+    c, q, cu = make([1] * n, [0] * n, 2, 2, D, dt, page, True, seed=3)
+    codes = torch.arange(256, dtype=torch.int64).to(torch.uint8)
+    c.k.view(torch.uint8).zero_()
+    for b in range(n):
+        pg = int(c.table[b, 0])
+        c.v.view(torch.uint8)[pg, :, 0] = codes.view(2, D)
+        c.scales[1][pg, :, 0] = b  # 2^-127 .. 2^126
+    o, lse = run(c, q, cu)
+    assert api.last_path() == 1
+    d = c.cuda()
+    _, v = api.cache_read(d["k_cache"], d["v_cache"], d["block_table"], None, cu.cuda(), num_rows=n,
+                          k_scale=d["k_scale"], v_scale=d["v_scale"], dtype=DT[dt])
+    same = (o == v) | (torch.isnan(o) & torch.isnan(v))
+    assert same.all(), same.logical_not().nonzero()[:5]
