@@ -34,7 +34,6 @@ constexpr int kGatherWarps = 8;
 constexpr int chunk_threads(int NQ, ChunkSource src) {
   return packed_threads(NQ) + (src == kChunkBoxes ? 0 : 32 * kGatherWarps);
 }
-constexpr int kChunkAhead = 3;  // half tiles that the gathering warps copy ahead
 // Half tiles of codes in flight by TMA: what the shared memory left holds.
 constexpr int chunk_ahead(int D) { return D > 64 ? 4 : 8; }
 template <int D, int NQ, ChunkSource SRC>
@@ -196,9 +195,9 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       }
       mbar_init(&ctrl->drain, 1);
       for (int s = 0; s < NS; ++s) {
-        mbar_init(&ctrl->k_full[s], kGather ? kGatherWarps : 1);
+        mbar_init(&ctrl->k_full[s], kGather ? kGatherWarps / 2 : 1);
         mbar_init(&ctrl->k_empty[s], 1);
-        mbar_init(&ctrl->v_full[s], kGather ? kGatherWarps : 1);
+        mbar_init(&ctrl->v_full[s], kGather ? kGatherWarps / 2 : 1);
         mbar_init(&ctrl->v_empty[s], 1);
         mbar_init(&ctrl->v_issued[s], 1);
         mbar_init(&ctrl->v_checked[s], 1);
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       }
       for (int s = 0; s < L::AHEAD; ++s) {
         mbar_init(&ctrl->stage_full[s], 1);
-        mbar_init(&ctrl->stage_empty[s], kGatherWarps);
+        mbar_init(&ctrl->stage_empty[s], 2);
       }
       ctrl->abort = 0;
       fence_barrier_init();
@@ -545,37 +544,42 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
     }
   } else if (kGather && warp < kSoftmax) {
     // ------------------------------------------------------------ gathering warps
-    // Of each half of a tile a warp takes 8 rows, PR lanes a row, RI rows at once: keys
-    // 64 half + 8 gw + RI i + lane / PR.
+    // Two warps for each half of a tile's keys or values, so that each has one half to
+    // wait for, fill and hand on in a tile: 32 rows, of which lane l looks up row l (its
+    // block-table entry two tiles ahead, its scale one ahead).  A row's 8-element pieces
+    // are PR lanes', RI rows at once.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     using TC = typename std::conditional<kCodes, uint8_t, T>::type;
-    constexpr int PR = D / 8, RI = 32 / PR, HP = 8 / RI;  // HP: pieces of a lane in half a tile
-    const int gw = warp - 4, piece = lane % PR, sub = lane / PR;
-    const bool in_row = piece * 8 < c.D;
-    // a piece's place in its half of a tile (16 bytes, swizzled by the row modulo 8) and
-    // in the staging area (8 bytes)
-    const uint32_t in_tile = (piece / 8) * BN * 128 + (gw * 8 + sub) * 128;
-    auto tile_at = [&](int i) { return in_tile + RI * i * 128 + (((piece % 8) ^ sub ^ (RI * i)) << 4); };
-    const uint32_t stage = smem_u32(smem + L::OFF_STAGE) + (gw * 8 + sub) * D + piece * 8;
-    int base = 0, seen = 0, halves = 0;
+    constexpr int PR = D / 8, RI = 32 / PR, HP = 32 / RI;
+    static_assert(kGatherWarps == 8 && L::AHEAD % 4 == 0, "two warps a half");
+    const int gw = warp - 4, quarter = gw >> 1, piece = lane % PR, sub = lane / PR;
+    const bool v = quarter >= 2, in_row = piece * 8 < c.D;
+    const int row0 = (quarter & 1) * (BN / 2) + (gw & 1) * 32;  // of the tile
+    uint64_t* const full = v ? ctrl->v_full : ctrl->k_full;
+    uint64_t* const empty = v ? ctrl->v_empty : ctrl->k_empty;
+    const Strides& stride = v ? c.sv : c.sk;
+    const uint8_t* const scales = v ? c.v_scale : c.k_scale;
+    const uint32_t ring = smem_u32(smem + (v ? L::OFF_V : L::OFF_K)) + (piece / 8) * BN * 128 +
+                          (row0 + sub) * 128;
+    // piece i of this lane (16 bytes, swizzled by the row modulo 8)
+    auto tile_at = [&](int i) { return RI * i * 128 + (((piece % 8) ^ ((sub + RI * i) & 7)) << 4); };
+    const uint32_t stage = smem_u32(smem + L::OFF_STAGE) + ((gw & 1) * 32 + sub) * D + piece * 8;
+    int base = 0, seen = 0;
     bool ok = true;
     for (int job_k = 0; ok; ++job_k) {
       const ChunkJob* const job = take_job(job_k);
       if (!job) break;
       const ChunkJob &w = *job, &g = *job;
       const int n = g.n;
-      const TC* const kc = static_cast<const TC*>(c.k) + w.head * c.sk.h + piece * 8;
-      const TC* const vc = static_cast<const TC*>(c.v) + w.head * c.sv.h + piece * 8;
-      // Lane l looks up key l % 16 of the warp's 16 of a tile (8 of each half), for K (l <
-      // 16) and V alike: the block-table entry two tiles ahead, the scale one ahead.
+      const TC* const rows = static_cast<const TC*>(v ? c.v : c.k) + w.head * stride.h + piece * 8;
       int raw = -1, raw_row = 0, page = 0, row = 0;
       bool looked = false, have = false, none = false;  // looked up; there; its page is not
-      unsigned next_scale = 127, scale = 127, tile_gone = 0;
+      unsigned next_scale = 127, scale = 127;
       long long place = -1;  // of the current tile, in elements from the start of the cache
       auto look_up = [&](int t) {  // the entry
         looked = false;
         if (t >= n) return;
-        const int j = g.first_key(t) + (lane & 8) * 8 + gw * 8 + (lane & 7);
+        const int j = g.first_key(t) + row0 + lane;
         if (w.see.unseen(j, 1) || j >= w.keys) return;
         looked = true;
         int entry;
@@ -589,60 +593,38 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
         if (kCodes) {
           next_scale = 127;
           if (have)
-            next_scale = __ldg((lane < 16 ? c.k_scale : c.v_scale) +
-                               (static_cast<long long>(page) * c.Hkv + w.head) * c.page_size + row);
+            next_scale = __ldg(scales + (static_cast<long long>(page) * c.Hkv + w.head) * c.page_size +
+                               row);
         }
       };
       auto take = [&](int t) {  // tile t becomes the current one; the next tiles' lookups
-        const Strides& s = lane < 16 ? c.sk : c.sv;
-        if (SRC != kChunkStaged) place = have ? page * s.b + row * s.n : -1;
+        if (SRC != kChunkStaged) place = have ? page * stride.b + row * stride.n : -1;
         scale = next_scale;
         const uint32_t gone = __ballot_sync(0xffffffffu, none);
-        if (lane == 0) {
-          volatile uint8_t* bytes = reinterpret_cast<uint8_t*>(ctrl->missing[(base + t) & 7]);
-          bytes[gw] = static_cast<uint8_t>(gone), bytes[8 + gw] = static_cast<uint8_t>(gone >> 8);
+        if (!v && lane == 0) {
+          *static_cast<volatile uint32_t*>(&ctrl->missing[(base + t) & 7][row0 / 32]) = gone;
           if (gone) atomicOr(c.status, kStatusIndex);
         }
         resolve();
         look_up(t + 2);
       };
-      // the lane that has looked up the key of piece i of half h (4 t + 0, 1 of K's tile t,
-      // + 2, 3 of V's)
-      auto lane_of = [&](int h, int i) { return (h & 2) * 8 + (h & 1) * 8 + RI * i + sub; };
-      auto wait_empty = [&](int t, bool v) {
-        const int s = (base + t) % NS;
-        return wait(v ? &ctrl->v_empty[s] : &ctrl->k_empty[s], ((base + t) / NS) ^ 1);
+      auto wait_empty = [&](int t) {
+        return wait(&empty[(base + t) % NS], ((base + t) / NS) ^ 1);
       };
-      auto half_of = [&](int h) {  // half tile h in the ring
-        return smem_u32(smem + ((h & 2) ? L::OFF_V : L::OFF_K)) +
-               (base + (h >> 2)) % NS * L::KV_BYTES + (h & 1) * (BN / 2) * 128;
-      };
-      unsigned scales_behind = 127;  // of the tile before the current one
-      auto issue = [&](int h) {
-        const int t = h >> 2;
-        if ((h & 3) == 0) {
-          scales_behind = scale;
-          if (t < n) take(t);
-        }
+      // Starts the copies of tile t, to its place or (codes) to the staging area.
+      auto issue = [&](int t) {
         if (ok && t < n) {
-          const bool v = (h & 2) != 0;
-          if (SRC == kChunkRows && (h & 1) == 0) ok = wait_empty(t, v);
-          if (ok) {
-            const uint32_t to =
-                SRC == kChunkE4M3 ? stage + h % kChunkAhead * L::HALF_CODES : half_of(h);
-            const TC* from = v ? vc : kc;
-            long long at[HP];
-#pragma unroll
-            for (int i = 0; i < HP; ++i) at[i] = __shfl_sync(0xffffffffu, place, lane_of(h, i));
-#pragma unroll
-            for (int i = 0; i < HP; ++i) {
-              const bool on = in_row && at[i] >= 0;
-              if (!JVP_CHECK(tile_at(i) + 16 <= L::KV_BYTES, c.status, kChkSmem)) continue;
-              if constexpr (SRC == kChunkE4M3)
-                chunk_copy<8>(to + i * RI * D, from + (on ? at[i] : 0), on);
-              else
-                chunk_copy<16>(to + tile_at(i), from + (on ? at[i] : 0), on);
-            }
+          take(t);
+          if (SRC == kChunkRows) ok = wait_empty(t);
+          const uint32_t to = kCodes ? stage + quarter * L::HALF_CODES
+                                     : ring + (base + t) % NS * L::KV_BYTES;
+#pragma unroll 4
+          for (int i = 0; i < HP; ++i) {
+            const long long at = __shfl_sync(0xffffffffu, place, RI * i + sub);
+            const bool on = ok && in_row && at >= 0;
+            if (!JVP_CHECK(row0 + RI * i + sub < BN, c.status, kChkSmem)) continue;
+            if constexpr (kCodes) chunk_copy<8>(to + i * RI * D, rows + (on ? at : 0), on);
+            else chunk_copy<16>(to + tile_at(i), rows + (on ? at : 0), on);
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -650,73 +632,64 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       look_up(0);
       resolve();
       look_up(1);
-      if constexpr (SRC != kChunkStaged)
-        for (int h = 0; h < kChunkAhead; ++h) issue(h);
-      for (int h = 0; h < 4 * n; ++h) {
-        const int t = h >> 2;
-        const bool v = (h & 2) != 0;
-        int slot = h % kChunkAhead;
+      if (SRC != kChunkStaged) issue(0);
+      for (int t = 0; t < n; ++t) {
+        const int halves = 4 * (base + t) + quarter, slot = halves % L::AHEAD;
         if constexpr (SRC == kChunkStaged) {
-          if ((h & 3) == 0) take(t);
-          slot = halves % L::AHEAD;
-          ok = ok && wait(&ctrl->stage_full[slot], halves / L::AHEAD);
+          take(t);
+          ok = wait(&ctrl->stage_full[slot], halves / L::AHEAD);
+        } else if constexpr (SRC == kChunkRows) {
+          issue(t + 1);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
         } else {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kChunkAhead - 1) : "memory");
-          __syncwarp();
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         if constexpr (kCodes) {
-          if (ok && (h & 1) == 0) ok = wait_empty(t, v);
-          if (ok) {
-            const uint32_t from = stage + slot * L::HALF_CODES, to = half_of(h);
-            // (the warp's own copies are three halves ahead: those of tile t + 1 begin behind
-            // K's second half of tile t)
-            const unsigned mine = SRC == kChunkStaged || !v ? scale : scales_behind;
-            // (a loop: what counts here is the instruction cache, which 20 warps at six
-            // different places share; unrolled, half a tile took 900 cycles, not @@LOOPFIG@@)
-#pragma unroll 1
-            for (int i = 0; i < HP; ++i) {
-              uint32_t x[2], y[4];
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                           : "=r"(x[0]), "=r"(x[1])
-                           : "r"(from + i * RI * D)
-                           : "memory");
-              const unsigned byte = __shfl_sync(0xffffffffu, mine, lane_of(h, i));
-              using S = ChunkShift<T>;
-              const int e = static_cast<int>(byte) + S::kExp - 127;
-              // NaN among the codes
-              const uint32_t nan = (((x[0] & 0x7F7F7F7Fu) + 0x01010101u) |
-                                    ((x[1] & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
-              if (nan == 0u && e >= S::kMin && e <= S::kMax) {
-                const uint32_t f = S::factor(e);
+          ok = ok && wait_empty(t);
+          if (!ok) break;
+          const uint32_t from = stage + (SRC == kChunkStaged ? slot : quarter) * L::HALF_CODES;
+          const uint32_t to = ring + (base + t) % NS * L::KV_BYTES;
+          // (a loop: what counts here is the instruction cache, which 20 warps at six
+          // different places share.  Unrolled, and with all warps at one half of a tile
+          // after the other, a tile took 4.3 us, not @@LOOPFIG@@)
+#pragma unroll 2
+          for (int i = 0; i < HP; ++i) {
+            uint32_t x[2], y[4];
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(x[0]), "=r"(x[1])
+                         : "r"(from + i * RI * D)
+                         : "memory");
+            const unsigned byte = __shfl_sync(0xffffffffu, scale, RI * i + sub);
+            using S = ChunkShift<T>;
+            const int e = static_cast<int>(byte) + S::kExp - 127;
+            // NaN among the codes
+            const uint32_t nan = (((x[0] & 0x7F7F7F7Fu) + 0x01010101u) |
+                                  ((x[1] & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+            if (nan == 0u && e >= S::kMin && e <= S::kMax) {
+              const uint32_t f = S::factor(e);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  y[k] = S::times(S::place(__byte_perm(x[k / 2], 0, k & 1 ? 0x3424 : 0x1404)), f);
-              } else {
-                const float f = scale_value(byte);
-                e4m3x4_to_half2x2(x[0], y[0], y[1]);
-                e4m3x4_to_half2x2(x[1], y[2], y[3]);
+              for (int k = 0; k < 4; ++k)
+                y[k] = S::times(S::place(__byte_perm(x[k / 2], 0, k & 1 ? 0x3424 : 0x1404)), f);
+            } else {
+              const float f = scale_value(byte);
+              e4m3x4_to_half2x2(x[0], y[0], y[1]);
+              e4m3x4_to_half2x2(x[1], y[2], y[3]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f);
-              }
-              st_shared_v4(to + tile_at(i), y[0], y[1], y[2], y[3]);
+              for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f);
             }
-            __syncwarp();
+            if (JVP_CHECK(row0 + RI * i + sub < BN, c.status, kChkSmem))
+              st_shared_v4(to + tile_at(i), y[0], y[1], y[2], y[3]);
           }
-          if constexpr (SRC == kChunkStaged) {
-            if (ok && lane == 0) mbar_arrive(&ctrl->stage_empty[slot]);
-            ++halves;
-          }
-        }
-        // (the staging area's next half tile takes the place of the one just read)
-        if (ok && v && (h & 1) == 0 && g.inspected(t) && gw == 0 && lane == 0)
-          mbar_arrive(&ctrl->v_issued[(seen + g.before(t)) % NS]);
-        if (ok && (h & 1) == 1) {
-          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(v ? &ctrl->v_full[(base + t) % NS] : &ctrl->k_full[(base + t) % NS]);
+          if (SRC == kChunkStaged && lane == 0) mbar_arrive(&ctrl->stage_empty[slot]);
         }
-        if constexpr (SRC != kChunkStaged) issue(h + kChunkAhead);
         if (!ok) break;
+        if (v && gw == 4 && lane == 0 && g.inspected(t))
+          mbar_arrive(&ctrl->v_issued[(seen + g.before(t)) % NS]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[(base + t) % NS]);
+        if (SRC == kChunkE4M3) issue(t + 1);
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       base += n, seen += g.before(n);
