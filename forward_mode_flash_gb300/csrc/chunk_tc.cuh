@@ -747,6 +747,11 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           if (h0 < h1) bits &= ~((0xFFFFFFFFu << h0) & (0xFFFFFFFFu >> (32 - h1)));
           return bits & ~ctrl->missing[(base + t) & 7][q / 32];
         };
+        auto hide = [&](float (&y)[32], uint32_t bits) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(bits & (1u << e))) y[e] = -INFINITY;
+        };
         // (Gathering leaves the softmax 72 registers fewer: it reads the scores twice,
         // for the maximum and for the weights, in loops that are short for the
         // instruction cache, instead of holding the row.)
@@ -757,11 +762,10 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           for (int q = 0; q < BN; q += 32) {
             uint32_t a[32];
             tmem_ld32(s_tm + q, a);
-            const uint32_t bits = masked ? visible(q) : 0xFFFFFFFFu;
             float y[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              y[e] = bits & (1u << e) ? __uint_as_float(a[e]) : -INFINITY;
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(a[e]);
+            if (masked) hide(y, visible(q));
             m_tile = fmaxf(m_tile, packed_max(y));
           }
         } else {
@@ -777,12 +781,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           }
           if (masked) {
 #pragma unroll
-            for (int q = 0; q < BN; q += 32) {
-              const uint32_t bits = visible(q);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(bits & (1u << e))) s[q + e] = -INFINITY;
-            }
+            for (int q = 0; q < BN; q += 32) hide(*reinterpret_cast<float(*)[32]>(&s[q]), visible(q));
           }
           m_tile = packed_max(s);
         }
@@ -826,11 +825,10 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           for (int q = 0; q < BN; q += 32) {
             uint32_t a[32];
             tmem_ld32(s_tm + q, a);
-            const uint32_t bits = masked ? visible(q) : 0xFFFFFFFFu;
             float y[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              y[e] = bits & (1u << e) ? __uint_as_float(a[e]) : -INFINITY;
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(a[e]);
+            if (masked) hide(y, visible(q));
             weights(y, q);
           }
         } else {
