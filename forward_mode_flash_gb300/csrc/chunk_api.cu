@@ -19,14 +19,15 @@ struct ChunkPlan {
   int tile = 0, grid = 0, cut = 0;
   size_t bytes = 0, at_count = 0, at_lse = 0, at_o = 0;  // workspace: items, ...
 };
-// Query tiles of a CTA; 0: the CUDA cores' kernel.  Two share each K/V tile; a chunk that
-// fills no more than two tiles is better off with one per CTA and two CTAs per SM, and
-// so is one whose window is so narrow that a second tile's tokens see much else.
-// Gathered rows leave room for one CTA per SM.  (One against two, us: @@NQFIG@@)
-int chunk_query_tiles(const jvp_cache_t* c, int64_t H, int64_t T, bool boxes, int64_t window) {
-  const int64_t group = H / c->Hkv, tok = kPackedTileRows / group;
-  const bool narrow = window > 0 && tok * (c->D > 64 ? 4 : 8) >= window;
-  return boxes && (narrow || T * group <= 2 * kPackedTileRows * c->B) ? 1 : 2;
+// Query tiles of a CTA (0 stands for the CUDA cores' kernel): two share each K/V tile,
+// unless a chunk fills no more than one on average, when one per CTA and two CTAs per SM
+// hide each other's beginnings and ends.  One against two, us, pages of 16: D = 128, 8/8
+// heads, 64 chunks of 128 tokens over 2048 positions 123 / 132, 32 of 256 111 / 98, 8 of
+// 1024 over 8192 290 / 216; 16/2 heads, 32 of 16 over 5120 60 / 58; D = 64, 8/8 heads, 32
+// of 16 85 / 110, 64 of 128 84 / 103, 4 of 4096 with a window of 1024 111 / 100.  Gathered
+// rows leave room for one CTA per SM.
+int chunk_query_tiles(const jvp_cache_t* c, int64_t H, int64_t T, bool boxes) {
+  return boxes && T * (H / c->Hkv) <= kPackedTileRows * c->B ? 1 : 2;
 }
 ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, int query_tiles, int num_sms,
                      int64_t window, int64_t sinks) {
@@ -208,8 +209,7 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
       source = e4m3 ? kChunkStaged : kChunkBoxes;
     }
   }
-  const int query_tiles =
-      tc ? chunk_query_tiles(cache, H, T, source == kChunkBoxes, p.window) : 0;
+  const int query_tiles = tc ? chunk_query_tiles(cache, H, T, source == kChunkBoxes) : 0;
   const ChunkPlan d = plan_chunk(cache, H, T, query_tiles, sms, p.window, p.sinks);
   if (!workspace || workspace_bytes < d.bytes)
     return api_fail(JVP_ERR_WORKSPACE,
