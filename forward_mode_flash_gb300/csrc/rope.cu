@@ -27,6 +27,7 @@
 #include "debug_checks.cuh"
 #include "paged.cuh"
 #include "rows.cuh"
+#include "sm103_ptx.cuh"
 
 namespace jvp {
 namespace {
@@ -82,6 +83,12 @@ __device__ __forceinline__ void turn_pair(float c, float s, float* a, float* b) 
   const float x = *a, y = *b;
   *a = fmaf(x, c, -__fmul_rn(y, s)), *b = fmaf(y, c, __fmul_rn(x, s));
 }
+// Elements e, e + 1 as a pair: 16-bit rows are near the issue rate, and the paired
+// forms halve the arithmetic (same roundings).
+__device__ __forceinline__ float2 two(const float* x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ void put2(float* x, const float2& y) { x[0] = y.x, x[1] = y.y; }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 minus(const float2& x) { return make_float2(-x.x, -x.y); }
 __device__ __forceinline__ float inverse_root(float squares, const RopeParams& p) {
   return rsqrtf(fmaf(squares, p.inv_d, p.eps));
 }
@@ -128,7 +135,12 @@ struct Angles {
       }
     } else if (lane.turned[0]) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) turn_pair(c[e], f * s[e], &x[0][e], &x[1][e]);
+      for (int e = 0; e < N; e += 2) {
+        const float2 cc = two(&c[e]), ss = mul2(both(f), two(&s[e]));
+        const float2 a = two(&x[0][e]), b = two(&x[1][e]);
+        put2(&x[0][e], fma2(a, cc, minus(mul2(b, ss))));
+        put2(&x[1][e], fma2(b, cc, mul2(a, ss)));
+      }
     }
   }
 };
@@ -157,12 +169,30 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 template <int N>
 __device__ __forceinline__ float dot(const float (&a)[2][N], const float (&b)[2][N]) {
-  float x = 0.f;
+  float2 x = both(0.f);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int e = 0; e < N; ++e) x = fmaf(a[i][e], b[i][e], x);
-  return x;
+    for (int e = 0; e < N; e += 2) x = fma2(two(&a[i][e]), two(&b[i][e]), x);
+  return x.x + x.y;
+}
+// x = f w x
+template <int N>
+__device__ __forceinline__ void weigh(float (&x)[2][N], const float (&w)[2][N], float f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < N; e += 2)
+      put2(&x[i][e], mul2(mul2(both(f), two(&w[i][e])), two(&x[i][e])));
+}
+// x = f (x - m n)
+template <int N>
+__device__ __forceinline__ void project(float (&x)[2][N], const float (&n)[2][N], float m, float f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < N; e += 2)
+      put2(&x[i][e], mul2(both(f), fma2(both(-m), two(&n[i][e]), two(&x[i][e]))));
 }
 
 template <typename T>
@@ -176,11 +206,7 @@ __device__ __forceinline__ void norm_and_turn(const RopeParams& p, const Lane<T,
                                               const Angles<T, LANES, IL>& angles,
                                               const float (&w)[2][N], float (&x)[2][N]) {
   if constexpr (NORM) {
-    const float r = inverse_root(row_sum<LANES>(dot(x, x)), p);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[i][e] *= r * w[i][e];
+    weigh(x, w, inverse_root(row_sum<LANES>(dot(x, x)), p));
   }
   angles.turn(lane, x);
 }
@@ -267,18 +293,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) 
         }
         if constexpr (NORM) {
           const float r = inverse_root(row_sum<LANES>(dot(x, x)), p);
-          if constexpr (TAN) {
+          if constexpr (TAN) {  // w r (dx - m n), n = r x
             const float m = r * row_sum<LANES>(dot(x, t)) * p.inv_d;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < N; ++e)
-                t[i][e] = r * w[i][e] * fmaf(-m, r * x[i][e], t[i][e]);
+            project(t, x, m * r, 1.f);
+            weigh(t, w, r);
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[i][e] *= r * w[i][e];
+          weigh(x, w, r);
         }
         angles.turn(lane, x);
         if constexpr (TAN) angles.turn(lane, t);
@@ -299,8 +319,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) 
 
 // gx (and gdx) of every row; the block's sums of the weights' gradients go to
 // the workspace, [grid][2][D].
+//
+// Blocks of an SM: 4, or 3 with tangents in 16 bits, whose rows need the registers
+// (bf16, 4 x 4096 tokens, 16 + 4 heads of 128: 64 us at 4 against 72 at 3, with
+// tangents 129 us at 3 against 165 at 4; fp32 with tangents 171 us at 4, 206 at 3).
 template <typename T, int LANES, bool IL, bool TAN>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeDense d) {
+__global__ void __launch_bounds__(kThreads, TAN && sizeof(T) == 2 ? 3 : 4)
+    norm_rope_bwd_kernel(const RopeDense d) {
   constexpr int N = Piece<T>::N, PER = 32 / LANES;
   constexpr int UN = TAN ? 1 : 2;
   const RopeParams& p = d.r;
@@ -364,10 +389,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeDense
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-              x[i][e] *= r;  // n
-              gw[i][e] = fmaf(g[i][e], x[i][e], gw[i][e]);
-              g[i][e] *= w[i][e];  // u
+            for (int e = 0; e < N; e += 2) {
+              const float2 nn = mul2(both(r), two(&x[i][e])), a = two(&g[i][e]);
+              put2(&x[i][e], nn);
+              put2(&gw[i][e], fma2(a, nn, two(&gw[i][e])));
+              put2(&g[i][e], mul2(a, two(&w[i][e])));  // u
             }
           const float un = row_sum<LANES>(dot(g, x)) * p.inv_d;
           if constexpr (TAN) {
@@ -380,31 +406,32 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeDense
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < N; ++e) {
-                gw[i][e] = fmaf(v[i][e], r * fmaf(-m, x[i][e], t[i][e]), gw[i][e]);
-                v[i][e] *= w[i][e];
+              for (int e = 0; e < N; e += 2) {
+                const float2 dn =
+                    mul2(both(r), fma2(both(-m), two(&x[i][e]), two(&t[i][e])));
+                put2(&gw[i][e], fma2(two(&v[i][e]), dn, two(&gw[i][e])));
+                put2(&v[i][e], mul2(two(&v[i][e]), two(&w[i][e])));
               }
             const float vn = row_sum<LANES>(dot(v, x)) * p.inv_d;
             const float vt = row_sum<LANES>(dot(v, t)) * p.inv_d;
+            // gx = r (u + of_n n - r (vn dx + m v)), gdx = r (v - vn n)
             const float of_n = r * (3.f * m * vn - vt) - un;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < N; ++e) {
-                // r (u + of_n n - r (vn dx + m v)) and r (v - vn n)
-                g[i][e] = r * (fmaf(of_n, x[i][e], g[i][e]) - r * fmaf(vn, t[i][e], m * v[i][e]));
-                v[i][e] = r * fmaf(-vn, x[i][e], v[i][e]);
+              for (int e = 0; e < N; e += 2) {
+                const float2 y = fma2(both(of_n), two(&x[i][e]), two(&g[i][e]));
+                const float2 z = fma2(both(vn), two(&t[i][e]), mul2(both(m), two(&v[i][e])));
+                put2(&g[i][e], mul2(both(r), fma2(both(-r), z, y)));
               }
+            project(v, x, vn, r);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               if (ons[i])
                 *reinterpret_cast<uint4*>(ot_at + (h + k - first) * sto.h + lane.at[i]) =
                     Piece<T>::put(v[i]);
           } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < N; ++e) g[i][e] = r * fmaf(-un, x[i][e], g[i][e]);
+            project(g, x, un, r);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -808,8 +835,9 @@ cudaError_t with_type(DType dt, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-// Units (warps' work): all heads of a group of tokens, or so few that the
-// GPU has `want` warps.
+// Units (warps' work): all heads of a group of tokens, or so few that the GPU has
+// `want` warps.  Dense rows want 8 an SM: fewer heads a unit load the angles and
+// weights more often (fp16, 1024 tokens, 32 heads of 64: 9.5 us at 8, 14.4 at 32).
 void split_heads(long long groups, int heads, long long want, int least, int* per_unit, int* chunks) {
   int n = heads;
   while (n > least && groups * ((heads + n - 1) / n) < want) n = (n + 1) / 2;
@@ -855,7 +883,7 @@ cudaError_t launch_norm_rope(DType dt, bool vec, bool bwd, RopeDense d, int num_
     return with_lanes<T>(d.r.D, [&](auto lanes) -> cudaError_t {
       constexpr int LANES = decltype(lanes)::value;
       const long long groups = (d.tokens + 32 / LANES - 1) / (32 / LANES);
-      split_heads(groups, d.H + d.Hkv, 16ll * num_sms, tan ? 2 : 4, &d.heads_per_unit,
+      split_heads(groups, d.H + d.Hkv, 8ll * num_sms, tan ? 2 : 4, &d.heads_per_unit,
                   &d.head_chunks);
       d.units = groups * d.head_chunks;
       const long long blocks = (d.units + kWarps - 1) / kWarps;
