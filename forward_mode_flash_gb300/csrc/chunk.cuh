@@ -8,7 +8,7 @@
 // one that others end.  So CTAs are equally loaded whatever the lengths, which only
 // the device knows, and an item is cut only where a CTA's part ends (and not within
 // kChunkSnap tiles of its ends).  Each CTA finds its part by itself: the costs of all
-// items are summed by its threads, an item each, some 2 us (a kernel of one block in
+// items are summed by its threads, some 2 us (a kernel of one block in
 // front that did it for all, its successor's set-up beside it, took 5.5).  Parts of
 // cut items leave normalised outputs and log-sum-exps in the workspace, two slots
 // per CTA, for the join.
@@ -121,117 +121,118 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
   const int tid = static_cast<int>(threadIdx.x), B = p.c.B, step = chunk_step(p);
   bool bad = false;
   int b0 = 0, nb = 0;  // sequences in shared memory
-  auto load_round = [&](int from) {  // their items
+  // A thread takes neighbouring sequences, and neighbouring items, so that there is one
+  // sum over the block for each, however many there are.
+  auto load_round = [&](int from) {  // returns their items
     b0 = from, nb = min(B - from, kChunkSeqs);
-    long long items = 0;
-    for (int i0 = 0; i0 < nb; i0 += THREADS) {
-      const int i = i0 + tid;
-      ChunkSequence s{};
-      if (i < nb) s = chunk_sequence(p, step, b0 + i, &bad);
-      long long total;
-      const long long before = items + chunk_block_sum<THREADS>(s.items, sh->part, &total);
-      if (i < nb)
-        sh->first[i] = static_cast<int>(before), sh->r0[i] = s.r0, sh->len[i] = s.len,
-        sh->keys[i] = s.keys;
-      items += total;
+    const int per = (nb + THREADS - 1) / THREADS, i0 = min(nb, tid * per), i1 = min(nb, i0 + per);
+    int items = 0;
+    for (int i = i0; i < i1; ++i) {
+      const ChunkSequence s = chunk_sequence(p, step, b0 + i, &bad);
+      sh->first[i] = items, sh->r0[i] = s.r0, sh->len[i] = s.len, sh->keys[i] = s.keys;
+      items += s.items;
     }
-    if (tid == 0) sh->first[nb] = static_cast<int>(items);
+    long long total;
+    const int before = static_cast<int>(chunk_block_sum<THREADS>(items, sh->part, &total));
+    for (int i = i0; i < i1; ++i) sh->first[i] += before;
+    if (tid == 0) sh->first[nb] = static_cast<int>(total);
     __syncthreads();
-    return static_cast<int>(items);
+    return static_cast<int>(total);
   };
-  auto cost_of = [&](int i, int* b, int* in_seq) {  // of item i of the round
-    int lo = 0, hi = nb;  // the last sequence with first <= i
+  int b = 0, in_seq = 0;  // of an item
+  auto seek = [&](int i) {  // item i of the round: the last sequence with first <= i
+    int lo = 0, hi = nb;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sh->first[mid] <= i) lo = mid;
       else hi = mid;
     }
-    *b = b0 + lo, *in_seq = i - sh->first[lo];
-    ChunkSequence s;
-    s.r0 = sh->r0[lo], s.len = sh->len[lo], s.keys = sh->keys[lo];
-    ChunkKeys<TILE> keys;
-    return kChunkStart + chunk_tiles(p, s, *in_seq, &keys);
+    b = lo;
   };
-  // ---- all costs
-  long long all = 0, before = 0;
-  int cost = 0, b = 0, in_seq = 0, steps = 0;  // (kept where one step covers the items)
-  for (int from = 0; from < B; from += kChunkSeqs) {
-    const int I = load_round(from);
-    for (int i0 = 0; i0 < I; i0 += THREADS, ++steps) {
-      cost = i0 + tid < I ? cost_of(i0 + tid, &b, &in_seq) : 0;
-      long long total;
-      before = all + chunk_block_sum<THREADS>(cost, sh->part, &total);
-      all += total;
-    }
-  }
+  auto cost_of = [&](int i) {  // of item i, the one sought or behind it
+    while (sh->first[b + 1] <= i) ++b;
+    in_seq = i - sh->first[b];
+    ChunkSequence s;
+    s.r0 = sh->r0[b], s.len = sh->len[b], s.keys = sh->keys[b];
+    ChunkKeys<TILE> keys;
+    return kChunkStart + chunk_tiles(p, s, in_seq, &keys);
+  };
   const int c = static_cast<int>(blockIdx.x);
-  const long long W = all * p.heads;
-  long long parts = W / kChunkLeast;
-  parts = parts < 1 ? 1 : parts > p.grid ? p.grid : parts;
-  const int count = W == 0 ? 0 : static_cast<int>(parts);
-  if (c == 0) {
-    if (bad) atomicOr(p.c.status, kStatusIndex);
-    if (tid == 0) *p.ws_count = count;
-  }
-  if (c >= count) return false;
+  int i0 = 0, i1 = 0, count = 0;  // the thread's items; parts
+  // the thread's items' cost, that of the items in front, of all, and with all heads
+  long long mine = 0, before = 0, all = 0, W = 0;
   // 32-bit arithmetic where it does: a 64-bit division takes a fifth of a microsecond
-  const bool narrow = W < (1ll << 31);
-  auto position = [&](int k) -> long long {
+  bool narrow = true;
+  auto position = [&](int k) -> long long {  // where part k begins
     if (narrow) {
       const unsigned w = static_cast<unsigned>(W), n = static_cast<unsigned>(count);
       return w / n * k + w % n * k / n;
     }
     return W / count * k + W % count * k / count;
   };
-  const long long x0 = position(c), x1 = position(c + 1);
-  // ---- the items in which the part begins and ends
-  auto place = [&](long long x, int which) {  // by the thread whose item holds position x
-    const long long from = x - before * p.heads;
-    const int h = narrow ? static_cast<int>(static_cast<unsigned>(from) / static_cast<unsigned>(cost))
-                         : static_cast<int>(from / cost);
-    const int d = static_cast<int>(from - static_cast<long long>(h) * cost);
-    int4 y;
-    if (d < kChunkStart + (p.cut ? kChunkSnap : 0) && (p.cut || d == 0)) {
-      y = make_int4(b, in_seq, h, 0);
-    } else if (p.cut && cost - d >= kChunkSnap) {
-      y = make_int4(b, in_seq, h, d - kChunkStart);
-      if (which) sh->cut_first = x - d, sh->cut_cost = cost;
-    } else if (h + 1 < p.heads) {  // the next item is the first of the next part
-      y = make_int4(b, in_seq, h + 1, 0);
-    } else {
-      bool ignore = false;
-      ChunkSequence s = chunk_sequence(p, step, b, &ignore);
-      y = make_int4(b, in_seq + 1, 0, 0);
-      while (y.y == s.items) {
-        y.x += 1, y.y = 0, s.items = 0;
-        if (y.x == B) break;
-        s = chunk_sequence(p, step, y.x, &ignore);
+  // All costs first, then the items in which the part begins and ends.  (One loop for
+  // both, and short ones: a kernel's first pass over its instructions is slow.)
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      W = all * p.heads, narrow = W < (1ll << 31);
+      const long long parts = W / kChunkLeast;
+      count = static_cast<int>(W == 0 ? 0 : parts < 1 ? 1 : parts > p.grid ? p.grid : parts);
+      if (c == 0) {
+        if (bad) atomicOr(p.c.status, kStatusIndex);
+        if (tid == 0) *p.ws_count = count;
       }
+      if (c >= count) return false;
+      if (tid == 0 && c + 1 == count) sh->plan[1] = make_int4(B, 0, 0, 0);
+      if (B > kChunkSeqs) all = 0;
     }
-    sh->plan[which] = y;
-  };
-  if (tid == 0 && c + 1 == count) sh->plan[1] = make_int4(B, 0, 0, 0);
-  auto look = [&]() {
-    const long long lo = before * p.heads, hi = lo + static_cast<long long>(cost) * p.heads;
-    if (x0 >= lo && x0 < hi) place(x0, 0);
-    if (c + 1 < count && x1 >= lo && x1 < hi) place(x1, 1);
-  };
-  if (steps == 1) {
-    look();
-  } else {
-    all = 0;
+#pragma unroll 1
     for (int from = 0; from < B; from += kChunkSeqs) {
-      const int I = B > kChunkSeqs ? load_round(from) : sh->first[nb];
-      for (int i0 = 0; i0 < I; i0 += THREADS) {
-        cost = i0 + tid < I ? cost_of(i0 + tid, &b, &in_seq) : 0;
+      if (pass == 0 || B > kChunkSeqs) {
+        const int I = load_round(from);
+        const int per = static_cast<int>((static_cast<unsigned>(I) + THREADS - 1) / THREADS);
+        i0 = static_cast<int>(min(static_cast<long long>(I), static_cast<long long>(tid) * per));
+        i1 = min(I, i0 + per);
+        mine = 0;
+        if (i0 < i1) seek(i0);
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) mine += cost_of(i);
         long long total;
-        before = all + chunk_block_sum<THREADS>(cost, sh->part, &total);
+        before = all + chunk_block_sum<THREADS>(mine, sh->part, &total);
         all += total;
-        look();
       }
+      if (pass == 0) continue;
+#pragma unroll 1
+      for (int which = 0; which < (c + 1 < count ? 2 : 1); ++which) {
+        const long long x = position(c + which);
+        long long first = before * p.heads;
+        if (x < first || x >= first + mine * p.heads) continue;
+        // the item at x is the thread's
+        if (i1 - i0 > 1) seek(i0);
+        int i = i0, cost;
+#pragma unroll 1
+        while (cost = cost_of(i), x >= first + static_cast<long long>(cost) * p.heads)
+          first += static_cast<long long>(cost) * p.heads, ++i;
+        const long long in = x - first;
+        const int h = narrow
+                          ? static_cast<int>(static_cast<unsigned>(in) / static_cast<unsigned>(cost))
+                          : static_cast<int>(in / cost);
+        const int d = static_cast<int>(in - static_cast<long long>(h) * cost);
+        int4 y = make_int4(b0 + b, in_seq, h, 0);
+        if (p.cut ? d < kChunkStart + kChunkSnap : d == 0) {
+        } else if (p.cut && cost - d >= kChunkSnap) {
+          y.w = d - kChunkStart;
+          if (which) sh->cut_first = x - d, sh->cut_cost = cost;
+        } else if (++y.z == p.heads) {  // the next item is the first of the next part
+          y.y += 1, y.z = 0;
+          bool ignore = false;
+          while (y.x < B && y.y >= chunk_sequence(p, step, y.x, &ignore).items) y.x += 1, y.y = 0;
+        }
+        sh->plan[which] = y;
+      }
+      __syncthreads();
     }
   }
-  __syncthreads();
   *start = sh->plan[0], *end = sh->plan[1];
   if (tid == 0) {
     int4 item = make_int4(0, 0, 0, 0);
@@ -241,7 +242,8 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
       // the CTA in whose part its last unit lies, unless that part begins so near the
       // item's end that it leaves it to the one before
       const long long last = sh->cut_first + sh->cut_cost - 1;
-      int c1 = static_cast<int>(min((last + 1) * count / W, static_cast<long long>(count - 1)));
+      // (near it, within the rounding of fp32)
+      int c1 = min(static_cast<int>(static_cast<float>(last) / static_cast<float>(W) * count), count - 1);
       while (position(c1) > last) --c1;
       while (c1 + 1 < count && position(c1 + 1) <= last) ++c1;
       if (last + 1 - position(c1) < kChunkSnap) --c1;

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
   if (warp < 4) {
     if (kGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0 || warp == 2) {
       // ---------------------------------------------------------- copies
       // Warp 0 copies query tiles and K, warp 2 V (a copy's issue takes some 40 cycles, and
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
     // ------------------------------------------------------------ softmax
     if (kGather) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     else if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int x = (warp - kSoftmax) >> 2;  // query tile
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..
     const int r = sub * 32 + lane;

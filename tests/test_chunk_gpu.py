@@ -165,6 +165,17 @@ def test_many_sequences_of_few_tokens_over_long_contexts(dt):
     check(c, q, cu, o, lse, heads=[0, 3])
 
 
+@pytest.mark.parametrize("dt,page", [("bf16", 16), ("f16", 5), ("f32", 16)])
+def test_thousands_of_sequences(dt, page):
+    """More than the division holds at a time, some of no tokens, one long one among them."""
+    new = [(0, 1, 3, 0, 2)[i % 5] for i in range(5003)]
+    past = [(7 * i) % 41 for i in range(5003)]
+    new[3100], past[3100] = 700, 5000
+    c, q, cu = make(new, past, 2, 1, 64, dt, page, seed=17)
+    o, lse = run(c, q, cu)
+    check(c, q, cu, o, lse, heads=[1], rows=40)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 def test_whole_prompts_agree_with_packed_attention(dt):
     """Chunks without a past are packed prompts (same definition, same bounds)."""
