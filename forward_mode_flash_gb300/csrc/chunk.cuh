@@ -112,12 +112,28 @@ __device__ __forceinline__ long long chunk_block_sum(long long x, long long* par
   return before + incl - x;
 }
 
-// Where the part of CTA blockIdx.x begins and ends (sequence, item, head, key tile);
-// false if it has none.  Executed by the whole block.  Also names for the join the
-// item that the CTA begins and others end, and (CTA 0) reports bad offsets and lengths.
+// Where part k of `count` of a list of cost W begins.
+__device__ __forceinline__ long long chunk_position(long long W, int count, int k) {
+  // 32-bit arithmetic where it does: a 64-bit division takes a fifth of a microsecond
+  if (W < (1ll << 31)) {
+    const unsigned w = static_cast<unsigned>(W), n = static_cast<unsigned>(count);
+    return w / n * k + w % n * k / n;
+  }
+  return W / count * k + W % count * k / count;
+}
+
+// A CTA's part: where it begins and ends (sequence, item, head, key tile), and of the item
+// in which it ends.
+struct ChunkSpan {
+  int4 start, end;
+  long long W, cut_first;  // the list's cost; where the item begins
+  int count, cut_cost;     // parts; the item's cost
+};
+// The part of CTA blockIdx.x; false if it has none.  Executed by the whole block.  CTA 0
+// reports bad offsets and lengths.
 template <int TILE, int THREADS>
-__device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch* sh, int4* start,
-                                             int4* end) {
+__device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch* sh,
+                                             ChunkSpan* span) {
   const int tid = static_cast<int>(threadIdx.x), B = p.c.B, step = chunk_step(p);
   bool bad = false;
   int b0 = 0, nb = 0;  // sequences in shared memory
@@ -161,28 +177,19 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
   int i0 = 0, i1 = 0, count = 0;  // the thread's items; parts
   // the thread's items' cost, that of the items in front, of all, and with all heads
   long long mine = 0, before = 0, all = 0, W = 0;
-  // 32-bit arithmetic where it does: a 64-bit division takes a fifth of a microsecond
-  bool narrow = true;
-  auto position = [&](int k) -> long long {  // where part k begins
-    if (narrow) {
-      const unsigned w = static_cast<unsigned>(W), n = static_cast<unsigned>(count);
-      return w / n * k + w % n * k / n;
-    }
-    return W / count * k + W % count * k / count;
-  };
   // All costs first, then the items in which the part begins and ends.  (One loop for
   // both, and short ones: a kernel's first pass over its instructions is slow.)
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
-      W = all * p.heads, narrow = W < (1ll << 31);
+      W = all * p.heads;
       const long long parts = W / kChunkLeast;
       count = static_cast<int>(W == 0 ? 0 : parts < 1 ? 1 : parts > p.grid ? p.grid : parts);
-      if (c == 0) {
-        if (bad) atomicOr(p.c.status, kStatusIndex);
-        if (tid == 0) *p.ws_count = count;
+      if (c == 0 && bad) atomicOr(p.c.status, kStatusIndex);
+      if (c >= count) {
+        if (tid == 0) p.ws_item[c] = make_int4(0, 0, 0, 0);
+        return false;
       }
-      if (c >= count) return false;
       if (tid == 0 && c + 1 == count) sh->plan[1] = make_int4(B, 0, 0, 0);
       if (B > kChunkSeqs) all = 0;
     }
@@ -204,7 +211,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
       if (pass == 0) continue;
 #pragma unroll 1
       for (int which = 0; which < (c + 1 < count ? 2 : 1); ++which) {
-        const long long x = position(c + which);
+        const long long x = chunk_position(W, count, c + which);
         long long first = before * p.heads;
         if (x < first || x >= first + mine * p.heads) continue;
         // the item at x is the thread's
@@ -214,7 +221,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
         while (cost = cost_of(i), x >= first + static_cast<long long>(cost) * p.heads)
           first += static_cast<long long>(cost) * p.heads, ++i;
         const long long in = x - first;
-        const int h = narrow
+        const int h = W < (1ll << 31)
                           ? static_cast<int>(static_cast<unsigned>(in) / static_cast<unsigned>(cost))
                           : static_cast<int>(in / cost);
         const int d = static_cast<int>(in - static_cast<long long>(h) * cost);
@@ -233,29 +240,34 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
       __syncthreads();
     }
   }
-  *start = sh->plan[0], *end = sh->plan[1];
-  if (tid == 0) {
-    int4 item = make_int4(0, 0, 0, 0);
-    const bool goes_on =
-        start->x == end->x && start->y == end->y && start->z == end->z && start->w > 0;
-    if (end->w > 0 && !goes_on) {
-      // the CTA in whose part its last unit lies, unless that part begins so near the
-      // item's end that it leaves it to the one before
-      const long long last = sh->cut_first + sh->cut_cost - 1;
-      // (near it, within the rounding of fp32)
-      int c1 = min(static_cast<int>(static_cast<float>(last) / static_cast<float>(W) * count), count - 1);
-      while (position(c1) > last) --c1;
-      while (c1 + 1 < count && position(c1 + 1) <= last) ++c1;
-      if (last + 1 - position(c1) < kChunkSnap) --c1;
-      bool ignore = false;
-      const ChunkSequence s = chunk_sequence(p, step, end->x, &ignore);
-      const int tok0 = end->y * step;
-      item = make_int4(c1 - c + 1, s.r0 + tok0, min(s.len - tok0, step), end->z);
-    }
-    p.ws_item[c] = item;
-  }
+  span->start = sh->plan[0], span->end = sh->plan[1];
+  span->W = W, span->count = count;
+  span->cut_first = sh->cut_first, span->cut_cost = sh->cut_cost;
   __syncthreads();  // the scratch has been read
   return true;
+}
+// Names for the join the item that the CTA begins and others end.  One thread.
+__device__ __forceinline__ void chunk_name(const ChunkParams& p, const ChunkSpan& x) {
+  const int c = static_cast<int>(blockIdx.x);
+  const int4 &start = x.start, &end = x.end;
+  int4 item = make_int4(0, 0, 0, 0);
+  const bool goes_on = start.x == end.x && start.y == end.y && start.z == end.z && start.w > 0;
+  if (end.w > 0 && !goes_on) {
+    // the CTA in whose part its last unit lies, unless that part begins so near the
+    // item's end that it leaves it to the one before
+    const long long last = x.cut_first + x.cut_cost - 1;
+    // (near it, within the rounding of fp32)
+    int c1 = min(static_cast<int>(static_cast<float>(last) / static_cast<float>(x.W) * x.count),
+                 x.count - 1);
+    while (chunk_position(x.W, x.count, c1) > last) --c1;
+    while (c1 + 1 < x.count && chunk_position(x.W, x.count, c1 + 1) <= last) ++c1;
+    if (last + 1 - chunk_position(x.W, x.count, c1) < kChunkSnap) --c1;
+    bool ignore = false;
+    const int step = chunk_step(p), tok0 = end.y * step;
+    const ChunkSequence s = chunk_sequence(p, step, end.x, &ignore);
+    item = make_int4(c1 - c + 1, s.r0 + tok0, min(s.len - tok0, step), end.z);
+  }
+  p.ws_item[c] = item;
 }
 
 // A CTA's part of one item: key tiles [t0, t1) of `all`, in slot `slot` of the

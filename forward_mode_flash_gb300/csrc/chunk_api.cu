@@ -17,7 +17,7 @@ struct ChunkPlan {
   int rows = 0;  // of an item
   int64_t heads = 0;
   int tile = 0, grid = 0, cut = 0;
-  size_t bytes = 0, at_count = 0, at_lse = 0, at_o = 0;  // workspace: items, ...
+  size_t bytes = 0, at_lse = 0, at_o = 0;  // workspace: items, ...
 };
 // Query tiles of a CTA (0 stands for the CUDA cores' kernel): two share each K/V tile,
 // unless a chunk fills no more than one on average, when one per CTA and two CTAs per SM
@@ -69,7 +69,6 @@ ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, int query_tiles
   const size_t grid = static_cast<size_t>(d.grid);
   size_t at_item;
   place(&at_item, grid * 16);
-  place(&d.at_count, 4);
   if (d.cut) {
     const size_t rows = 2 * grid * d.rows;
     place(&d.at_lse, rows * 4);
@@ -221,7 +220,6 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
   p.grid = d.grid, p.cut = d.cut;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.ws_item = reinterpret_cast<int4*>(ws);
-  p.ws_count = reinterpret_cast<int*>(ws + d.at_count);
   p.ws_lse = reinterpret_cast<float*>(ws + d.at_lse);
   p.ws_o = reinterpret_cast<float*>(ws + d.at_o);
   const int kernel_d = D <= 64 ? 64 : 128;

@@ -14,7 +14,7 @@ namespace jvp {
 namespace {
 
 constexpr int kJoinWarps = 8, kJoinRows = 4;  // rows of a warp at once
-constexpr int kUnit = kJoinWarps * kJoinRows;  // rows of a block at once
+constexpr int kUnit = kJoinWarps * kJoinRows;  // rows of a block
 
 template <typename T, int DPAD>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const ChunkParams p, int rows) {
@@ -22,76 +22,73 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Chunk
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile_rows = rows / p.query_tiles, per = rows / kUnit;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int units = *static_cast<volatile int*>(p.ws_count) * per;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int cta = u / per;
-    const int4 item = p.ws_item[cta];  // CTAs, first row, tokens, head
-    if (item.x == 0) continue;
-    const int hk = item.w / p.head_blocks;
-    const int head0 = (item.w - hk * p.head_blocks) * p.group_rows;
-    const int row0 = u % per * kUnit + warp * R;
-    int token[R], in_group[R];
-    bool on[R], any = false;
+  const int cta = blockIdx.x / per;
+  const int4 item = p.ws_item[cta];  // CTAs, first row, tokens, head
+  if (item.x == 0) return;
+  const int hk = item.w / p.head_blocks;
+  const int head0 = (item.w - hk * p.head_blocks) * p.group_rows;
+  const int row0 = blockIdx.x % per * kUnit + warp * R;
+  int token[R], in_group[R];
+  bool on[R], any = false;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int x = (row0 + k) / tile_rows, r = row0 + k - x * tile_rows;
-      const int rt = r / p.group_rows;
-      token[k] = x * p.tok + rt, in_group[k] = head0 + r - rt * p.group_rows;
-      on[k] = rt < p.tok && token[k] < item.z && in_group[k] < p.group;
-      any |= on[k];
-    }
-    if (!any) continue;  // uniform over the warp
-    float M[R], L[R], acc[R][C];
+  for (int k = 0; k < R; ++k) {
+    const int x = (row0 + k) / tile_rows, r = row0 + k - x * tile_rows;
+    const int rt = r / p.group_rows;
+    token[k] = x * p.tok + rt, in_group[k] = head0 + r - rt * p.group_rows;
+    on[k] = rt < p.tok && token[k] < item.z && in_group[k] < p.group;
+    any |= on[k];
+  }
+  if (!any) return;  // uniform over the warp
+  float M[R], L[R], acc[R][C];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      M[k] = -INFINITY, L[k] = 0.f;
+  for (int k = 0; k < R; ++k) {
+    M[k] = -INFINITY, L[k] = 0.f;
 #pragma unroll
-      for (int d = 0; d < C; ++d) acc[k][d] = 0.f;
-    }
+    for (int d = 0; d < C; ++d) acc[k][d] = 0.f;
+  }
 #pragma unroll 2
-    for (int i = 0; i < item.x; ++i) {
-      const long long at = (2ll * (cta + i) + (i == 0 ? 1 : 0)) * rows + row0;
-      float y[R], v[R][C];
+  for (int i = 0; i < item.x; ++i) {
+    const long long at = (2ll * (cta + i) + (i == 0 ? 1 : 0)) * rows + row0;
+    float y[R], v[R][C];
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        y[k] = -INFINITY;
+    for (int k = 0; k < R; ++k) {
+      y[k] = -INFINITY;
 #pragma unroll
-        for (int d = 0; d < C; ++d) v[k][d] = 0.f;
-        if (!on[k] || !JVP_CHECK(at + k < 2ll * p.grid * rows, p.c.status, kChkGlobalRow)) continue;
-        y[k] = p.ws_lse[at + k];
-        if constexpr (C == 4) {
-          const float4 w = *reinterpret_cast<const float4*>(p.ws_o + (at + k) * DPAD + lane * C);
-          v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
-        } else {
-          const float2 w = *reinterpret_cast<const float2*>(p.ws_o + (at + k) * DPAD + lane * C);
-          v[k][0] = w.x, v[k][1] = w.y;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const float m = fmaxf(M[k], y[k]), mu = m == -INFINITY ? 0.f : m;
-        const float a = exp2f(M[k] - mu), w = exp2f(y[k] - mu);
-        M[k] = m;
-        L[k] = L[k] * a + w;
-#pragma unroll
-        for (int d = 0; d < C; ++d) acc[k][d] = fmaf(w, v[k][d], acc[k][d] * a);
+      for (int d = 0; d < C; ++d) v[k][d] = 0.f;
+      if (!on[k] || !JVP_CHECK(at + k < 2ll * p.grid * rows, p.c.status, kChkGlobalRow)) continue;
+      y[k] = p.ws_lse[at + k];
+      if constexpr (C == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(p.ws_o + (at + k) * DPAD + lane * C);
+        v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
+      } else {
+        const float2 w = *reinterpret_cast<const float2*>(p.ws_o + (at + k) * DPAD + lane * C);
+        v[k][0] = w.x, v[k][1] = w.y;
       }
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      if (!on[k]) continue;
-      const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
-      const int h = hk * p.group + in_group[k];
-      const long long t = static_cast<long long>(item.y) + token[k];
-      if (!JVP_CHECK(t < p.T && h < p.H, p.c.status, kChkGlobalRow)) continue;
-      T* dst = static_cast<T*>(p.o) + t * p.so.n + h * p.so.h;
+      const float m = fmaxf(M[k], y[k]), mu = m == -INFINITY ? 0.f : m;
+      const float a = exp2f(M[k] - mu), w = exp2f(y[k] - mu);
+      M[k] = m;
+      L[k] = L[k] * a + w;
 #pragma unroll
-      for (int d = 0; d < C; ++d)
-        if (lane * C + d < p.c.D) dst[lane * C + d] = Rows<T>::put(acc[k][d] * inv);
-      if (lane == 0 && p.lse)
-        p.lse[h * static_cast<long long>(p.T) + t] =
-            L[k] == 0.f ? -INFINITY : (M[k] + log2f(L[k])) * 0.6931471805599453f;
+      for (int d = 0; d < C; ++d) acc[k][d] = fmaf(w, v[k][d], acc[k][d] * a);
     }
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (!on[k]) continue;
+    const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+    const int h = hk * p.group + in_group[k];
+    const long long t = static_cast<long long>(item.y) + token[k];
+    if (!JVP_CHECK(t < p.T && h < p.H, p.c.status, kChkGlobalRow)) continue;
+    T* dst = static_cast<T*>(p.o) + t * p.so.n + h * p.so.h;
+#pragma unroll
+    for (int d = 0; d < C; ++d)
+      if (lane * C + d < p.c.D) dst[lane * C + d] = Rows<T>::put(acc[k][d] * inv);
+    if (lane == 0 && p.lse)
+      p.lse[h * static_cast<long long>(p.T) + t] =
+          L[k] == 0.f ? -INFINITY : (M[k] + log2f(L[k])) * 0.6931471805599453f;
   }
 }
 

@@ -87,10 +87,11 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
   const bool vec = p.vec != 0;
   const int tid = static_cast<int>(threadIdx.x), tx = tid & 15, ty = tid >> 4;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int4 begin, end;
+  ChunkSpan span;
   static_assert(sizeof(ChunkScratch) <= L::FLOATS * 4, "the tiles' space");
-  if (!chunk_divide<BN, kThreads>(p, reinterpret_cast<ChunkScratch*>(sm), &begin, &end)) return;
-  ChunkWalk<BN> walk(p, begin, end);
+  if (!chunk_divide<BN, kThreads>(p, reinterpret_cast<ChunkScratch*>(sm), &span)) return;
+  if (p.cut && tid == 0) chunk_name(p, span);
+  ChunkWalk<BN> walk(p, span.start, span.end);
   ChunkPart<BN> it;
   while (walk.next(p, &it)) {
     const int hk = it.head / p.head_blocks, hb = it.head - hk * p.head_blocks;

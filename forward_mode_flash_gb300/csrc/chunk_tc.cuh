@@ -216,9 +216,9 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
     }
     if (lane < 16) (&ctrl->special[0][0])[lane] = 0;
   }
-  int4 begin, end;
+  ChunkSpan span;
   static_assert(sizeof(ChunkScratch) <= L::OFF_CTRL - L::OFF_K, "the tiles' space");
-  if (!chunk_divide<BN, THREADS>(p, reinterpret_cast<ChunkScratch*>(smem + L::OFF_K), &begin, &end))
+  if (!chunk_divide<BN, THREADS>(p, reinterpret_cast<ChunkScratch*>(smem + L::OFF_K), &span))
     return;
   if (warp == 1) {
     tmem_alloc(&ctrl->tmem_base, L::TM_COLS);
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
       mbar_wait(&ctrl->drain, 0, &zero);
     } else if (warp == 3) {
       // ---------------------------------------------------------- the parts, V's inspection
-      ChunkWalk<BN> walk(p, begin, end);
+      ChunkWalk<BN> walk(p, span.start, span.end);
       bool more = true;
       auto publish = [&](int k) {  // part k for all, n = 0 behind the last
         if (!more) return true;
@@ -700,6 +700,8 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
     if (kGather) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     else if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if (p.cut && threadIdx.x == THREADS - 1) chunk_name(p, span);  // (before the first scores)
+    __syncwarp();
     const int x = (warp - kSoftmax) >> 2;  // query tile
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..
     const int r = sub * 32 + lane;
@@ -910,42 +912,39 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           }
         };
 #pragma unroll 1
-        for (int col = 0; col < D; col += 64) {
-          uint32_t o[2][32];
-          tmem_ld32x2(o_tm + col, o_tm + col + 32, o[0], o[1]);
+        for (int col = 0; col < D; col += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_tm + col, o);
           if (special && row_ok) {  // (rare: through local memory, to stay short)
-            float sums[64];
+            float sums[32];
 #pragma unroll 1
-            for (int e = 0; e < 64; e += 8)
+            for (int e = 0; e < 32; e += 8)
               add_special(col + e, *reinterpret_cast<float(*)[8]>(&sums[e]));
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              o[e / 32][e % 32] = __float_as_uint(__uint_as_float(o[e / 32][e % 32]) + sums[e]);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + sums[e]);
           }
           if (w.slot >= 0) {
             if (row_ok && JVP_CHECK(w.slot < 2 * p.grid, c.status, kChkGlobalRow)) {
               float4* to = reinterpret_cast<float4*>(p.ws_o + ws_row * D + col);
 #pragma unroll
-              for (int e = 0; e < 64; e += 4)
-                to[e / 4] = make_float4(__uint_as_float(o[e / 32][e % 32]) * inv,
-                                        __uint_as_float(o[e / 32][e % 32 + 1]) * inv,
-                                        __uint_as_float(o[e / 32][e % 32 + 2]) * inv,
-                                        __uint_as_float(o[e / 32][e % 32 + 3]) * inv);
+              for (int e = 0; e < 32; e += 4)
+                to[e / 4] = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
             }
             continue;
           }
 #pragma unroll
-          for (int e = 0; e < 64; e += 8) {
+          for (int e = 0; e < 32; e += 8) {
             uint32_t y4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              y4[k] = PackedElem<T>::pack(__uint_as_float(o[e / 32][e % 32 + 2 * k]) * inv,
-                                         __uint_as_float(o[e / 32][e % 32 + 2 * k + 1]) * inv);
+              y4[k] = PackedElem<T>::pack(__uint_as_float(o[e + 2 * k]) * inv,
+                                         __uint_as_float(o[e + 2 * k + 1]) * inv);
             if (!JVP_CHECK((col / 64) * BM * 128 + r * 128 + 128 <= L::Q_BYTES, c.status, kChkSmem))
               continue;
             if (whole)
-              st_shared_v4(stage + (col / 64) * BM * 128 + (((e / 8) ^ (r & 7)) << 4), y4[0], y4[1],
-                           y4[2], y4[3]);
+              st_shared_v4(stage + (col / 64) * BM * 128 + ((((col % 64 + e) / 8) ^ (r & 7)) << 4),
+                           y4[0], y4[1], y4[2], y4[3]);
             else if (row_ok && in_t && col + e < c.D &&
                      JVP_CHECK(col + e + 8 <= c.D, c.status, kChkGlobalCol))
               *reinterpret_cast<uint4*>(dst + col + e) = make_uint4(y4[0], y4[1], y4[2], y4[3]);

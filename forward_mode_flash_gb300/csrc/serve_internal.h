@@ -206,7 +206,6 @@ struct ChunkParams {
   int cut;           // 0: items are not cut (their key tiles are few)
   int4* ws_item;     // [grid] the item that a CTA begins and others end: CTAs, first row,
                      // tokens, head (CTAs 0: none)
-  int* ws_count;     // CTAs with work
   float* ws_o;       // [grid][2][rows of an item][64 or 128] normalised partial outputs
   float* ws_lse;     // [grid][2][rows of an item], log2 units
   int box_rows;      // tensor cores: keys of a copied box, a divisor of 128 and the page size
