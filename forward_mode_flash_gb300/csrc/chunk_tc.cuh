@@ -6,21 +6,32 @@
 // `tok` tokens times the query heads of a key/value head, two tiles (NQ) per CTA
 // against the same ring of 128-key K/V tiles.  What differs:
 //   - Key tiles are collected from pages.  SRC = kChunkBoxes: the largest power of
-//     two of rows that divides a page (8 at least) is one TMA box; the lanes of the
-//     copying warp each look up one box's page and issue its copy, K's and V's from
-//     one lookup, made a tile ahead.  A box that no row sees, or whose page does not
-//     exist, is copied from behind the last page, where TMA writes zeros.
-//     SRC = kChunkRows (pages of any size) and kChunkE4M3: four more warps gather
-//     the rows in 8-element pieces by asynchronous copies three half tiles ahead, one
-//     thread looking up each key's place a tile ahead.  e4m3 pieces land in a staging
-//     area, and the thread that copied a piece converts it (a code is exact in fp16
-//     and bf16; times its scale, rounded to T as cache_read does).
+//     two of rows that divides a page (8 at least) is one TMA box; the lanes of two
+//     copying warps, one for Q and K, one for V, each look up one box's page a tile ahead
+//     and issue its copy.  A box that no row sees, or whose page does not exist, is copied
+//     from behind the last page, where TMA writes zeros.
+//     The other sources have eight gathering warps, two for each half of a tile's keys or
+//     values, a lane looking up a row two tiles ahead.  kChunkRows (16-bit pages of any
+//     size): asynchronous 16-byte copies straight into the tile.  kChunkStaged (e4m3,
+//     pages of 8-row boxes): TMA copies boxes of codes to a staging ring several half tiles
+//     ahead, and the warps convert them.  kChunkE4M3 (other pages): the warps copy the codes
+//     themselves, in 8-byte pieces.  A code is exact in fp16 and bf16; times its scale, it
+//     is rounded to T as cache_read does.
 //   - A row sees an interval of keys and the sinks (ChunkKeys); tiles that no row
-//     sees are left out.
+//     sees are left out.  What is hidden is one word of bits per 32 keys.
 //   - A CTA takes an equal part of all work, whatever the lengths (chunk.cuh), its items
 //     one behind the other: copies and products of the next go on behind the last one's
-//     epilogue.  Parts of cut items are joined by another kernel in a fixed order.
+//     epilogue.  One warp finds the parts and puts them into shared memory for the others,
+//     and inspects those V tiles of which some rows see only a part.  Parts of cut items
+//     are joined by another kernel in a fixed order.
 // Keys of pages that do not exist are masked by a bit each.
+//
+// Bound: at D = 128 a pair of query tiles takes 1.55 us a key tile from boxes, 2.0 us
+// from rows, 2.25 us from codes (1.1 us would be the tensor core's at its measured rate,
+// and the exponentials alone 1.07 us); at D = 64 1.4, 1.87 and 1.93 us.  A call begins and
+// ends with some 20 us that no tile hides: 3.5 us until a CTA knows its part, 4 us to its
+// first scores, 2.5 us of epilogue, 5 us for the join: most of it first passes over
+// instructions.
 #pragma once
 
 #include "chunk.cuh"
@@ -115,42 +126,6 @@ __device__ __forceinline__ uint32_t chunk_decode(uint32_t half2, float scale) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&half2));
   return PackedElem<T>::pack(f.x * scale, f.y * scale);
 }
-
-// The same by shifts, for pairs of codes in the high bytes of 16-bit halves: sign,
-// exponent and fraction moved to T's places are the code times 2^-120 (bf16) or 2^-8
-// (fp16), subnormal codes too, and one product with the scale's power of two, 2^E,
-// gives the value, rounded once.  For factors that T holds as normal numbers, and no
-// NaN among the codes (which would become 480).  (Conversions by the dedicated
-// instruction and through fp32 are the slower half of the converting warps' time:
-// @@CVTFIG@@)
-template <typename T>
-struct ChunkShift;
-template <>
-struct ChunkShift<__nv_bfloat16> {
-  static constexpr int kExp = 120, kMin = -126, kMax = 127;
-  static __device__ __forceinline__ uint32_t place(uint32_t w) {
-    return (w >> 4 & 0x07F007F0u) | (w & 0x80008000u);
-  }
-  static __device__ __forceinline__ uint32_t factor(int e) { return (e + 127) * 0x00800080u; }
-  static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
-};
-template <>
-struct ChunkShift<__half> {
-  static constexpr int kExp = 8, kMin = -14, kMax = 15;
-  static __device__ __forceinline__ uint32_t place(uint32_t w) {
-    return (w >> 1 & 0x3F803F80u) | (w & 0x80008000u);
-  }
-  static __device__ __forceinline__ uint32_t factor(int e) { return (e + 15) * 0x04000400u; }
-  static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
-    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a),
-                              *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
-};
 
 template <typename T, int D, int NQ, ChunkSource SRC>
 __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3 - NQ : 1)
@@ -651,8 +626,10 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           const uint32_t to = ring + (base + t) % NS * L::KV_BYTES;
           // (a loop: what counts here is the instruction cache, which 20 warps at six
           // different places share.  Unrolled, and with all warps at one half of a tile
-          // after the other, a tile took 4.3 us, not @@LOOPFIG@@)
-#pragma unroll 2
+          // after the other, a tile of 128 keys at D = 128 took 4.3 us, not 2.25.  Codes
+          // moved to T's places by shifts and scaled there by one product, 16-bit, were
+          // slower too, 3.0 us: more instructions.)
+#pragma unroll 4
           for (int i = 0; i < HP; ++i) {
             uint32_t x[2], y[4];
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
@@ -660,23 +637,11 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
                          : "r"(from + i * RI * D)
                          : "memory");
             const unsigned byte = __shfl_sync(0xffffffffu, scale, RI * i + sub);
-            using S = ChunkShift<T>;
-            const int e = static_cast<int>(byte) + S::kExp - 127;
-            // NaN among the codes
-            const uint32_t nan = (((x[0] & 0x7F7F7F7Fu) + 0x01010101u) |
-                                  ((x[1] & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
-            if (nan == 0u && e >= S::kMin && e <= S::kMax) {
-              const uint32_t f = S::factor(e);
+            const float f = scale_value(byte);
+            e4m3x4_to_half2x2(x[0], y[0], y[1]);
+            e4m3x4_to_half2x2(x[1], y[2], y[3]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[k] = S::times(S::place(__byte_perm(x[k / 2], 0, k & 1 ? 0x3424 : 0x1404)), f);
-            } else {
-              const float f = scale_value(byte);
-              e4m3x4_to_half2x2(x[0], y[0], y[1]);
-              e4m3x4_to_half2x2(x[1], y[2], y[3]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f);
-            }
+            for (int k = 0; k < 4; ++k) y[k] = chunk_decode<T>(y[k], f);
             if (JVP_CHECK(row0 + RI * i + sub < BN, c.status, kChkSmem))
               st_shared_v4(to + tile_at(i), y[0], y[1], y[2], y[3]);
           }
