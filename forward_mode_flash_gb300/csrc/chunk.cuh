@@ -2,12 +2,12 @@
 // and which keys its rows see.
 //
 // An item is a tile of a sequence's new tokens and a head; its cost is its key
-// tiles and kChunkStart for its beginning and end.  The items of all sequences form
+// tiles and ChunkCost::start for its beginning and end.  The items of all sequences form
 // a list, heads innermost, and CTA c takes the c-th of `count` equal parts of the
 // list's cost: it continues an item that others began, takes whole ones, and begins
 // one that others end.  So CTAs are equally loaded whatever the lengths, which only
 // the device knows, and an item is cut only where a CTA's part ends (and not within
-// kChunkSnap tiles of its ends).  Each CTA finds its part by itself: the costs of all
+// ChunkCost::snap tiles of its ends).  Each CTA finds its part by itself: the costs of all
 // items are summed by its threads, some 2 us (a kernel of one block in
 // front that did it for all, its successor's set-up beside it, took 5.5).  Parts of
 // cut items leave normalised outputs and log-sum-exps in the workspace, two slots
@@ -135,6 +135,7 @@ template <int TILE, int THREADS>
 __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch* sh,
                                              ChunkSpan* span) {
   const int tid = static_cast<int>(threadIdx.x), B = p.c.B, step = chunk_step(p);
+  constexpr ChunkCost kCost = chunk_cost(TILE);
   bool bad = false;
   int b0 = 0, nb = 0;  // sequences in shared memory
   // A thread takes neighbouring sequences, and neighbouring items, so that there is one
@@ -171,7 +172,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
     ChunkSequence s;
     s.r0 = sh->r0[b], s.len = sh->len[b], s.keys = sh->keys[b];
     ChunkKeys<TILE> keys;
-    return kChunkStart + chunk_tiles(p, s, in_seq, &keys);
+    return kCost.start + chunk_tiles(p, s, in_seq, &keys);
   };
   const int c = static_cast<int>(blockIdx.x);
   int i0 = 0, i1 = 0, count = 0;  // the thread's items; parts
@@ -183,7 +184,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
       W = all * p.heads;
-      const long long parts = W / kChunkLeast;
+      const long long parts = W / kCost.least;
       count = static_cast<int>(W == 0 ? 0 : parts < 1 ? 1 : parts > p.grid ? p.grid : parts);
       if (c == 0 && bad) atomicOr(p.c.status, kStatusIndex);
       if (c >= count) {
@@ -226,9 +227,9 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
                           : static_cast<int>(in / cost);
         const int d = static_cast<int>(in - static_cast<long long>(h) * cost);
         int4 y = make_int4(b0 + b, in_seq, h, 0);
-        if (p.cut ? d < kChunkStart + kChunkSnap : d == 0) {
-        } else if (p.cut && cost - d >= kChunkSnap) {
-          y.w = d - kChunkStart;
+        if (p.cut ? d < kCost.start + kCost.snap : d == 0) {
+        } else if (p.cut && cost - d >= kCost.snap) {
+          y.w = d - kCost.start;
           if (which) sh->cut_first = x - d, sh->cut_cost = cost;
         } else if (++y.z == p.heads) {  // the next item is the first of the next part
           y.y += 1, y.z = 0;
@@ -247,6 +248,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
   return true;
 }
 // Names for the join the item that the CTA begins and others end.  One thread.
+template <int TILE>
 __device__ __forceinline__ void chunk_name(const ChunkParams& p, const ChunkSpan& x) {
   const int c = static_cast<int>(blockIdx.x);
   const int4 &start = x.start, &end = x.end;
@@ -261,7 +263,7 @@ __device__ __forceinline__ void chunk_name(const ChunkParams& p, const ChunkSpan
                  x.count - 1);
     while (chunk_position(x.W, x.count, c1) > last) --c1;
     while (c1 + 1 < x.count && chunk_position(x.W, x.count, c1 + 1) <= last) ++c1;
-    if (last + 1 - chunk_position(x.W, x.count, c1) < kChunkSnap) --c1;
+    if (last + 1 - chunk_position(x.W, x.count, c1) < chunk_cost(TILE).snap) --c1;
     bool ignore = false;
     const int step = chunk_step(p), tok0 = end.y * step;
     const ChunkSequence s = chunk_sequence(p, step, end.x, &ignore);

@@ -59,9 +59,10 @@ ChunkPlan plan_chunk(const jvp_cache_t* c, int64_t H, int64_t T, int query_tiles
   tiles = std::max<int64_t>(tiles, 1);
   // (items of so few tiles are not worth a join; items * heads <= 2^31 - 1, checked by the
   // caller, tiles < 2^31)
-  d.cut = tiles >= 2 * kChunkSnap ? 1 : 0;
+  const ChunkCost cost = chunk_cost(d.tile);
+  d.cut = tiles >= 2 * cost.snap ? 1 : 0;
   d.grid = static_cast<int>(
-      std::min<int64_t>(ctas, items * d.heads * (tiles + kChunkStart) / kChunkLeast + 1));
+      std::min<int64_t>(ctas, items * d.heads * (tiles + cost.start) / cost.least + 1));
   auto place = [&](size_t* at, size_t bytes) {
     *at = d.bytes;
     d.bytes += (bytes + 255) & ~static_cast<size_t>(255);

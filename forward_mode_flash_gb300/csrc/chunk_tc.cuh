@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
     if (kGather) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     else if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    if (p.cut && threadIdx.x == THREADS - 1) chunk_name(p, span);  // (before the first scores)
+    if (p.cut && threadIdx.x == THREADS - 1) chunk_name<BN>(p, span);  // (before the first scores)
     __syncwarp();
     const int x = (warp - kSoftmax) >> 2;  // query tile
     const int sub = warp & 3;       // its TMEM lanes 32 sub ..

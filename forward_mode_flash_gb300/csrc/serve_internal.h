@@ -215,9 +215,17 @@ struct ChunkMaps {
   CUtensorMap q, o, k, v;
 };
 constexpr int kChunkTile = 128, kChunkSimtTile = 64, kChunkSimtRows = 32;  // keys per tile, rows
-// Cost of an item beside its key tiles, in tiles, and the least cost for a CTA.
-constexpr int kChunkStart = 4, kChunkLeast = 9;
-constexpr int kChunkSnap = 4;  // fewest tiles of a part of a cut item
+// Cost of an item beside its key tiles, in tiles, the least cost for a CTA, and the fewest
+// tiles of a part of a cut item.  A tile of the CUDA cores' kernel takes 3 us, so one is
+// worth a CTA: 1, 3, 1 against the other's 4, 9, 4, us, fp32, 8/2 heads: 4 chunks of 150
+// tokens over 512 positions 36 / 57, a token over 5120 36 / 54, 100 over 1024 66 / 85, 2 of
+// 2000 over 4096 796 / 825.  (3, 8, 3 and 4, 8, 2 on the tensor cores: within 3%.)
+struct ChunkCost {
+  int start, least, snap;
+};
+constexpr ChunkCost chunk_cost(int tile) {
+  return tile == kChunkTile ? ChunkCost{4, 9, 4} : ChunkCost{1, 3, 1};
+}
 // source of the key tiles: boxes of parts of pages by TMA, rows gathered by threads,
 // e4m3 rows gathered and converted, or copied by TMA and converted
 enum ChunkSource { kChunkBoxes, kChunkRows, kChunkE4M3, kChunkStaged };
