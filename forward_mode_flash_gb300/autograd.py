@@ -32,6 +32,7 @@ from typing import Optional
 
 import torch
 import torch.autograd.forward_ad as fwAD
+from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -224,6 +225,7 @@ class _NormRopeDual(torch.autograd.Function):
                                   interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *g):
         q, k, dq, dk, q_weight, k_weight, rope, positions = ctx.saved_tensors
         g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k, q, k))]
@@ -259,6 +261,7 @@ class _NormRope(torch.autograd.Function):
         return t
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *g):
         q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
         g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k))]

@@ -76,9 +76,12 @@ jvp_status_t norm_rope(bool bwd, const jvp_shape_t* shape, jvp_dtype_t dtype, co
   if (B > kMax || H > kMax || N > kMax || Hkv > kMax || (N > 0 && B > kMax / N) ||
       (B * N > 0 && H + Hkv > kMax / (B * N)))
     return api_fail(JVP_ERR_UNSUPPORTED, "problem too large for one launch");
-  const bool norm = d.r.wq != nullptr, tangents = x[2] || x[3];
+  const bool norm = d.r.wq != nullptr;
+  const bool tangents = x[2] || x[3] || (bwd && !norm && (x[6] || x[7]));
   const int sides[4] = {0, 1, 2, 3};
-  for (int i = 0; i < (bwd ? 8 : 4); ++i) {
+  // (without norms the gradients do not depend on the rows)
+  const int first = bwd && !norm ? 4 : 0, inputs = bwd ? 8 : 4;
+  for (int i = first; i < inputs; ++i) {
     if ((i & 2) && !tangents) continue;
     st = check_strides(in[i], "innermost (d) stride must be 1", "negative stride");
     if (st != JVP_OK) return st;
@@ -103,7 +106,7 @@ jvp_status_t norm_rope(bool bwd, const jvp_shape_t* shape, jvp_dtype_t dtype, co
   const int64_t e = elem_bytes(dtype);
   bool vec = pieces(d.r, e);
   if (!empty) {
-    for (int i = 0; i < (bwd ? 8 : 4); ++i) {
+    for (int i = first; i < inputs; ++i) {
       const int64_t heads = (i & 1) ? Hkv : H;
       if (((i & 2) && !tangents) || heads == 0) continue;
       if (!x[i]) return api_fail(JVP_ERR_INVALID_ARG, "an input is NULL");

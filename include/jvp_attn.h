@@ -591,8 +591,7 @@ jvp_status_t jvp_attn_chunk(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dty
 
 /* Workspace bytes of jvp_attn_chunk on the current device, for any window: partial
  * outputs of one resident wave of CTAs, whatever the lengths (40 MiB at most at D =
- * 128), and some bytes per sequence and tile of new tokens; 0 for an empty problem, an
- * invalid description or no device. */
+ * 128); 0 for an empty problem, an invalid description or no device. */
 size_t jvp_attn_chunk_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype,
                                      int64_t T);
 
@@ -646,11 +645,12 @@ jvp_status_t jvp_attn_norm_rope(const jvp_shape_t* shape, jvp_dtype_t dtype, con
  * Gradients of <g_q, q_out> + <g_k, k_out> (+ <g_dq, dq_out> + <g_dk, dk_out> with
  * tangents) with respect to q, k (dq, dk) and the norm weights.
  *
- *   q, k, dq, dk   the inputs of jvp_attn_norm_rope (dq, dk NULL without tangents)
+ *   q, k, dq, dk   the inputs of jvp_attn_norm_rope (dq, dk NULL without tangents;
+ *                without norms none is read, and all may be NULL)
  *   in_strides     8 records: q, k, dq, dk, g_q, g_k, g_dq, g_dk
  *   g_q_weight, g_k_weight   float32 [D]; sums over all rows in fp32, in an order
  *                that depends on the sizes only (the same call gives the same
- *                bits).  Unused without norms, as are q, k and the workspace.
+ *                bits).  Unused without norms, as is the workspace.
  *   workspace    device scratch of at least jvp_attn_norm_rope_bwd_workspace_size()
  *                bytes, 4-byte aligned; its contents on entry do not matter.
  *

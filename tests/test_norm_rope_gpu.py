@@ -309,3 +309,68 @@ def test_another_stream():
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_a_captured_training_step():
+    """Values and gradients captured together; replays follow the inputs, and eager graphs of the
+    same leaves come before and after."""
+    rows, w = make(1, 4, 2, 40, 64, "bf16")
+    table = api.rope_table(40, 64).cuda()
+    leaves = [x.cuda().requires_grad_() for x in (*rows[:2], *w)]
+    c = [x.cuda() for x in rows[4:6]]
+
+    def step():
+        y = autograd.norm_rope(*leaves[:2], table, None, *leaves[2:], EPS)
+        return torch.autograd.grad(y, leaves, c)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        with torch.no_grad():
+            for x in (*leaves, *c):
+                x.mul_(0.75).add_(0.125)
+        graph.replay()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
+def test_gradients_of_gradients_are_refused():
+    rows, w = make(1, 2, 1, 6, 32, "f32")
+    leaves = [x.cuda().requires_grad_() for x in (*rows[:2], *w)]
+    y = autograd.norm_rope(*leaves[:2], api.rope_table(6, 32).cuda(), None, *leaves[2:], EPS)
+    g = torch.autograd.grad((y[0] ** 2).sum(), leaves[0], create_graph=True)[0]
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
+@pytest.mark.parametrize("tangents", [False, True])
+@pytest.mark.parametrize("dt,D,rot", [("bf16", 64, 64), ("f32", 33, 6)])
+def test_rotations_alone_do_not_read_the_rows_backwards(dt, D, rot, tangents):
+    """The C entry takes NULL for them."""
+    rows, _ = make(2, 3, 1, 9, D, dt)
+    q, k, dq, dk, *c = (x.cuda() for x in rows)
+    table = api.rope_table(9, rot).cuda()
+    if tangents:
+        want = api.norm_rope_bwd_dual(q, k, dq, dk, *c, table)[:4]
+    else:
+        want, c = api.norm_rope_bwd(q, k, *c[:2], table)[:2], c[:2]
+    out = [torch.full_like(x, 7.0) for x in want]
+    st = [_abi.Strides(*x.stride()[:3], 1) for x in (q, k) * 4]
+    p = lambda t, i: t[i].data_ptr() if i < len(t) else None  # noqa: E731
+    lib = _abi.load()
+    rope = _abi.Rope(table.data_ptr(), 9, rot, 0, 0, None, None, 0.0)
+    torch.cuda.synchronize()
+    r = lib.jvp_attn_norm_rope_bwd(
+        _abi.Shape(2, 3, 9, 9, D, 1), {"bf16": _abi.JVP_BF16, "f32": _abi.JVP_F32}[dt], rope, None, 0,
+        None, None, None, None, *(p(c, i) for i in range(4)), (_abi.Strides * 8)(*st),
+        *(p(out, i) for i in range(4)), (_abi.Strides * 4)(*st[:4]), None, None, None, 0, None)
+    assert r == _abi.JVP_OK
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
