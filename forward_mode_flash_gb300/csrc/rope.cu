@@ -21,6 +21,12 @@
 // columns of its pairs, so the rotation needs no exchange.  A warp takes
 // 32 / LANES tokens that follow one another and walks the heads, so the angles
 // are loaded once per token and the weights once per side (queries, keys).
+//
+// Measured, 4 x 4096 tokens, 16 + 4 heads of 128, % of the copy rate: fp32 forward 54 us
+// (91 %), with tangents 107 (92 %), gradients 95 (78 %), with tangents 171 (87 %); bf16
+// 35 (70 %), 68 (72 %), 64 (58 %) and 129 (58 %): as many instructions for half the bytes,
+// which is why elements are taken in pairs (bf16 with tangents 72 us one by one).  Rows
+// into the cache, 52k tokens, 16/8 heads of 128: 121 us, 94 %; 48 single rows 4.1 us.
 #include <cmath>
 #include <type_traits>
 
