@@ -22,11 +22,13 @@
 // 32 / LANES tokens that follow one another and walks the heads, so the angles
 // are loaded once per token and the weights once per side (queries, keys).
 //
-// Measured, 4 x 4096 tokens, 16 + 4 heads of 128, % of the copy rate: fp32 forward 54 us
-// (91 %), with tangents 107 (92 %), gradients 95 (78 %), with tangents 171 (87 %); bf16
-// 35 (70 %), 68 (72 %), 64 (58 %) and 129 (58 %): as many instructions for half the bytes,
-// which is why elements are taken in pairs (bf16 with tangents 72 us one by one).  Rows
-// into the cache, 52k tokens, 16/8 heads of 128: 121 us, 94 %; 48 single rows 4.1 us.
+// A head's rows are fetched again as soon as they are unpacked, so that loads never pause.
+//
+// Measured, 4 x 4096 tokens, 16 + 4 heads of 128, % of the copy rate: fp32 forward 55 us
+// (90 %), with tangents 106 (93 %), gradients 96 (78 %), with tangents 174 (85 %); bf16
+// 33 (75 %), 60 (82 %), 57 (65 %) and 132 (56 %): as many instructions and registers for
+// half the bytes, which is why elements are taken in pairs.  Rows into the cache, 52k
+// tokens, 16/8 heads of 128: 121 us, 94 %; 48 single rows 4.3 us.
 #include <cmath>
 #include <type_traits>
 
@@ -253,7 +255,9 @@ __device__ __forceinline__ Unit unit_of(const RopeDense& d, long long u, int per
 template <typename T, int LANES, bool IL, bool NORM, bool TAN>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) {
   constexpr int N = Piece<T>::N, PER = 32 / LANES;
-  constexpr int UN = TAN ? 2 : 4;  // heads in flight
+  // heads whose rows are on their way (bf16 33 us with 3, 38 with 2; fp32 55 with 2, 61 with 3;
+  // with tangents 60 with 1, 64 with 2)
+  constexpr int UN = TAN ? 1 : sizeof(T) == 2 ? 3 : 2;  // heads in flight
   const RopeParams& p = d.r;
   const long long u = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (u >= d.units) return;
@@ -278,16 +282,18 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) 
     const T* t_at = static_cast<const T*>(d.x[2 + side]) + (TAN ? b * st.b + n * st.n : 0);
     T* y_at = static_cast<T*>(d.y[side]) + b * so.b + n * so.n;
     T* ty_at = static_cast<T*>(d.y[2 + side]) + (TAN ? b * sto.b + n * sto.n : 0);
+    uint4 raw[UN][2], raw_t[UN][2];
+    auto fetch = [&](int k, int h) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool o = ons[i] && h < h1;
+        raw[k][i] = load_piece(x_at + (h - first) * si.h, lane.at[i], o);
+        if constexpr (TAN) raw_t[k][i] = load_piece(t_at + (h - first) * st.h, lane.at[i], o);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < UN; ++k) fetch(k, h0 + k);
     for (int h = h0; h < h1; h += UN) {
-      uint4 raw[UN][2], raw_t[UN][2];
-#pragma unroll
-      for (int k = 0; k < UN; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool o = ons[i] && h + k < h1;
-          raw[k][i] = load_piece(x_at + (h + k - first) * si.h, lane.at[i], o);
-          if constexpr (TAN) raw_t[k][i] = load_piece(t_at + (h + k - first) * st.h, lane.at[i], o);
-        }
 #pragma unroll
       for (int k = 0; k < UN; ++k) {
         if (h + k >= h1) break;  // uniform over the warp
@@ -297,6 +303,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) 
           Piece<T>::get(raw[k][i], x[i]);
           if constexpr (TAN) Piece<T>::get(raw_t[k][i], t[i]);
         }
+        fetch(k, h + k + UN);
         if constexpr (NORM) {
           const float r = inverse_root(row_sum<LANES>(dot(x, x)), p);
           if constexpr (TAN) {  // w r (dx - m n), n = r x
@@ -326,14 +333,24 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) 
 // gx (and gdx) of every row; the block's sums of the weights' gradients go to
 // the workspace, [grid][2][D].
 //
-// Blocks of an SM: 4, or 3 with tangents in 16 bits, whose rows need the registers
-// (bf16, 4 x 4096 tokens, 16 + 4 heads of 128: 64 us at 4 against 72 at 3, with
-// tangents 129 us at 3 against 165 at 4; fp32 with tangents 171 us at 4, 206 at 3).
+// Blocks of an SM, and heads whose rows are on their way: bound by latency (ncu: 34 % of
+// issue slots, 49 % of DRAM at 4 x 4096 tokens, bf16, loads waited for first), by the
+// registers that hold them in turn.  us, 16 + 4 heads of 128: bf16 57 with 4 blocks and 1
+// head (2 heads 67, 3 blocks and 2 heads 67), with tangents 132 with 2 blocks and 2 heads
+// (heads of 64 33; 3 blocks and 1 head 130, 44); fp32 96 with 4 and 3 (2 heads 99, 3 blocks
+// 116), with tangents 174 with 4 and 1 (3 and 2: 194).
+template <typename T>
+constexpr int bwd_blocks(bool tangents) {
+  return tangents && sizeof(T) == 2 ? 2 : 4;
+}
+template <typename T>
+constexpr int bwd_heads(bool tangents) {
+  return sizeof(T) == 2 ? (tangents ? 2 : 1) : (tangents ? 1 : 3);
+}
 template <typename T, int LANES, bool IL, bool TAN>
-__global__ void __launch_bounds__(kThreads, TAN && sizeof(T) == 2 ? 3 : 4)
-    norm_rope_bwd_kernel(const RopeDense d) {
+__global__ void __launch_bounds__(kThreads, bwd_blocks<T>(TAN)) norm_rope_bwd_kernel(const RopeDense d) {
   constexpr int N = Piece<T>::N, PER = 32 / LANES;
-  constexpr int UN = TAN ? 1 : 2;
+  constexpr int UN = bwd_heads<T>(TAN);
   const RopeParams& p = d.r;
   __shared__ float sums[kWarps][LANES][2 * N];
   const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
@@ -368,27 +385,33 @@ __global__ void __launch_bounds__(kThreads, TAN && sizeof(T) == 2 ? 3 : 4)
       const T* gt_at = static_cast<const T*>(d.x[6 + side]) + (TAN ? b * sgt.b + n * sgt.n : 0);
       T* o_at = static_cast<T*>(d.y[side]) + b * so.b + n * so.n;
       T* ot_at = static_cast<T*>(d.y[2 + side]) + (TAN ? b * sto.b + n * sto.n : 0);
-      for (int h = h0; h < h1; h += UN) {
-        uint4 rx[UN][2], rg[UN][2], rt[UN][2], rgt[UN][2];
+      uint4 rx[UN][2], rg[UN][2], rt[UN][2], rgt[UN][2];
+      auto fetch = [&](int k, int h) {
 #pragma unroll
-        for (int k = 0; k < UN; ++k)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool o = ons[i] && h + k < h1;
-            const int hh = h + k - first;
-            rx[k][i] = load_piece(x_at + hh * sx.h, lane.at[i], o);
-            rg[k][i] = load_piece(g_at + hh * sg.h, lane.at[i], o);
-            if constexpr (TAN) {
-              rt[k][i] = load_piece(t_at + hh * st.h, lane.at[i], o);
-              rgt[k][i] = load_piece(gt_at + hh * sgt.h, lane.at[i], o);
-            }
+        for (int i = 0; i < 2; ++i) {
+          const bool o = ons[i] && h < h1;
+          const int hh = h - first;
+          rx[k][i] = load_piece(x_at + hh * sx.h, lane.at[i], o);
+          rg[k][i] = load_piece(g_at + hh * sg.h, lane.at[i], o);
+          if constexpr (TAN) {
+            rt[k][i] = load_piece(t_at + hh * st.h, lane.at[i], o);
+            rgt[k][i] = load_piece(gt_at + hh * sgt.h, lane.at[i], o);
           }
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < UN; ++k) fetch(k, h0 + k);
+      for (int h = h0; h < h1; h += UN) {
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
           if (h + k >= h1) break;  // uniform over the warp
-          float x[2][N], g[2][N];
+          float x[2][N], g[2][N], t[2][N], v[2][N];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) Piece<T>::get(rx[k][i], x[i]), Piece<T>::get(rg[k][i], g[i]);
+          for (int i = 0; i < 2; ++i) {
+            Piece<T>::get(rx[k][i], x[i]), Piece<T>::get(rg[k][i], g[i]);
+            if constexpr (TAN) Piece<T>::get(rt[k][i], t[i]), Piece<T>::get(rgt[k][i], v[i]);
+          }
+          fetch(k, h + k + UN);
           const float root = inverse_root(row_sum<LANES>(dot(x, x)), p);
           const float r = on ? root : 0.f;  // (no token: eps may be 0)
           angles.turn(lane, g);
@@ -403,10 +426,6 @@ __global__ void __launch_bounds__(kThreads, TAN && sizeof(T) == 2 ? 3 : 4)
             }
           const float un = row_sum<LANES>(dot(g, x)) * p.inv_d;
           if constexpr (TAN) {
-            float t[2][N], v[2][N];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              Piece<T>::get(rt[k][i], t[i]), Piece<T>::get(rgt[k][i], v[i]);
             angles.turn(lane, v);
             const float m = row_sum<LANES>(dot(x, t)) * p.inv_d;
 #pragma unroll
@@ -841,14 +860,18 @@ cudaError_t with_type(DType dt, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-// Units (warps' work): all heads of a group of tokens, or so few that the GPU has
-// `want` warps.  Dense rows want 8 an SM: fewer heads a unit load the angles and
-// weights more often (fp16, 1024 tokens, 32 heads of 64: 9.5 us at 8, 14.4 at 32).
-void split_heads(long long groups, int heads, long long want, int least, int* per_unit, int* chunks) {
-  int n = heads;
-  while (n > least && groups * ((heads + n - 1) / n) < want) n = (n + 1) / 2;
-  *per_unit = n < 1 ? 1 : n;
-  *chunks = (heads + *per_unit - 1) / *per_unit;
+// Units (warps' work) of a group of tokens: its heads in so many parts that `warps` at a
+// time take the fewest rounds of heads, a unit's beginning (angles, weights, first loads)
+// counted as one and a half.
+void split_heads(long long groups, int heads, long long warps, int* per_unit, int* chunks) {
+  long long best = -1;
+  *per_unit = 1, *chunks = heads > 0 ? heads : 1;
+  for (int c = 1; c <= heads; ++c) {
+    const int n = (heads + c - 1) / c;
+    if (c > 1 && n == (heads + c - 2) / (c - 1)) continue;  // (as many parts are not needed)
+    const long long cost = (groups * c + warps - 1) / warps * (2 * n + 3);
+    if (best < 0 || cost < best) best = cost, *per_unit = n, *chunks = c;
+  }
 }
 
 cudaError_t launch_join(const RopeDense& d, int blocks, cudaStream_t stream) {
@@ -871,8 +894,8 @@ cudaError_t launch_norm_rope(DType dt, bool vec, bool bwd, RopeDense d, int num_
                              cudaStream_t stream) {
   const bool norm = d.r.wq != nullptr, tan = d.x[2] != nullptr || d.x[3] != nullptr;
   // (one at least: without rows the weights' gradients are zeros)
-  auto blocks_within = [&](long long blocks) {
-    const long long most = static_cast<long long>(num_sms) * rope_blocks_per_sm();
+  auto blocks_within = [&](long long blocks, int per_sm) {
+    const long long most = static_cast<long long>(num_sms) * per_sm;
     return static_cast<int>(blocks < 1 ? 1 : blocks < most ? blocks : most);
   };
   return with_type(dt, [&](auto t) -> cudaError_t {
@@ -880,7 +903,7 @@ cudaError_t launch_norm_rope(DType dt, bool vec, bool bwd, RopeDense d, int num_
     if (!vec) {
       const long long rows = d.tokens * (d.H > d.Hkv ? d.H : d.Hkv);
       const long long blocks = (rows + kWarps - 1) / kWarps;
-      const int grid = blocks_within(blocks);
+      const int grid = blocks_within(blocks, rope_blocks_per_sm());
       if (bwd && norm) norm_rope_any_kernel<T, true><<<grid, kThreads, 0, stream>>>(d);
       else norm_rope_any_kernel<T, false><<<grid, kThreads, 0, stream>>>(d);
       const cudaError_t e = cudaGetLastError();
@@ -889,15 +912,16 @@ cudaError_t launch_norm_rope(DType dt, bool vec, bool bwd, RopeDense d, int num_
     return with_lanes<T>(d.r.D, [&](auto lanes) -> cudaError_t {
       constexpr int LANES = decltype(lanes)::value;
       const long long groups = (d.tokens + 32 / LANES - 1) / (32 / LANES);
-      split_heads(groups, d.H + d.Hkv, 8ll * num_sms, tan ? 2 : 4, &d.heads_per_unit,
-                  &d.head_chunks);
+      const int per_sm = bwd && norm ? bwd_blocks<T>(tan) : rope_blocks_per_sm();
+      split_heads(groups, d.H + d.Hkv, static_cast<long long>(num_sms) * per_sm * kWarps,
+                  &d.heads_per_unit, &d.head_chunks);
       d.units = groups * d.head_chunks;
       const long long blocks = (d.units + kWarps - 1) / kWarps;
       return with_bool(d.r.interleaved, [&](auto il) -> cudaError_t {
         return with_bool(tan, [&](auto tg) -> cudaError_t {
           constexpr bool IL = decltype(il)::value, TAN = decltype(tg)::value;
           if (bwd && norm) {
-            const int grid = blocks_within(blocks);
+            const int grid = blocks_within(blocks, per_sm);
             norm_rope_bwd_kernel<T, LANES, IL, TAN><<<grid, kThreads, 0, stream>>>(d);
             const cudaError_t e = cudaGetLastError();
             return e != cudaSuccess ? e : launch_join(d, grid, stream);
@@ -935,7 +959,8 @@ cudaError_t launch_cache_append(DType dt, bool e4m3, bool vec, AppendParams a, i
       return with_lanes<T>(a.r.D, [&](auto lanes) -> cudaError_t {
         constexpr int LANES = decltype(lanes)::value;
         const long long groups = (a.T + 32 / LANES - 1) / (32 / LANES);
-        split_heads(groups, all, 16ll * num_sms, 1, &a.heads_per_unit, &a.head_chunks);
+        split_heads(groups, all, static_cast<long long>(num_sms) * rope_blocks_per_sm() * kWarps,
+                    &a.heads_per_unit, &a.head_chunks);
         a.units = groups * a.head_chunks;
         return with_bool(a.r.interleaved, [&](auto il) -> cudaError_t {
           return with_bool(a.r.wq != nullptr, [&](auto nm) -> cudaError_t {
