@@ -480,12 +480,14 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
           const int from = max(hidden, min(rows, max(0, w.past + w.tok0 + 1 - j0)));
           using E = PackedElem<T>;
           uint32_t found[4] = {0u, 0u, 0u, 0u};
-          for (int ch = 0; ch < KCH; ++ch) {
-            const uint32_t at = v + ch * BN * 128;
+#pragma unroll 1
+          for (int part = 0; part < 2 * KCH; ++part) {
+            const uint32_t at = v + (part >> 1) * BN * 128;
+            const uint32_t last = at + (part & 1 ? rows : hidden) * 128;
 #pragma unroll 4
-            for (int e = lane; e < (hidden + rows - from) * 8; e += 32) {
+            for (uint32_t to = at + (part & 1 ? from : 0) * 128 + lane * 16; to < last; to += 512) {
               uint32_t x[4];
-              ld_shared_v4(at + (e < hidden * 8 ? e : e + (from - hidden) * 8) * 16, x);
+              ld_shared_v4(to, x);
 #pragma unroll
               for (int i = 0; i < 4; ++i) E::zeros(x[i], &found[i]);
             }
