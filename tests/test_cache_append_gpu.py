@@ -159,3 +159,12 @@ def test_captured_graph_follows_positions():
     want = q.clone()
     got, e = append(c, x, w, None, start, table)
     assert torch.equal(got, want) and torch.equal(e["k_cache"], d["k_cache"])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dt,D,rot", [("bf16", 128, 128), ("f16", 64, 32), ("f32", 33, 6), ("bf16", 40, 20)])
+def test_queries_in_place(dt, D, rot, interleaved):
+    a = case([30, 1], [3, 70], 4, 2, D, dt, rot=rot, seed=6)
+    want, _ = append(*a, interleaved=interleaved)
+    got, _ = append(*a, interleaved=interleaved, out=a[1]["q"])
+    assert got.data_ptr() == a[1]["q"].data_ptr() and torch.equal(got, want)

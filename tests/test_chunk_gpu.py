@@ -439,3 +439,22 @@ def test_every_code_of_an_e4m3_cache(dt, page):
                           k_scale=d["k_scale"], v_scale=d["v_scale"], dtype=DT[dt])
     same = (o == v) | (torch.isnan(o) & torch.isnan(v))
     assert same.all(), same.logical_not().nonzero()[:5]
+
+
+@pytest.mark.parametrize("window,sinks", [(5, 900), (5, 2 ** 40), (2 ** 40, 7), (130, 128), (128, 129)])
+@pytest.mark.parametrize("dt,H,Hkv,D,page,e4m3", [
+    ("bf16", 8, 2, 128, 16, False), ("f16", 4, 4, 64, 20, False), ("bf16", 8, 2, 128, 16, True),
+    ("f32", 4, 2, 64, 16, False)])
+def test_sinks_that_reach_into_the_window(dt, H, Hkv, D, page, e4m3, window, sinks):
+    c, q, cu = make(NEW, PAST, H, Hkv, D, dt, page, e4m3, seed=D + 1)
+    o, lse = run(c, q, cu, window, sinks)
+    check(c, q, cu, o, lse, window, sinks, heads=[0, H - 1])
+
+
+@pytest.mark.parametrize("dt,e4m3", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_sequences_that_share_pages(dt, e4m3):
+    """A common beginning, cached once: each sequence as by itself."""
+    c, q, cu = make([40, 40, 3], [600, 600, 600], 4, 2, 64, dt, 16, e4m3, seed=9)
+    c.table[1:, :40] = c.table[0, :40]  # (the last pages are each one's own)
+    o, lse = run(c, q, cu)
+    check(c, q, cu, o, lse)

@@ -135,3 +135,14 @@ def test_refusals():
             call(q, c, window, sinks)
     with pytest.raises(TypeError):
         call(q, c, 2.5, 0)
+
+
+@pytest.mark.parametrize("window,sinks", [(5, 5000), (1, 700), (64, 65), (2 ** 40, 3)])
+@pytest.mark.parametrize("dt,H,Hkv,D,page,e4m3", [
+    ("bf16", 8, 2, 128, 16, False), ("f16", 4, 4, 64, 20, False), ("bf16", 16, 1, 128, 64, True),
+    ("f32", 4, 2, 64, 16, False)])
+def test_sinks_that_reach_into_the_window(dt, H, Hkv, D, page, e4m3, window, sinks):
+    c = Cache(LENS, Hkv, D, page, DT[dt], e4m3, seed=3)
+    q = queries(c, H, dt)
+    o, lse = call(q, c, window, sinks)
+    check(q, c, window, sinks, o, lse)

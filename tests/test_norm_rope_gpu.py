@@ -374,3 +374,16 @@ def test_rotations_alone_do_not_read_the_rows_backwards(dt, D, rot, tangents):
     assert r == _abi.JVP_OK
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_broadcast_inputs():
+    """Queries and keys expanded over the batch: the gradients of what was expanded are sums."""
+    rows, w = make(1, 4, 2, 30, 64, "f32", seed=8)
+    table = api.rope_table(30, 64).cuda()
+    c = [torch.randn(3, h, 30, 64, generator=torch.Generator().manual_seed(h)).cuda() for h in (4, 2)]
+    got = []
+    for expand in (lambda x: x.expand(3, -1, -1, -1), lambda x: x.repeat(3, 1, 1, 1)):
+        leaves = [x.cuda().requires_grad_() for x in (*rows[:2], *w)]
+        y = autograd.norm_rope(*(expand(x) for x in leaves[:2]), table, None, *leaves[2:], EPS)
+        got.append((*y, *torch.autograd.grad(y, leaves, c)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
