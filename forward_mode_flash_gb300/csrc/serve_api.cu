@@ -99,11 +99,17 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms, in
           : decode_simt_ctas_per_sm(d.heads_per_block));
   const int tile = decode_tile(tc, D, c->dtype == JVP_E4M3);
   int64_t tiles = (most + tile - 1) / tile;
-  // (a window's keys begin anywhere in a tile)
-  if (window > 0) tiles = std::min(tiles, (window + tile - 2) / tile + 1 + (sinks + tile - 1) / tile);
   // B * Hkv * head_blocks <= B * H <= 2^31 - 1 (checked by the caller), tiles < 2^31
   const int64_t segments = c->B * c->Hkv * d.head_blocks;
-  if (tiles > 0 && tiles <= kDecodeDirectTiles) {
+  int direct = kDecodeDirectTiles;
+  if (window > 0) {  // (its keys begin anywhere in a tile)
+    const int64_t seen = (window + tile - 2) / tile + 1 + (sinks + tile - 1) / tile;
+    if (seen < tiles) {
+      tiles = seen;
+      if (tc) direct = decode_window_direct(D, segments >= num_sms);
+    }
+  }
+  if (tiles > 0 && tiles <= direct) {
     d.grid = static_cast<int>(segments), d.direct = 1;
     return d;
   }
@@ -133,11 +139,11 @@ jvp_status_t check_decode(const jvp_cache_t* c, int64_t H, int dtype) {
 
 // window: 0 for none.
 jvp_status_t decode(const jvp_cache_t* cache, int64_t H, jvp_dtype_t dtype, const void* q,
-                             const jvp_strides_t* q_strides, const void* k_cache,
-                             const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
-                             const int32_t* block_table, const int32_t* seq_lens, int64_t window,
-                    int64_t sinks, float scale,                             void* o, const jvp_strides_t* o_strides, float* lse, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+                    const jvp_strides_t* q_strides, const void* k_cache, const void* v_cache,
+                    const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                    const int32_t* seq_lens, int64_t window, int64_t sinks, float scale, void* o,
+                    const jvp_strides_t* o_strides, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   api_set_path(0);
   jvp_status_t st = check_decode(cache, H, dtype);
   if (st != JVP_OK) return st;

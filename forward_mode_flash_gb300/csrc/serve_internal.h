@@ -145,6 +145,14 @@ constexpr int decode_ctas_per_sm(int D, int head_groups, bool e4m3) {
 // Where no sequence can have more tiles than this, a CTA takes a whole segment
 // and nothing is joined.
 constexpr int kDecodeDirectTiles = 4;
+// The same on the tensor cores where a window leaves every sequence so few tiles: more, and with a segment for
+// every SM as many as a CTA reads while the others' parts would be joined.  Direct against
+// split, us in a graph, bf16, 16/4 heads of 128 (tiles of 64 keys): window 200, 1 / 8 / 48 /
+// 200 sequences 7.1 / 7.6 / 8.4 / 22 against 7.4 / 8.3 / 14.6 / 30; 500 9.9 / 10.5 / 12 / 35
+// against 7.5 / 9.5 / 16.4 / 39; 1000 16 / 16 / 18.7 / 56 against 7.5 / 10.5 / 20.7 / 57.
+// 16/8 heads of 64 (128 keys): 500 7.6 / 8.0 / 16.3 / 49 against 7.3 / 9.3 / 18.1 / 50; 1000
+// 11 / 11 / 23 / 71 against 7.4 / 11.9 / 22.5 / 69.
+constexpr int decode_window_direct(int D, bool enough) { return enough && D > 64 ? 18 : 6; }
 
 cudaError_t launch_decode(DType dt, bool e4m3, bool tc, bool vec, const DecodeParams& p,
                           cudaStream_t stream);
