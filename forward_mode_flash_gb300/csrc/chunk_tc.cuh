@@ -39,8 +39,9 @@
 
 namespace jvp {
 
-// The gathering sources: threads, and registers (65536 / 640 a thread, 96: 48 + 2 * 72 +
-// 2 * 144 = 5 * 96); their staging area lies behind the control block.
+// The gathering sources: 640 threads of 96 registers at launch (copies and products 80, two
+// warpgroups of gathering 64 each, two of softmax 136: 480 = 5 * 96); their staging area lies
+// behind the control block.
 constexpr int kGatherWarps = 8;
 constexpr int chunk_threads(int NQ, ChunkSource src) {
   return packed_threads(NQ) + (src == kChunkBoxes ? 0 : 32 * kGatherWarps);
