@@ -214,15 +214,33 @@ def _weight_grads(g, weights):
     return tuple(None if w is None else x.to(w.dtype) for x, w in zip(g, weights))
 
 
+def _tangents(given, tensors):
+    """Tangents that the kernels can read, zeros for none (a zero without storage among
+    them); None for tensors that are not there."""
+    def usable(t, x):
+        if t is None or t._is_zerotensor():
+            return torch.zeros_like(x)
+        return t if t.stride(-1) == 1 else t.contiguous()
+    return tuple(None if x is None else usable(t, x) for t, x in zip(given, tensors))
+
+
 class _NormRopeDual(torch.autograd.Function):
     """(q, k, dq, dk) of one norm_rope_dual call; backward = reverse mode of the dual map."""
 
     @staticmethod
-    def forward(ctx, q, k, dq, dk, q_weight, k_weight, rope, positions, eps, interleaved):
-        ctx.save_for_backward(q, k, dq, dk, q_weight, k_weight, rope, positions)
-        ctx.options = eps, interleaved
+    def forward(q, k, dq, dk, q_weight, k_weight, rope, positions, eps, interleaved):
         return api.norm_rope_dual(q, k, dq, dk, rope, positions, q_weight, k_weight, eps,
                                   interleaved)
+
+    @staticmethod
+    def setup_context(ctx, inputs, output):
+        ctx.save_for_forward(*inputs[:8])
+        ctx.save_for_backward(*inputs[:8])
+        ctx.options = inputs[8:]
+
+    @staticmethod
+    def jvp(ctx, *_):
+        raise RuntimeError("norm_rope: tangents of tangents are not supported")
 
     @staticmethod
     @once_differentiable
@@ -249,15 +267,14 @@ class _NormRope(torch.autograd.Function):
 
     @staticmethod
     def jvp(ctx, dq, dk, dqw, dkw, *_):
-        with torch._C._DisableFuncTorch():  # (as in JVPAttn.jvp)
-            q, k, q_weight, k_weight, rope, positions = (_plain(t) for t in ctx.saved_tensors)
-            dq, dk = (_zeros_if_none(_plain(t), x) for t, x in ((dq, q), (dk, k)))
-            t = api.norm_rope_dual(q, k, dq, dk, rope, positions, q_weight, k_weight,
-                                   *ctx.options)[2:]
-            if dqw is not None or dkw is not None:  # the outputs are linear in the weights
-                dw = [_zeros_if_none(_plain(x), w) for x, w in ((dqw, q_weight), (dkw, k_weight))]
-                more = api.norm_rope(q, k, rope, positions, *dw, *ctx.options)
-                t = tuple(x + y for x, y in zip(t, more))
+        # (by functions again, so that the tangents have a history at every level)
+        q, k, q_weight, k_weight, *rest = ctx.saved_tensors
+        t = _NormRopeDual.apply(q, k, *_tangents((dq, dk), (q, k)), q_weight, k_weight, *rest,
+                                *ctx.options)[2:]
+        if dqw is not None or dkw is not None:  # the outputs are linear in the weights
+            dw = _tangents((dqw, dkw), (q_weight, k_weight))
+            more = _NormRope.apply(q, k, *dw, *rest, *ctx.options)
+            t = tuple(x + y for x, y in zip(t, more))
         return t
 
     @staticmethod
@@ -270,7 +287,10 @@ class _NormRope(torch.autograd.Function):
 
 
 def _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved):
-    """(q, k) as forward-mode duals from one fused call, or None (see _fused_under_jvp)."""
+    """(q, k) as forward-mode duals from one fused call, or None (see _fused_under_jvp).
+
+    Any of q, k and the weights may carry a tangent at this level; what is of no level
+    is taken as it is.  What is of another one is left to the generic rule."""
     level = _ft.maybe_current_level()
     if level is None:
         return None
@@ -279,10 +299,8 @@ def _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interle
         return _ft.is_functorch_wrapped_tensor(x) and _ft.maybe_get_level(x) == level
 
     def one_level(t):
-        return _ft.get_unwrapped(t) if t is not None and _ft.is_functorch_wrapped_tensor(t) else t
+        return _ft.get_unwrapped(t) if t is not None and here(t) else t
 
-    if not here(q) or not here(k):
-        return None
     xs = (q, k, q_weight, k_weight)
     pairs = [fwAD.unpack_dual(x) if x is not None and here(x) else (x, None) for x in xs]
     if all(t is None for _, t in pairs):
@@ -292,12 +310,12 @@ def _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interle
     if any(t is not None and _ft.is_functorch_wrapped_tensor(t) for t in (*ps, *ts, *rest)):
         return None  # nested transforms: the generic forward-mode rule handles them
     with torch._C._DisableFuncTorch():
-        d = [_zeros_if_none(t, p) for t, p in zip(ts[:2], ps[:2])]
+        d = _tangents(ts[:2], ps[:2])
     y = _record(_NormRopeDual, *ps[:2], *d, *ps[2:], *rest, eps, interleaved)
     out, tangents = y[:2], y[2:]
     if ts[2] is not None or ts[3] is not None:  # the outputs are linear in the weights
         with torch._C._DisableFuncTorch():
-            dw = [_zeros_if_none(t, w) for t, w in zip(ts[2:], ps[2:])]
+            dw = _tangents(ts[2:], ps[2:])
         more = _record(_NormRope, *ps[:2], *dw, *rest, eps, interleaved)
         with torch._C._DisableFuncTorch():
             tangents = tuple(x + z for x, z in zip(tangents, more))
@@ -310,9 +328,10 @@ def norm_rope(q, k, rope: Optional[torch.Tensor] = None, positions: Optional[tor
               eps: float = 1e-6, interleaved: bool = False):
     """Differentiable ``api.norm_rope``: (q, k), for ``jvp_attention``.
 
-    Inside torch.func.jvp the outputs carry their tangents, from one fused pass, and
-    values and tangents are differentiable with respect to q, k, their tangents and
-    the norm weights (rope and positions are constants)."""
+    With forward-mode tangents of any of q, k and the norm weights the outputs carry
+    theirs (inside torch.func.jvp from one fused pass), and values and tangents are
+    differentiable with respect to q, k, the norm weights and their tangents (rope and
+    positions are constants)."""
     fused = _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
     if fused is not None:
         return fused
