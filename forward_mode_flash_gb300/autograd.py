@@ -32,7 +32,6 @@ from typing import Optional
 
 import torch
 import torch.autograd.forward_ad as fwAD
-from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -224,6 +223,37 @@ def _tangents(given, tensors):
     return tuple(None if x is None else usable(t, x) for t, x in zip(given, tensors))
 
 
+def _run(function, *args):
+    """function.apply, without its cost where nothing can differentiate the result."""
+    if torch.is_grad_enabled() or _ft.maybe_current_level() is not None or fwAD._current_level >= 0:
+        return function.apply(*args)
+    return function.forward(*args)
+
+
+class _NormRopeDualGrads(torch.autograd.Function):
+    """Gradients of _NormRopeDual's results for cotangents g."""
+
+    @staticmethod
+    def forward(q, k, dq, dk, q_weight, k_weight, rope, positions, eps, interleaved, *g):
+        g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k, q, k))]
+        out = api.norm_rope_bwd_dual(q, k, dq, dk, *g, rope, positions, q_weight, k_weight, eps,
+                                     interleaved)
+        return (*out[:4], *_weight_grads(out[4:], (q_weight, k_weight)))
+
+    @staticmethod
+    def setup_context(ctx, inputs, output):
+        pass
+
+    @staticmethod
+    def jvp(ctx, *_):
+        raise RuntimeError("norm_rope: gradients of tangents have no tangents of their own (with "
+                           "torch.autograd.forward_ad, call backward behind the dual_level)")
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("norm_rope is once_differentiable: its gradients have none of their own")
+
+
 class _NormRopeDual(torch.autograd.Function):
     """(q, k, dq, dk) of one norm_rope_dual call; backward = reverse mode of the dual map."""
 
@@ -243,13 +273,29 @@ class _NormRopeDual(torch.autograd.Function):
         raise RuntimeError("norm_rope: tangents of tangents are not supported")
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, *g):
-        q, k, dq, dk, q_weight, k_weight, rope, positions = ctx.saved_tensors
-        g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k, q, k))]
-        out = api.norm_rope_bwd_dual(q, k, dq, dk, *g, rope, positions, q_weight, k_weight,
-                                     *ctx.options)
-        return (*out[:4], *_weight_grads(out[4:], (q_weight, k_weight)), None, None, None, None)
+        return (*_run(_NormRopeDualGrads, *ctx.saved_tensors, *ctx.options, *g), None, None, None,
+                None)
+
+
+class _NormRopeGrads(torch.autograd.Function):
+    """Gradients of _NormRope's results for cotangents g."""
+
+    @staticmethod
+    def forward(q, k, q_weight, k_weight, rope, positions, eps, interleaved, *g):
+        g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k))]
+        out = api.norm_rope_bwd(q, k, *g, rope, positions, q_weight, k_weight, eps, interleaved)
+        return (*out[:2], *_weight_grads(out[2:], (q_weight, k_weight)))
+
+    @staticmethod
+    def setup_context(ctx, inputs, output):
+        pass
+
+    @staticmethod
+    def jvp(ctx, *_):
+        raise RuntimeError("norm_rope: gradients have no tangents of their own")
+
+    backward = _NormRopeDualGrads.backward
 
 
 class _NormRope(torch.autograd.Function):
@@ -278,12 +324,8 @@ class _NormRope(torch.autograd.Function):
         return t
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, *g):
-        q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
-        g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k))]
-        out = api.norm_rope_bwd(q, k, *g, rope, positions, q_weight, k_weight, *ctx.options)
-        return (*out[:2], *_weight_grads(out[2:], (q_weight, k_weight)), None, None, None, None)
+        return (*_run(_NormRopeGrads, *ctx.saved_tensors, *ctx.options, *g), None, None, None, None)
 
 
 def _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved):
@@ -331,7 +373,8 @@ def norm_rope(q, k, rope: Optional[torch.Tensor] = None, positions: Optional[tor
     With forward-mode tangents of any of q, k and the norm weights the outputs carry
     theirs (inside torch.func.jvp from one fused pass), and values and tangents are
     differentiable with respect to q, k, the norm weights and their tangents (rope and
-    positions are constants)."""
+    positions are constants).  Gradients come once: what would need gradients or
+    tangents of them raises."""
     fused = _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
     if fused is not None:
         return fused

@@ -178,6 +178,39 @@ def at_list(f, args, which, some):
     return g
 
 
+def gradients(f, args, tangents, c, which):
+    """torch.func.grad of a loss of the values."""
+    return torch.func.grad(lambda *x: loss(f(*x), (), c), argnums=which)(*args)
+
+
+def pulled_back(f, args, tangents, c, which):
+    """torch.func.vjp by some arguments."""
+    y, back = torch.func.vjp(at(f, args, which), *(args[i] for i in which))
+    return (*y, *back(tuple(c[:2])))
+
+
+def tangents_of_gradients(f, args, tangents, c, which):
+    """torch.func.jvp over torch.func.grad, of a loss whose cotangents depend on the values."""
+    def grads(*some):
+        return torch.func.grad(lambda *x: sum((a * b).sin().sum() for a, b in zip(f(*x), c)),
+                               argnums=(0, 1, 2, 3))(*at_list(lambda *x: x, args, which, some)(*args))
+    g, t = torch.func.jvp(grads, tuple(args[i] for i in which), tuple(tangents[i] for i in which))
+    return (*g, *t)
+
+
+def tangents_of_gradients_by_dual_tensors(f, args, tangents, c, which):
+    """The same by torch.autograd.forward_ad and torch.autograd.grad within its level."""
+    with fwAD.dual_level():
+        leaves = [x.clone().requires_grad_() for x in args]
+        full = list(leaves)
+        for i in which:
+            full[i] = fwAD.make_dual(leaves[i], tangents[i])
+        g = torch.autograd.grad(sum((a * b).sin().sum() for a, b in zip(f(*full), c)), leaves)
+        pairs = [fwAD.unpack_dual(x) for x in g]
+        return [p.primal.clone() for p in pairs] + [
+            torch.zeros_like(p.primal) if p.tangent is None else p.tangent.clone() for p in pairs]
+
+
 def compare(way, to, table, *rest, dtype=torch.float32, **kw):
     """Asserts that a way gives the same of the framework's function and of the definition's."""
     args, tangents, c = data(dtype)

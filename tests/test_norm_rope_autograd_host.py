@@ -22,3 +22,31 @@ ways = pytest.mark.parametrize("way", [ra.train_through_jvp, ra.train_through_du
 @ways
 def test_tangents_of_some_arguments(way, which):
     ra.compare(way, lambda x: x, TABLE, which)
+
+
+@some
+@pytest.mark.parametrize("way", [ra.gradients, ra.pulled_back], ids=lambda f: f.__name__)
+def test_transforms_of_torch_func(way, which):
+    ra.compare(way, lambda x: x, TABLE, which)
+
+
+@some
+def test_gradients_of_tangents(which):
+    ra.compare(ra.grad_of_jvp, lambda x: x, TABLE, which)
+    if len(which) < 4:
+        ra.compare(ra.grad_of_others, lambda x: x, TABLE, which)
+
+
+def test_gradients_of_gradients_are_refused():
+    """Also where the cotangents are constants, and within torch.func."""
+    c, table = ra.data()[2], TABLE
+    args = [x.requires_grad_() for x in ra.data()[0]]
+    y = ra.own(table)(*args)
+    g = torch.autograd.grad(ra.loss(y, (), c), args[0], create_graph=True)[0]
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        ((g ** 2).sum() + args[0].sum()).backward()
+
+    def first(q):
+        return torch.func.grad(lambda q: ra.loss(ra.own(table)(q, *args[1:]), (), c))(q).sum()
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        torch.func.grad(first)(args[0].detach())
