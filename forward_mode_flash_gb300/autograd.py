@@ -289,11 +289,25 @@ class _NormRopeGrads(torch.autograd.Function):
 
     @staticmethod
     def setup_context(ctx, inputs, output):
-        pass
+        ctx.save_for_forward(*inputs[:6], *inputs[8:])
+        ctx.options = inputs[6:8]
 
     @staticmethod
-    def jvp(ctx, *_):
-        raise RuntimeError("norm_rope: gradients have no tangents of their own")
+    def jvp(ctx, dq, dk, dqw, dkw, _rope, _positions, _eps, _interleaved, *dg):
+        # The gradients are those of <g, y>, so their tangents are the gradients of
+        # <dg, y> + <g, dy> by the same tensors.
+        q, k, q_weight, k_weight, rope, positions, *g = ctx.saved_tensors
+        weights, rest = (q_weight, k_weight), (rope, positions, *ctx.options)
+        cotangents = *_tangents(dg, (q, k)), *_tangents(g, (q, k))
+        out = _NormRopeDualGrads.apply(q, k, *_tangents((dq, dk), (q, k)), *weights, *rest,
+                                       *cotangents)
+        t = *out[:2], *out[4:]
+        if dqw is not None or dkw is not None:
+            # dy is linear in the weights, so this changes those of q and k alone
+            more = _NormRopeGrads.apply(q, k, *_tangents((dqw, dkw), weights), *rest,
+                                        *cotangents[2:])
+            t = *(x + y for x, y in zip(t, more[:2])), *t[2:]
+        return t
 
     backward = _NormRopeDualGrads.backward
 
@@ -373,8 +387,8 @@ def norm_rope(q, k, rope: Optional[torch.Tensor] = None, positions: Optional[tor
     With forward-mode tangents of any of q, k and the norm weights the outputs carry
     theirs (inside torch.func.jvp from one fused pass), and values and tangents are
     differentiable with respect to q, k, the norm weights and their tangents (rope and
-    positions are constants).  Gradients come once: what would need gradients or
-    tangents of them raises."""
+    positions are constants).  Gradients may have tangents, but no gradients of their
+    own: what would need these raises, as do tangents of tangents."""
     fused = _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
     if fused is not None:
         return fused

@@ -50,3 +50,27 @@ def test_gradients_of_gradients_are_refused():
         return torch.func.grad(lambda q: ra.loss(ra.own(table)(q, *args[1:]), (), c))(q).sum()
     with pytest.raises(RuntimeError, match="once_differentiable"):
         torch.func.grad(first)(args[0].detach())
+
+
+@some
+@pytest.mark.parametrize("way", [ra.tangents_of_gradients, ra.tangents_of_gradients_by_dual_tensors],
+                         ids=lambda f: f.__name__)
+def test_tangents_of_gradients(way, which):
+    ra.compare(way, cuda, TABLE, which)
+
+
+def test_what_has_no_derivative_is_refused():
+    """Tangents of tangents, and of the gradients of tangents."""
+    args, tangents, c = ([x.cuda() for x in z] for z in ra.data())
+    f = ra.own(TABLE.cuda())
+
+    def tangent(q):
+        return torch.func.jvp(lambda q: f(q, *args[1:]), (q,), (tangents[0],))[1]
+    with pytest.raises(RuntimeError, match="tangents of tangents"):
+        torch.func.jvp(tangent, (args[0],), (tangents[0],))
+
+    with ra.fwAD.dual_level():
+        y = f(ra.fwAD.make_dual(args[0].requires_grad_(), tangents[0]), *args[1:])
+        t = ra.fwAD.unpack_dual(y[0]).tangent
+        with pytest.raises(RuntimeError, match="gradients of tangents"):
+            t.sum().backward()
