@@ -223,6 +223,11 @@ def _tangents(given, tensors):
     return tuple(None if x is None else usable(t, x) for t, x in zip(given, tensors))
 
 
+def _weight_tangents(given, weights):
+    """Tangents of both weights, or of none."""
+    return (None, None) if all(t is None for t in given) else _tangents(given, weights)
+
+
 def _run(function, *args):
     """function.apply, without its cost where nothing can differentiate the result."""
     if torch.is_grad_enabled() or _ft.maybe_current_level() is not None or fwAD._current_level >= 0:
@@ -230,15 +235,27 @@ def _run(function, *args):
     return function.forward(*args)
 
 
+def _wide(*tensors):
+    return [x.float() for x in tensors]
+
+
 class _NormRopeDualGrads(torch.autograd.Function):
     """Gradients of _NormRopeDual's results for cotangents g."""
 
     @staticmethod
-    def forward(q, k, dq, dk, q_weight, k_weight, rope, positions, eps, interleaved, *g):
+    def forward(q, k, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, eps,
+                interleaved, *g):
         g = [_dense_cotangent(x, like) for x, like in zip(g, (q, k, q, k))]
-        out = api.norm_rope_bwd_dual(q, k, dq, dk, *g, rope, positions, q_weight, k_weight, eps,
-                                     interleaved)
-        return (*out[:4], *_weight_grads(out[4:], (q_weight, k_weight)))
+        w, dw, options = (q_weight, k_weight), (dq_weight, dk_weight), (eps, interleaved)
+        if dq_weight is None:
+            out = api.norm_rope_bwd_dual(q, k, dq, dk, *g, rope, positions, *w, *options)
+            return (*out[:4], *_weight_grads(out[4:], w), None, None)
+        rows, g = _wide(q, k, dq, dk), _wide(*g)
+        out = api.norm_rope_bwd_dual(*rows, *g, rope, positions, *w, *options)
+        more = api.norm_rope_bwd(*rows[:2], *g[2:], rope, positions, *dw, *options)
+        out = (*(x + y for x, y in zip(out[:2], more)), *out[2:])
+        return (*(x.to(q.dtype) for x in out[:4]), *_weight_grads(out[4:], w),
+                *_weight_grads(more[2:], dw))
 
     @staticmethod
     def setup_context(ctx, inputs, output):
@@ -255,18 +272,32 @@ class _NormRopeDualGrads(torch.autograd.Function):
 
 
 class _NormRopeDual(torch.autograd.Function):
-    """(q, k, dq, dk) of one norm_rope_dual call; backward = reverse mode of the dual map."""
+    """(q, k, dq, dk) of one norm_rope_dual call; backward = reverse mode of the dual map.
+
+    Tangents of the weights (None: none): the outputs are linear in the weights, so a
+    second call that has these for weights gives what they add.  Both take 16-bit
+    rows in 32 bits then, so that the sums are rounded once."""
 
     @staticmethod
-    def forward(q, k, dq, dk, q_weight, k_weight, rope, positions, eps, interleaved):
-        return api.norm_rope_dual(q, k, dq, dk, rope, positions, q_weight, k_weight, eps,
-                                  interleaved)
+    def forward(q, k, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, eps,
+                interleaved):
+        w, dw, options = (q_weight, k_weight), (dq_weight, dk_weight), (eps, interleaved)
+        if dq_weight is None:
+            return api.norm_rope_dual(q, k, dq, dk, rope, positions, *w, *options)
+        rows = _wide(q, k, dq, dk)
+        y = api.norm_rope_dual(*rows, rope, positions, *w, *options)
+        more = api.norm_rope(*rows[:2], rope, positions, *dw, *options)
+        if q.dtype == torch.float32:
+            values = y[:2]
+        else:
+            values = api.norm_rope(q, k, rope, positions, *w, *options)
+        return (*values, *((x + z).to(q.dtype) for x, z in zip(y[2:], more)))
 
     @staticmethod
     def setup_context(ctx, inputs, output):
-        ctx.save_for_forward(*inputs[:8])
-        ctx.save_for_backward(*inputs[:8])
-        ctx.options = inputs[8:]
+        ctx.save_for_forward(*inputs[:10])
+        ctx.save_for_backward(*inputs[:10])
+        ctx.options = inputs[10:]
 
     @staticmethod
     def jvp(ctx, *_):
@@ -297,17 +328,11 @@ class _NormRopeGrads(torch.autograd.Function):
         # The gradients are those of <g, y>, so their tangents are the gradients of
         # <dg, y> + <g, dy> by the same tensors.
         q, k, q_weight, k_weight, rope, positions, *g = ctx.saved_tensors
-        weights, rest = (q_weight, k_weight), (rope, positions, *ctx.options)
-        cotangents = *_tangents(dg, (q, k)), *_tangents(g, (q, k))
-        out = _NormRopeDualGrads.apply(q, k, *_tangents((dq, dk), (q, k)), *weights, *rest,
-                                       *cotangents)
-        t = *out[:2], *out[4:]
-        if dqw is not None or dkw is not None:
-            # dy is linear in the weights, so this changes those of q and k alone
-            more = _NormRopeGrads.apply(q, k, *_tangents((dqw, dkw), weights), *rest,
-                                        *cotangents[2:])
-            t = *(x + y for x, y in zip(t, more[:2])), *t[2:]
-        return t
+        w = q_weight, k_weight
+        out = _NormRopeDualGrads.apply(q, k, *_tangents((dq, dk), (q, k)), *w,
+                                       *_weight_tangents((dqw, dkw), w), rope, positions,
+                                       *ctx.options, *_tangents((*dg, *g), (q, k, q, k)))
+        return (*out[:2], *out[4:6])
 
     backward = _NormRopeDualGrads.backward
 
@@ -327,15 +352,12 @@ class _NormRope(torch.autograd.Function):
 
     @staticmethod
     def jvp(ctx, dq, dk, dqw, dkw, *_):
-        # (by functions again, so that the tangents have a history at every level)
-        q, k, q_weight, k_weight, *rest = ctx.saved_tensors
-        t = _NormRopeDual.apply(q, k, *_tangents((dq, dk), (q, k)), q_weight, k_weight, *rest,
-                                *ctx.options)[2:]
-        if dqw is not None or dkw is not None:  # the outputs are linear in the weights
-            dw = _tangents((dqw, dkw), (q_weight, k_weight))
-            more = _NormRope.apply(q, k, *dw, *rest, *ctx.options)
-            t = tuple(x + y for x, y in zip(t, more))
-        return t
+        # (by a function again, so that the tangents have a history at every level)
+        q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
+        w = q_weight, k_weight
+        return _NormRopeDual.apply(q, k, *_tangents((dq, dk), (q, k)), *w,
+                                   *_weight_tangents((dqw, dkw), w), rope, positions,
+                                   *ctx.options)[2:]
 
     @staticmethod
     def backward(ctx, *g):
@@ -366,17 +388,10 @@ def _norm_rope_under_jvp(q, k, q_weight, k_weight, rope, positions, eps, interle
     if any(t is not None and _ft.is_functorch_wrapped_tensor(t) for t in (*ps, *ts, *rest)):
         return None  # nested transforms: the generic forward-mode rule handles them
     with torch._C._DisableFuncTorch():
-        d = _tangents(ts[:2], ps[:2])
-    y = _record(_NormRopeDual, *ps[:2], *d, *ps[2:], *rest, eps, interleaved)
-    out, tangents = y[:2], y[2:]
-    if ts[2] is not None or ts[3] is not None:  # the outputs are linear in the weights
-        with torch._C._DisableFuncTorch():
-            dw = _tangents(ts[2:], ps[2:])
-        more = _record(_NormRope, *ps[:2], *dw, *rest, eps, interleaved)
-        with torch._C._DisableFuncTorch():
-            tangents = tuple(x + z for x, z in zip(tangents, more))
+        d, dw = _tangents(ts[:2], ps[:2]), _weight_tangents(ts[2:], ps[2:])
+    y = _record(_NormRopeDual, *ps[:2], *d, *ps[2:], *dw, *rest, eps, interleaved)
     return tuple(fwAD.make_dual(_ft._wrap_for_grad(o, level), _ft._wrap_for_grad(t, level))
-                 for o, t in zip(out, tangents))
+                 for o, t in zip(y[:2], y[2:]))
 
 
 def norm_rope(q, k, rope: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,

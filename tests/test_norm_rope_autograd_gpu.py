@@ -74,3 +74,12 @@ def test_what_has_no_derivative_is_refused():
         t = ra.fwAD.unpack_dual(y[0]).tangent
         with pytest.raises(RuntimeError, match="gradients of tangents"):
             t.sum().backward()
+
+
+@some
+@pytest.mark.parametrize("way", [ra.train_through_jvp, ra.values_by_dual_tensors],
+                         ids=lambda f: f.__name__)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_one_rounding_of_the_result(dtype, way, which):
+    """In 16 bits, also where the tangents are sums of those by the rows and the weights."""
+    ra.compare(way, cuda, TABLE, which, dtype=dtype)
