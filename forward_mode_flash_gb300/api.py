@@ -999,8 +999,8 @@ def cache_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: tor
     A row's position in its sequence (``start_pos[b]`` + its place among the sequence's
     rows) is its row of ``rope``; rope, weights, eps and interleaved are those of
     ``norm_rope``, and the rest of the arguments those of ``cache_write``.  Returns the
-    normalised and rotated queries [T, H, D] (``out`` if given), for
-    ``attention_chunk`` or ``attention_decode``.  The cache holds what ``norm_rope``
+    normalised and rotated queries [T, H, D] (``out`` if given; it may be q itself),
+    for ``attention_chunk`` or ``attention_decode``.  The cache holds what ``norm_rope``
     and ``cache_write`` would leave there.  Tokens whose place is out of range, or
     whose position is no row of rope, are skipped whole and reported by
     ``device_status`` (JVP_ERR_INDEX); rows that belong to no sequence are ignored.

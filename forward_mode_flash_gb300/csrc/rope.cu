@@ -711,8 +711,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
       for (int k = 0; k < UN; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          raw[k][i] =
-              load_piece(x_at + (h + k - first) * si.h, lane.at[i], ons[i] && h + k < h1);
+          raw[k][i] =  // (not the read-only path: q_out may be q)
+              ons[i] && h + k < h1
+                  ? *reinterpret_cast<const uint4*>(x_at + (h + k - first) * si.h + lane.at[i])
+                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int k = 0; k < UN; ++k) {
         if (h + k >= h1) break;  // uniform over the warp
@@ -812,6 +814,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_any_kernel(const Append
     y[k] = side < 2 ? Rows<T>::put(any.turned(u_of, d, false)) : x[d];
     top = fmaxf(top, fabsf(Rows<T>::get(y[k])));
   }
+  __syncwarp();  // q_out may be q, of which lanes read one another's columns
   const Strides& sc = side == 1 ? c.sk : c.sv;
   const long long to = side == 0 ? r * a.sq_out.n + h * a.sq_out.h
                                  : page * sc.b + row * sc.n + h * sc.h;

@@ -681,6 +681,7 @@ size_t jvp_attn_norm_rope_bwd_workspace_size(int64_t D);
  *
  *   H            query heads (any number, 0: none).
  *   in_strides   3 records: q, k, v.
+ *   q_out        may be q, with the same strides; no other output may overlap an input.
  *
  * The other arguments, and what is skipped and reported, are those of
  * jvp_attn_cache_write; a token whose position is no row of the table, or whose
