@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(chunk_threads(NQ, SRC), SRC == kChunkBoxes ? 3
   static_assert(sizeof(ChunkScratch) <= L::OFF_CTRL - L::OFF_K, "the tiles' space");
   if (!chunk_divide<BN, THREADS>(p, reinterpret_cast<ChunkScratch*>(smem + L::OFF_K), &span))
     return;
+  fence_proxy_async_smem();  // TMA writes tiles where the division's scratch was
   if (warp == 1) {
     tmem_alloc(&ctrl->tmem_base, L::TM_COLS);
     tmem_relinquish();
