@@ -136,7 +136,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
                                              ChunkSpan* span) {
   const int tid = static_cast<int>(threadIdx.x), B = p.c.B, step = chunk_step(p);
   constexpr ChunkCost kCost = chunk_cost(TILE);
-  bool bad = false;
+  bool bad = false, over = false;
   int b0 = 0, nb = 0;  // sequences in shared memory
   // A thread takes neighbouring sequences, and neighbouring items, so that there is one
   // sum over the block for each, however many there are.
@@ -150,8 +150,12 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
       items += s.items;
     }
     long long total;
-    const int before = static_cast<int>(chunk_block_sum<THREADS>(items, sh->part, &total));
-    for (int i = i0; i < i1; ++i) sh->first[i] += before;
+    long long before = chunk_block_sum<THREADS>(items, sh->part, &total);
+    // More items than rows and sequences: sequences overlap, however good the offsets of
+    // each, and none is taken (the sum may pass an int, and the work any bound).
+    over |= total > static_cast<long long>(p.T) + nb;
+    if (over) bad = true, before = total = 0;
+    for (int i = i0; i < i1; ++i) sh->first[i] = over ? 0 : sh->first[i] + static_cast<int>(before);
     if (tid == 0) sh->first[nb] = static_cast<int>(total);
     __syncthreads();
     return static_cast<int>(total);
@@ -183,7 +187,7 @@ __device__ __forceinline__ bool chunk_divide(const ChunkParams& p, ChunkScratch*
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
-      W = all * p.heads;
+      W = over ? 0 : all * p.heads;
       const long long parts = W / kCost.least;
       count = static_cast<int>(W == 0 ? 0 : parts < 1 ? 1 : parts > p.grid ? p.grid : parts);
       if (c == 0 && bad) atomicOr(p.c.status, kStatusIndex);

@@ -562,7 +562,8 @@ size_t jvp_attn_decode_workspace_size(const jvp_cache_t* cache, int64_t H, jvp_d
  *   seq_lens     int32 [B]: positions of each sequence, its new tokens included.  A
  *                token whose position is negative (n < len) sees nothing.
  *   cu_seqlens   int32 [B + 1] as in jvp_attn_fwd_packed: rows of no sequence are
- *                not written, bad offsets are reported and their sequences skipped.
+ *                not written, bad offsets are reported and their sequences skipped (all,
+ *                where sequences overlap so much that their tiles outnumber the rows).
  *   window       0: none.  Positions that no token of a sequence's chunk sees are not
  *                read, and their block-table entries may hold anything.
  *   sinks        not negative; without a window of no effect.
