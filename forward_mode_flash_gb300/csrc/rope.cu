@@ -869,11 +869,13 @@ cudaError_t with_type(DType dt, F&& f) {
 void split_heads(long long groups, int heads, long long warps, int* per_unit, int* chunks) {
   long long best = -1;
   *per_unit = 1, *chunks = heads > 0 ? heads : 1;
-  for (int c = 1; c <= heads; ++c) {
-    const int n = (heads + c - 1) / c;
-    if (c > 1 && n == (heads + c - 2) / (c - 1)) continue;  // (as many parts are not needed)
+  for (long long c = 1; c <= heads;) {
+    const long long n = (heads + c - 1) / c;
     const long long cost = (groups * c + warps - 1) / warps * (2 * n + 3);
-    if (best < 0 || cost < best) best = cost, *per_unit = n, *chunks = c;
+    if (best < 0 || cost < best)
+      best = cost, *per_unit = static_cast<int>(n), *chunks = static_cast<int>(c);
+    if (n == 1) break;
+    c = (heads + n - 2) / (n - 1);  // the fewest parts that are smaller
   }
 }
 
