@@ -106,7 +106,9 @@ DecodePlan plan_decode(const jvp_cache_t* c, int64_t H, bool tc, int num_sms, in
     const int64_t seen = (window + tile - 2) / tile + 1 + (sinks + tile - 1) / tile;
     if (seen < tiles) {
       tiles = seen;
-      if (tc) direct = decode_window_direct(D, segments >= num_sms);
+      if (tc)
+        direct = decode_window_direct(D, c->dtype == JVP_E4M3, d.heads_per_block,
+                                      segments >= num_sms);
     }
   }
   if (tiles > 0 && tiles <= direct) {

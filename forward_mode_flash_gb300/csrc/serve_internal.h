@@ -145,14 +145,26 @@ constexpr int decode_ctas_per_sm(int D, int head_groups, bool e4m3) {
 // Where no sequence can have more tiles than this, a CTA takes a whole segment
 // and nothing is joined.
 constexpr int kDecodeDirectTiles = 4;
-// The same on the tensor cores where a window leaves every sequence so few tiles: more, and with a segment for
-// every SM as many as a CTA reads while the others' parts would be joined.  Direct against
-// split, us in a graph, bf16, 16/4 heads of 128 (tiles of 64 keys): window 200, 1 / 8 / 48 /
-// 200 sequences 7.1 / 7.6 / 8.4 / 22 against 7.4 / 8.3 / 14.6 / 30; 500 9.9 / 10.5 / 12 / 35
-// against 7.5 / 9.5 / 16.4 / 39; 1000 16 / 16 / 18.7 / 56 against 7.5 / 10.5 / 20.7 / 57.
-// 16/8 heads of 64 (128 keys): 500 7.6 / 8.0 / 16.3 / 49 against 7.3 / 9.3 / 18.1 / 50; 1000
-// 11 / 11 / 23 / 71 against 7.4 / 11.9 / 22.5 / 69.
-constexpr int decode_window_direct(int D, bool enough) { return enough && D > 64 ? 18 : 6; }
+// The same on the tensor cores where a window leaves every sequence so few tiles: more, since
+// a split and its join cost 2 us and more, and with a segment for every SM as many as a CTA
+// reads while the others' parts would be joined.  A tile is 64 keys of 16 bits at D > 64, else
+// 128.  Direct against split, us in a graph, D = 128 (96 is alike), by window:
+//   few segments     8 x 16/4 heads, bf16   300 7.8 / 8.1    500 9.8 / 9.2
+//                    8 x 16/1 heads, bf16   200 8.1 / 8.4    300 9.6 / 8.7
+//                    8 x 16/4 heads, e4m3   300 8.2 / 8.2    400 9.2 / 8.6
+//                    8 x 16/1 heads, e4m3   300 10.5 / 9.8   400 11.8 / 10.0
+//   one for each SM  40 x 16/4 heads, bf16  700 13.7 / 16.0  1000 18.0 / 17.4  2000 32 / 33
+//                    160 x 16/1 heads, bf16 700 17.6 / 25.2  1000 22.8 / 27.1  2000 40 / 42
+//                    40 x 16/4 heads, e4m3  1000 16.4 / 17.2 1500 21.2 / 19.7  2000 27 / 22
+//                    160 x 16/1 heads, e4m3 1000 21.1 / 31.4 1500 27.7 / 33.6  2000 34 / 36
+//   many             200 x 16/4 heads, bf16 700 52 / 57      1000 69 / 74
+//                    200 x 16/4 heads, e4m3 1000 44 / 52     2000 76 / 81
+// and D = 64: 8 x 16/4 heads, bf16, 600 7.5 / 8.0, e4m3 500 8.0 / 8.6; 8 x 16/1 heads, bf16, 500
+// 8.3 / 8.1, e4m3 300 9.1 / 8.9; 40 x 16/4 heads, bf16, 700 9.2 / 12.7, e4m3 700 10.8 / 13.5.
+constexpr int decode_window_direct(int D, bool e4m3, int heads_per_block, bool enough) {
+  if (enough) return D <= 64 ? 6 : e4m3 ? 9 : 18;  // (some 750 and 1100 keys)
+  return 6 - (e4m3 ? 1 : 0) - (heads_per_block > 8 ? 1 : 0);
+}
 
 cudaError_t launch_decode(DType dt, bool e4m3, bool tc, bool vec, const DecodeParams& p,
                           cudaStream_t stream);
