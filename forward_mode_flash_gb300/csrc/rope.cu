@@ -128,23 +128,20 @@ struct Angles {
     }
   }
   // x = R x, or R^T x with the angles loaded for the way back
-  __device__ __forceinline__ void turn(const Lane<T, LANES, IL>& lane, float (&x)[2][N],
-                                       bool back = false) const {
-    const float f = back ? -1.f : 1.f;
+  __device__ __forceinline__ void turn(const Lane<T, LANES, IL>& lane, float (&x)[2][N]) const {
     if constexpr (IL) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (!lane.turned[i]) continue;
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-          const float cc = c[(i * N + e) / 2], ss = f * s[(i * N + e) / 2];
-          turn_pair(cc, ss, &x[i][e], &x[i][e + 1]);
+          turn_pair(c[(i * N + e) / 2], s[(i * N + e) / 2], &x[i][e], &x[i][e + 1]);
         }
       }
     } else if (lane.turned[0]) {
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
-        const float2 cc = two(&c[e]), ss = mul2(both(f), two(&s[e]));
+        const float2 cc = two(&c[e]), ss = two(&s[e]);
         const float2 a = two(&x[0][e]), b = two(&x[1][e]);
         put2(&x[0][e], fma2(a, cc, minus(mul2(b, ss))));
         put2(&x[1][e], fma2(b, cc, mul2(a, ss)));
@@ -208,7 +205,7 @@ __device__ __forceinline__ uint4 load_piece(const T* row, int at, bool on) {
   return on ? __ldg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// y = R (w n) of a row in place; returns r (for its tangent).
+// y = R (w n) of a row in place.
 template <typename T, int LANES, bool IL, bool NORM, int N>
 __device__ __forceinline__ void norm_and_turn(const RopeParams& p, const Lane<T, LANES, IL>& lane,
                                               const Angles<T, LANES, IL>& angles,
@@ -880,17 +877,8 @@ void split_heads(long long groups, int heads, long long warps, int* per_unit, in
 }
 
 cudaError_t launch_join(const RopeDense& d, int blocks, cudaStream_t stream) {
-  // placed while the kernel in front still runs; it waits for it
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((d.r.D + kJoinCols - 1) / kJoinCols), 2);
-  cfg.blockDim = dim3(kJoinCols * kJoinRows);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_join_kernel, d, blocks);
+  const dim3 grid(static_cast<unsigned>((d.r.D + kJoinCols - 1) / kJoinCols), 2);
+  return launch_dependent(norm_rope_join_kernel, grid, kJoinCols * kJoinRows, 0, stream, d, blocks);
 }
 
 }  // namespace

@@ -229,7 +229,7 @@ struct ChunkParams {
   float* ws_o;       // [grid][2][rows of an item][64 or 128] normalised partial outputs
   float* ws_lse;     // [grid][2][rows of an item], log2 units
   int box_rows;      // tensor cores: keys of a copied box, a divisor of 128 and the page size
-  int vec;           // CUDA cores: 16-byte aligned rows of whole 16-byte pieces
+  int vec;           // CUDA cores: rows of whole pieces of four elements, aligned to these
 };
 struct ChunkMaps {
   CUtensorMap q, o, k, v;
@@ -258,10 +258,10 @@ cudaError_t launch_chunk_join(DType dt, int kernel_d, int rows, const ChunkParam
 // Launches a kernel that may be placed while the one before it on the stream runs,
 // and waits for it by itself (griddepcontrol.wait).
 template <typename... P>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, int smem,
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem,
                              cudaStream_t stream, const P&... params) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.gridDim = grid, cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
