@@ -794,8 +794,10 @@ def attention_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     anything).  H is a multiple of the cache's heads (grouped-query attention).
     Returns o [T, H, D], or (o, lse) with ``return_lse`` (float32 [H, T]); a token that
     sees nothing gets o = 0 and lse = -inf, and rows that belong to no sequence are not
-    written.  ``workspace`` as in ``attention_decode`` (``chunk_workspace_size`` bytes).
-    Forward only, as ``attention_packed``.
+    written.  Over an e4m3 cache float16 and bfloat16 queries take its entries as
+    ``cache_read`` gives them in that type (float16: infinite beyond 65504, where
+    ``attention_decode`` keeps the scale apart).  ``workspace`` as in ``attention_decode``
+    (``chunk_workspace_size`` bytes).  Forward only, as ``attention_packed``.
     """
     if workspace is not None and (workspace.device != k_cache.device
                                   or not workspace.is_contiguous()):

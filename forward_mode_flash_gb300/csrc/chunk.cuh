@@ -7,9 +7,9 @@
 // list's cost: it continues an item that others began, takes whole ones, and begins
 // one that others end.  So CTAs are equally loaded whatever the lengths, which only
 // the device knows, and an item is cut only where a CTA's part ends (and not within
-// ChunkCost::snap tiles of its ends).  Each CTA finds its part by itself: the costs of all
-// items are summed by its threads, some 2 us (a kernel of one block in
-// front that did it for all, its successor's set-up beside it, took 5.5).  Parts of
+// ChunkCost::snap tiles of its ends).  Each CTA finds its part by itself, from the costs of
+// all items, which its threads sum: it knows it 3.7 us after its start (a kernel of one
+// block in front that did it for all, its successor's set-up beside it, took 5.5 by itself).  Parts of
 // cut items leave normalised outputs and log-sum-exps in the workspace, two slots
 // per CTA, for the join.
 #pragma once

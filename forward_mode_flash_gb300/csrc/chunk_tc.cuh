@@ -29,7 +29,7 @@
 // Bound: at D = 128 a pair of query tiles takes 1.55 us a key tile from boxes, 2.0 us
 // from rows, 2.25 us from codes (1.27 us is the tensor core's at its measured rate,
 // and the exponentials alone 1.07 us); at D = 64 1.4, 1.87 and 1.93 us.  A call begins and
-// ends with some 20 us that no tile hides: 3.5 us until a CTA knows its part, 4 us to its
+// ends with some 20 us that no tile hides: 3.7 us until a CTA knows its part, 4 to 6 us to its
 // first scores, 2.5 us of epilogue, 5 us for the join: most of it first passes over
 // instructions.
 #pragma once

@@ -26,9 +26,12 @@
 //
 // Measured, 4 x 4096 tokens, 16 + 4 heads of 128, % of the copy rate: fp32 forward 55 us
 // (90 %), with tangents 106 (93 %), gradients 96 (78 %), with tangents 174 (85 %); bf16
-// 33 (75 %), 60 (82 %), 57 (65 %) and 132 (56 %): as many instructions and registers for
-// half the bytes, which is why elements are taken in pairs.  Rows into the cache, 52k
-// tokens, 16/8 heads of 128: 121 us, 94 %; 48 single rows 4.3 us.
+// 33 (75 %), 60 (82 %), 57 (65 %) and 130 (57 %): as many instructions and registers for
+// half the bytes, which is why elements are taken in pairs.  Rows into the cache, 47k
+// tokens, 16/8 heads of 128, 64 columns rotated: 121 us, 94 %; 48 single rows 4.3 us.
+// Rows of any layout cost far more, since a warp takes one and reads its columns one by
+// one: bf16 heads of 40, or 80 of which 40 are rotated, 205 and 257 us forward, 244 and
+// 375 backward, 52k rows into the cache 690 and 790 us (4 to 10 %).
 #include <cmath>
 #include <type_traits>
 
@@ -330,10 +333,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeDense d) 
 // gx (and gdx) of every row; the block's sums of the weights' gradients go to
 // the workspace, [grid][2][D].
 //
-// Blocks of an SM, and heads whose rows are on their way: bound by latency (ncu: 34 % of
-// issue slots, 49 % of DRAM at 4 x 4096 tokens, bf16, loads waited for first), by the
+// Blocks of an SM, and heads whose rows are on their way: bound by latency (ncu: 45 % of
+// issue slots, 56 % of DRAM at 4 x 4096 tokens, bf16, loads waited for first), by the
 // registers that hold them in turn.  us, 16 + 4 heads of 128: bf16 57 with 4 blocks and 1
-// head (2 heads 67, 3 blocks and 2 heads 67), with tangents 132 with 2 blocks and 2 heads
+// head (2 heads 67, 3 blocks and 2 heads 67), with tangents 130 with 2 blocks and 2 heads
 // (heads of 64 33; 3 blocks and 1 head 130, 44); fp32 96 with 4 and 3 (2 heads 99, 3 blocks
 // 116), with tangents 174 with 4 and 1 (3 and 2: 194).
 template <typename T>
