@@ -53,19 +53,14 @@ def _dense_cotangent(g, like):
     return g.contiguous()
 
 
-def _plain(t):
-    """The storage-backed tensor under torch.func's wrappers.
-
-    Under torch.func.jvp the tensors a function sees are wrapper tensors
-    without storage; the kernels need the underlying device buffers.  The
-    underlying tensor is the one of the enclosing (ordinary autograd) level,
-    with its autograd history.
-    """
-    if t is None:
-        return None
-    while _ft.is_functorch_wrapped_tensor(t):
-        t = _ft.get_unwrapped(t)
-    return t
+def _tangents(given, tensors):
+    """Tangents that the kernels can read, zeros for none (a zero without storage among
+    them); None for tensors that are not there."""
+    def usable(t, x):
+        if t is None or t._is_zerotensor():
+            return torch.zeros_like(x)
+        return t if t.stride(-1) == 1 else t.contiguous()
+    return tuple(None if x is None else usable(t, x) for t, x in zip(given, tensors))
 
 
 class _FwdDual(torch.autograd.Function):
@@ -107,28 +102,28 @@ def _record(function, *args):
 def _fused_under_jvp(q, k, v, attn_mask, is_causal, scale):
     """O as a forward-mode dual (O, tO) from one fused call, or None.
 
-    Applies when q, k, v are torch.func wrappers of the innermost transform
-    level and at least one of them carries a forward-mode tangent there (the
-    body of torch.func.jvp).  The primals and tangents are unwrapped to the
-    enclosing level's tensors, one _FwdDual node is recorded in that level's
-    autograd graph (so O and tO are differentiable through bwd_dual), and O
-    and tO are wrapped back as the dual output of this level.  Anything else
-    (no transform, other transforms such as vmap at this level, jvp nested in
-    another transform) returns None.
+    Applies when any of q, k, v is a torch.func wrapper of the innermost transform
+    level that carries a forward-mode tangent there (the body of torch.func.jvp);
+    what is of no level is taken as it is, without a tangent.  The primals and
+    tangents are unwrapped to the enclosing level's tensors, one _FwdDual node is
+    recorded in that level's autograd graph (so O and tO are differentiable through
+    bwd_dual), and O and tO are wrapped back as the dual output of this level.
+    Anything else (no transform, other transforms such as vmap at this level, jvp
+    nested in another transform) returns None.
     """
     level = _ft.maybe_current_level()
     if level is None:
         return None
-    xs = (q, k, v)
-    if not all(_ft.is_functorch_wrapped_tensor(x) and _ft.maybe_get_level(x) == level for x in xs):
-        return None
-    pairs = [fwAD.unpack_dual(x) for x in xs]
-    if all(t is None for _, t in pairs):
-        return None
+
+    def here(x):
+        return _ft.is_functorch_wrapped_tensor(x) and _ft.maybe_get_level(x) == level
 
     def one_level(t):  # the enclosing level's tensor (must be a plain one)
-        return _ft.get_unwrapped(t) if _ft.is_functorch_wrapped_tensor(t) else t
+        return _ft.get_unwrapped(t) if here(t) else t
 
+    pairs = [fwAD.unpack_dual(x) if here(x) else (x, None) for x in (q, k, v)]
+    if all(t is None for _, t in pairs):
+        return None
     ps = [one_level(p) for p, _ in pairs]
     ts = [torch.zeros_like(p) if t is None else one_level(t) for p, (_, t) in zip(ps, pairs)]
     mask = None if attn_mask is None else one_level(attn_mask)
@@ -136,6 +131,30 @@ def _fused_under_jvp(q, k, v, attn_mask, is_causal, scale):
         return None  # nested transforms: the generic forward-mode rule handles them
     o, t_o = _record(_FwdDual, *ps, *ts, mask, is_causal, scale)
     return fwAD.make_dual(_ft._wrap_for_grad(o, level), _ft._wrap_for_grad(t_o, level))
+
+
+class _FwdDualRule(torch.autograd.Function):
+    """_FwdDual for the forward-mode rule of JVPAttn, at every level of torch.func: also
+    lse and its tangent, which have no gradients."""
+
+    @staticmethod
+    def forward(q, k, v, dq, dk, dv, attn_mask, is_causal, scale):
+        return api.fwd_dual(q, k, v, dq, dk, dv, attn_mask=attn_mask, is_causal=is_causal,
+                            scale=scale, return_stats=True)
+
+    @staticmethod
+    def setup_context(ctx, inputs, output):
+        ctx.mark_non_differentiable(*output[2:])
+        ctx.save_for_backward(*inputs[:6], *output)
+        ctx.attn_mask, ctx.is_causal, ctx.scale = inputs[6:]
+
+    @staticmethod
+    def jvp(ctx, *_):
+        raise RuntimeError("jvp_attention: tangents of tangents are not supported")
+
+    @staticmethod
+    def backward(ctx, g_o, g_to, *_):
+        return _FwdDual.backward(ctx, g_o, g_to)
 
 
 class JVPAttn(torch.autograd.Function):
@@ -157,16 +176,12 @@ class JVPAttn(torch.autograd.Function):
 
     @staticmethod
     def jvp(ctx, dq, dk, dv, *_):
-        # Outside torch.func's dispatch, so that the output buffers the binding
-        # allocates are plain device tensors too.  (Reached for forward-mode AD
-        # that the fused route above does not take, e.g. torch.autograd's
-        # forward_ad dual tensors; the returned tangent has no autograd history.)
-        with torch._C._DisableFuncTorch():
-            q, k, v, _o, lse = (_plain(t) for t in ctx.saved_tensors)
-            dq, dk, dv = (_zeros_if_none(_plain(t), x) for t, x in ((dq, q), (dk, k), (dv, v)))
-            _, t_o, _, mu = api.fwd_dual(q, k, v, dq, dk, dv, attn_mask=_plain(ctx.attn_mask),
-                                         is_causal=ctx.is_causal, scale=ctx.scale,
-                                         return_stats=True)
+        # (Reached for forward-mode AD that the fused route above does not take, e.g.
+        # torch.autograd's forward_ad dual tensors; by a function again, so that the
+        # tangent has a history at every level.)
+        q, k, v = ctx.saved_tensors[:3]
+        _, t_o, _, mu = _FwdDualRule.apply(q, k, v, *_tangents((dq, dk, dv), (q, k, v)),
+                                           ctx.attn_mask, ctx.is_causal, ctx.scale)
         return t_o, mu  # mu is the tangent of lse
 
     @staticmethod
@@ -211,16 +226,6 @@ def jvp_attention(q, k, v, attn_mask: Optional[torch.Tensor] = None, is_causal: 
 # ---- norms of queries and keys, and rotation
 def _weight_grads(g, weights):
     return tuple(None if w is None else x.to(w.dtype) for x, w in zip(g, weights))
-
-
-def _tangents(given, tensors):
-    """Tangents that the kernels can read, zeros for none (a zero without storage among
-    them); None for tensors that are not there."""
-    def usable(t, x):
-        if t is None or t._is_zerotensor():
-            return torch.zeros_like(x)
-        return t if t.stride(-1) == 1 else t.contiguous()
-    return tuple(None if x is None else usable(t, x) for t, x in zip(given, tensors))
 
 
 def _weight_tangents(given, weights):

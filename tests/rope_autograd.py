@@ -143,9 +143,8 @@ def train_through_dual_tensors(f, args, tangents, c, which):
             full[i] = fwAD.make_dual(leaves[i], x)
         pairs = [fwAD.unpack_dual(x) for x in f(*full)]
     y, t = [p.primal for p in pairs], [p.tangent for p in pairs]
-    on = [i for i in (0, 1) if t[i] is not None]  # (a side without tangents has none)
-    t = [torch.zeros_like(a) if b is None else b for a, b in zip(y, t)]
-    assert on
+    assert any(x is not None for x in t)
+    t = [torch.zeros_like(a) if b is None else b for a, b in zip(y, t)]  # (of a side without)
     return (*y, *t, *torch.autograd.grad(loss(y, t, c), leaves + moving))
 
 
